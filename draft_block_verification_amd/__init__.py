@@ -13,7 +13,11 @@ from ._lib import (EXPORTED, FLAG_WAIT, FLAG_NO_RESIDUAL, FLAG_ROW_OFFSETS, FLAG
                    sd_verify_contraction, sd_verify_contraction_w12, sd_verify_greedy,
                    sd_verify_greedy_noalloc, sd_verify_greedy_w12, NOALLOC_SCRATCH_BYTES,
                    sd_verify_logits, sd_verify_logits_w12, stats_to_numpy, verify_workspace_bytes,
-                   w12_encode)
+                   w12_encode,
+                   FLAG_EMPTY_ROW, FLAG_SAMPLING, Mxfp4Weights, SamplingParams,
+                   accept_filtered_workspace_bytes, mxfp4_columns,
+                   mxfp4_logits_workspace_bytes, sample_workspace_bytes, sd_accept_filtered,
+                   sd_mxfp4_dequantize, sd_mxfp4_logits, sd_mxfp4_quantize, sd_sample)
 
 __all__ = ["EXPORTED", "FLAG_WAIT", "FLAG_NO_RESIDUAL", "FLAG_ROW_OFFSETS", "FLAG_VERIFY_LEN", "LIB_PATH",
            "LM_HEAD_BLOCKED", "LM_HEAD_ROWS", "LM_HEAD_W12", "sd_verify_rejection",
@@ -25,4 +29,8 @@ __all__ = ["EXPORTED", "FLAG_WAIT", "FLAG_NO_RESIDUAL", "FLAG_ROW_OFFSETS", "FLA
            "sd_verify_contraction", "sd_verify_contraction_w12", "sd_verify_greedy",
            "sd_verify_greedy_noalloc", "sd_verify_greedy_w12", "NOALLOC_SCRATCH_BYTES",
            "sd_verify_logits",
-           "sd_verify_logits_w12", "stats_to_numpy", "verify_workspace_bytes", "w12_encode"]
+           "sd_verify_logits_w12", "stats_to_numpy", "verify_workspace_bytes", "w12_encode",
+           "FLAG_EMPTY_ROW", "FLAG_SAMPLING", "Mxfp4Weights", "SamplingParams",
+           "accept_filtered_workspace_bytes", "mxfp4_columns", "mxfp4_logits_workspace_bytes",
+           "sample_workspace_bytes", "sd_accept_filtered", "sd_mxfp4_dequantize",
+           "sd_mxfp4_logits", "sd_mxfp4_quantize", "sd_sample"]

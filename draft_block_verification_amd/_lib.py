@@ -24,7 +24,8 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-_i32, _f32, _sz, _vp = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_i32, _i64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_sz, _vp = ctypes.c_size_t, ctypes.c_void_p
 _SIGS = {
     "sd_abi_version": (_i32, []),
     "sd_status_string": (ctypes.c_char_p, [_i32]),
@@ -65,6 +66,18 @@ _SIGS = {
     "sd_verify_rejection": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz,
                                    _vp]),
+    "sd_mxfp4_columns": (_i32, [_i32]),
+    "sd_mxfp4_quantize": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
+    "sd_mxfp4_dequantize": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp]),
+    "sd_mxfp4_logits_workspace_bytes": (_sz, [_i32, _i32]),
+    "sd_mxfp4_logits": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _vp, _sz,
+                               _vp]),
+    "sd_sample_workspace_bytes": (_sz, [_i32, _i32]),
+    "sd_sample": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp,
+                         _sz, _vp]),
+    "sd_accept_filtered_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "sd_accept_filtered": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp,
+                                  _vp, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -79,6 +92,7 @@ ROW_STATS_DTYPE = np.dtype([("argmax", "<i4"), ("top1", "<f4"), ("top2", "<f4"),
 assert ROW_STATS_DTYPE.itemsize == 32
 
 FLAG_VERIFY_LEN, FLAG_ROW_OFFSETS, FLAG_NO_RESIDUAL, FLAG_WAIT = 1, 2, 4, 8
+FLAG_SAMPLING, FLAG_EMPTY_ROW = 16, 32
 LM_HEAD_ROWS, LM_HEAD_BLOCKED, LM_HEAD_W12 = 0, 1, 2
 
 
@@ -623,6 +637,310 @@ def sd_verify_rejection(hidden: torch.Tensor, lm_head, draft_tokens: torch.Tenso
     return logits, stats, accept_len, next_token
 
 
+# --------------------------------------------------------------- MXFP4 and sampling
+
+_TYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None) -> None:
+    """A device matrix of an element type the library takes, with contiguous rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPE_CODES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1:
+        raise ValueError(f"{name} must have contiguous, separate rows, got strides {t.stride()}")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return max(t.stride(0), t.shape[1])
+
+
+def _same_device(dev: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev and t.device is not None:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call(name: str, dev: torch.device, stream, *args) -> None:
+    """The entry point on dev's current stream (or `stream`), with dev current."""
+    if dev.index == torch.cuda.current_device():
+        _check(name, getattr(_lib, name)(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(name, getattr(_lib, name)(*args, _stream(stream)))
+
+
+def mxfp4_columns(d: int) -> int:
+    """Stored columns of an MXFP4 row: d rounded up to a multiple of 128."""
+    kp = int(_lib.sd_mxfp4_columns(d))
+    if kp == 0:
+        raise ValueError(f"MXFP4 rows need a positive multiple of 8 columns, got {d}")
+    return kp
+
+
+def mxfp4_logits_workspace_bytes(rows: int, d: int) -> int:
+    return int(_lib.sd_mxfp4_logits_workspace_bytes(rows, d))
+
+
+def sample_workspace_bytes(rows: int, V: int) -> int:
+    return int(_lib.sd_sample_workspace_bytes(rows, V))
+
+
+def accept_filtered_workspace_bytes(B: int, gamma: int, V: int) -> int:
+    return int(_lib.sd_accept_filtered_workspace_bytes(B, gamma, V))
+
+
+def sd_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, stream=None):
+    """MXFP4 form of the rows of x (float32, bfloat16 or float16, any row stride): returns
+    (codes uint8 [rows][kp / 2], scales uint8 [rows][kp / 32]), kp = mxfp4_columns(d)."""
+    _rows(x, "x")
+    rows, d = x.shape
+    kp = mxfp4_columns(d)
+    if codes is None:
+        codes = torch.empty((rows, kp // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows, kp // 32), dtype=torch.uint8, device=x.device)
+    _need(codes, "codes", torch.uint8, (rows, kp // 2))
+    _need(scales, "scales", torch.uint8, (rows, kp // 32))
+    _same_device(x.device, codes=codes, scales=scales)
+    _call("sd_mxfp4_quantize", x.device, stream, _ptr(x), _TYPE_CODES[x.dtype], rows, d,
+          _row_stride(x), _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def sd_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
+                        dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """The values that MXFP4 rows stand for, [rows][d] of `dtype` (or into out)."""
+    kp = mxfp4_columns(d)
+    _need(codes, "codes", torch.uint8)
+    rows = codes.shape[0]
+    _need(codes, "codes", torch.uint8, (rows, kp // 2))
+    _need(scales, "scales", torch.uint8, (rows, kp // 32))
+    if out is None:
+        out = torch.empty((rows, d), dtype=dtype, device=codes.device)
+    _rows(out, "out")
+    if tuple(out.shape) != (rows, d):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, d)}")
+    _same_device(codes.device, scales=scales, out=out)
+    _call("sd_mxfp4_dequantize", codes.device, stream, _ptr(codes), _ptr(scales), rows, d,
+          _ptr(out), _TYPE_CODES[out.dtype], _row_stride(out))
+    return out
+
+
+class _SdMxfp4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class Mxfp4Weights:
+    """An MXFP4 LM head in device memory (codes uint8 [V][kp / 2], scales uint8 [V][kp / 32],
+    kp = mxfp4_columns(d)), for sd_mxfp4_logits. Rows without the padding, [V][d / 2] and
+    [V][d / 32] for d a multiple of 32, are copied into padded ones."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d: int):
+        kp = mxfp4_columns(d)
+        _need(codes, "codes", torch.uint8)
+        _need(scales, "scales", torch.uint8)
+        V = codes.shape[0]
+        if d % 32 == 0 and kp != d and tuple(codes.shape) == (V, d // 2):
+            _need(scales, "scales", torch.uint8, (V, d // 32))
+            codes = torch.nn.functional.pad(codes, (0, (kp - d) // 2))
+            scales = torch.nn.functional.pad(scales, (0, (kp - d) // 32))
+        _need(codes, "codes", torch.uint8, (V, kp // 2))
+        _need(scales, "scales", torch.uint8, (V, kp // 32))
+        _same_device(codes.device, scales=scales)
+        self.codes, self.scales = codes, scales
+        self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
+        self.nbytes = codes.numel() + scales.numel()
+        self._desc = _SdMxfp4(codes.data_ptr(), scales.data_ptr())
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def from_tensor(cls, lm_head: torch.Tensor, stream=None) -> "Mxfp4Weights":
+        """Quantise a [V][d] LM head (float32, bfloat16 or float16)."""
+        return cls(*sd_mxfp4_quantize(lm_head, stream=stream), lm_head.shape[1])
+
+
+def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
+                    logits: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Logits [M][V] of hidden rows [M][d] (float32, bfloat16 or float16, any row stride)
+    under an MXFP4 LM head, as `dtype` or into `logits` (any row stride)."""
+    _rows(hidden, "hidden")
+    if not isinstance(lm_head, Mxfp4Weights):
+        raise TypeError("lm_head must be Mxfp4Weights")
+    M, d = hidden.shape
+    if d != lm_head.d:
+        raise ValueError("lm_head must be [V][d] with the hidden size of `hidden`")
+    dev = hidden.device
+    if logits is None:
+        logits = torch.empty((M, lm_head.V), dtype=dtype, device=dev)
+    _rows(logits, "logits")
+    if tuple(logits.shape) != (M, lm_head.V):
+        raise ValueError(f"logits has shape {tuple(logits.shape)}, expected {(M, lm_head.V)}")
+    if workspace is None:
+        workspace = new_workspace(mxfp4_logits_workspace_bytes(M, d), dev, stream)
+    _same_device(dev, lm_head=lm_head, logits=logits, workspace=workspace)
+    _call("sd_mxfp4_logits", dev, stream, _ptr(hidden), _TYPE_CODES[hidden.dtype], M, d,
+          _row_stride(hidden), lm_head._ref, lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
+          _row_stride(logits), _ptr(workspace), workspace.numel())
+    return logits
+
+
+class _SdSampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
+class SamplingParams:
+    """Sampling settings of n requests in device memory, for sd_sample, sd_accept_filtered and
+    VerifyRound. Each of temperature (default 1; 0 is greedy), top_k (< 1: off), top_p
+    (>= 1: off) and min_p (<= 0: off) is None (its filter is off), one number for every
+    request, a sequence of n numbers, or a device tensor of n values that is used as it is
+    (float32; int32 for top_k), so that writing to it changes later calls."""
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None,
+                 n: Optional[int] = None, device="cuda"):
+        given = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+        for name, v in given.items():
+            if v is None or isinstance(v, (int, float)):
+                continue
+            size = v.numel() if isinstance(v, torch.Tensor) else len(v)
+            if isinstance(v, torch.Tensor):
+                device = v.device if v.is_cuda else device
+            if n is None:
+                n = size
+            if size != n or size < 1:
+                raise ValueError(f"{name} has {size} values, expected {n}")
+        self.n = 1 if n is None else int(n)
+        if self.n < 1:
+            raise ValueError("sampling settings need at least one request")
+        self.device = torch.device(device)
+        for name, v in given.items():
+            setattr(self, name, self._array(name, v))
+        # Without any array the settings are those of no device in particular.
+        self.device = next((t.device for t in self._arrays() if t is not None), None)
+        _same_device(self.device, **{k: getattr(self, k) for k in given})
+        self._desc = _SdSampling(*[None if t is None else t.data_ptr() for t in self._arrays()])
+        self._ref = ctypes.byref(self._desc)
+
+    def _arrays(self):
+        return (self.temperature, self.top_k, self.top_p, self.min_p)
+
+    def _array(self, name, v):
+        if v is None:
+            return None
+        dtype = torch.int32 if name == "top_k" else torch.float32
+        if isinstance(v, torch.Tensor) and v.is_cuda:
+            _need(v, name, dtype, (self.n,))
+            return v
+        if isinstance(v, torch.Tensor):
+            v = v.tolist()
+        v = [v] * self.n if isinstance(v, (int, float)) else list(v)
+        for x in v:
+            if name == "top_k":
+                if int(x) != x or not -2**31 <= x < 2**31:
+                    raise ValueError(f"top_k must be whole 32-bit numbers, got {x}")
+            elif x != x or (name == "temperature" and not 0 <= x < float("inf")):
+                raise ValueError(f"{name} cannot be {x}")
+        return torch.tensor([int(x) if name == "top_k" else float(x) for x in v], dtype=dtype,
+                            device=self.device)
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor of {dtype}")
+    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) < 1):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, stride {t.stride()}, expected {(n,)}")
+
+
+def sd_sample(logits: torch.Tensor, u: torch.Tensor, params: SamplingParams,
+              tokens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+              logprob: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None):
+    """One token per row of logits [R][V] (float32, bfloat16 or float16, any row stride) under
+    `params` (of R requests, or of R / k: then k rows in turn share an entry), from the
+    uniforms u float32 [R]. Returns (tokens int32 [R], kept int32 [R], logprob float32 [R]);
+    a tokens tensor passed in may have any stride (a column of draft tokens)."""
+    _rows(logits, "logits")
+    R, V = logits.shape
+    dev = logits.device
+    _need(u, "u", torch.float32, (R,))
+    if not isinstance(params, SamplingParams):
+        raise TypeError("params must be SamplingParams")
+    if R % params.n != 0:
+        raise ValueError(f"{R} rows cannot share the settings of {params.n} requests")
+    if tokens is None:
+        tokens = torch.empty(R, dtype=torch.int32, device=dev)
+    if kept is None:
+        kept = torch.empty(R, dtype=torch.int32, device=dev)
+    if logprob is None:
+        logprob = torch.empty(R, dtype=torch.float32, device=dev)
+    _vector(tokens, "tokens", torch.int32, R)
+    _need(kept, "kept", torch.int32, (R,))
+    _need(logprob, "logprob", torch.float32, (R,))
+    if workspace is None:
+        workspace = new_workspace(sample_workspace_bytes(R, V), dev, stream)
+    _same_device(dev, u=u, params=params, tokens=tokens, kept=kept, logprob=logprob,
+                 workspace=workspace)
+    _call("sd_sample", dev, stream, _ptr(logits), _TYPE_CODES[logits.dtype], _row_stride(logits), R,
+          V, _ptr(u), params._ref, R // params.n, _ptr(tokens), max(1, tokens.stride(0)),
+          _ptr(kept), _ptr(logprob), _ptr(workspace), workspace.numel())
+    return tokens, kept, logprob
+
+
+def sd_accept_filtered(logits: torch.Tensor, draft_logits: torch.Tensor,
+                       draft_tokens: torch.Tensor, verify_len: Optional[torch.Tensor],
+                       row_offsets: Optional[torch.Tensor], u_accept: torch.Tensor,
+                       u_resample: torch.Tensor, params: SamplingParams,
+                       accept_len: Optional[torch.Tensor] = None,
+                       next_token: Optional[torch.Tensor] = None,
+                       counters: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Rejection acceptance when target and drafter are both sampled under `params` (of B
+    requests): returns (accept_len, next_token). Other arguments as for sd_accept_rejection."""
+    _need(draft_tokens, "draft_tokens", torch.int32)
+    B, g = draft_tokens.shape
+    dev = draft_tokens.device
+    _need(draft_logits, "draft_logits", torch.bfloat16)
+    V = draft_logits.shape[2]
+    _need(draft_logits, "draft_logits", torch.bfloat16, (B, g, V))
+    _need(logits, "logits", torch.float32, (B * (g + 1), V))
+    if verify_len is not None:
+        _need(verify_len, "verify_len", torch.int32, (B,))
+    if row_offsets is not None:
+        _need(row_offsets, "row_offsets", torch.int32, (B + 1,))
+    _need(u_accept, "u_accept", torch.float32, (B, g))
+    _need(u_resample, "u_resample", torch.float32, (B, g + 1))
+    if not isinstance(params, SamplingParams):
+        raise TypeError("params must be SamplingParams")
+    if params.n != B:
+        raise ValueError(f"params holds the settings of {params.n} requests, expected {B}")
+    accept_len = torch.empty(B, dtype=torch.int32, device=dev) if accept_len is None else accept_len
+    next_token = torch.empty(B, dtype=torch.int32, device=dev) if next_token is None else next_token
+    _need(accept_len, "accept_len", torch.int32, (B,))
+    _need(next_token, "next_token", torch.int32, (B,))
+    if counters is not None:
+        _need(counters, "counters", torch.int64, (2,))
+    if workspace is None:
+        workspace = new_workspace(accept_filtered_workspace_bytes(B, g, V), dev, stream)
+    _same_device(dev, logits=logits, draft_logits=draft_logits, verify_len=verify_len,
+                 row_offsets=row_offsets, u_accept=u_accept, u_resample=u_resample, params=params,
+                 accept_len=accept_len, next_token=next_token, counters=counters,
+                 workspace=workspace)
+    _call("sd_accept_filtered", dev, stream, _ptr(logits), _ptr(draft_logits), _ptr(draft_tokens),
+          _ptr(verify_len), _ptr(row_offsets), _ptr(u_accept), _ptr(u_resample), params._ref, B, g,
+          V, _ptr(accept_len), _ptr(next_token), _ptr(counters), _ptr(workspace),
+          workspace.numel())
+    return accept_len, next_token
+
+
 # --------------------------------------------------------------- a whole round
 
 class VerifyRound:
@@ -632,14 +950,21 @@ class VerifyRound:
     all on one stream with no host synchronisation. The verify and accept steps run
     through sd_verify_greedy at temperature 0 and sd_verify_rejection otherwise (fewer
     launches, for every LM-head format); fused=False keeps the separate sd_verify_logits
-    + sd_accept_* calls.
+    + sd_accept_* calls. With `sampling` (SamplingParams of B requests) the accept step is
+    sd_accept_filtered under those settings, after sd_verify_logits at `temperature`.
     """
 
     def __init__(self, B: int, gamma: int, d: int, V: int, temperature: float,
                  truncate: bool, threshold: float = 0.3, device="cuda", stream=None,
                  fused: bool = True, accept_rate: bool = False, scheduler: Optional[int] = None,
-                 sps: Optional[torch.Tensor] = None):
+                 sps: Optional[torch.Tensor] = None,
+                 sampling: Optional[SamplingParams] = None):
         self.B, self.gamma, self.d, self.V = B, gamma, d, V
+        self.sampling = sampling
+        if sampling is not None and (not isinstance(sampling, SamplingParams) or sampling.n != B):
+            raise ValueError("sampling must be SamplingParams of B requests")
+        if sampling is not None and accept_rate:
+            raise ValueError("the acceptance rate is not computed under sampling filters")
         # With a scheduler mode (SCHED_EARLY_STOP / SCHED_TOP_K) and an SPS table, the
         # prefix scheduler replaces the confidence threshold.
         self.scheduler, self.sps = scheduler, sps
@@ -653,12 +978,14 @@ class VerifyRound:
         self.row_offsets = torch.empty(B + 1, dtype=torch.int32, device=dev) if truncate else None
         self.stats = new_stats(B, gamma, dev)
         self.logits = (torch.empty((rows, V), dtype=torch.float32, device=dev)
-                       if self.T > 0 else None)
+                       if self.T > 0 or sampling is not None else None)
         self.accept_len = torch.empty(B, dtype=torch.int32, device=dev)
         self.next_token = torch.empty(B, dtype=torch.int32, device=dev)
         self.counters = torch.zeros(2, dtype=torch.int64, device=dev)
         self.ws_verify = new_workspace(verify_workspace_bytes(B, gamma, d, V), dev, stream)
-        self.ws_accept = (new_workspace(accept_workspace_bytes(B, gamma, V), dev, stream)
+        self.ws_accept = (new_workspace(accept_filtered_workspace_bytes(B, gamma, V), dev, stream)
+                          if sampling is not None else
+                          new_workspace(accept_workspace_bytes(B, gamma, V), dev, stream)
                           if self.T > 0 else None)
         # Analytic acceptance rate per verified draft position (rejection rounds only).
         self.accept_rate = (torch.empty((B, gamma), dtype=torch.float64, device=dev)
@@ -673,6 +1000,14 @@ class VerifyRound:
         elif self.truncate:
             sd_truncate_by_confidence(conf, self.threshold, self.verify_len, self.row_offsets,
                                       stream=stream)
+        if self.sampling is not None:
+            sd_verify_logits(hidden, lm_head, draft_tokens, self.verify_len, self.row_offsets,
+                             self.T, self.logits, self.stats, self.ws_verify, stream=stream)
+            sd_accept_filtered(self.logits, draft_logits, draft_tokens, self.verify_len,
+                               self.row_offsets, u_accept, u_resample, self.sampling,
+                               self.accept_len, self.next_token, self.counters, self.ws_accept,
+                               stream=stream)
+            return self.accept_len, self.next_token
         if self.T == 0 and self.fused:
             sd_verify_greedy(hidden, lm_head, draft_tokens, self.verify_len, self.row_offsets,
                              self.stats, self.accept_len, self.next_token, self.counters,

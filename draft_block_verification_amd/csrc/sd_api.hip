@@ -34,6 +34,31 @@ int32_t check_sizes(int32_t B, int32_t gamma, int32_t d, int32_t V) {
   return SD_OK;
 }
 
+bool known_type(int32_t t) { return t == SD_F32 || t == SD_BF16 || t == SD_F16; }
+
+size_t type_size(int32_t t) { return t == SD_F32 ? 4 : 2; }
+
+constexpr int kMaxMxColumns = 1 << 20;
+
+// Shared checks of the MXFP4 calls: [rows][d] of `type` beside its codes and scales.
+int32_t check_mx(const void *x, int32_t type, int32_t rows, int32_t d, int64_t stride,
+                 const uint8_t *codes, const uint8_t *scales) {
+  if (!x || !codes || !scales || !known_type(type)) return SD_EINVAL;
+  if (rows < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns || stride < d ||
+      stride > ((int64_t)1 << 40) || (int64_t)rows * mx_padded(d) > ((int64_t)1 << 38))
+    return SD_ESHAPE;
+  if (!aligned(x, type_size(type)) || !aligned(codes, 16) || !aligned(scales, 4)) return SD_EALIGN;
+  return SD_OK;
+}
+
+SampleSettings settings(const sd_sampling &s) {
+  return SampleSettings{s.temperature, s.top_k, s.top_p, s.min_p};
+}
+
+bool aligned_settings(const sd_sampling &s) {
+  return aligned(s.temperature, 4) && aligned(s.top_k, 4) && aligned(s.top_p, 4) && aligned(s.min_p, 4);
+}
+
 size_t verify_ws_bytes(int32_t B, int32_t gamma, int32_t V) {
   return verify_workspace_layout(B, gamma, V, nullptr, nullptr, nullptr);
 }
@@ -550,6 +575,101 @@ int32_t sd_verify_rejection(const uint16_t *hidden, const void *lm_head,
   return launch_status(launch_verify_rejection(a, u_accept, u_resample, accept_len, next_token,
                                                counters, accept_rate, accept_workspace,
                                                (hipStream_t)stream));
+}
+
+int32_t sd_mxfp4_columns(int32_t d) { return d < 8 || d % 8 != 0 || d > kMaxMxColumns ? 0 : mx_padded(d); }
+
+int32_t sd_mxfp4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d, int64_t x_stride,
+                          uint8_t *codes, uint8_t *scales, void *stream) {
+  const int32_t st = check_mx(x, x_type, rows, d, x_stride, codes, scales);
+  if (st != SD_OK) return st;
+  return launch_status(launch_mx_quantize(x, x_type, rows, d, x_stride, codes, scales,
+                                          (hipStream_t)stream));
+}
+
+int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t d,
+                            void *x, int32_t x_type, int64_t x_stride, void *stream) {
+  const int32_t st = check_mx(x, x_type, rows, d, x_stride, codes, scales);
+  if (st != SD_OK) return st;
+  return launch_status(launch_mx_dequantize(codes, scales, rows, d, x, x_type, x_stride,
+                                            (hipStream_t)stream));
+}
+
+size_t sd_mxfp4_logits_workspace_bytes(int32_t M, int32_t d) {
+  if (M < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns) return 0;
+  return mx_logits_workspace_layout(M, d, nullptr, nullptr);
+}
+
+int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d,
+                        int64_t hidden_stride, const sd_mxfp4 *lm_head, int32_t V, void *logits,
+                        int32_t logits_type, int64_t logits_stride, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+  if (!lm_head || !logits || !known_type(logits_type)) return SD_EINVAL;
+  const int32_t st = check_mx(hidden, hidden_type, M, d, hidden_stride, lm_head->codes, lm_head->scales);
+  if (st != SD_OK) return st;
+  if (V < 1 || V > kMaxVocab || logits_stride < V || logits_stride > ((int64_t)1 << 40)) return SD_ESHAPE;
+  if (!aligned(logits, type_size(logits_type))) return SD_EALIGN;
+  if (!workspace || workspace_bytes < mx_logits_workspace_layout(M, d, nullptr, nullptr))
+    return SD_EWORKSPACE;
+  if (!aligned(workspace, 256)) return SD_EALIGN;
+  return launch_status(launch_mx_logits(hidden, hidden_type, M, d, hidden_stride, lm_head->codes,
+                                        lm_head->scales, V, logits, logits_type, logits_stride,
+                                        workspace, (hipStream_t)stream));
+}
+
+size_t sd_sample_workspace_bytes(int32_t R, int32_t V) {
+  if (R < 1 || V < 1 || V > kMaxVocab) return 0;
+  return sample_workspace_layout(R, V);
+}
+
+int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits_stride, int32_t R, int32_t V,
+                  const float *u, const sd_sampling *sampling, int32_t rows_per_request,
+                  int32_t *tokens, int64_t token_stride, int32_t *kept, float *logprob,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+  if (!logits || !u || !sampling || !tokens || !known_type(logits_type)) return SD_EINVAL;
+  if (R < 1 || V < 1 || V > kMaxVocab || rows_per_request < 1 || logits_stride < V ||
+      logits_stride > ((int64_t)1 << 40) || token_stride < 1 || token_stride > ((int64_t)1 << 30))
+    return SD_ESHAPE;
+  if (!aligned(logits, type_size(logits_type)) || !aligned(u, 4) || !aligned(tokens, 4) ||
+      (kept && !aligned(kept, 4)) || (logprob && !aligned(logprob, 4)) || !aligned_settings(*sampling))
+    return SD_EALIGN;
+  if (!workspace || workspace_bytes < sample_workspace_layout(R, V)) return SD_EWORKSPACE;
+  if (!aligned(workspace, 256)) return SD_EALIGN;
+  return launch_status(launch_sample(logits, logits_type, logits_stride, R, V, u, settings(*sampling),
+                                     rows_per_request, tokens, token_stride, kept, logprob,
+                                     workspace, (hipStream_t)stream));
+}
+
+size_t sd_accept_filtered_workspace_bytes(int32_t B, int32_t gamma, int32_t V) {
+  if (check_sizes(B, gamma, 8, V) != SD_OK) return 0;
+  return accept_filtered_workspace_layout(B, gamma, nullptr, nullptr);
+}
+
+int32_t sd_accept_filtered(const float *logits, const uint16_t *draft_logits,
+                           const int32_t *draft_tokens, const int32_t *verify_len,
+                           const int32_t *row_offsets, const float *u_accept,
+                           const float *u_resample, const sd_sampling *sampling, int32_t B,
+                           int32_t gamma, int32_t V, int32_t *accept_len, int32_t *next_token,
+                           int64_t *counters, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+  if (!logits || !draft_logits || !draft_tokens || !u_accept || !u_resample || !sampling ||
+      !accept_len || !next_token)
+    return SD_EINVAL;
+  if ((verify_len == nullptr) != (row_offsets == nullptr)) return SD_EINVAL;
+  if (check_sizes(B, gamma, 8, V) != SD_OK) return SD_ESHAPE;
+  if (!aligned(logits, 16) || !aligned(draft_logits, 16) || !aligned(draft_tokens, 4) ||
+      !aligned(u_accept, 4) || !aligned(u_resample, 4) || !aligned(accept_len, 4) ||
+      !aligned(next_token, 4) || (counters && !aligned(counters, 8)) || !aligned_settings(*sampling) ||
+      (verify_len && (!aligned(verify_len, 4) || !aligned(row_offsets, 4))))
+    return SD_EALIGN;
+  if (!workspace || workspace_bytes < accept_filtered_workspace_layout(B, gamma, nullptr, nullptr))
+    return SD_EWORKSPACE;
+  if (!aligned(workspace, 256)) return SD_EALIGN;
+  RowMap rm{row_offsets, B, gamma};
+  return launch_status(launch_accept_filtered(logits, draft_logits, draft_tokens, verify_len, rm,
+                                              u_accept, u_resample, settings(*sampling), V,
+                                              accept_len, next_token, counters, workspace,
+                                              (hipStream_t)stream));
 }
 
 }  // extern "C"

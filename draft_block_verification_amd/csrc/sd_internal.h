@@ -244,4 +244,13 @@ constexpr int kLmBlocked = 2;   // stage-major blocked bf16
 // Prefix scheduler: one workgroup sorts all R * gamma candidates in LDS.
 constexpr int kSchedMaxCandidates = 16384;
 
+// Per-request sampling settings in device memory; a null pointer leaves that filter off
+// (temperature 1).
+struct SampleSettings {
+  const float *temperature;
+  const int32_t *top_k;
+  const float *top_p;
+  const float *min_p;
+};
+
 }  // namespace sdv

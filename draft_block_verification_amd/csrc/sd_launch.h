@@ -1,5 +1,5 @@
 // Host-side launchers and workspace layouts of the HIP library (defined in sd_gemm.hip,
-// sd_accept.hip and sd_sched.hip; called by sd_api.hip). Each launcher enqueues its
+// sd_accept.hip, sd_sched.hip, sd_sample.hip and sd_mxfp4.hip; called by sd_api.hip). Each launcher enqueues its
 // kernels on `stream` and returns the hipError_t of the launch.
 #pragma once
 
@@ -83,4 +83,32 @@ hipError_t launch_accept_rejection(const float *logits, const sd_row_stats *stat
                                    float temperature, int32_t *accept_len, int32_t *next_token,
                                    int64_t *counters, double *accept_rate, void *workspace,
                                    hipStream_t stream);
+
+// MXFP4 rows: columns padded to one matrix instruction's depth.
+constexpr int mx_padded(int d) { return (d + 127) / 128 * 128; }
+
+hipError_t launch_mx_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride,
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int d,
+                                void *x, int32_t type, int64_t stride, hipStream_t stream);
+
+// Logits under an MXFP4 LM head; the workspace holds the quantised hidden rows.
+size_t mx_logits_workspace_layout(int M, int d, size_t *codes, size_t *scales);
+hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
+                            const uint8_t *w_codes, const uint8_t *w_scales, int V, void *logits,
+                            int32_t type, int64_t ld, void *workspace, hipStream_t stream);
+
+// Filtered sampling and acceptance.
+hipError_t launch_sample(const void *logits, int32_t type, int64_t stride, int R, int V,
+                         const float *u, const SampleSettings &set, int rows_per,
+                         int32_t *tokens, int64_t token_stride, int32_t *kept, float *logprob,
+                         void *workspace, hipStream_t stream);
+size_t sample_workspace_layout(int R, int V);
+size_t accept_filtered_workspace_layout(int B, int gamma, size_t *cut_p, size_t *cut_q);
+hipError_t launch_accept_filtered(const float *logits, const uint16_t *draft_logits,
+                                  const int32_t *draft_tokens, const int32_t *verify_len,
+                                  const RowMap &rm, const float *u_accept,
+                                  const float *u_resample, const SampleSettings &set, int V,
+                                  int32_t *accept_len, int32_t *next_token, int64_t *counters,
+                                  void *workspace, hipStream_t stream);
 }  // namespace sdv

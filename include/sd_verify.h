@@ -8,6 +8,10 @@
  *                                 bonus position, with per-row statistics
  *   3. sd_accept_greedy           greedy prefix acceptance + correction/bonus token
  *      sd_accept_rejection        rejection-sampling acceptance + residual/bonus draw
+ *      sd_accept_filtered         the same under top-k, top-p and min-p
+ * and, on the drafter's side:
+ *      sd_mxfp4_logits            logits under a 4-bit copy of the LM head
+ *      sd_sample                  draws under temperature, top-k, top-p and min-p
  *
  * Conventions shared by every call
  *   - All tensors are row-major, contiguous, caller-owned DEVICE memory unless
@@ -65,7 +69,8 @@ extern "C" {
 enum {
     SD_OK = 0,
     SD_EINVAL = 1,      /* null required pointer, bad temperature or threshold   */
-    SD_ESHAPE = 2,      /* B < 1, gamma outside [1, 64], d % 8 != 0, V < 1, size overflow */
+    SD_ESHAPE = 2,      /* B < 1, gamma outside [1, 64], d % 8 != 0, V < 1, a row stride
+                           shorter than its row, size overflow                            */
     SD_EALIGN = 3,      /* a bf16 / fp32 tensor not 16-byte aligned, stats not 8-byte aligned */
     SD_EWORKSPACE = 4,  /* workspace pointer null or smaller than required       */
     SD_EDEVICE = 5,     /* a HIP launch or copy failed                           */
@@ -78,10 +83,13 @@ enum {
     SD_FLAG_VERIFY_LEN = 1,   /* a verify_len entry was outside [0, gamma] and was clamped */
     SD_FLAG_ROW_OFFSETS = 2,  /* row_offsets disagreed with verify_len or overflowed the row capacity */
     SD_FLAG_NO_RESIDUAL = 4,  /* a residual max(0, p - q) had no positive mass; drew from p instead */
-    SD_FLAG_WAIT = 8          /* a workgroup's bounded wait for results that other workgroups
+    SD_FLAG_WAIT = 8,         /* a workgroup's bounded wait for results that other workgroups
                                  of the same launch publish ran out (sd_verify_rejection's
                                  one-launch draw, sd_verify_greedy's in-launch decision);
                                  the tokens of that call are not valid */
+    SD_FLAG_SAMPLING = 16,    /* a sampling setting was not a number (temperature: or negative
+                                 or infinite) and was replaced as sd_sampling documents      */
+    SD_FLAG_EMPTY_ROW = 32    /* a sampled row had no logit above -inf: its token is -1      */
 };
 
 /* Per verified row statistics (32 bytes, 8-byte aligned). */
@@ -487,6 +495,145 @@ SD_API int32_t sd_verify_rejection(const uint16_t *hidden, const void *lm_head,
                                    void *verify_workspace, size_t verify_workspace_bytes,
                                    void *accept_workspace, size_t accept_workspace_bytes,
                                    void *stream);
+
+/* Element types of the calls that take more than one. */
+enum {
+    SD_F32 = 0,
+    SD_BF16 = 1,
+    SD_F16 = 2
+};
+
+/*
+ * MXFP4 (OCP Microscaling Formats): a block of 32 consecutive columns of a row shares one
+ * scale 2^e; a value is a 4-bit code, sign in bit 3, magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * for codes 0..7. With kp = d rounded up to a multiple of 128 (sd_mxfp4_columns):
+ *   codes   uint8 [rows][kp / 2]   column 2 i in the low half of byte i, 2 i + 1 in the high
+ *   scales  uint8 [rows][kp / 32]  e + 127; 255: the block's values are NaN
+ * Columns d .. kp - 1 hold code 0, whole blocks of them under scale byte 0. For d a multiple
+ * of 128 this is the plain row-major form that checkpoints hold.
+ * Quantisation: a = the block's largest magnitude, e = max(floor(log2 a) - 2, -127) (-127 for
+ * a block of zeros), code = x / 2^e rounded to the nearest magnitude, ties to the even code,
+ * over 6 to 6. A block that holds a NaN or an infinity gets scale byte 255.
+ */
+SD_API int32_t sd_mxfp4_columns(int32_t d);
+
+/*
+ * Quantise rows of x, and the values back.
+ *   x       [rows][d] of type x_type (SD_F32, SD_BF16, SD_F16), row stride x_stride elements
+ *           (>= d; any alignment of the element type, 16-byte aligned rows are fastest)
+ *   rows    >= 1; d a positive multiple of 8
+ *   codes, scales  as above, 16-byte and 4-byte aligned
+ * sd_mxfp4_dequantize writes x rounded once to x_type (exact in fp32 and, unless the scale
+ * leaves its normal range, in bf16); nothing between row ends and strides is written.
+ * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE, SD_EALIGN, SD_EDEVICE.
+ */
+SD_API int32_t sd_mxfp4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d,
+                                 int64_t x_stride, uint8_t *codes, uint8_t *scales, void *stream);
+SD_API int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows,
+                                   int32_t d, void *x, int32_t x_type, int64_t x_stride,
+                                   void *stream);
+
+/* An MXFP4 LM head [V][d]: device pointers to codes and scales in the form above. */
+typedef struct sd_mxfp4 {
+    const uint8_t *codes;
+    const uint8_t *scales;
+} sd_mxfp4;
+
+/*
+ * Logits of hidden rows under an MXFP4 LM head (LFM2.5-DSpark blog, "Training &
+ * Architecture", and DSpark summary, "Training": drafter and target share the LM head). For
+ * a drafter: verification keeps the target's distribution whatever the drafter's logits are,
+ * so its copy of the LM head may be coarse.
+ *   hidden   [M][d] of type hidden_type, row stride hidden_stride elements; quantised to
+ *            MXFP4 in the call (into the workspace)
+ *   lm_head  MXFP4 [V][d] (host struct)
+ *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
+ *   workspace  sd_mxfp4_logits_workspace_bytes(M, d) bytes
+ * logits[m][v] = sum over blocks of 2^(eh + ew) sum of the code products, accumulated in
+ * fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives NaN.
+ * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (M < 1, d not a positive multiple
+ * of 8, V outside [1, 2^21], short strides), SD_EALIGN (codes, scales), SD_EWORKSPACE,
+ * SD_EDEVICE.
+ */
+SD_API size_t sd_mxfp4_logits_workspace_bytes(int32_t M, int32_t d);
+SD_API int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d,
+                               int64_t hidden_stride, const sd_mxfp4 *lm_head, int32_t V,
+                               void *logits, int32_t logits_type, int64_t logits_stride,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Sampling settings (host struct of device pointers, each may be NULL: that filter is off,
+ * temperature 1). One value per request:
+ *   temperature  fp32, finite and >= 0; 0 keeps the likeliest id alone
+ *   top_k        int32; < 1 or >= V: off
+ *   top_p        fp32; >= 1: off; <= 0 keeps the likeliest id alone
+ *   min_p        fp32; <= 0: off; over 1 counts as 1
+ * Out-of-range temperatures (NaN, infinite, negative) count as 0, a NaN top_p or min_p as
+ * off; each raises SD_FLAG_SAMPLING.
+ * The filtered distribution of a logit row z: rank the ids by larger logit, then lower id
+ * (NaN counts as -inf; ids at -inf are never kept), with weights w = exp((z - max) / T);
+ * top-k keeps the first k; top-p of these the shortest leading run that holds a share of at
+ * least top_p of their weight; min-p of these the ids with w >= min_p. Probabilities are the
+ * kept weights over their sum. With a logit of +inf the ids at +inf share the whole weight.
+ */
+typedef struct sd_sampling {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+} sd_sampling;
+
+/*
+ * Draw one token per logit row from its filtered distribution, by inverse CDF in ascending
+ * vocabulary id: the smallest kept id whose running weight exceeds u times the total.
+ *   logits    [R][V] of type logits_type, row stride logits_stride elements (>= V)
+ *   u         fp32 [R], uniforms in [0, 1) (values outside count as the nearest in it)
+ *   sampling  settings, row i reads entry i / rows_per_request of each
+ *   tokens    int32 [R], element stride token_stride (>= 1): out; -1 for a row without any
+ *             logit above -inf (SD_FLAG_EMPTY_ROW)
+ *   kept      int32 [R] or NULL: out, size of the kept set
+ *   logprob   fp32 [R] or NULL: out, log of the token's filtered probability (-inf with -1)
+ *   workspace sd_sample_workspace_bytes(R, V) bytes
+ * Weights are formed in fp64 and summed exactly in units of about 2^-46 of the largest: an id
+ * whose weight is below half a unit is never drawn.
+ * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (R < 1, V outside [1, 2^21],
+ * rows_per_request < 1, short strides), SD_EALIGN (an array not aligned to its elements),
+ * SD_EWORKSPACE, SD_EDEVICE.
+ */
+SD_API size_t sd_sample_workspace_bytes(int32_t R, int32_t V);
+SD_API int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits_stride, int32_t R,
+                         int32_t V, const float *u, const sd_sampling *sampling,
+                         int32_t rows_per_request, int32_t *tokens, int64_t token_stride,
+                         int32_t *kept, float *logprob, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * Rejection acceptance (sd_accept_rejection's rule) when the target is sampled through
+ * temperature, top-k, top-p and min-p and the drafts were drawn from the drafter's logits
+ * through the same settings (sd_sample): with p' and q' the filtered distributions of the
+ * target row and the drafter row,
+ *   position j < L_r survives iff u_accept[r][j] < min(1, p'_j(x_j) / q'_j(x_j)) (a token
+ *   with p' = 0 never does);
+ *   a_r = first failing j, else L_r;
+ *   if a_r < L_r the token is drawn from norm(max(0, p'_a - q'_a)) (from p'_a, raising
+ *   SD_FLAG_NO_RESIDUAL, when that has no mass), else from p'_{L_r}; draws as in sd_sample.
+ * Lossless: the emitted tokens follow p'.
+ *   logits    fp32 [B * (gamma + 1)][V] written by sd_verify_logits (any temperature)
+ *   draft_logits bf16 [B][gamma][V], draft_tokens, verify_len, row_offsets, u_accept,
+ *   u_resample, accept_len, next_token, counters   as for sd_accept_rejection
+ *   sampling  settings of each request (temperature 0: both sides keep their likeliest id)
+ *   workspace sd_accept_filtered_workspace_bytes(B, gamma, V) bytes
+ * A target row without any logit above -inf emits -1 and raises SD_FLAG_EMPTY_ROW.
+ * Errors: as for sd_accept_rejection.
+ */
+SD_API size_t sd_accept_filtered_workspace_bytes(int32_t B, int32_t gamma, int32_t V);
+SD_API int32_t sd_accept_filtered(const float *logits, const uint16_t *draft_logits,
+                                  const int32_t *draft_tokens, const int32_t *verify_len,
+                                  const int32_t *row_offsets, const float *u_accept,
+                                  const float *u_resample, const sd_sampling *sampling, int32_t B,
+                                  int32_t gamma, int32_t V, int32_t *accept_len,
+                                  int32_t *next_token, int64_t *counters, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
