@@ -69,6 +69,8 @@ _SIGS = {
     "sd_mxfp4_columns": (_i32, [_i32]),
     "sd_mxfp4_quantize": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
     "sd_mxfp4_dequantize": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp]),
+    "sd_mxfp4_head_bytes": (_sz, [_i32, _i32]),
+    "sd_mxfp4_head": (_i32, [_vp, _vp, _i32, _i32, _vp, _sz, _vp]),
     "sd_mxfp4_logits_workspace_bytes": (_sz, [_i32, _i32]),
     "sd_mxfp4_logits": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _vp, _sz,
                                _vp]),
@@ -734,16 +736,12 @@ def sd_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
     return out
 
 
-class _SdMxfp4(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
-
-
 class Mxfp4Weights:
-    """An MXFP4 LM head in device memory (codes uint8 [V][kp / 2], scales uint8 [V][kp / 32],
-    kp = mxfp4_columns(d)), for sd_mxfp4_logits. Rows without the padding, [V][d / 2] and
-    [V][d / 32] for d a multiple of 32, are copied into padded ones."""
+    """An MXFP4 LM head in the form sd_mxfp4_logits reads (sd_mxfp4_head), made once from codes
+    uint8 [V][kp / 2] and scales uint8 [V][kp / 32], kp = mxfp4_columns(d), or from rows
+    without the padding, [V][d / 2] and [V][d / 32] for d a multiple of 32."""
 
-    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d: int):
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d: int, stream=None):
         kp = mxfp4_columns(d)
         _need(codes, "codes", torch.uint8)
         _need(scales, "scales", torch.uint8)
@@ -755,16 +753,19 @@ class Mxfp4Weights:
         _need(codes, "codes", torch.uint8, (V, kp // 2))
         _need(scales, "scales", torch.uint8, (V, kp // 32))
         _same_device(codes.device, scales=scales)
-        self.codes, self.scales = codes, scales
+        nbytes = int(_lib.sd_mxfp4_head_bytes(V, d))
+        if nbytes == 0:
+            raise ValueError(f"no MXFP4 LM head of [{V}][{d}]")
         self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
-        self.nbytes = codes.numel() + scales.numel()
-        self._desc = _SdMxfp4(codes.data_ptr(), scales.data_ptr())
-        self._ref = ctypes.byref(self._desc)
+        self.nbytes = nbytes
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        _call("sd_mxfp4_head", codes.device, stream, _ptr(codes), _ptr(scales), self.V, self.d,
+              _ptr(self.buf), nbytes)
 
     @classmethod
     def from_tensor(cls, lm_head: torch.Tensor, stream=None) -> "Mxfp4Weights":
         """Quantise a [V][d] LM head (float32, bfloat16 or float16)."""
-        return cls(*sd_mxfp4_quantize(lm_head, stream=stream), lm_head.shape[1])
+        return cls(*sd_mxfp4_quantize(lm_head, stream=stream), lm_head.shape[1], stream=stream)
 
 
 def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
@@ -788,7 +789,7 @@ def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
         workspace = new_workspace(mxfp4_logits_workspace_bytes(M, d), dev, stream)
     _same_device(dev, lm_head=lm_head, logits=logits, workspace=workspace)
     _call("sd_mxfp4_logits", dev, stream, _ptr(hidden), _TYPE_CODES[hidden.dtype], M, d,
-          _row_stride(hidden), lm_head._ref, lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
+          _row_stride(hidden), _ptr(lm_head.buf), lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
           _row_stride(logits), _ptr(workspace), workspace.numel())
     return logits
 

@@ -584,7 +584,7 @@ int32_t sd_mxfp4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d
   const int32_t st = check_mx(x, x_type, rows, d, x_stride, codes, scales);
   if (st != SD_OK) return st;
   return launch_status(launch_mx_quantize(x, x_type, rows, d, x_stride, codes, scales,
-                                          (hipStream_t)stream));
+                                          false, (hipStream_t)stream));
 }
 
 int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t d,
@@ -595,26 +595,47 @@ int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t
                                             (hipStream_t)stream));
 }
 
+size_t sd_mxfp4_head_bytes(int32_t V, int32_t d) {
+  if (V < 1 || V > kMaxVocab || d < 8 || d % 8 != 0 || d > kMaxMxColumns ||
+      (int64_t)V * mx_padded(d) > ((int64_t)1 << 38))
+    return 0;
+  return mx_tiled_bytes(V, d, nullptr);
+}
+
+int32_t sd_mxfp4_head(const uint8_t *codes, const uint8_t *scales, int32_t V, int32_t d, uint8_t *head,
+                      size_t head_bytes, void *stream) {
+  if (!codes || !scales || !head) return SD_EINVAL;
+  const size_t need = sd_mxfp4_head_bytes(V, d);
+  if (need == 0) return SD_ESHAPE;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(head, 256)) return SD_EALIGN;
+  if (head_bytes < need) return SD_EWORKSPACE;
+  return launch_status(launch_mx_head(codes, scales, V, d, head, (hipStream_t)stream));
+}
+
 size_t sd_mxfp4_logits_workspace_bytes(int32_t M, int32_t d) {
-  if (M < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns) return 0;
-  return mx_logits_workspace_layout(M, d, nullptr, nullptr);
+  if (M < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns ||
+      (int64_t)M * mx_padded(d) > ((int64_t)1 << 38))
+    return 0;
+  return mx_logits_workspace_bytes(M, d);
 }
 
 int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d,
-                        int64_t hidden_stride, const sd_mxfp4 *lm_head, int32_t V, void *logits,
+                        int64_t hidden_stride, const uint8_t *head, int32_t V, void *logits,
                         int32_t logits_type, int64_t logits_stride, void *workspace,
                         size_t workspace_bytes, void *stream) {
-  if (!lm_head || !logits || !known_type(logits_type)) return SD_EINVAL;
-  const int32_t st = check_mx(hidden, hidden_type, M, d, hidden_stride, lm_head->codes, lm_head->scales);
-  if (st != SD_OK) return st;
-  if (V < 1 || V > kMaxVocab || logits_stride < V || logits_stride > ((int64_t)1 << 40)) return SD_ESHAPE;
-  if (!aligned(logits, type_size(logits_type))) return SD_EALIGN;
-  if (!workspace || workspace_bytes < mx_logits_workspace_layout(M, d, nullptr, nullptr))
-    return SD_EWORKSPACE;
+  if (!hidden || !head || !logits || !known_type(hidden_type) || !known_type(logits_type)) return SD_EINVAL;
+  const size_t need = sd_mxfp4_logits_workspace_bytes(M, d);
+  if (need == 0 || sd_mxfp4_head_bytes(V, d) == 0 || hidden_stride < d || hidden_stride > ((int64_t)1 << 40) ||
+      logits_stride < V || logits_stride > ((int64_t)1 << 40))
+    return SD_ESHAPE;
+  // One workgroup per output tile of 64 x 64 at least; the grid counts them in 32 bits.
+  if ((int64_t)((M + 63) / 64) * ((V + 63) / 64) > ((int64_t)1 << 30)) return SD_ESHAPE;
+  if (!aligned(hidden, type_size(hidden_type)) || !aligned(head, 256) || !aligned(logits, type_size(logits_type)))
+    return SD_EALIGN;
+  if (!workspace || workspace_bytes < need) return SD_EWORKSPACE;
   if (!aligned(workspace, 256)) return SD_EALIGN;
-  return launch_status(launch_mx_logits(hidden, hidden_type, M, d, hidden_stride, lm_head->codes,
-                                        lm_head->scales, V, logits, logits_type, logits_stride,
-                                        workspace, (hipStream_t)stream));
+  return launch_status(launch_mx_logits(hidden, hidden_type, M, d, hidden_stride, head, V, logits,
+                                        logits_type, logits_stride, workspace, (hipStream_t)stream));
 }
 
 size_t sd_sample_workspace_bytes(int32_t R, int32_t V) {

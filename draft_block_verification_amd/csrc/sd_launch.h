@@ -87,16 +87,21 @@ hipError_t launch_accept_rejection(const float *logits, const sd_row_stats *stat
 // MXFP4 rows: columns padded to one matrix instruction's depth.
 constexpr int mx_padded(int d) { return (d + 127) / 128 * 128; }
 
+// Codes and scales by row, or (tiled) in the product's tiles.
 hipError_t launch_mx_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride,
-                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
+                              uint8_t *codes, uint8_t *scales, bool tiled, hipStream_t stream);
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int d,
                                 void *x, int32_t type, int64_t stride, hipStream_t stream);
+// Bytes of the tiled form of [rows][d]; *scales: where its scales start.
+size_t mx_tiled_bytes(int64_t rows, int d, size_t *scales);
+hipError_t launch_mx_head(const uint8_t *codes, const uint8_t *scales, int V, int d, uint8_t *head,
+                          hipStream_t stream);
 
-// Logits under an MXFP4 LM head; the workspace holds the quantised hidden rows.
-size_t mx_logits_workspace_layout(int M, int d, size_t *codes, size_t *scales);
+// Logits under a tiled MXFP4 LM head; the workspace holds the quantised hidden rows.
+size_t mx_logits_workspace_bytes(int M, int d);
 hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
-                            const uint8_t *w_codes, const uint8_t *w_scales, int V, void *logits,
-                            int32_t type, int64_t ld, void *workspace, hipStream_t stream);
+                            const uint8_t *head, int V, void *logits, int32_t type, int64_t ld,
+                            void *workspace, hipStream_t stream);
 
 // Filtered sampling and acceptance.
 hipError_t launch_sample(const void *logits, int32_t type, int64_t stride, int R, int V,

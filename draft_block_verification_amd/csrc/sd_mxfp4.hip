@@ -11,7 +11,19 @@
 // Rows are stored padded to a multiple of 128 columns (one matrix instruction's depth):
 // codes [rows][kp / 2] bytes, column 2 i in the low half of byte i, scales [rows][kp / 32]
 // bytes; padding is code 0 under scale byte 0, which adds nothing to any product.
+//
+// The product reads both operands tiled: a tile is 64 rows by 128 columns. Its codes are four
+// fragments of 16 rows (1 KB each), a fragment's 16 bytes for lane l being row l % 16 at
+// columns 32 (l / 16) .. + 31, so a wave loads a fragment as one contiguous KB in the very
+// order the matrix instruction takes it, from memory as from LDS without bank conflicts. Its
+// scales are one 32-bit word a lane, byte i the scale of row 16 i + l % 16 at block l / 16:
+// four fragments share the word, and the instruction's operand selects the byte.
+//   codes  [ceil(rows / 64)][kp / 128][4][64 lanes][16 bytes], then
+//   scales [ceil(rows / 64)][kp / 128][64 lanes][4 bytes]
 #include "sd_launch.h"
+
+#define LDSP __attribute__((address_space(3)))
+#define GLBP __attribute__((address_space(1)))
 
 namespace sdv {
 namespace {
@@ -59,8 +71,21 @@ struct MxArgs {
   int64_t rows, stride;    // elements from row to row
   int d, kp;
   bool vec;
+  bool tiled;              // codes and scales in tiles
   uint8_t *codes, *scales;
 };
+
+// Byte offsets in the tiled form of row `row`'s eight columns 8 c .. (codes) and of the scale
+// of their block.
+__device__ inline int64_t tiled_codes(int64_t row, int c, int steps) {
+  const int64_t tile = (row >> 6) * steps + (c >> 4);
+  return tile * 4096 + ((row >> 4) & 3) * 1024 + (((c >> 2) & 3) * 16 + (row & 15)) * 16 + (c & 3) * 4;
+}
+
+__device__ inline int64_t tiled_scale(int64_t row, int c, int steps) {
+  const int64_t tile = (row >> 6) * steps + (c >> 4);
+  return tile * 256 + (((c >> 2) & 3) * 16 + (row & 15)) * 4 + ((row >> 4) & 3);
+}
 
 // Eight columns a thread, four neighbouring threads a block: its largest magnitude comes
 // from two lane exchanges.
@@ -91,9 +116,31 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) word |= e2m1(v[i], ldexpf(fabsf(v[i]), -e)) << (4 * i);
   if (bad) word = 0;
-  *reinterpret_cast<uint32_t *>(a.codes + row * (a.kp / 2) + 4 * c) = word;
+  const int steps = a.kp / 128;
+  *reinterpret_cast<uint32_t *>(a.codes + (a.tiled ? tiled_codes(row, c, steps) : row * (a.kp / 2) + 4 * c)) = word;
   // Padding keeps scale byte 0.
-  if ((c & 3) == 0) a.scales[row * (a.kp / 32) + c / 4] = bad ? 255 : (left > 0 ? (uint8_t)(e + 127) : 0);
+  if ((c & 3) == 0)
+    a.scales[a.tiled ? tiled_scale(row, c, steps) : row * (a.kp / 32) + c / 4] =
+        bad ? 255 : (left > 0 ? (uint8_t)(e + 127) : 0);
+}
+
+// The tiled form of codes and scales stored by row: one workgroup a tile, thread t moves the
+// 16 bytes of fragment t / 64's lane t % 64; rows past the last are zero.
+__global__ __launch_bounds__(256) void k_mx_tile(const uint8_t *codes, const uint8_t *scales, int V, int kp,
+                                                 uint8_t *out_codes, uint8_t *out_scales) {
+  const int steps = kp / 128, t = threadIdx.x, lane = t & 63;
+  const int64_t tile = blockIdx.x;
+  const int group = (int)(tile / steps), step = (int)(tile - (int64_t)group * steps);
+  const int64_t row = 64 * (int64_t)group + 16 * (t >> 6) + (lane & 15);
+  const int blk = 4 * step + (lane >> 4);
+  u32x4 w = {0u, 0u, 0u, 0u};
+  uint8_t s = 0;
+  if (row < V) {
+    w = *reinterpret_cast<const u32x4 *>(codes + row * (kp / 2) + 16 * blk);
+    s = scales[row * (kp / 32) + blk];
+  }
+  *reinterpret_cast<u32x4 *>(out_codes + tile * 4096 + t * 16) = w;
+  out_scales[tile * 256 + lane * 4 + (t >> 6)] = s;
 }
 
 __device__ inline float e2m1_value(uint32_t c) {
@@ -153,9 +200,9 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxArgs a, void *x) {
 
 // ------------------------------------------------------------------ product
 struct MxGemmArgs {
-  const uint8_t *hc, *hs;   // hidden codes [M][kp/2] and scales [M][kp/32]
-  const uint8_t *wc, *ws;   // LM head codes [V][kp/2] and scales [V][kp/32]
-  int M, V, kp;
+  const uint8_t *hc, *hs;   // hidden rows, tiled
+  const uint8_t *wc, *ws;   // LM head, tiled
+  int M, V, steps;          // steps: 128-column steps
   void *out;
   int32_t type;
   int64_t ld;               // elements from row to row
@@ -163,13 +210,34 @@ struct MxGemmArgs {
 };
 
 // D += A B^T over 128 columns of MXFP4: lane l holds row l % 16 of each operand at columns
-// 32 (l / 16) .. + 31 (16 bytes, one scale), and of D the column l % 16 at rows
-// 4 (l / 16) .. + 3. The LM-head fragment is operand A, so a lane's four results are
-// consecutive vocabulary ids of one hidden row.
+// 32 (l / 16) .. + 31 (16 bytes), of D the column l % 16 at rows 4 (l / 16) .. + 3. sa and sb
+// hold four scales, one a byte; byte SA and SB apply. The LM-head fragment is operand A, so
+// a lane's four results are consecutive vocabulary ids of one hidden row.
+template <int SA, int SB>
 __device__ inline f32x4 mfma_mx(const u32x4 &a, int sa, const u32x4 &b, int sb, f32x4 c) {
   const i32x8 aa = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
   const i32x8 bb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aa, bb, c, 4, 4, 0, sa, 0, sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aa, bb, c, 4, 4, SA, sa, SB, sb);
+}
+
+// The byte selectors are immediates: a call per (tile % 4, tile % 4) pair.
+template <int SA>
+__device__ inline f32x4 mfma_mx_b(int sel_b, const u32x4 &a, int sa, const u32x4 &b, int sb, f32x4 c) {
+  switch (sel_b) {
+    case 0: return mfma_mx<SA, 0>(a, sa, b, sb, c);
+    case 1: return mfma_mx<SA, 1>(a, sa, b, sb, c);
+    case 2: return mfma_mx<SA, 2>(a, sa, b, sb, c);
+    default: return mfma_mx<SA, 3>(a, sa, b, sb, c);
+  }
+}
+
+__device__ inline f32x4 mfma_mx_sel(int sel_a, int sel_b, const u32x4 &a, int sa, const u32x4 &b, int sb, f32x4 c) {
+  switch (sel_a) {
+    case 0: return mfma_mx_b<0>(sel_b, a, sa, b, sb, c);
+    case 1: return mfma_mx_b<1>(sel_b, a, sa, b, sb, c);
+    case 2: return mfma_mx_b<2>(sel_b, a, sa, b, sb, c);
+    default: return mfma_mx_b<3>(sel_b, a, sa, b, sb, c);
+  }
 }
 
 __device__ inline void store4(const MxGemmArgs &a, int m, int v, const f32x4 &z) {
@@ -196,68 +264,305 @@ __device__ inline void store4(const MxGemmArgs &a, int m, int v, const f32x4 &z)
   }
 }
 
-// One 16 x 16 tile a wave.
-__global__ __launch_bounds__(256) void k_mx_gemm(MxGemmArgs a) {
-  const int lane = threadIdx.x & 63, row = lane & 15, blk = lane >> 4;
-  const int v0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 16, m0 = blockIdx.y * 16;
-  if (v0 >= a.V) return;
-  const int v = min(v0 + row, a.V - 1), m = min(m0 + row, a.M - 1);
-  const uint8_t *wc = a.wc + (size_t)v * (a.kp / 2), *ws = a.ws + (size_t)v * (a.kp / 32);
-  const uint8_t *hc = a.hc + (size_t)m * (a.kp / 2), *hs = a.hs + (size_t)m * (a.kp / 32);
-  f32x4 z = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < a.kp / 32; k += 4) {
-    const u32x4 w = *reinterpret_cast<const u32x4 *>(wc + 16 * (k + blk));
-    const u32x4 h = *reinterpret_cast<const u32x4 *>(hc + 16 * (k + blk));
-    z = mfma_mx(w, ws[k + blk], h, hs[k + blk], z);
+// ---------------------------------------------------------- few hidden rows
+// Up to 16 MT rows: the LM head's bytes bound the call. One workgroup per 64 ids; its four
+// waves take the 128-column steps in turn (wave w steps w, w + 4, ..), so a workgroup reads
+// one contiguous 17 KB run a round, straight into registers: each weight is used by one wave
+// only, so LDS would add a copy and share nothing. The hidden fragments are read by every
+// workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
+template <int MT>
+__global__ __launch_bounds__(256) void k_mx_skinny(MxGemmArgs a) {
+  constexpr int D = 3;                 // steps a wave has in flight
+  constexpr int LDR = 68;              // floats from row to row in LDS: rows start on other banks
+  __shared__ float red[4][16 * MT * LDR];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t g = blockIdx.x;
+  const u32x4 *wc = reinterpret_cast<const u32x4 *>(a.wc + g * a.steps * 4096) + lane;
+  const int *ws = reinterpret_cast<const int *>(a.ws + g * a.steps * 256) + lane;
+  const u32x4 *hc = reinterpret_cast<const u32x4 *>(a.hc) + lane;
+  const int *hs = reinterpret_cast<const int *>(a.hs) + lane;
+  f32x4 acc[4][MT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 w[D][4], h[D][MT];
+  int sw[D], sh[D];
+  auto load = [&](int s, int d) {
+    const int64_t k = min(s, a.steps - 1);      // past the end: the last step again, unused
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[d][i] = __builtin_nontemporal_load(wc + k * 256 + i * 64);
+    sw[d] = __builtin_nontemporal_load(ws + k * 64);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) h[d][m] = hc[k * 256 + m * 64];
+    sh[d] = hs[k * 64];
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(wave + 4 * d, d);
+  for (int s = wave; s < a.steps; s += 4 * D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (s + 4 * d < a.steps) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[i][m] = mfma_mx_sel(i, m, w[d][i], sw[d], h[d][m], sh[d], acc[i][m]);
+      }
+      load(s + 4 * (D + d), d);
+    }
   }
-  if (m0 + row < a.M) store4(a, m0 + row, v0 + 4 * blk, z);
+  const int col = lane & 15, blk = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f32x4 *>(&red[wave][(16 * m + col) * LDR + 16 * i + 4 * blk]) = acc[i][m];
+  __syncthreads();
+  for (int t = threadIdx.x; t < 16 * MT * 16; t += 256) {
+    const int m = t >> 4, v = 4 * (t & 15);
+    if (m >= a.M) break;
+    f32x4 z = *reinterpret_cast<const f32x4 *>(&red[0][m * LDR + v]);
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+      const f32x4 o = *reinterpret_cast<const f32x4 *>(&red[q][m * LDR + v]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] += o[e];
+    }
+    store4(a, m, 64 * (int)g + v, z);
+  }
+}
+
+// ------------------------------------------------------------- many hidden rows
+__device__ inline void raw_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// At most N of this wave's memory reads pending, no LDS read.
+template <int N>
+__device__ inline void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (((N >> 4) & 3) << 14) | (0x7 << 4));
+}
+
+// The matrix instruction with its accumulator as both operand and result, in accumulation
+// registers: left to itself the compiler gives this instruction another result register and
+// moves accumulators about, some 200 moves for 64 instructions. It also knows no hazards of
+// inline assembly, so two idle states stand before each (a vector write of an operand needs
+// them) and settle() stands between the last one and the first read of a result.
+#define SD_MX_INTO(SA0, SA1, SB0, SB1)                                                         \
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" #SA0       \
+      "," #SB0 ",0] op_sel_hi:[" #SA1 "," #SB1 ",0] cbsz:4 blgp:4"                              \
+      : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb))
+
+__device__ __forceinline__ void mfma_mx_into(int sel_a, int sel_b, const u32x4 &a, int sa, const u32x4 &b, int sb,
+                                             f32x4 &c) {
+  switch (sel_a * 4 + sel_b) {
+    case 0: SD_MX_INTO(0, 0, 0, 0); break;
+    case 1: SD_MX_INTO(0, 0, 1, 0); break;
+    case 2: SD_MX_INTO(0, 0, 0, 1); break;
+    case 3: SD_MX_INTO(0, 0, 1, 1); break;
+    case 4: SD_MX_INTO(1, 0, 0, 0); break;
+    case 5: SD_MX_INTO(1, 0, 1, 0); break;
+    case 6: SD_MX_INTO(1, 0, 0, 1); break;
+    case 7: SD_MX_INTO(1, 0, 1, 1); break;
+    case 8: SD_MX_INTO(0, 1, 0, 0); break;
+    case 9: SD_MX_INTO(0, 1, 1, 0); break;
+    case 10: SD_MX_INTO(0, 1, 0, 1); break;
+    case 11: SD_MX_INTO(0, 1, 1, 1); break;
+    case 12: SD_MX_INTO(1, 1, 0, 0); break;
+    case 13: SD_MX_INTO(1, 1, 1, 0); break;
+    case 14: SD_MX_INTO(1, 1, 0, 1); break;
+    default: SD_MX_INTO(1, 1, 1, 1); break;
+  }
+}
+#undef SD_MX_INTO
+
+__device__ __forceinline__ void settle() { asm volatile("s_nop 12"); }
+
+// A workgroup of four waves computes 64 GV ids by 64 GM hidden rows, each wave 16 TV by 16 TM
+// (WV by WM waves). A step's 128 columns of both operands come into one of NS LDS buffers by
+// direct loads, NS - 1 steps ahead. While a wave's matrix instructions consume step k from
+// registers it reads step k + 1's fragments from LDS, so with one wave a SIMD the matrix
+// units still run back to back. One barrier a step: behind it every wave has read step k
+// out of LDS, so its buffer takes step k + NS.
+template <int WV, int WM, int TV, int TM, int NS>
+__global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int n_vt) {
+  constexpr int GV = WV * TV / 4, GM = WM * TM / 4, G = GV + GM;
+  constexpr int STAGE = G * (4096 + 256);
+  constexpr int SPW = (G + 3) / 4;            // scale loads a wave
+  constexpr int DPT = G + SPW;                // loads a wave and step
+  static_assert(WV * WM == 4 && TV % 4 == 0 && TM % 4 == 0, "whole 64-row groups a wave");
+  __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wv = wave / WM, wm = wave % WM;
+  // Tiles go to the XCDs (workgroup id mod 8) in contiguous runs with the hidden tile
+  // running fastest: an XCD's workgroups share LM-head tiles and hidden tiles in its L2.
+  const int nb = n_mt * n_vt, hb = blockIdx.x;
+  const int per = nb / 8, rem = nb % 8, xcd = hb % 8, pos = hb / 8;
+  const int logical = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + pos;
+  const int mt = logical % n_mt, vt = logical / n_mt;
+  // Source of each of this wave's loads at step 0; a step further is 4096 (codes) or 256
+  // (scales) bytes. Groups past the end repeat the last one; their results are not stored.
+  const int last_v = (a.V - 1) / 64, last_m = (a.M - 1) / 64;
+  auto group = [&](int i, const uint8_t *w, const uint8_t *h, int64_t bytes) {
+    return i < GV ? w + (int64_t)min(vt * GV + i, last_v) * a.steps * bytes
+                  : h + (int64_t)min(mt * GM + i - GV, last_m) * a.steps * bytes;
+  };
+  const uint8_t *src[G], *ssrc[SPW];
+#pragma unroll
+  for (int i = 0; i < G; ++i) src[i] = group(i, a.wc, a.hc, 4096) + wave * 1024 + lane * 16;
+#pragma unroll
+  for (int i = 0; i < SPW; ++i) ssrc[i] = group(min(wave + 4 * i, G - 1), a.ws, a.hs, 256) + lane * 4;
+  auto issue = [&](int k) {
+    const int64_t kk = min(k, a.steps - 1);        // past the end: the last step again, unused
+    LDSP uint8_t *dst = (LDSP uint8_t *)S + (k % NS) * STAGE;
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      __builtin_amdgcn_global_load_lds((const GLBP void *)(src[i] + kk * 4096),
+                                       (LDSP void *)(dst + i * 4096 + wave * 1024), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < SPW; ++i)
+      __builtin_amdgcn_global_load_lds((const GLBP void *)(ssrc[i] + kk * 256),
+                                       (LDSP void *)(dst + G * 4096 + min(wave + 4 * i, G - 1) * 256), 4, 0, 0);
+  };
+  struct Frags {
+    u32x4 w[TV], h[TM];
+    int sw[TV / 4], sh[TM / 4];
+  };
+  auto fetch = [&](int k, Frags &f) {
+    const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE;
+    const LDSP uint8_t *wb = b + wv * TV * 1024 + lane * 16;
+    const LDSP uint8_t *hb = b + GV * 4096 + wm * TM * 1024 + lane * 16;
+    const LDSP uint8_t *sb = b + G * 4096 + lane * 4;
+#pragma unroll
+    for (int i = 0; i < TV / 4; ++i) f.sw[i] = *(const LDSP int *)(sb + (wv * TV / 4 + i) * 256);
+#pragma unroll
+    for (int i = 0; i < TM / 4; ++i) f.sh[i] = *(const LDSP int *)(sb + (GV + wm * TM / 4 + i) * 256);
+#pragma unroll
+    for (int i = 0; i < TV; ++i) f.w[i] = *(const LDSP u32x4 *)(wb + i * 1024);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) f.h[i] = *(const LDSP u32x4 *)(hb + i * 1024);
+  };
+  f32x4 acc[TV][TM];
+#pragma unroll
+  for (int i = 0; i < TV; ++i)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Frags &f) {
+#pragma unroll
+    for (int i = 0; i < TV; ++i)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+        mfma_mx_into(i % 4, m % 4, f.w[i], f.sw[i / 4], f.h[m], f.sh[m / 4], acc[i][m]);
+    settle();
+  };
+  // Step k: its fragments are in `now`; the next step's go to `next`.
+  auto step = [&](int k, const Frags &now, Frags &next) {
+    wait_loads<(NS - 2) * DPT>();      // step k + 1 has arrived
+    raw_barrier();
+    issue(k + NS);
+    fetch(k + 1, next);
+    multiply(now);
+  };
+#pragma unroll
+  for (int k = 0; k < NS; ++k) issue(k);
+  wait_loads<(NS - 1) * DPT>();
+  raw_barrier();
+  Frags f0, f1;
+  fetch(0, f0);
+  int k = 0;
+  for (; k + 1 < a.steps; k += 2) {
+    step(k, f0, f1);
+    step(k + 1, f1, f0);
+  }
+  if (k < a.steps) multiply(f0);
+  wait_loads<0>();                     // the trailing loads land before LDS is given up
+  const int col = lane & 15, blk = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int mm = mt * 64 * GM + (wm * TM + m) * 16 + col;
+    if (mm >= a.M) continue;
+#pragma unroll
+    for (int i = 0; i < TV; ++i) {
+      const int v = vt * 64 * GV + (wv * TV + i) * 16 + 4 * blk;
+      if (v < a.V) store4(a, mm, v, acc[i][m]);
+    }
+  }
 }
 
 int64_t blocks_of(int64_t threads) { return (threads + 255) / 256; }
 
+template <int WV, int WM, int TV, int TM, int NS>
+hipError_t launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
+  const int n_mt = (a.M + 16 * WM * TM - 1) / (16 * WM * TM), n_vt = (a.V + 16 * WV * TV - 1) / (16 * WV * TV);
+  hipLaunchKernelGGL((k_mx_tiled<WV, WM, TV, TM, NS>), dim3((unsigned)((int64_t)n_mt * n_vt)), dim3(256), 0,
+                     stream, a, n_mt, n_vt);
+  return hipGetLastError();
+}
+
+bool vec_rows(const void *x, int32_t type, int64_t stride, int elems) {
+  const int64_t size = type == SD_F32 ? 4 : 2, bytes = size * elems;
+  return reinterpret_cast<uintptr_t>(x) % bytes == 0 && stride * size % bytes == 0;
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride,
-                              uint8_t *codes, uint8_t *scales, hipStream_t stream) {
-  const int size = type == SD_F32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (stride * size) % 16 == 0;
-  const MxArgs a{x, type, rows, stride, d, mx_padded(d), vec, codes, scales};
+                              uint8_t *codes, uint8_t *scales, bool tiled, hipStream_t stream) {
+  const bool vec = vec_rows(x, type, stride, type == SD_F32 ? 4 : 8);
+  const MxArgs a{x, type, rows, stride, d, mx_padded(d), vec, tiled, codes, scales};
   hipLaunchKernelGGL(k_mx_quantize, dim3((unsigned)blocks_of(rows * (a.kp / 8))), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int d,
                                 void *x, int32_t type, int64_t stride, hipStream_t stream) {
-  const int size = type == SD_F32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (stride * size) % 16 == 0;
-  const MxArgs a{nullptr, type, rows, stride, d, mx_padded(d), vec, const_cast<uint8_t *>(codes),
+  const bool vec = vec_rows(x, type, stride, type == SD_F32 ? 4 : 8);
+  const MxArgs a{nullptr, type, rows, stride, d, mx_padded(d), vec, false, const_cast<uint8_t *>(codes),
                  const_cast<uint8_t *>(scales)};
   hipLaunchKernelGGL(k_mx_dequantize, dim3((unsigned)blocks_of(rows * ((d + 7) / 8))), dim3(256), 0,
                      stream, a, x);
   return hipGetLastError();
 }
 
-hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
-                            const uint8_t *w_codes, const uint8_t *w_scales, int V, void *logits,
-                            int32_t type, int64_t ld, void *workspace, hipStream_t stream) {
-  size_t co, so;
-  mx_logits_workspace_layout(M, d, &co, &so);
-  uint8_t *w = reinterpret_cast<uint8_t *>(workspace);
-  hipError_t e = launch_mx_quantize(hidden, hidden_type, M, d, stride, w + co, w + so, stream);
-  if (e != hipSuccess) return e;
-  const int size = type == SD_F32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(logits) % (4 * size) == 0 && (ld * size) % (4 * size) == 0;
-  const MxGemmArgs a{w + co, w + so, w_codes, w_scales, M, V, mx_padded(d), logits, type, ld, vec};
-  hipLaunchKernelGGL(k_mx_gemm, dim3((V + 63) / 64, (M + 15) / 16), dim3(256), 0, stream, a);
+size_t mx_tiled_bytes(int64_t rows, int d, size_t *scales) {
+  const size_t tiles = (size_t)((rows + 63) / 64) * (mx_padded(d) / 128);
+  if (scales) *scales = tiles * 4096;
+  return tiles * (4096 + 256);
+}
+
+hipError_t launch_mx_head(const uint8_t *codes, const uint8_t *scales, int V, int d, uint8_t *head,
+                          hipStream_t stream) {
+  size_t so;
+  const int64_t tiles = mx_tiled_bytes(V, d, &so) / (4096 + 256);
+  hipLaunchKernelGGL(k_mx_tile, dim3((unsigned)tiles), dim3(256), 0, stream, codes, scales, V, mx_padded(d),
+                     head, head + so);
   return hipGetLastError();
 }
 
-size_t mx_logits_workspace_layout(int M, int d, size_t *codes, size_t *scales) {
-  const size_t kp = mx_padded(d), c = sizeof(WsHeader);
-  const size_t s = align_up(c + (size_t)M * (kp / 2), 256);
-  if (codes) *codes = c;
-  if (scales) *scales = s;
-  return align_up(s + (size_t)M * (kp / 32), 256);
+size_t mx_logits_workspace_bytes(int M, int d) {
+  return align_up(sizeof(WsHeader) + mx_tiled_bytes(M, d, nullptr), 256);
+}
+
+hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
+                            const uint8_t *head, int V, void *logits, int32_t type, int64_t ld,
+                            void *workspace, hipStream_t stream) {
+  size_t hs, ws;
+  mx_tiled_bytes(M, d, &hs);
+  mx_tiled_bytes(V, d, &ws);
+  uint8_t *h = reinterpret_cast<uint8_t *>(workspace) + sizeof(WsHeader);
+  hipError_t e = launch_mx_quantize(hidden, hidden_type, M, d, stride, h, h + hs, true, stream);
+  if (e != hipSuccess) return e;
+  const MxGemmArgs a{h, h + hs, head, head + ws, M, V, mx_padded(d) / 128, logits, type, ld,
+                     vec_rows(logits, type, ld, 4)};
+  if (M <= 64) {
+    auto *k = M <= 16 ? &k_mx_skinny<1> : M <= 32 ? &k_mx_skinny<2> : &k_mx_skinny<4>;
+    hipLaunchKernelGGL(k, dim3((V + 63) / 64), dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
+  if (M <= 128) return launch_tiled<2, 2, 8, 4, 4>(a, stream);
+  return launch_tiled<2, 2, 8, 8, 4>(a, stream);
 }
 
 }  // namespace sdv

@@ -533,11 +533,19 @@ SD_API int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, 
                                    int32_t d, void *x, int32_t x_type, int64_t x_stride,
                                    void *stream);
 
-/* An MXFP4 LM head [V][d]: device pointers to codes and scales in the form above. */
-typedef struct sd_mxfp4 {
-    const uint8_t *codes;
-    const uint8_t *scales;
-} sd_mxfp4;
+/*
+ * The form of an MXFP4 LM head that sd_mxfp4_logits reads: the codes and scales above, re-laid
+ * once into tiles of 64 rows by 128 columns (rows past V zero), in one device buffer.
+ * sd_mxfp4_head_bytes: its size (0 unless V is in [1, 2^21] and d is a positive multiple of 8).
+ * sd_mxfp4_head: writes it on `stream`.
+ *   codes, scales  as above, [V] rows
+ *   head           sd_mxfp4_head_bytes(V, d) bytes, 256-byte aligned, apart from the inputs
+ *   Errors: SD_EINVAL (null pointer), SD_ESHAPE, SD_EALIGN, SD_EWORKSPACE (head_bytes too
+ *   small), SD_EDEVICE.
+ */
+SD_API size_t sd_mxfp4_head_bytes(int32_t V, int32_t d);
+SD_API int32_t sd_mxfp4_head(const uint8_t *codes, const uint8_t *scales, int32_t V, int32_t d,
+                             uint8_t *head, size_t head_bytes, void *stream);
 
 /*
  * Logits of hidden rows under an MXFP4 LM head (LFM2.5-DSpark blog, "Training &
@@ -546,18 +554,17 @@ typedef struct sd_mxfp4 {
  * so its copy of the LM head may be coarse.
  *   hidden   [M][d] of type hidden_type, row stride hidden_stride elements; quantised to
  *            MXFP4 in the call (into the workspace)
- *   lm_head  MXFP4 [V][d] (host struct)
+ *   head     the [V][d] LM head as sd_mxfp4_head wrote it
  *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
  *   workspace  sd_mxfp4_logits_workspace_bytes(M, d) bytes
  * logits[m][v] = sum over blocks of 2^(eh + ew) sum of the code products, accumulated in
  * fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives NaN.
  * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (M < 1, d not a positive multiple
- * of 8, V outside [1, 2^21], short strides), SD_EALIGN (codes, scales), SD_EWORKSPACE,
- * SD_EDEVICE.
+ * of 8, V outside [1, 2^21], short strides), SD_EALIGN, SD_EWORKSPACE, SD_EDEVICE.
  */
 SD_API size_t sd_mxfp4_logits_workspace_bytes(int32_t M, int32_t d);
 SD_API int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d,
-                               int64_t hidden_stride, const sd_mxfp4 *lm_head, int32_t V,
+                               int64_t hidden_stride, const uint8_t *head, int32_t V,
                                void *logits, int32_t logits_type, int64_t logits_stride,
                                void *workspace, size_t workspace_bytes, void *stream);
 

@@ -18,10 +18,6 @@ TWO = ctypes.c_void_p(0x10002)
 i64, sz = ctypes.c_int64, ctypes.c_size_t
 
 
-class Ptrs(ctypes.Structure):
-    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p)]
-
-
 class Four(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in "abcd"]
 
@@ -60,19 +56,34 @@ def test_mxfp4_rows_refusals(name):
     assert call(f, ok, codes=ctypes.c_void_p(0x10008)) == 3 and call(f, ok, scales=TWO) == 3
 
 
+def test_mxfp4_head_refusals():
+    size = lib.sd_mxfp4_head_bytes
+    size.restype = ctypes.c_size_t
+    assert size(64, 128) == 4096 + 256 and size(65, 136) == 4 * (4096 + 256)
+    assert size(0, 128) == size(5, 12) == size(5, 0) == size((1 << 21) + 1, 128) == 0
+    f = lib.sd_mxfp4_head
+    ok = dict(codes=FAKE, scales=FAKE, V=100, d=256, head=FAKE, n=sz(4 * 4352), stream=None)
+    for p in ("codes", "scales", "head"):
+        assert call(f, ok, **{p: None}) == 1
+    assert call(f, ok, V=0) == 2 and call(f, ok, d=100) == 2
+    assert call(f, ok, codes=ctypes.c_void_p(0x10008)) == 3 and call(f, ok, scales=TWO) == 3
+    assert call(f, ok, head=ctypes.c_void_p(0x10010)) == 3
+    assert call(f, ok, n=sz(4 * 4352 - 1)) == 4
+
+
 def test_mxfp4_logits_refusals():
     f = lib.sd_mxfp4_logits
-    w = Ptrs(0x10000, 0x10000)
-    ok = dict(hidden=FAKE, ht=1, M=3, d=256, hs=i64(256), head=ctypes.byref(w), V=100, out=FAKE, ot=0,
+    ok = dict(hidden=FAKE, ht=1, M=3, d=256, hs=i64(256), head=FAKE, V=100, out=FAKE, ot=0,
               ld=i64(100), ws=FAKE, wsb=sz(1 << 20), stream=None)
     for p in ("hidden", "head", "out"):
         assert call(f, ok, **{p: None}) == 1
-    assert call(f, ok, head=ctypes.byref(Ptrs(None, 0x10000))) == 1
     assert call(f, ok, ht=5) == 1 and call(f, ok, ot=5) == 1
     assert call(f, ok, M=0) == 2 and call(f, ok, d=100) == 2 and call(f, ok, V=0) == 2
     assert call(f, ok, V=(1 << 21) + 1, ld=i64(1 << 22)) == 2
+    assert call(f, ok, M=1 << 23, V=1 << 21, ld=i64(1 << 21), wsb=sz(1 << 40)) == 2
     assert call(f, ok, hs=i64(200)) == 2 and call(f, ok, ld=i64(99)) == 2
-    assert call(f, ok, out=TWO) == 3 and call(f, ok, head=ctypes.byref(Ptrs(0x10004, 0x10000))) == 3
+    assert call(f, ok, out=TWO) == 3 and call(f, ok, hidden=ODD) == 3
+    assert call(f, ok, head=ctypes.c_void_p(0x10010)) == 3
     assert call(f, ok, ws=None) == 4 and call(f, ok, wsb=sz(300)) == 4
     assert call(f, ok, ws=ctypes.c_void_p(0x10040)) == 3
 
