@@ -24,10 +24,13 @@
 
 namespace sdv {
 
-constexpr int kFilterThreads = 1024;
+constexpr int kFilterThreads = 512;
 constexpr int kFilterWaves = kFilterThreads / kWave;
-constexpr int kBins = 2048;          // linear bins of the mass histogram
-constexpr int kCandMax = 4096;       // ids of a cut bin that are ranked in LDS
+constexpr int kGrid = 4096;          // bins of the first pass's histogram, half on each side
+                                     // of its reference logit
+constexpr int kBins = 2048;          // bins of the narrowing path's histogram
+constexpr int kCandMax = 2048;       // ids that are ranked in LDS
+constexpr int kPerThread = kCandMax / kFilterThreads;
 constexpr int kFixBits = 46;         // most fraction bits of the summed weights
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // key of -inf (sort_key)
 
@@ -147,41 +150,75 @@ struct RowView {
     nv = (V - off + E::VE - 1) / E::VE;
   }
   __device__ int id(int j, int i) const { return off + j * E::VE + i; }
-  // Canonical values of vector j, -inf outside the row.
-  __device__ void load(int j, float (&v)[E::VE]) const {
+  __device__ bool whole(int j) const {
     const int b = off + j * E::VE;
-    if (b >= 0 && b + E::VE <= V) {
-      E::unpack(*reinterpret_cast<const u32x4 *>(p + b), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E::VE; ++i) v[i] = b + i >= 0 && b + i < V ? E::get(p[b + i]) : -INFINITY;
-    }
+    return b >= 0 && b + E::VE <= V;
+  }
+  __device__ float at(int x) const { return canonical(E::get(p[x])); }
+  // Canonical values of vector j, which lies in the row whole.
+  __device__ void load_whole(int j, float (&v)[E::VE]) const {
+    unpack(*reinterpret_cast<const u32x4 *>(p + off + j * E::VE), v);
+  }
+  __device__ static void unpack(const u32x4 &q, float (&v)[E::VE]) {
+    E::unpack(q, v);
 #pragma unroll
     for (int i = 0; i < E::VE; ++i) v[i] = canonical(v[i]);
   }
+  // Canonical values of any vector, -inf outside the row.
+  __device__ void load(int j, float (&v)[E::VE]) const {
+    if (whole(j)) {
+      load_whole(j, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E::VE; ++i) {
+        const int x = id(j, i);
+        v[i] = x >= 0 && x < V ? at(x) : -INFINITY;
+      }
+    }
+  }
 };
 
-// f(value, id) for the ids of vectors j0 .. j1 - 1, taken by the calling wave in order;
-// four vectors a lane are in flight at once.
-template <class E, class F>
-__device__ inline void wave_ids(const RowView<E> &r, int j0, int j1, F f) {
+// f(value, id) for the ids of vectors j0 .. j1 - 1, taken by the calling wave. The whole
+// vectors go first, a round's loads issued before the round ahead of it is used; then the
+// row's first and last vector if it holds them and they lie in it in part, lane i taking
+// element i. N: ids a lane and round.
+template <int N = 16, class E, class F>
+__device__ __forceinline__ void wave_ids(const RowView<E> &r, int j0, int j1, F f) {
   const int lane = threadIdx.x & 63;
-  constexpr int U = E::VE == 4 ? 2 : 1;
-  int j = j0 + lane;
-  for (; j + 64 * (U - 1) < j1; j += 64 * U) {
-    float v[U][E::VE];
+  constexpr int U = N > E::VE ? N / E::VE : 1;
+  const bool head = j0 == 0 && j0 < j1 && !r.whole(0);
+  const bool tail = j1 == r.nv && j0 < j1 && !r.whole(r.nv - 1) && !(head && r.nv == 1);
+  const int a = j0 + head, b = j1 - tail;
+  if (a < b) {
+    const typename E::S *base = r.p + r.off;
+    auto fetch = [&](int j) { return *reinterpret_cast<const u32x4 *>(base + (size_t)min(j, b - 1) * E::VE); };
+    u32x4 next[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r.load(j + 64 * u, v[u]);
+    for (int u = 0; u < U; ++u) next[u] = fetch(a + lane + 64 * u);
+    for (int j = a; j < b; j += 64 * U) {
+      u32x4 now[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) now[u] = next[u];
+      if (j + 64 * U < b) {
 #pragma unroll
-      for (int i = 0; i < E::VE; ++i) f(v[u][i], r.id(j + 64 * u, i));
+        for (int u = 0; u < U; ++u) next[u] = fetch(j + lane + 64 * (U + u));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = j + lane + 64 * u;
+        if (at < b) {
+          float v[E::VE];
+          r.unpack(now[u], v);
+#pragma unroll
+          for (int i = 0; i < E::VE; ++i) f(v[i], r.id(at, i));
+        }
+      }
+    }
   }
-  for (; j < j1; j += 64) {
-    float v[E::VE];
-    r.load(j, v);
-#pragma unroll
-    for (int i = 0; i < E::VE; ++i) f(v[i], r.id(j, i));
+  if ((head || tail) && lane < 2 * E::VE) {
+    const bool second = lane >= E::VE;
+    const int x = r.id(second ? r.nv - 1 : 0, second ? lane - E::VE : lane);
+    if ((second ? tail : head) && x >= 0 && x < r.V) f(r.at(x), x);
   }
 }
 
@@ -243,11 +280,16 @@ __device__ inline u64 wave_incl_scan_u64(u64 x) {
 
 // Shared memory of one workgroup's row.
 struct FilterSmem {
-  u64 mass[kBins];
-  uint32_t cnt[kBins];
+  union {
+    u64 grid[kGrid];       // first pass: weight (or count) by bin
+    struct {               // narrowing path
+      u64 mass[kBins];
+      uint32_t cnt[kBins];
+    };
+  };
   u64 cand[kCandMax];
   u64 red[kFilterWaves];
-  u64 red2[kFilterWaves];
+  u64 share[kFilterWaves];   // weight of the kept ids by wave's share of the row
   uint32_t n_cand;
   int hit;
   uint32_t key;
@@ -278,8 +320,27 @@ __device__ __forceinline__ u64 block_excl_scan_u64(u64 x, FilterSmem &s) {
   return before + incl - x;
 }
 
-// s.cand[0 .. n), n a power of two, sorted in descending order.
+// s.cand[0 .. n), n a power of two, sorted in descending order. Up to 128 of them are sorted
+// by the first wave alone: its LDS accesses take effect in order, so its steps need no barrier.
 __device__ __forceinline__ void sort_desc(FilterSmem &s, int n) {
+  __syncthreads();
+  if (n <= 128) {
+    if (threadIdx.x < 64) {
+      for (int size = 2; size <= n; size <<= 1) {
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+          const int t = threadIdx.x;
+          const int i = 2 * t - (t & (stride - 1)), j = i + stride;
+          if (t < n / 2) {
+            const u64 a = s.cand[i], b = s.cand[j];
+            if ((a < b) == ((i & size) == 0)) { s.cand[i] = b; s.cand[j] = a; }
+          }
+          asm volatile("" ::: "memory");
+        }
+      }
+    }
+    __syncthreads();
+    return;
+  }
   for (int size = 2; size <= n; size <<= 1) {
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
       __syncthreads();
@@ -293,37 +354,7 @@ __device__ __forceinline__ void sort_desc(FilterSmem &s, int n) {
   __syncthreads();
 }
 
-// ------------------------------------------------------------------ the cut
-// Largest logit of the row, the lowest id that attains it (-1 in a row without any), and the
-// count of ids above -inf.
-template <class E>
-__device__ __forceinline__ void row_max(const RowView<E> &r, FilterSmem &s, float *m, int *top, int *n) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
-  float best = -INFINITY;
-  int at = 0x7fffffff;
-  uint32_t any = 0;
-  wave_ids(r, wave * per, min(r.nv, wave * per + per), [&](float l, int id) {
-    if (l > best) { best = l; at = id; }
-    any += l > -INFINITY;
-  });
-  *n = (int)block_sum_u64(any, s);
-  // Larger key first, then lower id.
-  u64 k = best > -INFINITY ? ((u64)sort_key(best) << 32) | (uint32_t)~at : 0;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const u64 o = __shfl_xor(k, off);
-    k = o > k ? o : k;
-  }
-  __syncthreads();
-  if (lane == 0) s.red[wave] = k;
-  __syncthreads();
-  for (int w = 0; w < kFilterWaves; ++w) k = s.red[w] > k ? s.red[w] : k;
-  __syncthreads();
-  *m = k ? key_value((uint32_t)(k >> 32)) : -INFINITY;
-  *top = k ? (int)~(uint32_t)k : -1;
-}
-
+// ------------------------------------------------------------------ the narrowing path
 // Bins of the mass histogram: equal steps of (m - l), which falls as the rank rises, over
 // max(33 T, 16). A logit past that range weighs under 2^-47 (33 T are 47.6 octaves), so its
 // summed weight is 0 and no filter but the count of top-k can reach it: those ids are
@@ -344,14 +375,20 @@ struct BinScale {
 // Returns kBins when the sum over all bins stays under need.
 template <class F>
 __device__ __forceinline__ int find_bin(FilterSmem &s, u64 need, F f, u64 *before) {
-  const int b = 2 * threadIdx.x;
-  const u64 x0 = f(b), x1 = f(b + 1);
-  const u64 ex = block_excl_scan_u64(x0 + x1, s);
+  constexpr int P = kBins / kFilterThreads;
+  const int b = P * threadIdx.x;
+  u64 x[P], own = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) { x[i] = f(b + i); own += x[i]; }
+  u64 run = block_excl_scan_u64(own, s);
   if (threadIdx.x == 0) { s.hit = kBins; s.acc = 0; }
   __syncthreads();
   // Exactly one bin has before < need <= before + own (need >= 1).
-  if (ex < need && ex + x0 >= need) { s.hit = b; s.acc = ex; }
-  else if (ex + x0 < need && ex + x0 + x1 >= need) { s.hit = b + 1; s.acc = ex + x0; }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (run < need && run + x[i] >= need) { s.hit = b + i; s.acc = run; }
+    run += x[i];
+  }
   __syncthreads();
   const int hit = s.hit;
   *before = s.acc;
@@ -391,7 +428,7 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
     const int width = known == 22 ? 10 : 11, shift = 32 - known - width;
     for (int b = tid; b < kBins; b += kFilterThreads) { s.mass[b] = 0; s.cnt[b] = 0; }
     __syncthreads();
-    wave_ids(r, j0, j1, [&](float l, int) {
+    wave_ids<4>(r, j0, j1, [&](float l, int) {
       if (l == -INFINITY || bins.of(l) != cb) return;
       const uint32_t k = sort_key(l);
       if (known && (k >> (32 - known)) != prefix) return;
@@ -427,7 +464,7 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
       const int step = (b - a + kFilterWaves - 1) / kFilterWaves;
       const int w0 = a + wave * step, w1 = min(b, w0 + step);
       u64 c = 0;
-      wave_ids(r, w0, w1, [&](float l, int) { c += l > -INFINITY && sort_key(l) == prefix; });
+      wave_ids<4>(r, w0, w1, [&](float l, int) { c += l > -INFINITY && sort_key(l) == prefix; });
       c = wave_sum_u64(c);
       __syncthreads();
       if ((tid & 63) == 0) s.red[wave] = c;
@@ -466,7 +503,7 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
   // Rank the ids in LDS.
   if (tid == 0) s.n_cand = 0;
   __syncthreads();
-  wave_ids(r, j0, j1, [&](float l, int id) {
+  wave_ids<4>(r, j0, j1, [&](float l, int id) {
     if (l == -INFINITY || bins.of(l) != cb) return;
     const uint32_t k = sort_key(l);
     if (known && (known == 32 ? k : k >> (32 - known)) != prefix) return;
@@ -479,18 +516,18 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
   while (pow2 < n) pow2 <<= 1;
   for (int i = n + tid; i < pow2; i += kFilterThreads) s.cand[i] = 0;
   sort_desc(s, pow2);
-  // Thread t holds ranks 4 t .. 4 t + 3.
-  u64 w[4], own = 0;
+  // Thread t holds ranks kPerThread t .. .
+  u64 w[kPerThread], own = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = 4 * tid + i;
+  for (int i = 0; i < kPerThread; ++i) {
+    const int at = kPerThread * tid + i;
     w[i] = at < n ? to_fix(weight(key_value((uint32_t)(s.cand[at] >> 32)), bins.m, set.sl), set.unit) : 0;
     own += w[i];
   }
   u64 run = mass_before + block_excl_scan_u64(own, s);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = 4 * tid + i;
+  for (int i = 0; i < kPerThread; ++i) {
+    const int at = kPerThread * tid + i;
     const u64 incl = run + w[i];
     const bool is = at < n && (by_mass ? (run < need && incl >= need) : n_before + at + 1 == need);
     if (is) {
@@ -507,38 +544,25 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
   return c;
 }
 
-// The cut of one row; every thread of the workgroup gets it. The pass over the row that
-// forms the histogram is left out when neither top-k nor top-p is set. S is set only by
-// row_mass.
+// The narrowing path: the cut of a row whose largest logit c.m and lowest such id c.top are
+// known, for every row that the single-pass path leaves: more ids at the cut than are ranked
+// in LDS, or a top-k past them.
 template <class E>
-__device__ __forceinline__ RowCut row_cut(const RowView<E> &r, const RowSettings &set, FilterSmem &s) {
+__device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
   const int tid = threadIdx.x, wave = tid >> 6;
-  RowCut c;
-  c.S = 0;
-  c.pad = 0;
-  row_max(r, s, &c.m, &c.top, &c.n);
-  if (c.top < 0) {                       // nothing to keep: every id is masked
-    c.key = 0xffffffffu; c.id = -1; c.n = 0;
-    return c;
-  }
-  if (set.greedy || set.k == 1 || set.p <= 0.0) {
-    c.key = sort_key(c.m); c.id = c.top; c.n = 1;
-    return c;
-  }
-  c.key = kKeyNegInf; c.id = -1;
-  if (set.k >= r.V && set.p >= 1.0 && set.min_p <= 0.0) return c;
+  c.key = kKeyNegInf;
+  c.id = -1;
   const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
   const int j0 = wave * per, j1 = min(r.nv, j0 + per);
   const BinScale bins(c.m, set.T);
-  const bool ranks = set.k < r.V || set.p < 1.0;
+  __syncthreads();
   for (int b = tid; b < kBins; b += kFilterThreads) { s.mass[b] = 0; s.cnt[b] = 0; }
   __syncthreads();
   uint32_t n_m = 0, low = 0xffffffffu, past = 0;
-  wave_ids(r, j0, j1, [&](float l, int) {
+  wave_ids<4>(r, j0, j1, [&](float l, int) {
     if (l == -INFINITY) return;
     const double w = weight(l, c.m, set.sl);
     if (w >= set.min_p) { ++n_m; low = min(low, sort_key(l)); }
-    if (!ranks) return;
     const int b = bins.of(l);
     if (b == kBins - 1) { ++past; return; }
     atomicAdd(&s.cnt[b], 1u);
@@ -557,30 +581,24 @@ __device__ __forceinline__ RowCut row_cut(const RowView<E> &r, const RowSettings
   past = (uint32_t)(both >> 32);
   u64 n = n_m;                           // w >= min_p (all of them when min_p is off)
   if (set.min_p > 0.0) { c.key = low; c.id = 0x7fffffff; }
-  if (ranks) {
-    u64 mass_k, n_k = (u64)set.k, cnt_before, mass_before;
+  {
     u64 total = 0, in_bins = 0;
     for (int b = tid; b < kBins; b += kFilterThreads) { total += s.mass[b]; in_bins += s.cnt[b]; }
     total = block_sum_u64(total, s);
     in_bins = block_sum_u64(in_bins, s);
     CutAt at{kKeyNegInf, -1, in_bins + past, total};
-    if (n_k < in_bins) {
-      const int kb = find_bin(s, n_k, [&](int b) { return (u64)s.cnt[b]; }, &cnt_before);
-      mass_before = 0;
-      for (int b = tid; b < kb; b += kFilterThreads) mass_before += s.mass[b];
-      mass_before = block_sum_u64(mass_before, s);
-      at = cut_in_bin(r, s, bins, set, kb, false, n_k, cnt_before, mass_before);
-    } else if (n_k < in_bins + past) {
-      // The run ends among ids without weight: they count, and cannot be drawn.
-      at.n = n_k;
-    }
-    mass_k = at.mass;
-    if (set.p < 1.0) {
-      // The histogram again: narrowing the top-k cut may have overwritten it.
-      const u64 need = at_least(set.p * (double)mass_k);
+    // A top-k run that ends among ids without weight: they count, and cannot be drawn.
+    if ((u64)set.k >= in_bins && (u64)set.k < at.n) at.n = set.k;
+    // First the end of the top-k run, then that of the top-p run inside it.
+#pragma unroll 1
+    for (int by_mass = 0; by_mass < 2; ++by_mass) {
+      if (by_mass ? !(set.p < 1.0) : !((u64)set.k < in_bins)) continue;
+      const u64 need = by_mass ? at_least(set.p * (double)at.mass) : (u64)set.k;
+      // The histogram again: narrowing the top-k run may have overwritten it.
+      __syncthreads();
       for (int b = tid; b < kBins; b += kFilterThreads) { s.mass[b] = 0; s.cnt[b] = 0; }
       __syncthreads();
-      wave_ids(r, j0, j1, [&](float l, int) {
+      wave_ids<4>(r, j0, j1, [&](float l, int) {
         if (l == -INFINITY) return;
         const int b = bins.of(l);
         if (b == kBins - 1) return;
@@ -588,11 +606,12 @@ __device__ __forceinline__ RowCut row_cut(const RowView<E> &r, const RowSettings
         atomicAdd(&s.mass[b], to_fix(weight(l, c.m, set.sl), set.unit));
       });
       __syncthreads();
-      const int pb = find_bin(s, need, [&](int b) { return s.mass[b]; }, &mass_before);
-      cnt_before = 0;
-      for (int b = tid; b < pb; b += kFilterThreads) cnt_before += s.cnt[b];
-      cnt_before = block_sum_u64(cnt_before, s);
-      const CutAt q = cut_in_bin(r, s, bins, set, pb, true, need, cnt_before, mass_before);
+      u64 before, n_before = 0, mass_before = 0;
+      const int bin = find_bin(s, need, [&](int b) { return by_mass ? s.mass[b] : (u64)s.cnt[b]; }, &before);
+      for (int b = tid; b < bin; b += kFilterThreads) { n_before += s.cnt[b]; mass_before += s.mass[b]; }
+      n_before = block_sum_u64(n_before, s);
+      mass_before = block_sum_u64(mass_before, s);
+      const CutAt q = cut_in_bin(r, s, bins, set, bin, by_mass, need, n_before, mass_before);
       if (q.n < at.n) at = q;
     }
     // The shorter of the two runs.
@@ -603,7 +622,320 @@ __device__ __forceinline__ RowCut row_cut(const RowView<E> &r, const RowSettings
     }
   }
   c.n = (int)n;
-  return c;
+}
+
+// ------------------------------------------------------------------ the cut
+// Bins of the first pass: steps of the logit's distance from a reference logit, kGrid / 2 on
+// each side; 33 T (or 16 when ids are counted, so that small temperatures still spread them)
+// fill one side. With the row's largest logit at or above the reference and below the upper
+// end, a logit under the lower end weighs less than 2^-47 of it.
+struct Grid {
+  float ref;
+  double k;           // bins a logit
+  __device__ Grid(float ref_, float T, bool count)
+      : ref(ref_), k((double)(kGrid / 2) / (count ? fmax(33.0 * (double)T, 16.0) : 33.0 * (double)T)) {}
+  // Position in bins from the lower end; no id outside [0, kGrid) is binned.
+  __device__ double pos(float l) const {
+    return l == ref ? (double)(kGrid / 2) : ((double)l - (double)ref) * k + (double)(kGrid / 2);
+  }
+};
+
+// Octaves a bin of a weight grid: 33 log2(e) / (kGrid / 2). A bin sums its weights relative
+// to its own lower end, 2^(y octaves) for a position y in [0, 1) inside it -- five Taylor
+// terms leave (octaves ln 2)^6 / 720 = 2e-14 --, so bins need no common scale and the pass
+// over the row no maximum to start from.
+constexpr double kBinNats = 33.0 / (kGrid / 2);
+
+__device__ inline double bin_weight(double y) {
+  const double z = y * kBinNats;
+  double s = 1.0 / 120.0;
+  s = __builtin_fma(s, z, 1.0 / 24.0);
+  s = __builtin_fma(s, z, 1.0 / 6.0);
+  s = __builtin_fma(s, z, 0.5);
+  s = __builtin_fma(s, z, 1.0);
+  return __builtin_fma(s, z, 1.0);
+}
+
+// Smallest value (not -inf) for which `ok`, which holds from some value on; +inf has to be
+// one. Each wave searches by itself, 64 probes a step.
+template <class F>
+__device__ __forceinline__ float smallest(F ok) {
+  const int lane = threadIdx.x & 63;
+  uint32_t lo = kKeyNegInf + 1, hi = 0xff800000u;   // keys of the lowest finite value and +inf
+  while (hi > lo) {
+    const uint32_t step = (hi - lo + 63) / 64;
+    const uint32_t probe = (uint32_t)lane * step < hi - lo ? lo + (uint32_t)lane * step : hi;
+    const u64 m = __ballot(ok(key_value(probe)));
+    if (m == 0) { lo = lo + 63 * step < hi ? lo + 63 * step + 1 : hi; continue; }
+    const int first = __ffsll((long long)m) - 1;
+    const uint32_t at = (uint32_t)first * step < hi - lo ? lo + (uint32_t)first * step : hi;
+    if (first == 0) { hi = lo; break; }
+    lo = at - step + 1;
+    hi = at;
+  }
+  return key_value(hi);
+}
+
+// Where the kept ids' weights are after row_cut.
+enum RowMode {
+  kModeTop,      // at most one id
+  kModeList,     // s.cand[0 .. c.n), by rank
+  kModeShares,   // s.share, by wave's share of the vectors
+  kModeNone      // not summed yet (c.S unset)
+};
+
+// First pass over the row: its largest logit, the lowest id that attains it, the count of ids
+// above -inf, and (hist) the grid's counts or weights. Returns whether an id lies past the
+// grid's upper end.
+template <class E>
+__device__ __forceinline__ bool first_pass(const RowView<E> &r, const Grid &g, bool hist, bool count, double unit,
+                                           int j0, int j1, RowCut &c, u64 *any, FilterSmem &s) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float best = -INFINITY;
+  int at = 0x7fffffff;
+  uint32_t n = 0;
+  wave_ids(r, j0, j1, [&](float l, int id) {
+    if (l > best || (l == best && id < at)) { best = l; at = id; }
+    if (l == -INFINITY) return;
+    ++n;
+    if (!hist) return;
+    const double x = g.pos(l), fl = __builtin_floor(x);
+    if (fl >= 0.0 && fl < (double)kGrid)
+      atomicAdd(&s.grid[(int)fl], count ? 1ull : to_fix(bin_weight(x - fl), unit));
+  });
+  // Larger key first, then lower id.
+  u64 k = best > -INFINITY ? ((u64)sort_key(best) << 32) | (uint32_t)~at : 0;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const u64 o = __shfl_xor(k, off);
+    k = o > k ? o : k;
+  }
+  *any = block_sum_u64(n, s);
+  __syncthreads();
+  if (lane == 0) s.red[wave] = k;
+  __syncthreads();
+  for (int w = 0; w < kFilterWaves; ++w) k = s.red[w] > k ? s.red[w] : k;
+  __syncthreads();
+  c.m = k ? key_value((uint32_t)(k >> 32)) : -INFINITY;
+  c.top = k ? (int)~(uint32_t)k : -1;
+  return hist && k && !(g.pos(c.m) < (double)kGrid);
+}
+
+// Bin of the grid, counted from its upper end, at which the running total first reaches need,
+// with the total up to and including it (kGrid when the whole stays under need). f(b): the
+// total of bin b.
+template <class F>
+__device__ __forceinline__ int find_from_top(FilterSmem &s, u64 need, F f, u64 *upto) {
+  constexpr int P = kGrid / kFilterThreads;
+  const int b0 = P * threadIdx.x;
+  u64 own = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) own += f(kGrid - 1 - (b0 + i));
+  u64 run = block_excl_scan_u64(own, s);
+  if (threadIdx.x == 0) { s.hit = kGrid; s.acc = 0; }
+  __syncthreads();
+  if (run < need && run + own >= need) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const u64 x = f(kGrid - 1 - (b0 + i));
+      if (run < need && run + x >= need) { s.hit = b0 + i; s.acc = run + x; }
+      run += x;
+    }
+  }
+  __syncthreads();
+  const int hit = s.hit;
+  *upto = s.acc;
+  __syncthreads();
+  return hit;
+}
+
+// The cut of one row and the weight of what it keeps; every thread of the workgroup gets both.
+//   1. One pass bins the row (first_pass), around a reference taken from a few thousand of
+//      its logits; a row whose largest logit lies past the grid is passed again around that.
+//   2. The bin that holds the cut, and the smallest logits of it and of the bin above, follow
+//      from the bins' totals.
+//   3. A second pass sums the weights of the ids above that bin and lists the ids in it; when
+//      all kept ids are few they are all listed and nothing is summed by pass.
+//   4. The list is ranked in LDS and cut.
+// What bounds it: the first pass reads the row from memory, the second from the cache behind
+// it; weights take some 15 fp64 instructions an id.
+template <class E>
+__device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
+  const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
+  const bool one = set.greedy || set.k == 1 || set.p <= 0.0;
+  const bool count = !one && set.k < r.V, mass = !one && !count && set.p < 1.0;
+  c.S = 0;
+  c.pad = 0;
+  float ref = 0.f;
+  if (count || mass) {
+    ref = -INFINITY;
+    wave_ids(r, j0, min(j1, j0 + 128), [&](float l, int) { ref = fmaxf(ref, l); });
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) ref = fmaxf(ref, __shfl_xor(ref, off));
+    if ((tid & 63) == 0) s.red[wave] = __float_as_uint(ref);
+    __syncthreads();
+    for (int w = 0; w < kFilterWaves; ++w) ref = fmaxf(ref, __uint_as_float((uint32_t)s.red[w]));
+  }
+  // Weights in the bins: up to V of them, each under 1.02.
+  const double bin_unit = set.unit * 0.25;
+  u64 any;
+  for (int attempt = 0;; ++attempt) {
+    const Grid g(ref, set.T, count);
+    if (count || mass) {
+      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
+      __syncthreads();
+    }
+    const bool past = first_pass(r, g, count || mass, count, bin_unit, j0, j1, c, &any, s);
+    if (!past || attempt == 1) break;
+    ref = c.m;
+  }
+  if (c.top < 0) {                       // nothing to keep: every id is masked
+    c.key = 0xffffffffu; c.id = -1; c.n = 0;
+    return kModeTop;
+  }
+  c.key = sort_key(c.m); c.id = c.top; c.n = 1;
+  if (one) {
+    c.S = to_fix(1.0, set.unit);
+    return kModeTop;
+  }
+  // Smallest logit that is listed and smallest that is kept without ranking; min-p is a
+  // bound on the logit too.
+  const Grid g(ref, set.T, count);
+  float t_lo = key_value(kKeyNegInf + 1), t_hi = t_lo;
+  bool list = false, narrow = false;
+  u64 need = 0;
+  if (count) {
+    u64 upto;
+    const int kb = find_from_top(s, (u64)set.k, [&](int b) { return s.grid[b]; }, &upto);
+    if (kb == kGrid) {                   // fewer than k in the grid
+      u64 in = 0;
+      for (int b = tid; b < kGrid; b += kFilterThreads) in += s.grid[b];
+      upto = block_sum_u64(in, s);
+      if (upto != any) upto = kCandMax + 1;
+    } else {
+      t_lo = smallest([&](float l) { return g.pos(l) >= (double)(kGrid - 1 - kb); });
+    }
+    list = true;
+    narrow = upto > kCandMax;
+  } else if (mass) {
+    // Bin totals under the row's maximum, in its unit.
+    const double xm = g.pos(c.m);
+    auto total = [&](int b) {
+      const double w = ((double)b - xm) * (kBinNats * 1.4426950408889634);
+      return s.grid[b] ? (u64)((double)s.grid[b] * (set.unit / bin_unit) * exp2_neg(w < 0.0 ? w : 0.0)) : 0ull;
+    };
+    u64 sum = 0;
+    for (int b = tid; b < kGrid; b += kFilterThreads) sum += total(b);
+    need = at_least(set.p * (double)block_sum_u64(sum, s));
+    u64 upto;
+    const int pb = kGrid - 1 - find_from_top(s, need, total, &upto);
+    // No bin holds more ids than its weights say: each is at least 1 in bin_unit.
+    const u64 in_bin = s.grid[pb] / (u64)bin_unit;
+    u64 above = 0;
+    for (int b = pb + 1 + tid; b < kGrid; b += kFilterThreads) above += s.grid[b] / (u64)bin_unit + 1;
+    above = block_sum_u64(above, s);
+    narrow = in_bin > kCandMax;
+    t_lo = smallest([&](float l) { return g.pos(l) >= (double)pb; });
+    list = above + in_bin <= kCandMax;
+    if (!list) t_hi = smallest([&](float l) { return g.pos(l) >= (double)(pb + 1); });
+  }
+  if (narrow) {
+    cut_narrowing(r, set, c, s);
+    return kModeNone;
+  }
+  if (set.min_p > 0.0) {
+    const float t_m = smallest([&](float l) { return weight(l, c.m, set.sl) >= set.min_p; });
+    t_lo = fmaxf(t_lo, t_m);
+    t_hi = fmaxf(t_hi, t_m);
+  }
+  if (tid == 0) s.n_cand = 0;
+  __syncthreads();
+  u64 sum = 0;
+  uint32_t n_sum = 0;
+  wave_ids(r, j0, j1, [&](float l, int id) {
+    if (!(l >= t_lo)) return;
+    if (list || l < t_hi) {
+      const uint32_t at = atomicAdd(&s.n_cand, 1u);
+      if (at < kCandMax) s.cand[at] = ((u64)sort_key(l) << 32) | (uint32_t)~id;
+    } else {
+      ++n_sum;
+      sum += to_fix(weight(l, c.m, set.sl), set.unit);
+    }
+  });
+  sum = wave_sum_u64(sum);
+  __syncthreads();
+  if ((tid & 63) == 0) s.share[wave] = sum;
+  const u64 n_above = block_sum_u64(n_sum, s);
+  u64 mass_above = 0;
+  for (int w = 0; w < kFilterWaves; ++w) mass_above += s.share[w];
+  const int nc = (int)s.n_cand;
+  c.key = sort_key(t_hi); c.id = 0x7fffffff;
+  c.n = (int)n_above;
+  c.S = mass_above;
+  if (nc == 0) return kModeShares;
+  int pow2 = 2;
+  while (pow2 < nc) pow2 <<= 1;
+  for (int i = nc + tid; i < pow2; i += kFilterThreads) s.cand[i] = 0;
+  sort_desc(s, pow2);
+  u64 w[kPerThread], own = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int at = kPerThread * tid + i;
+    w[i] = at < nc ? to_fix(weight(key_value((uint32_t)(s.cand[at] >> 32)), c.m, set.sl), set.unit) : 0;
+    own += w[i];
+  }
+  const u64 first = mass_above + block_excl_scan_u64(own, s);
+  const int nk = min(nc, set.k);
+  if (count && set.p < 1.0) {
+    u64 run = first;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      run += w[i];
+      if (kPerThread * tid + i == nk - 1) s.acc = run;
+    }
+    __syncthreads();
+    need = at_least(set.p * (double)s.acc);
+  }
+  if (tid == 0) s.hit = nk;
+  __syncthreads();
+  if (set.p < 1.0) {
+    u64 run = first;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int at = kPerThread * tid + i;
+      if (at < nk && run < need && run + w[i] >= need) s.hit = at + 1;
+      run += w[i];
+    }
+    if (tid == 0 && mass_above >= need) s.hit = 0;
+  }
+  __syncthreads();
+  const int take = s.hit;
+  if (take > 0) {
+    u64 run = first;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int at = kPerThread * tid + i;
+      run += w[i];
+      if (at == take - 1) {
+        s.acc2 = run;
+        s.key = (uint32_t)(s.cand[at] >> 32);
+        s.id = (int)~(uint32_t)s.cand[at];
+      }
+      if (at < take && !list) {
+        const int share = (((int)~(uint32_t)s.cand[at]) - r.off) / E::VE / per;
+        atomicAdd(&s.share[share], w[i]);
+      }
+    }
+    __syncthreads();
+    c.S = s.acc2;
+    c.key = s.key;
+    c.id = s.id;
+    c.n = (int)n_above + take;
+  }
+  __syncthreads();
+  return list ? kModeList : kModeShares;
 }
 
 // ------------------------------------------------------------------ the draw
@@ -618,11 +950,11 @@ __device__ inline void kept_weights(const RowView<E> &r, const RowCut &c, const 
     w[i] = v[i] > -INFINITY && kept(c, v[i], r.id(j, i)) ? to_fix(weight(v[i], c.m, set.sl), set.unit) : 0;
 }
 
-// Sum of f's weights over vectors a .. b - 1, dealt to the waves in contiguous shares of
-// `step` vectors; s.red holds each wave's part afterwards. f(j, w) gives vector j's weights.
+// Weights f(j, w) of vectors a .. b - 1 summed over the waves' contiguous shares of `step`
+// vectors: s.share afterwards, and the total.
 template <int VE, class F>
-__device__ __forceinline__ u64 range_mass(F f, int a, int b, int step, FilterSmem &s) {
-  const int w0 = a + (int)(threadIdx.x >> 6) * step, w1 = min(b, w0 + step);
+__device__ __forceinline__ u64 sum_shares(F f, int a, int b, int step, FilterSmem &s) {
+  const int wave = threadIdx.x >> 6, w0 = a + wave * step, w1 = min(b, w0 + step);
   u64 m = 0;
 #pragma unroll 2
   for (int j = w0 + (int)(threadIdx.x & 63); j < w1; j += 64) {
@@ -631,28 +963,36 @@ __device__ __forceinline__ u64 range_mass(F f, int a, int b, int step, FilterSme
 #pragma unroll
     for (int i = 0; i < VE; ++i) m += w[i];
   }
-  return block_sum_u64(m, s);
+  m = wave_sum_u64(m);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s.share[wave] = m;
+  __syncthreads();
+  u64 total = 0;
+  for (int w = 0; w < kFilterWaves; ++w) total += s.share[w];
+  return total;
 }
 
-// Position (vector VE + element) of the first weight whose running sum passes u times the
-// total *S, -1 when the total is 0: shares of the vectors are summed by wave, and the
-// share that holds the crossing is split again until one wave load covers it. u outside
-// [0, 1) is taken as the nearest end of the range, NaN as 0.
+// What a draw for uniform u of total S has to pass. u outside [0, 1) is taken as the nearest
+// end of the range, NaN as 0.
+__device__ inline double draw_target(float u, u64 S) {
+  return (u >= 1.f ? 0.99999994 : (u > 0.f ? (double)u : 0.0)) * (double)S;
+}
+
+// Position (vector VE + element) of the first weight whose running sum passes t, given the
+// waves' shares of all nv vectors in s.share: the share that holds the crossing is split
+// again until one wave load covers it.
 template <int VE, class F>
-__device__ __forceinline__ int split_draw(F f, int nv, float u, u64 *S, FilterSmem &s) {
+__device__ __forceinline__ int draw_in_shares(F f, int nv, double t, FilterSmem &s) {
   int a = 0, b = nv, step = (b + kFilterWaves - 1) / kFilterWaves;
-  *S = range_mass<VE>(f, a, b, step, s);
-  if (*S == 0) return -1;
-  const double t = (u >= 1.f ? 0.99999994 : (u > 0.f ? (double)u : 0.0)) * (double)*S;
   u64 before = 0;
   for (;;) {
     int w = 0;
-    while (w < kFilterWaves - 1 && !((double)(before + s.red[w]) > t)) before += s.red[w++];
+    while (w < kFilterWaves - 1 && !((double)(before + s.share[w]) > t)) before += s.share[w++];
     a += w * step;
     b = min(b, a + step);
     if (b - a <= 64) break;
     step = (b - a + kFilterWaves - 1) / kFilterWaves;
-    range_mass<VE>(f, a, b, step, s);
+    sum_shares<VE>(f, a, b, step, s);
   }
   if (threadIdx.x < 64) {
     const int j = a + threadIdx.x;
@@ -679,28 +1019,54 @@ __device__ __forceinline__ int split_draw(F f, int nv, float u, u64 *S, FilterSm
   return at;
 }
 
-// Sets c.S and returns the row's draw for uniform u: the smallest kept id whose running
-// weight, in id order, passes u times the total; -1 for an empty row.
+// The row's draw for uniform u: the smallest kept id whose running weight, in id order, passes
+// u times the total (set in c.S when row_cut left it out); -1 for an empty row.
 template <class E>
-__device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const RowSettings &set, float u,
-                        FilterSmem &s) {
-  if (c.n <= 1) {
+__device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const RowSettings &set, RowMode mode, float u,
+                                        FilterSmem &s) {
+  const int tid = threadIdx.x;
+  if (mode == kModeTop || c.n <= 1) {
     c.S = c.n ? to_fix(1.0, set.unit) : 0;
     return c.n ? c.top : -1;
   }
-  const int at = split_draw<E::VE>([&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); },
-                                   r.nv, u, &c.S, s);
-  return r.off + at;
+  if (mode == kModeList) {
+    // The list by id: the complement makes the lowest id the largest word.
+    int pow2 = 2;
+    while (pow2 < c.n) pow2 <<= 1;
+    for (int i = tid; i < pow2; i += kFilterThreads) {
+      const u64 x = i < c.n ? s.cand[i] : 0;
+      s.cand[i] = (x << 32) | (x >> 32);
+    }
+    sort_desc(s, pow2);
+    u64 w[kPerThread], own = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int at = kPerThread * tid + i;
+      w[i] = at < c.n ? to_fix(weight(key_value((uint32_t)s.cand[at]), c.m, set.sl), set.unit) : 0;
+      own += w[i];
+    }
+    const double t = draw_target(u, c.S);
+    u64 run = block_excl_scan_u64(own, s);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (!((double)run > t) && (double)(run + w[i]) > t) s.id = (int)~(uint32_t)(s.cand[kPerThread * tid + i] >> 32);
+      run += w[i];
+    }
+    __syncthreads();
+    const int id = s.id;
+    __syncthreads();
+    return id;
+  }
+  auto f = [&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); };
+  if (mode == kModeNone) c.S = sum_shares<E::VE>(f, 0, r.nv, (r.nv + kFilterWaves - 1) / kFilterWaves, s);
+  return r.off + draw_in_shares<E::VE>(f, r.nv, draw_target(u, c.S), s);
 }
 
-// Sets c.S alone.
+// Sets c.S when row_cut left it out.
 template <class E>
-__device__ __forceinline__ void row_total(const RowView<E> &r, RowCut &c, const RowSettings &set, FilterSmem &s) {
-  if (c.n <= 1) {
-    c.S = c.n ? to_fix(1.0, set.unit) : 0;
-    return;
-  }
-  c.S = range_mass<E::VE>([&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); }, 0, r.nv,
+__device__ __forceinline__ void row_total(const RowView<E> &r, RowCut &c, const RowSettings &set, RowMode mode, FilterSmem &s) {
+  if (mode != kModeNone) return;
+  c.S = sum_shares<E::VE>([&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); }, 0, r.nv,
                           (r.nv + kFilterWaves - 1) / kFilterWaves, s);
 }
 

@@ -33,8 +33,9 @@ __global__ __launch_bounds__(kFilterThreads) void k_sample(SampleArgs a) {
   const int row = blockIdx.x;
   const RowView<E> r(reinterpret_cast<const typename E::S *>(a.logits) + row * a.stride, a.V);
   const RowSettings set = load_settings(a.set, row / a.rows_per, a.V, threadIdx.x == 0 ? a.ws : nullptr);
-  RowCut c = row_cut(r, set, s);
-  const int id = row_draw(r, c, set, a.u[row], s);
+  RowCut c;
+  const RowMode mode = row_cut(r, set, c, s);
+  const int id = row_draw(r, c, set, mode, a.u[row], s);
   if (threadIdx.x == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
     a.tokens[row * a.token_stride] = id;
@@ -97,13 +98,13 @@ __global__ __launch_bounds__(kFilterThreads) void k_filter_rows(FilteredArgs a) 
   const RowSettings set = load_settings(a.set, r, a.V, nullptr);
   if (draft) {
     const RowView<ElemBF16> v(a.draft_logits + (size_t)i * a.V, a.V);
-    RowCut c = row_cut(v, set, s);
-    row_total(v, c, set, s);
+    RowCut c;
+    row_total(v, c, set, row_cut(v, set, c, s), s);
     if (threadIdx.x == 0) a.cut_q[i] = c;
   } else {
     const RowView<ElemF32> v(a.logits + (size_t)(base + j) * a.V, a.V);
-    RowCut c = row_cut(v, set, s);
-    row_total(v, c, set, s);
+    RowCut c;
+    row_total(v, c, set, row_cut(v, set, c, s), s);
     if (threadIdx.x == 0) a.cut_p[i] = c;
   }
 }
@@ -169,8 +170,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_draw(FilteredArgs a
   if (acc < L && cp.n > 0) {
     const uint16_t *q = a.draft_logits + ((size_t)r * g + acc) * a.V;
     const RowCut cq = a.cut_q[(size_t)r * g + acc];
-    u64 S;
-    const int at = split_draw<4>([&](int j, u64 (&w)[4]) {
+    auto f = [&](int j, u64 (&w)[4]) {
       float l[4];
       v.load(j, l);
 #pragma unroll
@@ -179,11 +179,12 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_draw(FilteredArgs a
         const double p = prob(cp, set, l[i], x);
         w[i] = p > 0.0 ? to_fix(fmax(p - prob(cq, set, bf16_to_f32(q[x]), x), 0.0), kResidualUnit) : 0;
       }
-    }, v.nv, u, &S, s);
-    if (at >= 0) id = v.off + at;
+    };
+    const u64 S = sum_shares<4>(f, 0, v.nv, (v.nv + kFilterWaves - 1) / kFilterWaves, s);
+    if (S > 0) id = v.off + draw_in_shares<4>(f, v.nv, draw_target(u, S), s);
     else if (threadIdx.x == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
   }
-  if (id < 0) id = row_draw(v, cp, set, u, s);
+  if (id < 0) id = row_draw(v, cp, set, kModeNone, u, s);
   if (threadIdx.x == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
     a.next_token[r] = id;
