@@ -7,7 +7,7 @@
 //   n_m = ids with w >= min_p.
 // The kept set is then stated by its last member alone: the pair (key, id) of a RowCut.
 //
-// Weights are formed in fp64 (relative error about 1e-14) and summed as 64-bit integers in
+// Weights are formed in fp64 (relative error 4e-14) and summed as 64-bit integers in
 // units of 2^-b: integer sums do not depend on order, so results are the same whatever
 // the split over lanes, waves and workgroups, and every running sum is exact in those
 // units. b is 46, less for rows of more than 2^17 ids so that V 2^b stays under 2^63. One
@@ -31,6 +31,7 @@ constexpr int kGrid = 4096;          // bins of the first pass's histogram, half
 constexpr int kBins = 2048;          // bins of the narrowing path's histogram
 constexpr int kCandMax = 2048;       // ids that are ranked in LDS
 constexpr int kPerThread = kCandMax / kFilterThreads;
+constexpr int kMaxShares = 64;       // parts a row's vectors are summed in
 constexpr int kFixBits = 46;         // most fraction bits of the summed weights
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // key of -inf (sort_key)
 
@@ -76,25 +77,25 @@ __device__ inline RowSettings load_settings(const SampleSettings &s, int i, int 
   return r;
 }
 
-// What keeps an id of a row: sort key above `key`, or equal to it and id <= `id`.
+// What keeps an id of a row: a logit above `val`, or equal to it and id <= `id`.
 struct RowCut {
   float m;        // largest logit of the row, -inf when the row has none
-  uint32_t key;
+  float val;
   int32_t id;
-  int32_t n;      // ids kept
+  int32_t n;      // ids kept (at least: some calls only tell none from some)
   u64 S;          // their weight, in RowSettings::unit
-  int32_t top;    // lowest id that attains m, -1 when the row has none
-  int32_t pad;
+  int32_t pad[2];
 };
 static_assert(sizeof(RowCut) == 32, "row cuts are 32 bytes");
 
 // ------------------------------------------------------------------ elements
-// NaN counts as -inf (never kept) and -0 as +0, so that equal values have equal keys.
-__device__ inline float canonical(float x) { return x != x ? -INFINITY : x + 0.f; }
+// NaN counts as -inf (never kept): the maximum of a NaN and a number is the number.
+__device__ inline float canonical(float x) { return __builtin_fmaxf(x, -INFINITY); }
 
-// Order-preserving bits: a > b <=> sort_key(a) > sort_key(b) for canonical values.
+// Order-preserving bits: a > b <=> sort_key(a) > sort_key(b) for canonical values (-0 has the
+// key of +0).
 __device__ inline uint32_t sort_key(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
@@ -223,31 +224,36 @@ __device__ __forceinline__ void wave_ids(const RowView<E> &r, int j0, int j1, F 
 }
 
 // ------------------------------------------------------------------ weights
-// 2^x for x <= 0 in fp64: 2^n times the Taylor series of e^(f ln 2), |f| <= 1/2. The first
-// term left out, (ln(2) / 2)^12 / 12!, is 6e-15.
-__device__ inline double exp2_neg(double x) {
-  if (x < -1000.0) return 0.0;
-  const double n = __builtin_rint(x);
-  const double y = (x - n) * 0.6931471805599453;
-  double s = 1.0 / 39916800.0;
-  s = __builtin_fma(s, y, 1.0 / 3628800.0);
-  s = __builtin_fma(s, y, 1.0 / 362880.0);
-  s = __builtin_fma(s, y, 1.0 / 40320.0);
-  s = __builtin_fma(s, y, 1.0 / 5040.0);
-  s = __builtin_fma(s, y, 1.0 / 720.0);
-  s = __builtin_fma(s, y, 1.0 / 120.0);
-  s = __builtin_fma(s, y, 1.0 / 24.0);
-  s = __builtin_fma(s, y, 1.0 / 6.0);
-  s = __builtin_fma(s, y, 0.5);
-  s = __builtin_fma(s, y, 1.0);
-  s = __builtin_fma(s, y, 1.0);
+// 2^x in fp64: 2^n (1 + f q(f)) for the nearest whole n and f = x - n. q is the polynomial of
+// degree 8 through (2^f - 1) / f at the nine Chebyshev points of [-1/2, 1/2]; the relative
+// error of the result is at most 4e-14, and f = 0 gives exactly 2^n. Every fused step is
+// written out and the compiler may form no other: a weight formed in two places must be the
+// same number, or a running sum could miss a border by a unit.
+__device__ inline double exp2_f64(double x) {
+#pragma clang fp contract(off)
+  const double n = __builtin_rint(x), f = x - n;
+  double s = 1.0203121063391729e-07;
+  s = __builtin_fma(s, f, 1.3255224878668817e-06);
+  s = __builtin_fma(s, f, 1.525268684626772e-05);
+  s = __builtin_fma(s, f, 0.00015403455852453838);
+  s = __builtin_fma(s, f, 0.0013333558179043112);
+  s = __builtin_fma(s, f, 0.009618129159402558);
+  s = __builtin_fma(s, f, 0.055504108664760424);
+  s = __builtin_fma(s, f, 0.2402265069581299);
+  s = __builtin_fma(s, f, 0.6931471805599453);
+  s = __builtin_fma(s, f, 1.0);
   return __builtin_ldexp(s, (int)n);
 }
 
-// Weight of logit l under row maximum m. The maximum itself weighs 1 also when infinite.
-__device__ inline double weight(float l, float m, double sl) {
+// Weight of a finite logit l under a finite row maximum m.
+__device__ inline double weight_finite(float l, float m, double sl) {
 #pragma clang fp contract(off)
-  return l == m ? 1.0 : exp2_neg(((double)l - (double)m) * sl);
+  return exp2_f64(((double)l - (double)m) * sl);
+}
+
+// Weight of any logit above -inf: ids at a maximum of +inf share the whole weight.
+__device__ inline double weight(float l, float m, double sl) {
+  return l == m ? 1.0 : m == INFINITY ? 0.0 : weight_finite(l, m, sl);
 }
 
 // w * unit rounded to nearest, for results under 2^52: the fp64 sum's low 52 bits hold it.
@@ -257,8 +263,7 @@ __device__ inline u64 to_fix(double w, double unit) {
 }
 
 __device__ inline bool kept(const RowCut &c, float l, int id) {
-  const uint32_t k = sort_key(l);
-  return k > c.key || (k == c.key && id <= c.id);
+  return l > c.val || (l == c.val && id <= c.id);
 }
 
 // ------------------------------------------------------------------ workgroup sums
@@ -281,7 +286,7 @@ __device__ inline u64 wave_incl_scan_u64(u64 x) {
 // Shared memory of one workgroup's row.
 struct FilterSmem {
   union {
-    u64 grid[kGrid];       // first pass: weight (or count) by bin
+    u64 grid[kGrid + 64];  // first pass: weight (or count) by bin, then spare words
     struct {               // narrowing path
       u64 mass[kBins];
       uint32_t cnt[kBins];
@@ -289,7 +294,7 @@ struct FilterSmem {
   };
   u64 cand[kCandMax];
   u64 red[kFilterWaves];
-  u64 share[kFilterWaves];   // weight of the kept ids by wave's share of the row
+  u64 share[kMaxShares];     // weight of the kept ids by share of the row
   uint32_t n_cand;
   int hit;
   uint32_t key;
@@ -544,13 +549,12 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
   return c;
 }
 
-// The narrowing path: the cut of a row whose largest logit c.m and lowest such id c.top are
-// known, for every row that the single-pass path leaves: more ids at the cut than are ranked
-// in LDS, or a top-k past them.
+// The narrowing path: the cut of a row whose largest logit c.m is known, for every row that the single-pass path leaves: more ids at the cut than are ranked
+// in LDS, a top-k past them, logits too large for the grid's arithmetic, or +inf among them.
 template <class E>
 __device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
   const int tid = threadIdx.x, wave = tid >> 6;
-  c.key = kKeyNegInf;
+  c.val = -INFINITY;
   c.id = -1;
   const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
   const int j0 = wave * per, j1 = min(r.nv, j0 + per);
@@ -580,7 +584,7 @@ __device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSett
   n_m = (uint32_t)both;
   past = (uint32_t)(both >> 32);
   u64 n = n_m;                           // w >= min_p (all of them when min_p is off)
-  if (set.min_p > 0.0) { c.key = low; c.id = 0x7fffffff; }
+  if (set.min_p > 0.0) { c.val = key_value(low); c.id = 0x7fffffff; }
   {
     u64 total = 0, in_bins = 0;
     for (int b = tid; b < kBins; b += kFilterThreads) { total += s.mass[b]; in_bins += s.cnt[b]; }
@@ -617,7 +621,7 @@ __device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSett
     // The shorter of the two runs.
     if (at.n < n) {
       n = at.n;
-      c.key = at.key;
+      c.val = key_value(at.key);
       c.id = at.id;
     }
   }
@@ -625,36 +629,60 @@ __device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSett
 }
 
 // ------------------------------------------------------------------ the cut
-// Bins of the first pass: steps of the logit's distance from a reference logit, kGrid / 2 on
-// each side; 33 T (or 16 when ids are counted, so that small temperatures still spread them)
-// fill one side. With the row's largest logit at or above the reference and below the upper
-// end, a logit under the lower end weighs less than 2^-47 of it.
-struct Grid {
-  float ref;
-  double k;           // bins a logit
-  __device__ Grid(float ref_, float T, bool count)
-      : ref(ref_), k((double)(kGrid / 2) / (count ? fmax(33.0 * (double)T, 16.0) : 33.0 * (double)T)) {}
-  // Position in bins from the lower end; no id outside [0, kGrid) is binned.
-  __device__ double pos(float l) const {
-    return l == ref ? (double)(kGrid / 2) : ((double)l - (double)ref) * k + (double)(kGrid / 2);
-  }
+// How a row's cut is found.
+enum CutKind {
+  kCutOne,     // the likeliest id alone: no weights
+  kCutCount,   // top-k: ids are counted by bin
+  kCutMass,    // top-p without top-k (or totals alone are wanted): weights are summed by bin
+  kCutSum      // no ranking: weights are summed where they are drawn from
 };
 
-// Octaves a bin of a weight grid: 33 log2(e) / (kGrid / 2). A bin sums its weights relative
-// to its own lower end, 2^(y octaves) for a position y in [0, 1) inside it -- five Taylor
-// terms leave (octaves ln 2)^6 / 720 = 2e-14 --, so bins need no common scale and the pass
-// over the row no maximum to start from.
-constexpr double kBinNats = 33.0 / (kGrid / 2);
+// totals: only the kept set and its weight are wanted, not a draw.
+__device__ inline CutKind cut_kind(const RowSettings &set, int V, bool totals) {
+  if (set.greedy || set.k == 1 || set.p <= 0.0) return kCutOne;
+  if (set.k < V) return kCutCount;
+  return set.p < 1.0 || totals ? kCutMass : kCutSum;
+}
+
+// Bins of the first pass: steps of the logit's distance from a reference logit, kGrid / 2 on
+// each side; 33 T (or 16 when ids are counted, so that small temperatures still spread them)
+// fill one side. With the row's largest logit at or above the reference and inside the grid,
+// a logit under its lower end weighs less than 2^-47 of it.
+struct Grid {
+  double k, c;        // position of logit l in bins from the lower end: l k + c
+  bool fine;          // positions are good to 1e-12 bins
+  __device__ Grid(float ref, float T, bool count) {
+    k = (double)(kGrid / 2) / (count ? fmax(33.0 * (double)T, 16.0) : 33.0 * (double)T);
+    c = (double)(kGrid / 2) - (double)ref * k;
+    fine = fabs(c) < 16384.0 + kGrid;
+  }
+  __device__ double pos(float l) const { return __builtin_fma((double)l, k, c); }
+};
+
+// x towards 0, saturating (a C++ conversion leaves positions outside int undefined).
+__device__ inline uint32_t whole_part(double x) {
+  int i;
+  asm("v_cvt_i32_f64 %0, %1" : "=v"(i) : "v"(x));
+  return (uint32_t)i;
+}
+
+// A bin sums its weights relative to its own lower end, e^(a y) for the position y in [0, 1)
+// inside it with a = 33 / (kGrid / 2): bins need no common scale and the pass over the row no
+// maximum to start from. The polynomial goes through e^(a y) at five Chebyshev points of
+// [0, 1]; its relative error is 2e-14.
+constexpr double kBinOctaves = 33.0 * 1.4426950408889634 / (kGrid / 2);
 
 __device__ inline double bin_weight(double y) {
-  const double z = y * kBinNats;
-  double s = 1.0 / 120.0;
-  s = __builtin_fma(s, z, 1.0 / 24.0);
-  s = __builtin_fma(s, z, 1.0 / 6.0);
-  s = __builtin_fma(s, z, 0.5);
-  s = __builtin_fma(s, z, 1.0);
-  return __builtin_fma(s, z, 1.0);
+  static_assert(kGrid == 4096, "the coefficients are those of a = 33 / 2048");
+  double s = 2.8315539305093126e-09;
+  s = __builtin_fma(s, y, 6.972496547552619e-07);
+  s = __builtin_fma(s, y, 0.00012981892343785);
+  s = __builtin_fma(s, y, 0.016113281249110118);
+  return __builtin_fma(s, y, 1.0000000000000178);
 }
+
+// Unit of the bins' sums: up to V weights under 1.02 stay under 2^64.
+__device__ inline double bin_unit(const RowSettings &set) { return set.unit * 0.25; }
 
 // Smallest value (not -inf) for which `ok`, which holds from some value on; +inf has to be
 // one. Each wave searches by itself, 64 probes a step.
@@ -676,49 +704,57 @@ __device__ __forceinline__ float smallest(F ok) {
   return key_value(hi);
 }
 
-// Where the kept ids' weights are after row_cut.
-enum RowMode {
-  kModeTop,      // at most one id
-  kModeList,     // s.cand[0 .. c.n), by rank
-  kModeShares,   // s.share, by wave's share of the vectors
-  kModeNone      // not summed yet (c.S unset)
-};
-
-// First pass over the row: its largest logit, the lowest id that attains it, the count of ids
-// above -inf, and (hist) the grid's counts or weights. Returns whether an id lies past the
-// grid's upper end.
-template <class E>
-__device__ __forceinline__ bool first_pass(const RowView<E> &r, const Grid &g, bool hist, bool count, double unit,
-                                           int j0, int j1, RowCut &c, u64 *any, FilterSmem &s) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Lane's part of the first pass over vectors j0 .. j1 - 1: the largest logit (best), and by
+// kind the lowest id that attains it (at), the ids above -inf (any), the grid's bins in LDS.
+struct PassOut {
   float best = -INFINITY;
   int at = 0x7fffffff;
-  uint32_t n = 0;
-  wave_ids(r, j0, j1, [&](float l, int id) {
-    if (l > best || (l == best && id < at)) { best = l; at = id; }
-    if (l == -INFINITY) return;
-    ++n;
-    if (!hist) return;
-    const double x = g.pos(l), fl = __builtin_floor(x);
-    if (fl >= 0.0 && fl < (double)kGrid)
-      atomicAdd(&s.grid[(int)fl], count ? 1ull : to_fix(bin_weight(x - fl), unit));
-  });
-  // Larger key first, then lower id.
-  u64 k = best > -INFINITY ? ((u64)sort_key(best) << 32) | (uint32_t)~at : 0;
+  uint32_t any = 0;
+};
+
+template <class E>
+__device__ __forceinline__ void bin_pass(const RowView<E> &r, const Grid &g, CutKind kind, double unit, int j0, int j1,
+                                         PassOut &o, FilterSmem &s) {
+  // An id outside the grid adds to one of 64 words behind it, a lane's own, unread: without a
+  // branch around the add.
+  const uint32_t spare = kGrid + (threadIdx.x & 63);
+  if (kind == kCutMass) {
+    wave_ids(r, j0, j1, [&](float l, int) {
+      o.best = fmaxf(o.best, l);
+      const double x = g.pos(l);
+      const uint32_t b = whole_part(x);
+      atomicAdd(&s.grid[b < kGrid ? b : spare], to_fix(bin_weight(__builtin_amdgcn_fract(x)), unit));
+    });
+  } else if (kind == kCutCount) {
+    wave_ids(r, j0, j1, [&](float l, int) {
+      o.best = fmaxf(o.best, l);
+      o.any += l > -INFINITY;
+      const uint32_t b = whole_part(g.pos(l));
+      atomicAdd(reinterpret_cast<uint32_t *>(&s.grid[b < kGrid ? b : spare]), 1u);
+    });
+  } else {
+    wave_ids(r, j0, j1, [&](float l, int id) {
+      if (l > o.best || (l == o.best && id < o.at)) { o.best = l; o.at = id; }
+    });
+  }
+}
+
+// Larger logit first, then lower id; 0 for none.
+__device__ inline u64 rank_word(float l, int id) { return l > -INFINITY ? ((u64)sort_key(l) << 32) | (uint32_t)~id : 0; }
+__device__ inline float word_value(u64 w) { return w ? key_value((uint32_t)(w >> 32)) : -INFINITY; }
+__device__ inline int word_id(u64 w) { return w ? (int)~(uint32_t)w : -1; }
+
+__device__ __forceinline__ u64 block_max_u64(u64 k, FilterSmem &s) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     const u64 o = __shfl_xor(k, off);
     k = o > k ? o : k;
   }
-  *any = block_sum_u64(n, s);
   __syncthreads();
-  if (lane == 0) s.red[wave] = k;
+  if ((threadIdx.x & 63) == 0) s.red[threadIdx.x >> 6] = k;
   __syncthreads();
   for (int w = 0; w < kFilterWaves; ++w) k = s.red[w] > k ? s.red[w] : k;
-  __syncthreads();
-  c.m = k ? key_value((uint32_t)(k >> 32)) : -INFINITY;
-  c.top = k ? (int)~(uint32_t)k : -1;
-  return hist && k && !(g.pos(c.m) < (double)kGrid);
+  return k;
 }
 
 // Bin of the grid, counted from its upper end, at which the running total first reaches need,
@@ -749,132 +785,120 @@ __device__ __forceinline__ int find_from_top(FilterSmem &s, u64 need, F f, u64 *
   return hit;
 }
 
-// The cut of one row and the weight of what it keeps; every thread of the workgroup gets both.
-//   1. One pass bins the row (first_pass), around a reference taken from a few thousand of
-//      its logits; a row whose largest logit lies past the grid is passed again around that.
-//   2. The bin that holds the cut, and the smallest logits of it and of the bin above, follow
-//      from the bins' totals.
-//   3. A second pass sums the weights of the ids above that bin and lists the ids in it; when
-//      all kept ids are few they are all listed and nothing is summed by pass.
-//   4. The list is ranked in LDS and cut.
-// What bounds it: the first pass reads the row from memory, the second from the cache behind
-// it; weights take some 15 fp64 instructions an id.
-template <class E>
-__device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
-  const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
-  const bool one = set.greedy || set.k == 1 || set.p <= 0.0;
-  const bool count = !one && set.k < r.V, mass = !one && !count && set.p < 1.0;
-  c.S = 0;
-  c.pad = 0;
-  float ref = 0.f;
-  if (count || mass) {
-    ref = -INFINITY;
-    wave_ids(r, j0, min(j1, j0 + 128), [&](float l, int) { ref = fmaxf(ref, l); });
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) ref = fmaxf(ref, __shfl_xor(ref, off));
-    if ((tid & 63) == 0) s.red[wave] = __float_as_uint(ref);
-    __syncthreads();
-    for (int w = 0; w < kFilterWaves; ++w) ref = fmaxf(ref, __uint_as_float((uint32_t)s.red[w]));
-  }
-  // Weights in the bins: up to V of them, each under 1.02.
-  const double bin_unit = set.unit * 0.25;
-  u64 any;
-  for (int attempt = 0;; ++attempt) {
-    const Grid g(ref, set.T, count);
-    if (count || mass) {
-      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
-      __syncthreads();
-    }
-    const bool past = first_pass(r, g, count || mass, count, bin_unit, j0, j1, c, &any, s);
-    if (!past || attempt == 1) break;
-    ref = c.m;
-  }
-  if (c.top < 0) {                       // nothing to keep: every id is masked
-    c.key = 0xffffffffu; c.id = -1; c.n = 0;
-    return kModeTop;
-  }
-  c.key = sort_key(c.m); c.id = c.top; c.n = 1;
-  if (one) {
-    c.S = to_fix(1.0, set.unit);
-    return kModeTop;
-  }
-  // Smallest logit that is listed and smallest that is kept without ranking; min-p is a
-  // bound on the logit too.
-  const Grid g(ref, set.T, count);
-  float t_lo = key_value(kKeyNegInf + 1), t_hi = t_lo;
-  bool list = false, narrow = false;
-  u64 need = 0;
-  if (count) {
+// What the second pass does with an id: from t_hi up it is kept without ranking, from t_lo up
+// it is listed (with `list` every id from t_lo up is).
+struct CutPlan {
+  float t_lo, t_hi;
+  bool list;
+  bool narrow;     // left to the narrowing path
+  u64 need;        // weight at which the top-p run of a kCutMass row ends, 0 without one
+  u64 above;       // kCutMass: weight of the ids from t_hi up, by the bins
+};
+
+// The plan of a row with largest logit m (above -inf, inside the grid or plan.narrow results)
+// and `any` ids above -inf (kCutCount), from the grid in LDS. Every thread gets it.
+__device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kind, const Grid &g, float m, u64 any,
+                                             FilterSmem &s) {
+  const int tid = threadIdx.x;
+  const float lowest = key_value(kKeyNegInf + 1);
+  CutPlan p{lowest, lowest, false, m == INFINITY, 0, 0};
+  const bool min_p = set.min_p > 0.0;
+  if (kind == kCutCount || kind == kCutMass) p.narrow |= !g.fine || !(g.pos(m) < (double)kGrid);
+  if (p.narrow) return p;
+  const float t_m = min_p ? smallest([&](float l) { return l >= m || weight_finite(l, m, set.sl) >= set.min_p; }) : lowest;
+  if (kind == kCutSum) {
+    p.t_lo = p.t_hi = t_m;
+  } else if (kind == kCutCount) {
+    p.list = true;
     u64 upto;
-    const int kb = find_from_top(s, (u64)set.k, [&](int b) { return s.grid[b]; }, &upto);
+    auto f = [&](int b) { return (u64) * reinterpret_cast<const uint32_t *>(&s.grid[b]); };
+    const int kb = find_from_top(s, (u64)set.k, f, &upto);
     if (kb == kGrid) {                   // fewer than k in the grid
       u64 in = 0;
-      for (int b = tid; b < kGrid; b += kFilterThreads) in += s.grid[b];
+      for (int b = tid; b < kGrid; b += kFilterThreads) in += f(b);
       upto = block_sum_u64(in, s);
-      if (upto != any) upto = kCandMax + 1;
+      p.narrow = upto != any;
     } else {
-      t_lo = smallest([&](float l) { return g.pos(l) >= (double)(kGrid - 1 - kb); });
+      p.t_lo = smallest([&](float l) { return g.pos(l) >= (double)(kGrid - 1 - kb); });
     }
-    list = true;
-    narrow = upto > kCandMax;
-  } else if (mass) {
+    p.narrow |= upto > kCandMax;
+    p.t_lo = fmaxf(p.t_lo, t_m);
+  } else {
     // Bin totals under the row's maximum, in its unit.
-    const double xm = g.pos(c.m);
+    const double xm = g.pos(m), scale = set.unit / bin_unit(set);
     auto total = [&](int b) {
-      const double w = ((double)b - xm) * (kBinNats * 1.4426950408889634);
-      return s.grid[b] ? (u64)((double)s.grid[b] * (set.unit / bin_unit) * exp2_neg(w < 0.0 ? w : 0.0)) : 0ull;
+      return s.grid[b] ? (u64)((double)s.grid[b] * scale * exp2_f64(((double)b - xm) * kBinOctaves)) : 0ull;
     };
-    u64 sum = 0;
-    for (int b = tid; b < kGrid; b += kFilterThreads) sum += total(b);
-    need = at_least(set.p * (double)block_sum_u64(sum, s));
-    u64 upto;
-    const int pb = kGrid - 1 - find_from_top(s, need, total, &upto);
-    // No bin holds more ids than its weights say: each is at least 1 in bin_unit.
-    const u64 in_bin = s.grid[pb] / (u64)bin_unit;
-    u64 above = 0;
-    for (int b = pb + 1 + tid; b < kGrid; b += kFilterThreads) above += s.grid[b] / (u64)bin_unit + 1;
-    above = block_sum_u64(above, s);
-    narrow = in_bin > kCandMax;
-    t_lo = smallest([&](float l) { return g.pos(l) >= (double)pb; });
-    list = above + in_bin <= kCandMax;
-    if (!list) t_hi = smallest([&](float l) { return g.pos(l) >= (double)(pb + 1); });
-  }
-  if (narrow) {
-    cut_narrowing(r, set, c, s);
-    return kModeNone;
-  }
-  if (set.min_p > 0.0) {
-    const float t_m = smallest([&](float l) { return weight(l, c.m, set.sl) >= set.min_p; });
-    t_lo = fmaxf(t_lo, t_m);
-    t_hi = fmaxf(t_hi, t_m);
-  }
-  if (tid == 0) s.n_cand = 0;
-  __syncthreads();
-  u64 sum = 0;
-  uint32_t n_sum = 0;
-  wave_ids(r, j0, j1, [&](float l, int id) {
-    if (!(l >= t_lo)) return;
-    if (list || l < t_hi) {
-      const uint32_t at = atomicAdd(&s.n_cand, 1u);
-      if (at < kCandMax) s.cand[at] = ((u64)sort_key(l) << 32) | (uint32_t)~id;
-    } else {
-      ++n_sum;
-      sum += to_fix(weight(l, c.m, set.sl), set.unit);
+    // The bin with the cut: that of top-p, or of min-p's bound if that is higher.
+    int cb = -1;
+    if (set.p < 1.0) {
+      u64 sum = 0, upto;
+      for (int b = tid; b < kGrid; b += kFilterThreads) sum += total(b);
+      p.need = at_least(set.p * (double)block_sum_u64(sum, s));
+      cb = kGrid - 1 - find_from_top(s, p.need, total, &upto);
     }
-  });
-  sum = wave_sum_u64(sum);
-  __syncthreads();
-  if ((tid & 63) == 0) s.share[wave] = sum;
-  const u64 n_above = block_sum_u64(n_sum, s);
-  u64 mass_above = 0;
-  for (int w = 0; w < kFilterWaves; ++w) mass_above += s.share[w];
-  const int nc = (int)s.n_cand;
-  c.key = sort_key(t_hi); c.id = 0x7fffffff;
+    if (min_p) {
+      const int mb = max(0, (int)g.pos(t_m));
+      if (mb > cb) { cb = mb; p.need = 0; }
+    }
+    // No bin holds more ids than its weights say: each is at least 1 (to 2e-14).
+    const double per_id = 1.001 / bin_unit(set);
+    u64 above = 0, ids = 0;
+    for (int b = cb + 1 + tid; b < kGrid; b += kFilterThreads) {
+      above += total(b);
+      ids += (u64)((double)s.grid[b] * per_id);
+    }
+    p.above = block_sum_u64(above, s);
+    ids = block_sum_u64(ids, s);
+    if (cb >= 0) {
+      const u64 in_bin = (u64)((double)s.grid[cb] * per_id);
+      p.narrow = in_bin > kCandMax;
+      p.list = ids + in_bin <= kCandMax;
+      p.t_lo = fmaxf(smallest([&](float l) { return g.pos(l) >= (double)cb; }), t_m);
+      p.t_hi = smallest([&](float l) { return g.pos(l) >= (double)(cb + 1); });
+    }
+  }
+  return p;
+}
+
+// Second pass over vectors j0 .. j1 - 1: lists ids in s.cand (s.n_cand counts them) and, with
+// `sums`, adds up the rest of the kept ones.
+template <class E>
+__device__ __forceinline__ void collect_pass(const RowView<E> &r, const RowSettings &set, const CutPlan &p, float m,
+                                             bool sums, int j0, int j1, u64 *sum, uint32_t *n, FilterSmem &s) {
+  const float hi = p.list ? INFINITY : p.t_hi;
+  if (sums && !p.list) {
+    wave_ids(r, j0, j1, [&](float l, int id) {
+      if (!(l >= p.t_lo)) return;
+      if (l < hi) {
+        const uint32_t at = atomicAdd(&s.n_cand, 1u);
+        if (at < kCandMax) s.cand[at] = rank_word(l, id);
+      } else {
+        ++*n;
+        *sum += to_fix(weight_finite(l, m, set.sl), set.unit);
+      }
+    });
+  } else if (p.t_lo < hi) {
+    wave_ids(r, j0, j1, [&](float l, int id) {
+      if (l >= p.t_lo && l < hi) {
+        const uint32_t at = atomicAdd(&s.n_cand, 1u);
+        if (at < kCandMax) s.cand[at] = rank_word(l, id);
+      }
+    });
+  }
+}
+
+// Ranks s.cand[0 .. nc) and cuts it: c.val, c.id, c.n, c.S, given the ids kept without ranking
+// (n_above of them, weight c.S). share(id, w) is told the weight of each listed id that is
+// kept. Afterwards the list's kept ids are its first c.n - n_above.
+template <class F>
+__device__ __forceinline__ void rank_list(const RowSettings &set, CutKind kind, const CutPlan &p, int nc, uint32_t n_above,
+                                          RowCut &c, FilterSmem &s, F share) {
+  const int tid = threadIdx.x;
+  const u64 mass_above = c.S;
+  c.val = p.t_hi; c.id = 0x7fffffff;
   c.n = (int)n_above;
-  c.S = mass_above;
-  if (nc == 0) return kModeShares;
+  if (nc == 0) return;
   int pow2 = 2;
   while (pow2 < nc) pow2 <<= 1;
   for (int i = nc + tid; i < pow2; i += kFilterThreads) s.cand[i] = 0;
@@ -883,12 +907,13 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int at = kPerThread * tid + i;
-    w[i] = at < nc ? to_fix(weight(key_value((uint32_t)(s.cand[at] >> 32)), c.m, set.sl), set.unit) : 0;
+    w[i] = at < nc ? to_fix(weight_finite(word_value(s.cand[at]), c.m, set.sl), set.unit) : 0;
     own += w[i];
   }
   const u64 first = mass_above + block_excl_scan_u64(own, s);
   const int nk = min(nc, set.k);
-  if (count && set.p < 1.0) {
+  u64 need = p.need;
+  if (kind == kCutCount && set.p < 1.0) {
     u64 run = first;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -900,7 +925,7 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
   }
   if (tid == 0) s.hit = nk;
   __syncthreads();
-  if (set.p < 1.0) {
+  if (need > 0) {
     u64 run = first;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -918,24 +943,114 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
     for (int i = 0; i < kPerThread; ++i) {
       const int at = kPerThread * tid + i;
       run += w[i];
+      if (at < take) share(word_id(s.cand[at]), w[i]);
       if (at == take - 1) {
         s.acc2 = run;
         s.key = (uint32_t)(s.cand[at] >> 32);
-        s.id = (int)~(uint32_t)s.cand[at];
-      }
-      if (at < take && !list) {
-        const int share = (((int)~(uint32_t)s.cand[at]) - r.off) / E::VE / per;
-        atomicAdd(&s.share[share], w[i]);
+        s.id = word_id(s.cand[at]);
       }
     }
     __syncthreads();
     c.S = s.acc2;
-    c.key = s.key;
+    c.val = key_value(s.key);
     c.id = s.id;
     c.n = (int)n_above + take;
   }
   __syncthreads();
-  return list ? kModeList : kModeShares;
+}
+
+// Where the kept ids' weights are after the cut.
+enum RowMode {
+  kModeTop,      // at most one id, c.id
+  kModeList,     // s.cand[0 .. c.n), by rank
+  kModeShares,   // s.share, by share of the vectors
+  kModeNone      // not summed yet (c.S unset)
+};
+
+__device__ inline RowMode cut_top(const RowSettings &set, u64 top, RowCut &c) {
+  c.m = word_value(top);
+  c.id = word_id(top);
+  c.val = top ? c.m : INFINITY;
+  c.n = top ? 1 : 0;
+  c.S = top ? to_fix(1.0, set.unit) : 0;
+  return kModeTop;
+}
+
+// Reference of a row's grid: the largest of some of its first logits in each wave's share.
+template <class E>
+__device__ __forceinline__ float row_reference(const RowView<E> &r, FilterSmem &s) {
+  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves, j0 = min(r.nv, (int)(threadIdx.x >> 6) * per);
+  float ref = -INFINITY;
+  wave_ids(r, j0, min(min(r.nv, j0 + per), j0 + 128), [&](float l, int) { ref = fmaxf(ref, l); });
+  return word_value(block_max_u64(rank_word(ref, 0), s));
+}
+
+// The cut of one row by one workgroup and the weight of what it keeps; every thread gets both.
+//   1. One pass bins the row (bin_pass), around a reference taken from a few thousand of its
+//      logits; a row whose largest logit lies past the grid is passed again around that.
+//   2. The bin that holds the cut, and the smallest logits of it and of the bin above, follow
+//      from the bins' totals (make_plan).
+//   3. A second pass lists the ids in that bin and, where a draw follows, sums the weights of
+//      those above it by wave; when all kept ids are few they are listed and nothing is
+//      summed by pass (collect_pass).
+//   4. The list is ranked in LDS and cut (rank_list).
+// totals: only the kept set and its weight are wanted; the bins give the weight above the cut.
+template <class E>
+__device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, bool totals, RowCut &c,
+                                           FilterSmem &s) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
+  const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
+  const CutKind kind = cut_kind(set, r.V, totals);
+  const bool binned = kind == kCutCount || kind == kCutMass;
+  float ref = binned ? row_reference(r, s) : 0.f;
+  u64 any = 0, top;
+  for (int attempt = 0;; ++attempt) {
+    const Grid g(ref, set.T, kind == kCutCount);
+    if (binned) {
+      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
+      __syncthreads();
+    }
+    PassOut o;
+    bin_pass(r, g, kind, bin_unit(set), j0, j1, o, s);
+    top = block_max_u64(rank_word(o.best, o.at), s);
+    if (kind == kCutCount) any = block_sum_u64(o.any, s);
+    c.m = word_value(top);
+    if (!binned || attempt == 1 || !top || (g.fine && g.pos(c.m) < (double)kGrid)) break;
+    ref = c.m;
+    __syncthreads();
+  }
+  if (!top || kind == kCutOne) return cut_top(set, top, c);
+  __syncthreads();
+  const CutPlan p = make_plan(set, kind, Grid(ref, set.T, kind == kCutCount), c.m, any, s);
+  c.S = 0;
+  if (p.narrow) {
+    cut_narrowing(r, set, c, s);
+    return kModeNone;
+  }
+  const bool sums = !totals;
+  if (tid == 0) s.n_cand = 0;
+  __syncthreads();
+  u64 sum = 0;
+  uint32_t n_sum = 0;
+  collect_pass(r, set, p, c.m, sums, j0, j1, &sum, &n_sum, s);
+  if (!p.list && !sums) {
+    c.S = p.above;
+    n_sum = 1;                     // some
+  }
+  __syncthreads();
+  if (!p.list && sums) {
+    sum = wave_sum_u64(sum);
+    if ((tid & 63) == 0) s.share[wave] = sum;
+    n_sum = (uint32_t)block_sum_u64(n_sum, s);
+    for (int w = 0; w < kFilterWaves; ++w) c.S += s.share[w];
+  }
+  const int nc = min((int)s.n_cand, kCandMax);
+  rank_list(set, kind, p, nc, n_sum, c, s, [&](int id, u64 w) {
+    if (!p.list && sums) atomicAdd(&s.share[(id - r.off) / E::VE / per], w);
+  });
+  __syncthreads();
+  return p.list ? kModeList : sums ? kModeShares : kModeNone;
 }
 
 // ------------------------------------------------------------------ the draw
@@ -979,19 +1094,20 @@ __device__ inline double draw_target(float u, u64 S) {
 }
 
 // Position (vector VE + element) of the first weight whose running sum passes t, given the
-// waves' shares of all nv vectors in s.share: the share that holds the crossing is split
-// again until one wave load covers it.
+// sums of n contiguous shares of `step` of all nv vectors in s.share: the share that holds the
+// crossing is split again, a part to each wave, until one wave load covers it.
 template <int VE, class F>
-__device__ __forceinline__ int draw_in_shares(F f, int nv, double t, FilterSmem &s) {
-  int a = 0, b = nv, step = (b + kFilterWaves - 1) / kFilterWaves;
+__device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, double t, FilterSmem &s) {
+  int a = 0, b = nv;
   u64 before = 0;
   for (;;) {
     int w = 0;
-    while (w < kFilterWaves - 1 && !((double)(before + s.share[w]) > t)) before += s.share[w++];
+    while (w < n - 1 && !((double)(before + s.share[w]) > t)) before += s.share[w++];
     a += w * step;
     b = min(b, a + step);
     if (b - a <= 64) break;
-    step = (b - a + kFilterWaves - 1) / kFilterWaves;
+    n = kFilterWaves;
+    step = (b - a + n - 1) / n;
     sum_shares<VE>(f, a, b, step, s);
   }
   if (threadIdx.x < 64) {
@@ -1019,55 +1135,61 @@ __device__ __forceinline__ int draw_in_shares(F f, int nv, double t, FilterSmem 
   return at;
 }
 
-// The row's draw for uniform u: the smallest kept id whose running weight, in id order, passes
-// u times the total (set in c.S when row_cut left it out); -1 for an empty row.
+// Sets c.S when the cut left it out.
 template <class E>
-__device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const RowSettings &set, RowMode mode, float u,
-                                        FilterSmem &s) {
-  const int tid = threadIdx.x;
-  if (mode == kModeTop || c.n <= 1) {
-    c.S = c.n ? to_fix(1.0, set.unit) : 0;
-    return c.n ? c.top : -1;
-  }
-  if (mode == kModeList) {
-    // The list by id: the complement makes the lowest id the largest word.
-    int pow2 = 2;
-    while (pow2 < c.n) pow2 <<= 1;
-    for (int i = tid; i < pow2; i += kFilterThreads) {
-      const u64 x = i < c.n ? s.cand[i] : 0;
-      s.cand[i] = (x << 32) | (x >> 32);
-    }
-    sort_desc(s, pow2);
-    u64 w[kPerThread], own = 0;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int at = kPerThread * tid + i;
-      w[i] = at < c.n ? to_fix(weight(key_value((uint32_t)s.cand[at]), c.m, set.sl), set.unit) : 0;
-      own += w[i];
-    }
-    const double t = draw_target(u, c.S);
-    u64 run = block_excl_scan_u64(own, s);
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      if (!((double)run > t) && (double)(run + w[i]) > t) s.id = (int)~(uint32_t)(s.cand[kPerThread * tid + i] >> 32);
-      run += w[i];
-    }
-    __syncthreads();
-    const int id = s.id;
-    __syncthreads();
-    return id;
-  }
-  auto f = [&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); };
-  if (mode == kModeNone) c.S = sum_shares<E::VE>(f, 0, r.nv, (r.nv + kFilterWaves - 1) / kFilterWaves, s);
-  return r.off + draw_in_shares<E::VE>(f, r.nv, draw_target(u, c.S), s);
-}
-
-// Sets c.S when row_cut left it out.
-template <class E>
-__device__ __forceinline__ void row_total(const RowView<E> &r, RowCut &c, const RowSettings &set, RowMode mode, FilterSmem &s) {
-  if (mode != kModeNone) return;
+__device__ __forceinline__ void row_total(const RowView<E> &r, RowCut &c, const RowSettings &set, FilterSmem &s) {
+  if (c.n == 0 || c.S > 0) return;
   c.S = sum_shares<E::VE>([&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); }, 0, r.nv,
                           (r.nv + kFilterWaves - 1) / kFilterWaves, s);
+}
+
+// The draw of target t from the list s.cand[0 .. n) by rank: the smallest id whose running
+// weight, in id order, passes it.
+__device__ __forceinline__ int draw_in_list(const RowCut &c, const RowSettings &set, double t, FilterSmem &s) {
+  const int tid = threadIdx.x;
+  // The words by id: the complement makes the lowest id the largest word.
+  int pow2 = 2;
+  while (pow2 < c.n) pow2 <<= 1;
+  for (int i = tid; i < pow2; i += kFilterThreads) {
+    const u64 x = i < c.n ? s.cand[i] : 0;
+    s.cand[i] = (x << 32) | (x >> 32);
+  }
+  sort_desc(s, pow2);
+  u64 w[kPerThread], own = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int at = kPerThread * tid + i;
+    w[i] = at < c.n ? to_fix(weight_finite(key_value((uint32_t)s.cand[at]), c.m, set.sl), set.unit) : 0;
+    own += w[i];
+  }
+  u64 run = block_excl_scan_u64(own, s);
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    if (!((double)run > t) && (double)(run + w[i]) > t) s.id = (int)~(uint32_t)(s.cand[kPerThread * tid + i] >> 32);
+    run += w[i];
+  }
+  __syncthreads();
+  const int id = s.id;
+  __syncthreads();
+  return id;
+}
+
+// The row's draw for uniform u: the smallest kept id whose running weight, in id order, passes
+// u times the total (set in c.S when the cut left it out); -1 for an empty row. n shares of
+// `step` vectors are in s.share in kModeShares.
+template <class E>
+__device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const RowSettings &set, RowMode mode, int n, int step,
+                                        float u, FilterSmem &s) {
+  if (mode == kModeTop) return c.n ? c.id : -1;
+  if (mode == kModeList) return draw_in_list(c, set, draw_target(u, c.S), s);
+  auto f = [&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); };
+  if (mode == kModeNone) {
+    n = kFilterWaves;
+    step = (r.nv + n - 1) / n;
+    c.S = sum_shares<E::VE>(f, 0, r.nv, step, s);
+  }
+  if (c.n == 0 || c.S == 0) return -1;
+  return r.off + draw_in_shares<E::VE>(f, r.nv, n, step, draw_target(u, c.S), s);
 }
 
 }  // namespace sdv

@@ -28,14 +28,14 @@ struct SampleArgs {
 
 // One workgroup per row.
 template <class E>
-__global__ __launch_bounds__(kFilterThreads) void k_sample(SampleArgs a) {
+__global__ __launch_bounds__(kFilterThreads, 4) void k_sample(SampleArgs a) {
   __shared__ FilterSmem s;
   const int row = blockIdx.x;
   const RowView<E> r(reinterpret_cast<const typename E::S *>(a.logits) + row * a.stride, a.V);
   const RowSettings set = load_settings(a.set, row / a.rows_per, a.V, threadIdx.x == 0 ? a.ws : nullptr);
   RowCut c;
-  const RowMode mode = row_cut(r, set, c, s);
-  const int id = row_draw(r, c, set, mode, a.u[row], s);
+  const RowMode mode = row_cut(r, set, false, c, s);
+  const int id = row_draw(r, c, set, mode, kFilterWaves, (r.nv + kFilterWaves - 1) / kFilterWaves, a.u[row], s);
   if (threadIdx.x == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
     a.tokens[row * a.token_stride] = id;
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_sample(SampleArgs a) {
     if (a.logprob) {
       float lp = id < 0 ? -INFINITY : 0.f;
       if (c.n > 1) {
-        const double w = weight(canonical(E::get(r.p[id])), c.m, set.sl);
+        const double w = weight(r.at(id), c.m, set.sl);
         lp = (float)log(w * set.unit / (double)c.S);
       }
       a.logprob[row] = lp;
@@ -86,7 +86,7 @@ __device__ inline int first_row(const RowMap &rm, int r, int L, WsHeader *ws) {
   return base;
 }
 
-__global__ __launch_bounds__(kFilterThreads) void k_filter_rows(FilteredArgs a) {
+__global__ __launch_bounds__(kFilterThreads, 4) void k_filter_rows(FilteredArgs a) {
   __shared__ FilterSmem s;
   const int g = a.rm.gamma, targets = a.rm.B * (g + 1);
   const bool draft = (int)blockIdx.x >= targets;
@@ -99,12 +99,14 @@ __global__ __launch_bounds__(kFilterThreads) void k_filter_rows(FilteredArgs a) 
   if (draft) {
     const RowView<ElemBF16> v(a.draft_logits + (size_t)i * a.V, a.V);
     RowCut c;
-    row_total(v, c, set, row_cut(v, set, c, s), s);
+    row_cut(v, set, true, c, s);
+    row_total(v, c, set, s);
     if (threadIdx.x == 0) a.cut_q[i] = c;
   } else {
     const RowView<ElemF32> v(a.logits + (size_t)(base + j) * a.V, a.V);
     RowCut c;
-    row_total(v, c, set, row_cut(v, set, c, s), s);
+    row_cut(v, set, true, c, s);
+    row_total(v, c, set, s);
     if (threadIdx.x == 0) a.cut_p[i] = c;
   }
 }
@@ -180,11 +182,12 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_draw(FilteredArgs a
         w[i] = p > 0.0 ? to_fix(fmax(p - prob(cq, set, bf16_to_f32(q[x]), x), 0.0), kResidualUnit) : 0;
       }
     };
-    const u64 S = sum_shares<4>(f, 0, v.nv, (v.nv + kFilterWaves - 1) / kFilterWaves, s);
-    if (S > 0) id = v.off + draw_in_shares<4>(f, v.nv, draw_target(u, S), s);
+    const int step = (v.nv + kFilterWaves - 1) / kFilterWaves;
+    const u64 S = sum_shares<4>(f, 0, v.nv, step, s);
+    if (S > 0) id = v.off + draw_in_shares<4>(f, v.nv, kFilterWaves, step, draw_target(u, S), s);
     else if (threadIdx.x == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
   }
-  if (id < 0) id = row_draw(v, cp, set, kModeNone, u, s);
+  if (id < 0) id = row_draw(v, cp, set, kModeNone, 0, 0, u, s);
   if (threadIdx.x == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
     a.next_token[r] = id;
