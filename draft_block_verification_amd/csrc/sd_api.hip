@@ -663,7 +663,7 @@ int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits_stride
 
 size_t sd_accept_filtered_workspace_bytes(int32_t B, int32_t gamma, int32_t V) {
   if (check_sizes(B, gamma, 8, V) != SD_OK) return 0;
-  return accept_filtered_workspace_layout(B, gamma, nullptr, nullptr);
+  return accept_filtered_workspace_layout(B, gamma, V);
 }
 
 int32_t sd_accept_filtered(const float *logits, const uint16_t *draft_logits,
@@ -683,7 +683,7 @@ int32_t sd_accept_filtered(const float *logits, const uint16_t *draft_logits,
       !aligned(next_token, 4) || (counters && !aligned(counters, 8)) || !aligned_settings(*sampling) ||
       (verify_len && (!aligned(verify_len, 4) || !aligned(row_offsets, 4))))
     return SD_EALIGN;
-  if (!workspace || workspace_bytes < accept_filtered_workspace_layout(B, gamma, nullptr, nullptr))
+  if (!workspace || workspace_bytes < accept_filtered_workspace_layout(B, gamma, V))
     return SD_EWORKSPACE;
   if (!aligned(workspace, 256)) return SD_EALIGN;
   RowMap rm{row_offsets, B, gamma};

@@ -109,7 +109,7 @@ hipError_t launch_sample(const void *logits, int32_t type, int64_t stride, int R
                          int32_t *tokens, int64_t token_stride, int32_t *kept, float *logprob,
                          void *workspace, hipStream_t stream);
 size_t sample_workspace_layout(int R, int V);
-size_t accept_filtered_workspace_layout(int B, int gamma, size_t *cut_p, size_t *cut_q);
+size_t accept_filtered_workspace_layout(int B, int gamma, int V);
 hipError_t launch_accept_filtered(const float *logits, const uint16_t *draft_logits,
                                   const int32_t *draft_tokens, const int32_t *verify_len,
                                   const RowMap &rm, const float *u_accept,

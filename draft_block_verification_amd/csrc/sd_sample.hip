@@ -13,6 +13,8 @@
 namespace sdv {
 namespace {
 
+// Where rows come from and what becomes of them. with(i, f) calls f(view, settings) for row i
+// of the grid, or not at all for a row that is not used; finish() has the row's cut.
 struct SampleArgs {
   const void *logits;
   int64_t stride;        // elements from row to row
@@ -26,39 +28,31 @@ struct SampleArgs {
   WsHeader *ws;
 };
 
-// One workgroup per row.
 template <class E>
-__global__ __launch_bounds__(kFilterThreads, 4) void k_sample(SampleArgs a) {
-  __shared__ FilterSmem s;
-  const int row = blockIdx.x;
-  const RowView<E> r(reinterpret_cast<const typename E::S *>(a.logits) + row * a.stride, a.V);
-  const RowSettings set = load_settings(a.set, row / a.rows_per, a.V, threadIdx.x == 0 ? a.ws : nullptr);
-  RowCut c;
-  const RowMode mode = row_cut(r, set, false, c, s);
-  const int id = row_draw(r, c, set, mode, kFilterWaves, (r.nv + kFilterWaves - 1) / kFilterWaves, a.u[row], s);
-  if (threadIdx.x == 0) {
-    if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
-    a.tokens[row * a.token_stride] = id;
-    if (a.kept) a.kept[row] = c.n;
-    if (a.logprob) {
-      float lp = id < 0 ? -INFINITY : 0.f;
-      if (c.n > 1) {
-        const double w = weight(r.at(id), c.m, set.sl);
-        lp = (float)log(w * set.unit / (double)c.S);
+struct SampleRows {
+  SampleArgs a;
+  static constexpr bool kTotals = false;
+  template <class F>
+  __device__ __forceinline__ void with(int row, F f) const {
+    f(RowView<E>(reinterpret_cast<const typename E::S *>(a.logits) + row * a.stride, a.V),
+      load_settings(a.set, row / a.rows_per, a.V, threadIdx.x == 0 ? a.ws : nullptr));
+  }
+  __device__ __forceinline__ void finish(int row, const RowView<E> &r, const RowSettings &set, RowCut &c, RowMode mode,
+                                         int n, int step, FilterSmem &s) const {
+    const int id = row_draw(r, c, set, mode, n, step, a.u[row], s);
+    if (threadIdx.x == 0) {
+      if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
+      a.tokens[row * a.token_stride] = id;
+      if (a.kept) a.kept[row] = c.n;
+      if (a.logprob) {
+        float lp = id < 0 ? -INFINITY : 0.f;
+        if (c.n > 1) lp = (float)log(weight(r.at(id), c.m, set.sl) * set.unit / (double)c.S);
+        a.logprob[row] = lp;
       }
-      a.logprob[row] = lp;
     }
   }
-}
+};
 
-// ------------------------------------------------------------ filtered acceptance
-// Three kernels:
-//   k_filter_rows      (row): the cut and total of every verified target row and every kept
-//                      drafter row;
-//   k_filtered_decide  (request): p'_j(x_j) / q'_j(x_j) at each kept position, the first
-//                      rejection a_r, the counters;
-//   k_filtered_draw    (request): the token from norm(max(0, p' - q')) at a_r, or from p'
-//                      at the bonus row.
 struct FilteredArgs {
   const float *logits;           // [cap][V]
   const uint16_t *draft_logits;  // bf16 [B][gamma][V]
@@ -72,6 +66,7 @@ struct FilteredArgs {
   int64_t *counters;
   RowCut *cut_p;                 // [B][gamma + 1]
   RowCut *cut_q;                 // [B][gamma]
+  u64 *share;                    // [B][kMaxShares] sums of the draw's weights
   WsHeader *ws;
 };
 
@@ -86,80 +81,336 @@ __device__ inline int first_row(const RowMap &rm, int r, int L, WsHeader *ws) {
   return base;
 }
 
-__global__ __launch_bounds__(kFilterThreads, 4) void k_filter_rows(FilteredArgs a) {
+// The B (gamma + 1) target rows, then the B gamma drafter rows.
+struct AcceptRows {
+  FilteredArgs a;
+  static constexpr bool kTotals = true;
+  template <class F>
+  __device__ __forceinline__ void with(int row, F f) const {
+    const int g = a.rm.gamma, targets = a.rm.B * (g + 1);
+    const bool draft = row >= targets;
+    const int i = draft ? row - targets : row, per = draft ? g : g + 1;
+    const int r = i / per, j = i - r * per;
+    const int L = clamp_len(a.verify_len, r, g, nullptr);
+    const int base = first_row(a.rm, r, L, nullptr);
+    if (base < 0 || j > L || (draft && j == L)) return;
+    const RowSettings set = load_settings(a.set, r, a.V, nullptr);
+    if (draft) f(RowView<ElemBF16>(a.draft_logits + (size_t)i * a.V, a.V), set);
+    else f(RowView<ElemF32>(a.logits + (size_t)(base + j) * a.V, a.V), set);
+  }
+  template <class E>
+  __device__ __forceinline__ void finish(int row, const RowView<E> &r, const RowSettings &set, RowCut &c, RowMode, int,
+                                         int, FilterSmem &s) const {
+    row_total(r, c, set, s);
+    const int targets = a.rm.B * (a.rm.gamma + 1);
+    if (threadIdx.x == 0) (row < targets ? a.cut_p[row] : a.cut_q[row - targets]) = c;
+  }
+};
+
+// ------------------------------------------------------------------ one workgroup a row
+template <class Rows>
+__global__ __launch_bounds__(kFilterThreads, 4) void k_rows(Rows rows) {
   __shared__ FilterSmem s;
-  const int g = a.rm.gamma, targets = a.rm.B * (g + 1);
-  const bool draft = (int)blockIdx.x >= targets;
-  const int i = draft ? blockIdx.x - targets : blockIdx.x;
-  const int r = i / (draft ? g : g + 1), j = i - r * (draft ? g : g + 1);
-  const int L = clamp_len(a.verify_len, r, g, nullptr);
-  const int base = first_row(a.rm, r, L, nullptr);
-  if (base < 0 || j > L || (draft && j == L)) return;
-  const RowSettings set = load_settings(a.set, r, a.V, nullptr);
-  if (draft) {
-    const RowView<ElemBF16> v(a.draft_logits + (size_t)i * a.V, a.V);
+  const int row = blockIdx.x;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
     RowCut c;
-    row_cut(v, set, true, c, s);
-    row_total(v, c, set, s);
-    if (threadIdx.x == 0) a.cut_q[i] = c;
-  } else {
-    const RowView<ElemF32> v(a.logits + (size_t)(base + j) * a.V, a.V);
-    RowCut c;
-    row_cut(v, set, true, c, s);
-    row_total(v, c, set, s);
-    if (threadIdx.x == 0) a.cut_p[i] = c;
+    const RowMode mode = row_cut(r, set, Rows::kTotals, c, s);
+    rows.finish(row, r, set, c, mode, kFilterWaves, (r.nv + kFilterWaves - 1) / kFilterWaves, s);
+  });
+}
+
+// ------------------------------------------------------------------ several workgroups a row
+// For few rows: the steps of row_cut as launches, a row's vectors dealt to C workgroups in
+// contiguous shares. Bins and lists meet in the workspace through integer atomics, whose
+// order does not change a sum; the list is ranked before it is used.
+struct TeamRow {
+  u64 top, any;
+  uint32_t n_list, n_above;
+  float ref;
+  uint32_t pad;
+  CutPlan plan;
+};
+static_assert(sizeof(TeamRow) <= 128, "team rows are 128 bytes");
+
+struct Team {
+  int C;
+  TeamRow *row;       // [R], 128 bytes apart
+  u64 *grid;          // [R][kGrid]
+  u64 *list;          // [R][kCandMax]
+  u64 *share;         // [R][kMaxShares]
+  __device__ TeamRow &at(int i) const { return *reinterpret_cast<TeamRow *>(reinterpret_cast<char *>(row) + 128 * (size_t)i); }
+};
+
+// Reference of the row's grid, and its counters and bins cleared.
+template <class Rows>
+__global__ __launch_bounds__(kFilterThreads) void k_team_start(Rows rows, Team t) {
+  __shared__ FilterSmem s;
+  const int row = blockIdx.y;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
+    const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
+    const bool binned = kind == kCutCount || kind == kCutMass;
+    const float ref = binned ? row_reference(r, s) : 0.f;
+    if (binned)
+      for (int b = threadIdx.x; b < kGrid; b += kFilterThreads) t.grid[(size_t)row * kGrid + b] = 0;
+    if (threadIdx.x == 0) {
+      TeamRow &o = t.at(row);
+      o.top = o.any = 0;
+      o.n_list = o.n_above = 0;
+      o.ref = ref;
+    }
+  });
+}
+
+// Vectors of this workgroup's share and of the calling wave in it.
+struct Part {
+  int step, j0, j1;
+  __device__ Part(int nv, int C) {
+    step = (nv + C - 1) / C;
+    const int a = min(nv, (int)blockIdx.x * step), b = min(nv, a + step);
+    const int per = (b - a + kFilterWaves - 1) / kFilterWaves;
+    j0 = min(b, a + (int)(threadIdx.x >> 6) * per);
+    j1 = min(b, j0 + per);
   }
+};
+
+template <class Rows>
+__global__ __launch_bounds__(kFilterThreads, 4) void k_team_bins(Rows rows, Team t) {
+  __shared__ FilterSmem s;
+  const int row = blockIdx.y, tid = threadIdx.x;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
+    const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
+    const bool binned = kind == kCutCount || kind == kCutMass;
+    TeamRow &o = t.at(row);
+    const Grid g(o.ref, set.T, kind == kCutCount);
+    if (binned) {
+      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
+      __syncthreads();
+    }
+    const Part part(r.nv, t.C);
+    PassOut out;
+    bin_pass(r, g, kind, bin_unit(set), part.j0, part.j1, out, s);
+    const u64 top = block_max_u64(rank_word(out.best, out.at), s);
+    const u64 any = kind == kCutCount ? block_sum_u64(out.any, s) : 0;
+    __syncthreads();
+    if (binned)
+      for (int b = tid; b < kGrid; b += kFilterThreads)
+        if (s.grid[b]) atomicAdd(&t.grid[(size_t)row * kGrid + b], s.grid[b]);
+    if (tid == 0) {
+      atomicMax(&o.top, top);
+      if (any) atomicAdd(&o.any, any);
+    }
+  });
 }
 
-// Probability of id x, whose logit is l, under a row's cut.
-__device__ inline double prob(const RowCut &c, const RowSettings &set, float l, int x) {
-  l = canonical(l);
-  return l > -INFINITY && c.n > 0 && kept(c, l, x) ? weight(l, c.m, set.sl) * set.unit / (double)c.S : 0.0;
+template <class Rows>
+__global__ __launch_bounds__(kFilterThreads, 4) void k_team_collect(Rows rows, Team t) {
+  __shared__ FilterSmem s;
+  const int row = blockIdx.y, tid = threadIdx.x;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
+    const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
+    TeamRow &o = t.at(row);
+    const u64 top = o.top;
+    if (!top || kind == kCutOne) return;
+    const float m = word_value(top);
+    if (kind != kCutSum) {
+      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = t.grid[(size_t)row * kGrid + b];
+      __syncthreads();
+    }
+    const CutPlan p = make_plan(set, kind, Grid(o.ref, set.T, kind == kCutCount), m, o.any, s);
+    if (blockIdx.x == 0 && tid == 0) o.plan = p;
+    if (p.narrow) return;
+    if (tid == 0) s.n_cand = 0;
+    __syncthreads();
+    const Part part(r.nv, t.C);
+    u64 sum = 0;
+    uint32_t n = 0;
+    collect_pass(r, set, p, m, !Rows::kTotals, part.j0, part.j1, &sum, &n, s);
+    sum = block_sum_u64(sum, s);
+    n = (uint32_t)block_sum_u64(n, s);
+    const uint32_t nc = min(s.n_cand, (uint32_t)kCandMax);
+    if (tid == 0) {
+      t.share[(size_t)row * kMaxShares + blockIdx.x] = sum;
+      if (n) atomicAdd(&o.n_above, n);
+      s.key = nc ? atomicAdd(&o.n_list, nc) : 0;
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < nc; i += kFilterThreads)
+      if (s.key + i < (uint32_t)kCandMax) t.list[(size_t)row * kCandMax + s.key + i] = s.cand[i];
+  });
 }
 
-// One wave per request, lane j decides position j.
-__global__ __launch_bounds__(256) void k_filtered_decide(FilteredArgs a) {
+template <class Rows>
+__global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team t) {
+  __shared__ FilterSmem s;
+  const int row = blockIdx.y, tid = threadIdx.x;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
+    const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
+    const TeamRow o = t.at(row);
+    const int step = (r.nv + t.C - 1) / t.C;
+    RowCut c;
+    RowMode mode;
+    c.S = 0;
+    c.m = word_value(o.top);
+    if (!o.top || kind == kCutOne) {
+      mode = cut_top(set, o.top, c);
+    } else if (o.plan.narrow) {
+      cut_narrowing(r, set, c, s);
+      mode = kModeNone;
+    } else {
+      const int nc = min(o.n_list, (uint32_t)kCandMax);
+      for (int i = tid; i < nc; i += kFilterThreads) s.cand[i] = t.list[(size_t)row * kCandMax + i];
+      if (tid < t.C) s.share[tid] = t.share[(size_t)row * kMaxShares + tid];
+      __syncthreads();
+      const bool sums = !Rows::kTotals && !o.plan.list;
+      if (sums) for (int i = 0; i < t.C; ++i) c.S += s.share[i];
+      else if (!o.plan.list) c.S = o.plan.above;
+      rank_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s, [&](int id, u64 w) {
+        if (sums) atomicAdd(&s.share[(id - r.off) / (int)(16 / sizeof(*r.p)) / step], w);
+      });
+      __syncthreads();
+      mode = o.plan.list ? kModeList : sums ? kModeShares : kModeNone;
+    }
+    rows.finish(row, r, set, c, mode, t.C, step, s);
+  });
+}
+
+// Workgroups a row's vectors are dealt to: enough for about two on every compute unit, each
+// with at least 4096 ids; 1: the row is one workgroup's.
+int team_size(int rows, int V) {
+  const int c = rows < 1024 ? 1024 / rows : 0;
+  return c > V / 4096 ? (V / 4096 < kMaxShares ? V / 4096 : kMaxShares) : (c < kMaxShares ? c : kMaxShares);
+}
+
+struct TeamLayout {
+  size_t row, grid, list, share, end;
+  TeamLayout(size_t start, int rows, int V) : row(start), grid(start), list(start), share(start), end(start) {
+    if (team_size(rows, V) < 2) return;
+    grid = align_up(row + 128 * (size_t)rows, 256);
+    list = grid + (size_t)rows * kGrid * sizeof(u64);
+    share = list + (size_t)rows * kCandMax * sizeof(u64);
+    end = align_up(share + (size_t)rows * kMaxShares * sizeof(u64), 256);
+  }
+};
+
+template <class Rows>
+hipError_t launch_rows(const Rows &rows, int n, int V, char *ws, const TeamLayout &l, hipStream_t stream) {
+  const int C = team_size(n, V);
+  if (C < 2) {
+    hipLaunchKernelGGL(k_rows<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows);
+    return hipGetLastError();
+  }
+  const Team t{C, reinterpret_cast<TeamRow *>(ws + l.row), reinterpret_cast<u64 *>(ws + l.grid),
+               reinterpret_cast<u64 *>(ws + l.list), reinterpret_cast<u64 *>(ws + l.share)};
+  hipLaunchKernelGGL(k_team_start<Rows>, dim3(1, n), dim3(kFilterThreads), 0, stream, rows, t);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_team_bins<Rows>, dim3(C, n), dim3(kFilterThreads), 0, stream, rows, t);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(k_team_collect<Rows>, dim3(C, n), dim3(kFilterThreads), 0, stream, rows, t);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(k_team_finish<Rows>, dim3(1, n), dim3(kFilterThreads), 0, stream, rows, t);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ filtered acceptance
+// After the rows' cuts:
+//   k_filtered_shares  (request, share): p'_j(x_j) / q'_j(x_j) at each kept position and the
+//                      first rejection a_r (every workgroup decides for itself, the first
+//                      one writes), then the sum of the draw's weights over one share of the
+//                      row: max(0, p' - q') after a rejection, p' for the bonus row;
+//   k_filtered_pick    (request): the share that holds the draw, and the id in it.
+
+// Probability of an id with canonical logit l under a row's cut; per = unit / S.
+__device__ inline double prob(const RowCut &c, double per, const RowSettings &set, float l, int x) {
+  return l > -INFINITY && c.n > 0 && kept(c, l, x) ? weight(l, c.m, set.sl) * per : 0.0;
+}
+
+__device__ inline double per_weight(const RowCut &c, const RowSettings &set) {
+  return c.n > 0 ? set.unit / (double)c.S : 0.0;
+}
+
+// a_r of request r by one wave, lane j deciding position j.
+__device__ __forceinline__ int first_rejection(const FilteredArgs &a, int r, int L, int base, const RowSettings &set) {
   const int lane = threadIdx.x & 63, g = a.rm.gamma;
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= a.rm.B) return;
-  WsHeader *ws = lane == 0 ? a.ws : nullptr;
-  const int L = clamp_len(a.verify_len, r, g, ws);
-  const int base = first_row(a.rm, r, L, ws);
-  const RowSettings set = load_settings(a.set, r, a.V, ws);
-  if (base < 0) {
-    if (lane == 0) { a.accept_len[r] = 0; a.next_token[r] = -1; }
-    return;
-  }
   bool miss = false;
   if (lane < L) {
-    const int x = a.draft_tokens[(size_t)r * g + lane];
+    const size_t rj = (size_t)r * g + lane;
+    const int x = a.draft_tokens[rj];
     miss = true;
     if (x >= 0 && x < a.V) {
-      const double p = prob(a.cut_p[(size_t)r * (g + 1) + lane], set, a.logits[(size_t)(base + lane) * a.V + x], x);
-      const size_t rj = (size_t)r * g + lane;
-      const double q = prob(a.cut_q[rj], set, bf16_to_f32(a.draft_logits[rj * a.V + x]), x);
-      // 0 / 0 compares false: a token that neither side keeps is rejected.
+      const RowCut cp = a.cut_p[rj + r], cq = a.cut_q[rj];
+      const double p = prob(cp, per_weight(cp, set), set, canonical(a.logits[(size_t)(base + lane) * a.V + x]), x);
+      const double q = prob(cq, per_weight(cq, set), set, canonical(bf16_to_f32(a.draft_logits[rj * a.V + x])), x);
+      // A token that the target does not keep is rejected, whatever the drafter's.
       miss = !((double)a.u_accept[rj] < (p >= q ? (p > 0.0 ? 1.0 : 0.0) : p / q));
     }
   }
   const u64 m = __ballot(miss);
-  if (lane == 0) {
-    const int acc = m ? __ffsll((long long)m) - 1 : L;
+  return m ? __ffsll((long long)m) - 1 : L;
+}
+
+// Residual weights are summed in units of 2^-51: they add up to at most 1 (and a little), so a
+// sum over 2^21 ids is off by 2^-31 of a unit row at the very worst, 2^-42 for random roundings.
+constexpr double kResidualUnit = 2251799813685248.0;
+
+// Weights max(0, p' - q') of vector j of target row v in id order.
+struct Residual {
+  RowView<ElemF32> v;
+  const uint16_t *q;
+  RowCut cp, cq;
+  RowSettings set;
+  double pp, pq;
+  __device__ Residual(const FilteredArgs &a, const RowView<ElemF32> &v_, int r, int acc, const RowCut &cp_,
+                      const RowSettings &set_)
+      : v(v_), q(a.draft_logits + ((size_t)r * a.rm.gamma + acc) * a.V), cp(cp_),
+        cq(a.cut_q[(size_t)r * a.rm.gamma + acc]), set(set_) {
+    pp = per_weight(cp, set);
+    pq = per_weight(cq, set);
+  }
+  __device__ void operator()(int j, u64 (&w)[4]) const {
+    float l[4];
+    v.load(j, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = v.id(j, i);
+      const double p = prob(cp, pp, set, l[i], x);
+      w[i] = p > 0.0 ? to_fix(fmax(p - prob(cq, pq, set, canonical(bf16_to_f32(q[x])), x), 0.0), kResidualUnit) : 0;
+    }
+  }
+};
+
+__global__ __launch_bounds__(kFilterThreads) void k_filtered_shares(FilteredArgs a) {
+  __shared__ FilterSmem s;
+  const int r = blockIdx.x, part = blockIdx.y, g = a.rm.gamma, tid = threadIdx.x;
+  WsHeader *ws = part == 0 && tid == 0 ? a.ws : nullptr;
+  const int L = clamp_len(a.verify_len, r, g, ws);
+  const int base = first_row(a.rm, r, L, ws);
+  const RowSettings set = load_settings(a.set, r, a.V, ws);
+  if (base < 0) {
+    if (part == 0 && tid == 0) { a.accept_len[r] = 0; a.next_token[r] = -1; }
+    return;
+  }
+  const int acc = first_rejection(a, r, L, base, set);   // the same in every wave
+  if (part == 0 && tid == 0) {
     a.accept_len[r] = acc;
     if (a.counters) {
       atomicAdd(reinterpret_cast<u64 *>(a.counters), (u64)L);
       atomicAdd(reinterpret_cast<u64 *>(a.counters + 1), (u64)acc);
     }
   }
+  const RowView<ElemF32> v(a.logits + (size_t)(base + acc) * a.V, a.V);
+  const RowCut cp = a.cut_p[(size_t)r * (g + 1) + acc];
+  const int step = (v.nv + gridDim.y - 1) / gridDim.y, j0 = min(v.nv, part * step), j1 = min(v.nv, j0 + step);
+  const int per = (j1 - j0 + kFilterWaves - 1) / kFilterWaves;
+  u64 sum = 0;
+  if (acc < L) sum = sum_shares<4>(Residual(a, v, r, acc, cp, set), j0, j1, per, s);
+  else sum = sum_shares<4>([&](int j, u64 (&w)[4]) { kept_weights(v, cp, set, j, w); }, j0, j1, per, s);
+  if (tid == 0) a.share[(size_t)r * kMaxShares + part] = sum;
 }
 
-// Residual weights are summed in units of 2^-51: they add up to at most 1, so a sum over
-// 2^21 ids is off by 2^-31 of a unit row at the very worst, 2^-42 for random roundings.
-constexpr double kResidualUnit = 2251799813685248.0;
-
-__global__ __launch_bounds__(kFilterThreads) void k_filtered_draw(FilteredArgs a) {
+__global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a, int shares) {
   __shared__ FilterSmem s;
-  const int r = blockIdx.x, g = a.rm.gamma;
+  const int r = blockIdx.x, g = a.rm.gamma, tid = threadIdx.x;
   const int L = clamp_len(a.verify_len, r, g, nullptr);
   const int base = first_row(a.rm, r, L, nullptr);
   if (base < 0) return;
@@ -168,55 +419,65 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_draw(FilteredArgs a
   const RowView<ElemF32> v(a.logits + (size_t)(base + acc) * a.V, a.V);
   RowCut cp = a.cut_p[(size_t)r * (g + 1) + acc];
   const float u = a.u_resample[(size_t)r * (g + 1) + acc];
+  if (tid < shares) s.share[tid] = a.share[(size_t)r * kMaxShares + tid];
+  __syncthreads();
+  u64 S = 0;
+  for (int i = 0; i < shares; ++i) S += s.share[i];
+  const int step = (v.nv + shares - 1) / shares;
+  const bool residual = acc < L;
+  const double t = draw_target(u, S);
   int id = -1;
-  if (acc < L && cp.n > 0) {
-    const uint16_t *q = a.draft_logits + ((size_t)r * g + acc) * a.V;
-    const RowCut cq = a.cut_q[(size_t)r * g + acc];
-    auto f = [&](int j, u64 (&w)[4]) {
-      float l[4];
-      v.load(j, l);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int x = v.id(j, i);
-        const double p = prob(cp, set, l[i], x);
-        w[i] = p > 0.0 ? to_fix(fmax(p - prob(cq, set, bf16_to_f32(q[x]), x), 0.0), kResidualUnit) : 0;
-      }
-    };
-    const int step = (v.nv + kFilterWaves - 1) / kFilterWaves;
-    const u64 S = sum_shares<4>(f, 0, v.nv, step, s);
-    if (S > 0) id = v.off + draw_in_shares<4>(f, v.nv, kFilterWaves, step, draw_target(u, S), s);
-    else if (threadIdx.x == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
+  if (residual && S > 0)
+    id = v.off + draw_in_shares<4>(Residual(a, v, r, acc, cp, set), v.nv, shares, step, t, s);
+  else if (!residual && S > 0)
+    id = v.off + draw_in_shares<4>([&](int j, u64 (&w)[4]) { kept_weights(v, cp, set, j, w); }, v.nv, shares, step, t, s);
+  else if (cp.n > 0) {
+    // No residual mass: the target's own distribution.
+    if (tid == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
+    id = row_draw(v, cp, set, kModeNone, 0, 0, u, s);
   }
-  if (id < 0) id = row_draw(v, cp, set, kModeNone, 0, 0, u, s);
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
     a.next_token[r] = id;
   }
 }
 
+// Shares of the draw's row: about two workgroups on every compute unit over all requests, at
+// least 2048 ids each.
+int draw_shares(int B, int V) {
+  int c = B < 1024 ? 1024 / B : 1;
+  if (c > V / 2048) c = V / 2048;
+  return c < 1 ? 1 : (c > kMaxShares ? kMaxShares : c);
+}
+
+struct FilteredLayout {
+  size_t cut_p, cut_q, share;
+  TeamLayout team;
+  FilteredLayout(int B, int gamma, int V)
+      : cut_p(sizeof(WsHeader)),
+        cut_q(align_up(cut_p + (size_t)B * (gamma + 1) * sizeof(RowCut), 256)),
+        share(align_up(cut_q + (size_t)B * gamma * sizeof(RowCut), 256)),
+        team(align_up(share + (size_t)B * kMaxShares * sizeof(u64), 256), B * (2 * gamma + 1), V) {}
+};
+
 }  // namespace
 
-// One workgroup per row keeps all of a row's state in LDS: the workspace is its header.
-size_t sample_workspace_layout(int, int) { return sizeof(WsHeader); }
+size_t sample_workspace_layout(int R, int V) { return TeamLayout(sizeof(WsHeader), R, V).end; }
 
 hipError_t launch_sample(const void *logits, int32_t type, int64_t stride, int R, int V,
                          const float *u, const SampleSettings &set, int rows_per,
                          int32_t *tokens, int64_t token_stride, int32_t *kept, float *logprob,
                          void *workspace, hipStream_t stream) {
-  SampleArgs a{logits, stride, R, V, rows_per, u, set, tokens, token_stride, kept, logprob,
-               reinterpret_cast<WsHeader *>(workspace)};
-  auto *k = type == SD_F32 ? &k_sample<ElemF32> : type == SD_BF16 ? &k_sample<ElemBF16> : &k_sample<ElemF16>;
-  hipLaunchKernelGGL(k, dim3(R), dim3(kFilterThreads), 0, stream, a);
-  return hipGetLastError();
+  const SampleArgs a{logits, stride, R, V, rows_per, u, set, tokens, token_stride, kept, logprob,
+                     reinterpret_cast<WsHeader *>(workspace)};
+  char *ws = reinterpret_cast<char *>(workspace);
+  const TeamLayout l(sizeof(WsHeader), R, V);
+  if (type == SD_F32) return launch_rows(SampleRows<ElemF32>{a}, R, V, ws, l, stream);
+  if (type == SD_BF16) return launch_rows(SampleRows<ElemBF16>{a}, R, V, ws, l, stream);
+  return launch_rows(SampleRows<ElemF16>{a}, R, V, ws, l, stream);
 }
 
-size_t accept_filtered_workspace_layout(int B, int gamma, size_t *cut_p, size_t *cut_q) {
-  const size_t p = sizeof(WsHeader);
-  const size_t q = align_up(p + (size_t)B * (gamma + 1) * sizeof(RowCut), 256);
-  if (cut_p) *cut_p = p;
-  if (cut_q) *cut_q = q;
-  return align_up(q + (size_t)B * gamma * sizeof(RowCut), 256);
-}
+size_t accept_filtered_workspace_layout(int B, int gamma, int V) { return FilteredLayout(B, gamma, V).team.end; }
 
 hipError_t launch_accept_filtered(const float *logits, const uint16_t *draft_logits,
                                   const int32_t *draft_tokens, const int32_t *verify_len,
@@ -224,18 +485,18 @@ hipError_t launch_accept_filtered(const float *logits, const uint16_t *draft_log
                                   const float *u_resample, const SampleSettings &set, int V,
                                   int32_t *accept_len, int32_t *next_token, int64_t *counters,
                                   void *workspace, hipStream_t stream) {
-  size_t po, qo;
-  accept_filtered_workspace_layout(rm.B, rm.gamma, &po, &qo);
+  const FilteredLayout l(rm.B, rm.gamma, V);
   char *w = reinterpret_cast<char *>(workspace);
-  FilteredArgs a{logits, draft_logits, draft_tokens, verify_len, rm, u_accept, u_resample, set, V,
-                 accept_len, next_token, counters, reinterpret_cast<RowCut *>(w + po),
-                 reinterpret_cast<RowCut *>(w + qo), reinterpret_cast<WsHeader *>(workspace)};
-  hipLaunchKernelGGL(k_filter_rows, dim3(rm.B * (2 * rm.gamma + 1)), dim3(kFilterThreads), 0, stream, a);
-  hipError_t e = hipGetLastError();
+  const FilteredArgs a{logits, draft_logits, draft_tokens, verify_len, rm, u_accept, u_resample, set, V,
+                       accept_len, next_token, counters, reinterpret_cast<RowCut *>(w + l.cut_p),
+                       reinterpret_cast<RowCut *>(w + l.cut_q), reinterpret_cast<u64 *>(w + l.share),
+                       reinterpret_cast<WsHeader *>(workspace)};
+  hipError_t e = launch_rows(AcceptRows{a}, rm.B * (2 * rm.gamma + 1), V, w, l.team, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_filtered_decide, dim3((rm.B + 3) / 4), dim3(256), 0, stream, a);
+  const int shares = draw_shares(rm.B, V);
+  hipLaunchKernelGGL(k_filtered_shares, dim3(rm.B, shares), dim3(kFilterThreads), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(k_filtered_draw, dim3(rm.B), dim3(kFilterThreads), 0, stream, a);
+  hipLaunchKernelGGL(k_filtered_pick, dim3(rm.B), dim3(kFilterThreads), 0, stream, a, shares);
   return hipGetLastError();
 }
 
