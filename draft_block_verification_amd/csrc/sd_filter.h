@@ -267,39 +267,56 @@ __device__ inline bool kept(const RowCut &c, float l, int id) {
 }
 
 // ------------------------------------------------------------------ workgroup sums
-__device__ inline u64 wave_sum_u64(u64 x) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off);
+// x of the lane that a data-parallel-primitive control names, 0 where it names none.
+template <int CTRL, int ROWS>
+__device__ inline u64 dpp_u64(u64 x) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), CTRL, ROWS, 0xf, false);
+  return ((u64)hi << 32) | lo;
+}
+
+// Sum over lanes 0 .. own: by shifts inside each row of 16 lanes, then the rows' totals
+// broadcast onwards (all lanes of the wave take part).
+__device__ inline u64 wave_incl_scan_u64(u64 x) {
+  x += dpp_u64<0x111, 0xf>(x);    // from 1, 2, 4 and 8 lanes below in the row
+  x += dpp_u64<0x112, 0xf>(x);
+  x += dpp_u64<0x114, 0xf>(x);
+  x += dpp_u64<0x118, 0xf>(x);
+  x += dpp_u64<0x142, 0xa>(x);    // lane 15 of rows 0 and 2 into rows 1 and 3
+  x += dpp_u64<0x143, 0xc>(x);    // lane 31 into rows 2 and 3
   return x;
 }
 
-__device__ inline u64 wave_incl_scan_u64(u64 x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const u64 o = __shfl_up(x, off);
-    if (lane >= off) x += o;
-  }
-  return x;
+__device__ inline u64 wave_sum_u64(u64 x) {
+  x = wave_incl_scan_u64(x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, 63);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), 63);
+  return ((u64)hi << 32) | lo;
 }
 
 // Shared memory of one workgroup's row.
 struct FilterSmem {
   union {
     u64 grid[kGrid + 64];  // first pass: weight (or count) by bin, then spare words
+    double scale[kGrid + 64];   // second pass: a bin's lower end's weight, spare words 0
     struct {               // narrowing path
       u64 mass[kBins];
       uint32_t cnt[kBins];
     };
+    struct {               // choosing from the list
+      u64 bucket[kFilterThreads];
+      u64 sub[kCandMax], sub_w[kCandMax];
+    };
   };
   u64 cand[kCandMax];
   u64 red[kFilterWaves];
-  u64 share[kMaxShares];     // weight of the kept ids by share of the row
-  uint32_t n_cand;
+  u64 share[kMaxShares];   // weight of the kept ids by share of the row
+  uint32_t n_cand, n_sub;
   int hit;
   uint32_t key;
   int32_t id;
-  u64 acc, acc2;
+  float val;
+  u64 acc, acc2, word;
 };
 
 // Sum over the workgroup; every thread gets it.
@@ -650,11 +667,11 @@ __device__ inline CutKind cut_kind(const RowSettings &set, int V, bool totals) {
 // a logit under its lower end weighs less than 2^-47 of it.
 struct Grid {
   double k, c;        // position of logit l in bins from the lower end: l k + c
-  bool fine;          // positions are good to 1e-12 bins
+  bool fine;          // positions are good to 3e-11 bins, weights to 5e-13
   __device__ Grid(float ref, float T, bool count) {
     k = (double)(kGrid / 2) / (count ? fmax(33.0 * (double)T, 16.0) : 33.0 * (double)T);
     c = (double)(kGrid / 2) - (double)ref * k;
-    fine = fabs(c) < 16384.0 + kGrid;
+    fine = fabs(c) < 262144.0;
   }
   __device__ double pos(float l) const { return __builtin_fma((double)l, k, c); }
 };
@@ -757,34 +774,6 @@ __device__ __forceinline__ u64 block_max_u64(u64 k, FilterSmem &s) {
   return k;
 }
 
-// Bin of the grid, counted from its upper end, at which the running total first reaches need,
-// with the total up to and including it (kGrid when the whole stays under need). f(b): the
-// total of bin b.
-template <class F>
-__device__ __forceinline__ int find_from_top(FilterSmem &s, u64 need, F f, u64 *upto) {
-  constexpr int P = kGrid / kFilterThreads;
-  const int b0 = P * threadIdx.x;
-  u64 own = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) own += f(kGrid - 1 - (b0 + i));
-  u64 run = block_excl_scan_u64(own, s);
-  if (threadIdx.x == 0) { s.hit = kGrid; s.acc = 0; }
-  __syncthreads();
-  if (run < need && run + own >= need) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const u64 x = f(kGrid - 1 - (b0 + i));
-      if (run < need && run + x >= need) { s.hit = b0 + i; s.acc = run + x; }
-      run += x;
-    }
-  }
-  __syncthreads();
-  const int hit = s.hit;
-  *upto = s.acc;
-  __syncthreads();
-  return hit;
-}
-
 // What the second pass does with an id: from t_hi up it is kept without ranking, from t_lo up
 // it is listed (with `list` every id from t_lo up is).
 struct CutPlan {
@@ -795,177 +784,231 @@ struct CutPlan {
   u64 above;       // kCutMass: weight of the ids from t_hi up, by the bins
 };
 
-// The plan of a row with largest logit m (above -inf, inside the grid or plan.narrow results)
-// and `any` ids above -inf (kCutCount), from the grid in LDS. Every thread gets it.
+// The plan of a row with largest logit m (above -inf) and `any` ids above -inf (kCutCount),
+// from the grid in LDS. Every thread gets it. Thread t holds the kPlan bins from kGrid - 1 -
+// kPlan t down, so one scan over the threads runs in rank order.
+constexpr int kPlan = kGrid / kFilterThreads;
+
 __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kind, const Grid &g, float m, u64 any,
                                              FilterSmem &s) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
   const float lowest = key_value(kKeyNegInf + 1);
-  CutPlan p{lowest, lowest, false, m == INFINITY, 0, 0};
+  CutPlan p{lowest, lowest, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), 0, 0};
   const bool min_p = set.min_p > 0.0;
-  if (kind == kCutCount || kind == kCutMass) p.narrow |= !g.fine || !(g.pos(m) < (double)kGrid);
   if (p.narrow) return p;
   const float t_m = min_p ? smallest([&](float l) { return l >= m || weight_finite(l, m, set.sl) >= set.min_p; }) : lowest;
   if (kind == kCutSum) {
     p.t_lo = p.t_hi = t_m;
-  } else if (kind == kCutCount) {
+    return p;
+  }
+  // Bin totals: counts, or weights under the row's maximum in its unit.
+  const double xm = g.pos(m), scale = set.unit / bin_unit(set);
+  u64 raw[kPlan], total[kPlan], own = 0;
+#pragma unroll
+  for (int i = 0; i < kPlan; ++i) {
+    raw[i] = s.grid[b0 - i];
+    if (kind == kCutCount) total[i] = (uint32_t)raw[i];
+    else total[i] = raw[i] ? (u64)((double)raw[i] * scale * exp2_f64(((double)(b0 - i) - xm) * kBinOctaves)) : 0;
+    own += total[i];
+  }
+  const u64 before = block_excl_scan_u64(own, s);
+  if (tid == kFilterThreads - 1) s.acc = before + own;
+  if (tid == 0) s.hit = -1;
+  __syncthreads();
+  const u64 all = s.acc;
+  // The bin with the cut, counted from below, and the total up to and including it.
+  u64 need = 0;
+  if (kind == kCutCount) need = (u64)set.k;
+  else if (set.p < 1.0) need = p.need = at_least(set.p * (double)all);
+  if (need > before && need <= before + own) {
+    u64 run = before;
+#pragma unroll
+    for (int i = 0; i < kPlan; ++i) {
+      if (run < need && run + total[i] >= need) { s.hit = b0 - i; s.acc2 = run + total[i]; }
+      run += total[i];
+    }
+  }
+  __syncthreads();
+  int cb = s.hit;
+  if (kind == kCutCount) {
     p.list = true;
-    u64 upto;
-    auto f = [&](int b) { return (u64) * reinterpret_cast<const uint32_t *>(&s.grid[b]); };
-    const int kb = find_from_top(s, (u64)set.k, f, &upto);
-    if (kb == kGrid) {                   // fewer than k in the grid
-      u64 in = 0;
-      for (int b = tid; b < kGrid; b += kFilterThreads) in += f(b);
-      upto = block_sum_u64(in, s);
-      p.narrow = upto != any;
-    } else {
-      p.t_lo = smallest([&](float l) { return g.pos(l) >= (double)(kGrid - 1 - kb); });
-    }
-    p.narrow |= upto > kCandMax;
+    const u64 upto = cb < 0 ? all : s.acc2;
+    p.narrow = upto > kCandMax || (cb < 0 && all != any);   // fewer than k in the grid
+    if (cb >= 0) p.t_lo = smallest([&](float l) { return g.pos(l) >= (double)cb; });
     p.t_lo = fmaxf(p.t_lo, t_m);
-  } else {
-    // Bin totals under the row's maximum, in its unit.
-    const double xm = g.pos(m), scale = set.unit / bin_unit(set);
-    auto total = [&](int b) {
-      return s.grid[b] ? (u64)((double)s.grid[b] * scale * exp2_f64(((double)b - xm) * kBinOctaves)) : 0ull;
-    };
-    // The bin with the cut: that of top-p, or of min-p's bound if that is higher.
-    int cb = -1;
-    if (set.p < 1.0) {
-      u64 sum = 0, upto;
-      for (int b = tid; b < kGrid; b += kFilterThreads) sum += total(b);
-      p.need = at_least(set.p * (double)block_sum_u64(sum, s));
-      cb = kGrid - 1 - find_from_top(s, p.need, total, &upto);
-    }
-    if (min_p) {
-      const int mb = max(0, (int)g.pos(t_m));
-      if (mb > cb) { cb = mb; p.need = 0; }
-    }
-    // No bin holds more ids than its weights say: each is at least 1 (to 2e-14).
-    const double per_id = 1.001 / bin_unit(set);
-    u64 above = 0, ids = 0;
-    for (int b = cb + 1 + tid; b < kGrid; b += kFilterThreads) {
-      above += total(b);
-      ids += (u64)((double)s.grid[b] * per_id);
-    }
-    p.above = block_sum_u64(above, s);
+    return p;
+  }
+  // That of top-p, or of min-p's bound if it is higher.
+  if (min_p) {
+    const int mb = max(0, (int)g.pos(t_m));
+    if (mb > cb) { cb = mb; p.need = 0; }
+  }
+  // No bin holds more ids than its weights say: each is at least 1 (to 2e-14).
+  const double per_id = 1.001 / bin_unit(set);
+  u64 above = 0, ids = 0;
+#pragma unroll
+  for (int i = 0; i < kPlan; ++i) {
+    if (b0 - i > cb) above += total[i];
+    if (b0 - i >= cb) ids += (u64)((double)raw[i] * per_id);
+  }
+  p.above = block_sum_u64(above, s);
+  if (cb >= 0) {
     ids = block_sum_u64(ids, s);
-    if (cb >= 0) {
-      const u64 in_bin = (u64)((double)s.grid[cb] * per_id);
-      p.narrow = in_bin > kCandMax;
-      p.list = ids + in_bin <= kCandMax;
-      p.t_lo = fmaxf(smallest([&](float l) { return g.pos(l) >= (double)cb; }), t_m);
-      p.t_hi = smallest([&](float l) { return g.pos(l) >= (double)(cb + 1); });
-    }
+    const u64 in_bin = (u64)((double)s.grid[cb] * per_id);
+    p.narrow = in_bin > kCandMax;
+    p.list = ids <= kCandMax;
+    p.t_lo = fmaxf(smallest([&](float l) { return g.pos(l) >= (double)cb; }), t_m);
+    p.t_hi = smallest([&](float l) { return g.pos(l) >= (double)(cb + 1); });
   }
   return p;
 }
 
+// Weights of the bins' lower ends under maximum m, times the unit, in s.scale for collect_pass.
+__device__ __forceinline__ void scale_table(const Grid &g, float m, double unit, FilterSmem &s) {
+  const double xm = g.pos(m);
+  for (int b = threadIdx.x; b < kGrid + 64; b += kFilterThreads)
+    s.scale[b] = b < kGrid && (double)b <= xm ? unit * exp2_f64(((double)b - xm) * kBinOctaves) : 0.0;
+}
+
 // Second pass over vectors j0 .. j1 - 1: lists ids in s.cand (s.n_cand counts them) and, with
-// `sums`, adds up the rest of the kept ones.
+// `sums` (s.scale set), adds up the rest of the kept ones: a weight is its bin's scale times
+// its weight inside the bin, half the work of an exponential.
 template <class E>
-__device__ __forceinline__ void collect_pass(const RowView<E> &r, const RowSettings &set, const CutPlan &p, float m,
-                                             bool sums, int j0, int j1, u64 *sum, uint32_t *n, FilterSmem &s) {
+__device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan &p, const Grid &g, bool sums, int j0, int j1,
+                                             u64 *sum, uint32_t *n, FilterSmem &s) {
   const float hi = p.list ? INFINITY : p.t_hi;
+  auto list = [&](float l, int id) {
+    const uint32_t at = atomicAdd(&s.n_cand, 1u);
+    if (at < kCandMax) s.cand[at] = rank_word(l, id);
+  };
   if (sums && !p.list) {
     wave_ids(r, j0, j1, [&](float l, int id) {
       if (!(l >= p.t_lo)) return;
       if (l < hi) {
-        const uint32_t at = atomicAdd(&s.n_cand, 1u);
-        if (at < kCandMax) s.cand[at] = rank_word(l, id);
+        list(l, id);
       } else {
         ++*n;
-        *sum += to_fix(weight_finite(l, m, set.sl), set.unit);
+        const double x = g.pos(l);
+        const uint32_t b = whole_part(x);
+        const double w = __builtin_fma(bin_weight(__builtin_amdgcn_fract(x)), s.scale[b < kGrid ? b : kGrid], 4503599627370496.0);
+        *sum += (u64)__double_as_longlong(w) & 0xfffffffffffffull;
       }
     });
   } else if (p.t_lo < hi) {
     wave_ids(r, j0, j1, [&](float l, int id) {
-      if (l >= p.t_lo && l < hi) {
-        const uint32_t at = atomicAdd(&s.n_cand, 1u);
-        if (at < kCandMax) s.cand[at] = rank_word(l, id);
-      }
+      if (l >= p.t_lo && l < hi) list(l, id);
     });
   }
 }
 
-// Ranks s.cand[0 .. nc) and cuts it: c.val, c.id, c.n, c.S, given the ids kept without ranking
-// (n_above of them, weight c.S). share(id, w) is told the weight of each listed id that is
-// kept. Afterwards the list's kept ids are its first c.n - n_above.
-template <class F>
-__device__ __forceinline__ void rank_list(const RowSettings &set, CutKind kind, const CutPlan &p, int nc, uint32_t n_above,
-                                          RowCut &c, FilterSmem &s, F share) {
+// ------------------------------------------------------------------ choosing from the list
+// The item of s.cand[0 .. n) at which the running total of weights wt(word), taken in
+// descending order of the distinct numbers ord(word), first reaches need (at least 1, at most
+// the total): its ord, and the total up to and including it. bucket(word) in [0,
+// kFilterThreads) may not fall as ord falls. Two levels: the bucket that holds it, then every
+// item of that bucket against every other.
+template <class Ord, class Bucket, class Wt>
+__device__ __forceinline__ u64 pick(FilterSmem &s, int n, u64 need, Ord ord, Bucket bucket, Wt wt, u64 *upto) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  s.bucket[tid] = 0;
+  if (tid == 0) s.n_sub = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kFilterThreads) {
+    const u64 x = s.cand[i], w = wt(x);
+    if (w) atomicAdd(&s.bucket[bucket(x)], w);
+  }
+  __syncthreads();
+  const u64 own = s.bucket[tid], before = block_excl_scan_u64(own, s);
+  if (before < need && before + own >= need) { s.hit = tid; s.acc = before; }
+  __syncthreads();
+  const int hit = s.hit;
+  for (int i = tid; i < n; i += kFilterThreads) {
+    const u64 x = s.cand[i];
+    if (bucket(x) != hit) continue;
+    const u64 w = wt(x);
+    if (!w) continue;
+    const uint32_t at = atomicAdd(&s.n_sub, 1u);
+    s.sub[at] = ord(x);
+    s.sub_w[at] = w;
+  }
+  __syncthreads();
+  const int m = (int)s.n_sub;
+  for (int i = tid; i < m; i += kFilterThreads) {
+    const u64 x = s.sub[i], w = s.sub_w[i];
+    u64 run = s.acc;
+    for (int j = 0; j < m; ++j) run += s.sub[j] > x ? s.sub_w[j] : 0;
+    if (run < need && run + w >= need) { s.word = x; s.acc2 = run + w; }
+  }
+  __syncthreads();
+  *upto = s.acc2;
+  return s.word;
+}
+
+__device__ inline u64 swap_halves(u64 x) { return (x << 32) | (x >> 32); }
+
+// Cuts the list s.cand[0 .. nc) by rank: c.val, c.id, c.n, c.S, given the ids kept without
+// ranking (n_above of them, weight c.S). Returns the last listed word that is kept, 0 when
+// all are.
+__device__ __forceinline__ u64 cut_list(const RowSettings &set, CutKind kind, const CutPlan &p, int nc, uint32_t n_above,
+                                        RowCut &c, FilterSmem &s) {
   const int tid = threadIdx.x;
   const u64 mass_above = c.S;
   c.val = p.t_hi; c.id = 0x7fffffff;
   c.n = (int)n_above;
-  if (nc == 0) return;
-  int pow2 = 2;
-  while (pow2 < nc) pow2 <<= 1;
-  for (int i = nc + tid; i < pow2; i += kFilterThreads) s.cand[i] = 0;
-  sort_desc(s, pow2);
-  u64 w[kPerThread], own = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int at = kPerThread * tid + i;
-    w[i] = at < nc ? to_fix(weight_finite(word_value(s.cand[at]), c.m, set.sl), set.unit) : 0;
-    own += w[i];
+  if (nc == 0) return 0;
+  const float hi = p.list ? c.m : p.t_hi, per = (float)(kFilterThreads - 1) / (hi - p.t_lo);
+  auto ord = [](u64 x) { return x; };
+  auto bucket = [&](u64 x) { return (int)fminf(fmaxf((hi - word_value(x)) * per, 0.f), (float)(kFilterThreads - 1)); };
+  auto mass = [&](u64 x) { return to_fix(weight_finite(word_value(x), c.m, set.sl), set.unit); };
+  u64 last = 0, upto;
+  int n = nc;
+  if (kind == kCutCount && nc > set.k) {
+    last = pick(s, nc, (u64)set.k, ord, bucket, [](u64) { return 1ull; }, &upto);
+    n = set.k;
   }
-  const u64 first = mass_above + block_excl_scan_u64(own, s);
-  const int nk = min(nc, set.k);
-  u64 need = p.need;
-  if (kind == kCutCount && set.p < 1.0) {
-    u64 run = first;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      run += w[i];
-      if (kPerThread * tid + i == nk - 1) s.acc = run;
-    }
-    __syncthreads();
-    need = at_least(set.p * (double)s.acc);
+  u64 total = 0;
+  for (int i = tid; i < nc; i += kFilterThreads)
+    if (s.cand[i] >= last) total += mass(s.cand[i]);
+  total = block_sum_u64(total, s);
+  u64 need = 0;
+  if (kind == kCutCount && set.p < 1.0) need = at_least(set.p * (double)total);
+  if (kind == kCutMass && p.need > 0) {
+    if (p.need <= mass_above) return ~0ull;              // nothing of the list
+    need = p.need - mass_above < total ? p.need - mass_above : total;
   }
-  if (tid == 0) s.hit = nk;
-  __syncthreads();
   if (need > 0) {
-    u64 run = first;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int at = kPerThread * tid + i;
-      if (at < nk && run < need && run + w[i] >= need) s.hit = at + 1;
-      run += w[i];
-    }
-    if (tid == 0 && mass_above >= need) s.hit = 0;
+    const u64 k = last;
+    last = pick(s, nc, need, ord, bucket, [&](u64 x) { return x >= k ? mass(x) : 0ull; }, &total);
+    u64 at = 0;
+    for (int i = tid; i < nc; i += kFilterThreads) at += s.cand[i] >= last;
+    n = (int)block_sum_u64(at, s);
   }
-  __syncthreads();
-  const int take = s.hit;
-  if (take > 0) {
-    u64 run = first;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int at = kPerThread * tid + i;
-      run += w[i];
-      if (at < take) share(word_id(s.cand[at]), w[i]);
-      if (at == take - 1) {
-        s.acc2 = run;
-        s.key = (uint32_t)(s.cand[at] >> 32);
-        s.id = word_id(s.cand[at]);
-      }
-    }
-    __syncthreads();
-    c.S = s.acc2;
-    c.val = key_value(s.key);
-    c.id = s.id;
-    c.n = (int)n_above + take;
-  }
-  __syncthreads();
+  c.n = (int)n_above + n;
+  c.S = mass_above + total;
+  if (last) { c.val = word_value(last); c.id = word_id(last); }
+  else { c.val = p.t_lo; c.id = 0x7fffffff; }
+  return last;
 }
 
 // Where the kept ids' weights are after the cut.
 enum RowMode {
   kModeTop,      // at most one id, c.id
-  kModeList,     // s.cand[0 .. c.n), by rank
+  kModeList,     // the words of s.cand[0 .. s.n_cand) from `last` up
   kModeShares,   // s.share, by share of the vectors
   kModeNone      // not summed yet (c.S unset)
 };
+
+// Adds the kept listed ids' weights to the shares (of `step` vectors) they lie in.
+template <class E>
+__device__ __forceinline__ void add_listed(const RowView<E> &r, const RowSettings &set, const RowCut &c, int nc, u64 last,
+                                           int step, FilterSmem &s) {
+  for (int i = threadIdx.x; i < nc; i += kFilterThreads) {
+    const u64 x = s.cand[i];
+    if (x >= last)
+      atomicAdd(&s.share[(word_id(x) - r.off) / E::VE / step], to_fix(weight_finite(word_value(x), c.m, set.sl), set.unit));
+  }
+}
 
 __device__ inline RowMode cut_top(const RowSettings &set, u64 top, RowCut &c) {
   c.m = word_value(top);
@@ -993,11 +1036,11 @@ __device__ __forceinline__ float row_reference(const RowView<E> &r, FilterSmem &
 //   3. A second pass lists the ids in that bin and, where a draw follows, sums the weights of
 //      those above it by wave; when all kept ids are few they are listed and nothing is
 //      summed by pass (collect_pass).
-//   4. The list is ranked in LDS and cut (rank_list).
+//   4. The list is cut (cut_list).
 // totals: only the kept set and its weight are wanted; the bins give the weight above the cut.
 template <class E>
 __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, bool totals, RowCut &c,
-                                           FilterSmem &s) {
+                                           u64 *last, FilterSmem &s) {
   const int tid = threadIdx.x, wave = tid >> 6;
   const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
   const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
@@ -1022,33 +1065,35 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
   }
   if (!top || kind == kCutOne) return cut_top(set, top, c);
   __syncthreads();
-  const CutPlan p = make_plan(set, kind, Grid(ref, set.T, kind == kCutCount), c.m, any, s);
+  const Grid g(kind == kCutSum ? c.m : ref, set.T, kind == kCutCount);
+  const CutPlan p = make_plan(set, kind, g, c.m, any, s);
   c.S = 0;
   if (p.narrow) {
     cut_narrowing(r, set, c, s);
     return kModeNone;
   }
-  const bool sums = !totals;
+  const bool sums = !totals && !p.list;
+  __syncthreads();
+  if (sums) scale_table(g, c.m, set.unit, s);
   if (tid == 0) s.n_cand = 0;
   __syncthreads();
   u64 sum = 0;
   uint32_t n_sum = 0;
-  collect_pass(r, set, p, c.m, sums, j0, j1, &sum, &n_sum, s);
-  if (!p.list && !sums) {
+  collect_pass(r, p, g, sums, j0, j1, &sum, &n_sum, s);
+  if (totals && !p.list) {
     c.S = p.above;
     n_sum = 1;                     // some
   }
   __syncthreads();
-  if (!p.list && sums) {
+  if (sums) {
     sum = wave_sum_u64(sum);
     if ((tid & 63) == 0) s.share[wave] = sum;
     n_sum = (uint32_t)block_sum_u64(n_sum, s);
     for (int w = 0; w < kFilterWaves; ++w) c.S += s.share[w];
   }
   const int nc = min((int)s.n_cand, kCandMax);
-  rank_list(set, kind, p, nc, n_sum, c, s, [&](int id, u64 w) {
-    if (!p.list && sums) atomicAdd(&s.share[(id - r.off) / E::VE / per], w);
-  });
+  *last = cut_list(set, kind, p, nc, n_sum, c, s);
+  if (sums) add_listed(r, set, c, nc, *last, per, s);
   __syncthreads();
   return p.list ? kModeList : sums ? kModeShares : kModeNone;
 }
@@ -1087,22 +1132,28 @@ __device__ __forceinline__ u64 sum_shares(F f, int a, int b, int step, FilterSme
   return total;
 }
 
-// What a draw for uniform u of total S has to pass. u outside [0, 1) is taken as the nearest
-// end of the range, NaN as 0.
-__device__ inline double draw_target(float u, u64 S) {
-  return (u >= 1.f ? 0.99999994 : (u > 0.f ? (double)u : 0.0)) * (double)S;
+// The running total that a draw for uniform u of total S > 0 has to reach: the least whole
+// number over u S. u outside [0, 1) is taken as the nearest end of the range, NaN as 0.
+__device__ inline u64 draw_need(float u, u64 S) {
+  const u64 t = (u64)((u >= 1.f ? 0.99999994 : (u > 0.f ? (double)u : 0.0)) * (double)S) + 1;
+  return t < S ? t : S;
 }
 
-// Position (vector VE + element) of the first weight whose running sum passes t, given the
-// sums of n contiguous shares of `step` of all nv vectors in s.share: the share that holds the
-// crossing is split again, a part to each wave, until one wave load covers it.
+// Position (vector VE + element) of the first weight at which the running sum reaches need,
+// given the sums of n contiguous shares of `step` of all nv vectors in s.share: the share that
+// holds the crossing is split again, a part to each wave, until one wave load covers it. The
+// shares may come from another form of the weights, units apart: a need past the sum of the
+// parts is taken as that sum. -1 when nothing there has weight.
 template <int VE, class F>
-__device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, double t, FilterSmem &s) {
+__device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, u64 need, FilterSmem &s) {
   int a = 0, b = nv;
-  u64 before = 0;
   for (;;) {
+    u64 before = 0, total = 0;
+    for (int i = 0; i < n; ++i) total += s.share[i];
+    need = need < total ? need : total;
     int w = 0;
-    while (w < n - 1 && !((double)(before + s.share[w]) > t)) before += s.share[w++];
+    while (w < n - 1 && before + s.share[w] < need) before += s.share[w++];
+    need -= before;
     a += w * step;
     b = min(b, a + step);
     if (b - a <= 64) break;
@@ -1118,14 +1169,15 @@ __device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, doub
     if (j < b) f(j, w);
 #pragma unroll
     for (int i = 0; i < VE; ++i) own += w[i];
-    u64 run = before + wave_incl_scan_u64(own) - own;
-    // The total passes t (u < 1), so exactly one lane crosses it.
-    if (!((double)run > t) && (double)(run + own) > t) {
-      bool done = false;
+    const u64 incl = wave_incl_scan_u64(own), total = wave_sum_u64(own);
+    need = need < total ? need : total;
+    if (threadIdx.x == 0) s.id = -1;
+    u64 run = incl - own;
+    if (run < need && incl >= need) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
+        if (run < need && run + w[i] >= need) s.id = j * VE + i;
         run += w[i];
-        if (!done && (double)run > t) { s.id = j * VE + i; done = true; }
       }
     }
   }
@@ -1143,45 +1195,23 @@ __device__ __forceinline__ void row_total(const RowView<E> &r, RowCut &c, const 
                           (r.nv + kFilterWaves - 1) / kFilterWaves, s);
 }
 
-// The draw of target t from the list s.cand[0 .. n) by rank: the smallest id whose running
-// weight, in id order, passes it.
-__device__ __forceinline__ int draw_in_list(const RowCut &c, const RowSettings &set, double t, FilterSmem &s) {
-  const int tid = threadIdx.x;
-  // The words by id: the complement makes the lowest id the largest word.
-  int pow2 = 2;
-  while (pow2 < c.n) pow2 <<= 1;
-  for (int i = tid; i < pow2; i += kFilterThreads) {
-    const u64 x = i < c.n ? s.cand[i] : 0;
-    s.cand[i] = (x << 32) | (x >> 32);
-  }
-  sort_desc(s, pow2);
-  u64 w[kPerThread], own = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int at = kPerThread * tid + i;
-    w[i] = at < c.n ? to_fix(weight_finite(key_value((uint32_t)s.cand[at]), c.m, set.sl), set.unit) : 0;
-    own += w[i];
-  }
-  u64 run = block_excl_scan_u64(own, s);
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    if (!((double)run > t) && (double)(run + w[i]) > t) s.id = (int)~(uint32_t)(s.cand[kPerThread * tid + i] >> 32);
-    run += w[i];
-  }
-  __syncthreads();
-  const int id = s.id;
-  __syncthreads();
-  return id;
-}
-
 // The row's draw for uniform u: the smallest kept id whose running weight, in id order, passes
-// u times the total (set in c.S when the cut left it out); -1 for an empty row. n shares of
-// `step` vectors are in s.share in kModeShares.
+// u times the total (set in c.S when the cut left it out), with its logit; -1 for an empty row.
+// n shares of `step` vectors are in s.share in kModeShares, nc words in s.cand in kModeList.
 template <class E>
 __device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const RowSettings &set, RowMode mode, int n, int step,
-                                        float u, FilterSmem &s) {
+                                        int nc, u64 last, float u, float *l, FilterSmem &s) {
+  *l = c.m;
   if (mode == kModeTop) return c.n ? c.id : -1;
-  if (mode == kModeList) return draw_in_list(c, set, draw_target(u, c.S), s);
+  if (mode == kModeList) {
+    u64 upto;
+    const float per = (float)kFilterThreads / (float)r.V;
+    const u64 x = pick(s, nc, draw_need(u, c.S), swap_halves,
+                       [&](u64 w) { return min((int)((float)word_id(w) * per), kFilterThreads - 1); },
+                       [&](u64 w) { return w >= last ? to_fix(weight_finite(word_value(w), c.m, set.sl), set.unit) : 0ull; }, &upto);
+    *l = word_value(swap_halves(x));
+    return word_id(swap_halves(x));
+  }
   auto f = [&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); };
   if (mode == kModeNone) {
     n = kFilterWaves;
@@ -1189,7 +1219,10 @@ __device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const Ro
     c.S = sum_shares<E::VE>(f, 0, r.nv, step, s);
   }
   if (c.n == 0 || c.S == 0) return -1;
-  return r.off + draw_in_shares<E::VE>(f, r.nv, n, step, draw_target(u, c.S), s);
+  const int at = draw_in_shares<E::VE>(f, r.nv, n, step, draw_need(u, c.S), s);
+  if (at < 0) return -1;
+  *l = r.at(r.off + at);
+  return r.off + at;
 }
 
 }  // namespace sdv

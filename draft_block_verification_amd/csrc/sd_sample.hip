@@ -38,15 +38,16 @@ struct SampleRows {
       load_settings(a.set, row / a.rows_per, a.V, threadIdx.x == 0 ? a.ws : nullptr));
   }
   __device__ __forceinline__ void finish(int row, const RowView<E> &r, const RowSettings &set, RowCut &c, RowMode mode,
-                                         int n, int step, FilterSmem &s) const {
-    const int id = row_draw(r, c, set, mode, n, step, a.u[row], s);
+                                         int n, int step, int nc, u64 last, FilterSmem &s) const {
+    float l;
+    const int id = row_draw(r, c, set, mode, n, step, nc, last, a.u[row], &l, s);
     if (threadIdx.x == 0) {
       if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
       a.tokens[row * a.token_stride] = id;
       if (a.kept) a.kept[row] = c.n;
       if (a.logprob) {
         float lp = id < 0 ? -INFINITY : 0.f;
-        if (c.n > 1) lp = (float)log(weight(r.at(id), c.m, set.sl) * set.unit / (double)c.S);
+        if (id >= 0 && c.n > 1) lp = (float)log(weight(l, c.m, set.sl) * set.unit / (double)c.S);
         a.logprob[row] = lp;
       }
     }
@@ -100,7 +101,7 @@ struct AcceptRows {
   }
   template <class E>
   __device__ __forceinline__ void finish(int row, const RowView<E> &r, const RowSettings &set, RowCut &c, RowMode, int,
-                                         int, FilterSmem &s) const {
+                                         int, int, u64, FilterSmem &s) const {
     row_total(r, c, set, s);
     const int targets = a.rm.B * (a.rm.gamma + 1);
     if (threadIdx.x == 0) (row < targets ? a.cut_p[row] : a.cut_q[row - targets]) = c;
@@ -114,8 +115,10 @@ __global__ __launch_bounds__(kFilterThreads, 4) void k_rows(Rows rows) {
   const int row = blockIdx.x;
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     RowCut c;
-    const RowMode mode = row_cut(r, set, Rows::kTotals, c, s);
-    rows.finish(row, r, set, c, mode, kFilterWaves, (r.nv + kFilterWaves - 1) / kFilterWaves, s);
+    u64 last = 0;
+    const RowMode mode = row_cut(r, set, Rows::kTotals, c, &last, s);
+    const int nc = min((int)s.n_cand, kCandMax);
+    rows.finish(row, r, set, c, mode, kFilterWaves, (r.nv + kFilterWaves - 1) / kFilterWaves, nc, last, s);
   });
 }
 
@@ -216,15 +219,18 @@ __global__ __launch_bounds__(kFilterThreads, 4) void k_team_collect(Rows rows, T
       for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = t.grid[(size_t)row * kGrid + b];
       __syncthreads();
     }
-    const CutPlan p = make_plan(set, kind, Grid(o.ref, set.T, kind == kCutCount), m, o.any, s);
+    const Grid g(kind == kCutSum ? m : o.ref, set.T, kind == kCutCount);
+    const CutPlan p = make_plan(set, kind, g, m, o.any, s);
     if (blockIdx.x == 0 && tid == 0) o.plan = p;
     if (p.narrow) return;
+    __syncthreads();
+    if (!Rows::kTotals && !p.list) scale_table(g, m, set.unit, s);
     if (tid == 0) s.n_cand = 0;
     __syncthreads();
     const Part part(r.nv, t.C);
     u64 sum = 0;
     uint32_t n = 0;
-    collect_pass(r, set, p, m, !Rows::kTotals, part.j0, part.j1, &sum, &n, s);
+    collect_pass(r, p, g, !Rows::kTotals && !p.list, part.j0, part.j1, &sum, &n, s);
     sum = block_sum_u64(sum, s);
     n = (uint32_t)block_sum_u64(n, s);
     const uint32_t nc = min(s.n_cand, (uint32_t)kCandMax);
@@ -249,6 +255,8 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
     const int step = (r.nv + t.C - 1) / t.C;
     RowCut c;
     RowMode mode;
+    u64 last = 0;
+    const int nc = min(o.n_list, (uint32_t)kCandMax);
     c.S = 0;
     c.m = word_value(o.top);
     if (!o.top || kind == kCutOne) {
@@ -257,20 +265,18 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
       cut_narrowing(r, set, c, s);
       mode = kModeNone;
     } else {
-      const int nc = min(o.n_list, (uint32_t)kCandMax);
       for (int i = tid; i < nc; i += kFilterThreads) s.cand[i] = t.list[(size_t)row * kCandMax + i];
       if (tid < t.C) s.share[tid] = t.share[(size_t)row * kMaxShares + tid];
       __syncthreads();
       const bool sums = !Rows::kTotals && !o.plan.list;
       if (sums) for (int i = 0; i < t.C; ++i) c.S += s.share[i];
       else if (!o.plan.list) c.S = o.plan.above;
-      rank_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s, [&](int id, u64 w) {
-        if (sums) atomicAdd(&s.share[(id - r.off) / (int)(16 / sizeof(*r.p)) / step], w);
-      });
+      last = cut_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s);
+      if (sums) add_listed(r, set, c, nc, last, step, s);
       __syncthreads();
       mode = o.plan.list ? kModeList : sums ? kModeShares : kModeNone;
     }
-    rows.finish(row, r, set, c, mode, t.C, step, s);
+    rows.finish(row, r, set, c, mode, t.C, step, nc, last, s);
   });
 }
 
@@ -368,13 +374,22 @@ struct Residual {
     pq = per_weight(cq, set);
   }
   __device__ void operator()(int j, u64 (&w)[4]) const {
-    float l[4];
+    float l[4], lq[4];
     v.load(j, l);
+    const int x0 = v.id(j, 0);
+    if (v.whole(j) && (reinterpret_cast<uintptr_t>(q + x0) & 7) == 0) {
+      const uint2 h = *reinterpret_cast<const uint2 *>(q + x0);
+      lq[0] = __uint_as_float(h.x << 16); lq[1] = __uint_as_float(h.x & 0xffff0000u);
+      lq[2] = __uint_as_float(h.y << 16); lq[3] = __uint_as_float(h.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lq[i] = x0 + i >= 0 && x0 + i < v.V ? bf16_to_f32(q[x0 + i]) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int x = v.id(j, i);
-      const double p = prob(cp, pp, set, l[i], x);
-      w[i] = p > 0.0 ? to_fix(fmax(p - prob(cq, pq, set, canonical(bf16_to_f32(q[x])), x), 0.0), kResidualUnit) : 0;
+      w[i] = 0;
+      const double p = prob(cp, pp, set, l[i], x0 + i);
+      if (p > 0.0) w[i] = to_fix(fmax(p - prob(cq, pq, set, canonical(lq[i]), x0 + i), 0.0), kResidualUnit);
     }
   }
 };
@@ -425,16 +440,18 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
   for (int i = 0; i < shares; ++i) S += s.share[i];
   const int step = (v.nv + shares - 1) / shares;
   const bool residual = acc < L;
-  const double t = draw_target(u, S);
   int id = -1;
-  if (residual && S > 0)
-    id = v.off + draw_in_shares<4>(Residual(a, v, r, acc, cp, set), v.nv, shares, step, t, s);
-  else if (!residual && S > 0)
-    id = v.off + draw_in_shares<4>([&](int j, u64 (&w)[4]) { kept_weights(v, cp, set, j, w); }, v.nv, shares, step, t, s);
-  else if (cp.n > 0) {
+  if (S > 0) {
+    const u64 need = draw_need(u, S);
+    const int at = residual
+        ? draw_in_shares<4>(Residual(a, v, r, acc, cp, set), v.nv, shares, step, need, s)
+        : draw_in_shares<4>([&](int j, u64 (&w)[4]) { kept_weights(v, cp, set, j, w); }, v.nv, shares, step, need, s);
+    if (at >= 0) id = v.off + at;
+  } else if (cp.n > 0) {
     // No residual mass: the target's own distribution.
     if (tid == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
-    id = row_draw(v, cp, set, kModeNone, 0, 0, u, s);
+    float l;
+    id = row_draw(v, cp, set, kModeNone, 0, 0, 0, 0, u, &l, s);
   }
   if (tid == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
