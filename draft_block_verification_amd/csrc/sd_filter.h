@@ -104,6 +104,7 @@ __device__ inline float key_value(uint32_t k) {
 }
 
 struct ElemF32 {
+  static constexpr uint32_t kNegInf = 0xff800000u;   // a word of -inf
   using S = float;
   static constexpr int VE = 4;
   __device__ static float get(S x) { return x; }
@@ -114,6 +115,7 @@ struct ElemF32 {
 };
 
 struct ElemBF16 {
+  static constexpr uint32_t kNegInf = 0xff80ff80u;   // a word of -inf
   using S = uint16_t;
   static constexpr int VE = 8;
   __device__ static float get(S x) { return bf16_to_f32(x); }
@@ -127,6 +129,7 @@ struct ElemBF16 {
 };
 
 struct ElemF16 {
+  static constexpr uint32_t kNegInf = 0xfc00fc00u;   // a word of -inf
   using S = _Float16;
   static constexpr int VE = 8;
   __device__ static float get(S x) { return (float)x; }
@@ -179,12 +182,13 @@ struct RowView {
   }
 };
 
-// f(value, id) for the ids of vectors j0 .. j1 - 1, taken by the calling wave. The whole
-// vectors go first, a round's loads issued before the round ahead of it is used; then the
-// row's first and last vector if it holds them and they lie in it in part, lane i taking
-// element i. N: ids a lane and round.
+// f(v, id0) for vectors j0 .. j1 - 1, taken by the calling wave: VE values as they lie in
+// memory (NaN among them) and the first one's id. Lanes without a vector get -inf, so f needs
+// no mask. The whole vectors go first, a round's loads issued before the round ahead of it is
+// used; then the row's first and last vector if it holds them and they lie in it in part, an
+// element a lane. N: ids a lane and round.
 template <int N = 16, class E, class F>
-__device__ __forceinline__ void wave_ids(const RowView<E> &r, int j0, int j1, F f) {
+__device__ __forceinline__ void wave_vecs(const RowView<E> &r, int j0, int j1, F f) {
   const int lane = threadIdx.x & 63;
   constexpr int U = N > E::VE ? N / E::VE : 1;
   const bool head = j0 == 0 && j0 < j1 && !r.whole(0);
@@ -204,23 +208,39 @@ __device__ __forceinline__ void wave_ids(const RowView<E> &r, int j0, int j1, F 
 #pragma unroll
         for (int u = 0; u < U; ++u) next[u] = fetch(j + lane + 64 * (U + u));
       }
+      if (j + 64 * U > b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j + lane + 64 * u >= b) now[u] = u32x4{E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int at = j + lane + 64 * u;
-        if (at < b) {
-          float v[E::VE];
-          r.unpack(now[u], v);
-#pragma unroll
-          for (int i = 0; i < E::VE; ++i) f(v[i], r.id(at, i));
-        }
+        float v[E::VE];
+        E::unpack(now[u], v);
+        f(v, r.id(j + lane + 64 * u, 0));
       }
     }
   }
-  if ((head || tail) && lane < 2 * E::VE) {
+  if (head || tail) {
     const bool second = lane >= E::VE;
     const int x = r.id(second ? r.nv - 1 : 0, second ? lane - E::VE : lane);
-    if ((second ? tail : head) && x >= 0 && x < r.V) f(r.at(x), x);
+    const bool in = lane < 2 * E::VE && (second ? tail : head) && x >= 0 && x < r.V;
+    float v[E::VE];
+#pragma unroll
+    for (int i = 0; i < E::VE; ++i) v[i] = -INFINITY;
+    if (in) v[0] = E::get(r.p[x]);
+    f(v, x);
   }
+}
+
+// f(value, id) for their ids, canonical values above -inf only.
+template <int N = 16, class E, class F>
+__device__ __forceinline__ void wave_ids(const RowView<E> &r, int j0, int j1, F f) {
+  wave_vecs<N>(r, j0, j1, [&](const float (&v)[E::VE], int id) {
+#pragma unroll
+    for (int i = 0; i < E::VE; ++i)
+      if (v[i] > -INFINITY) f(v[i], id + i);
+  });
 }
 
 // ------------------------------------------------------------------ weights
@@ -733,22 +753,29 @@ template <class E>
 __device__ __forceinline__ void bin_pass(const RowView<E> &r, const Grid &g, CutKind kind, double unit, int j0, int j1,
                                          PassOut &o, FilterSmem &s) {
   // An id outside the grid adds to one of 64 words behind it, a lane's own, unread: without a
-  // branch around the add.
+  // branch around the add. A NaN's position converts to 0: bin 0 is not read either.
   const uint32_t spare = kGrid + (threadIdx.x & 63);
   if (kind == kCutMass) {
-    wave_ids(r, j0, j1, [&](float l, int) {
-      o.best = fmaxf(o.best, l);
-      const double x = g.pos(l);
-      const uint32_t b = whole_part(x);
-      atomicAdd(&s.grid[b < kGrid ? b : spare], to_fix(bin_weight(__builtin_amdgcn_fract(x)), unit));
+    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int) {
+#pragma unroll
+      for (int i = 0; i < E::VE; ++i) {
+        o.best = fmaxf(o.best, v[i]);
+        const double x = g.pos(v[i]);
+        const uint32_t b = whole_part(x);
+        atomicAdd(&s.grid[b < kGrid ? b : spare], to_fix(bin_weight(__builtin_amdgcn_fract(x)), unit));
+      }
     });
   } else if (kind == kCutCount) {
-    wave_ids(r, j0, j1, [&](float l, int) {
-      o.best = fmaxf(o.best, l);
-      o.any += l > -INFINITY;
-      const uint32_t b = whole_part(g.pos(l));
-      atomicAdd(reinterpret_cast<uint32_t *>(&s.grid[b < kGrid ? b : spare]), 1u);
+    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int) {
+#pragma unroll
+      for (int i = 0; i < E::VE; ++i) {
+        o.best = fmaxf(o.best, v[i]);
+        o.any += __popcll(__ballot(v[i] > -INFINITY));
+        const uint32_t b = whole_part(g.pos(v[i]));
+        atomicAdd(reinterpret_cast<uint32_t *>(&s.grid[b < kGrid ? b : spare]), 1u);
+      }
     });
+    o.any = (threadIdx.x & 63) == 0 ? o.any : 0;       // counted once a wave
   } else {
     wave_ids(r, j0, j1, [&](float l, int id) {
       if (l > o.best || (l == o.best && id < o.at)) { o.best = l; o.at = id; }
@@ -806,7 +833,7 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
   u64 raw[kPlan], total[kPlan], own = 0;
 #pragma unroll
   for (int i = 0; i < kPlan; ++i) {
-    raw[i] = s.grid[b0 - i];
+    raw[i] = b0 - i > 0 ? s.grid[b0 - i] : 0;
     if (kind == kCutCount) total[i] = (uint32_t)raw[i];
     else total[i] = raw[i] ? (u64)((double)raw[i] * scale * exp2_f64(((double)(b0 - i) - xm) * kBinOctaves)) : 0;
     own += total[i];
@@ -876,27 +903,43 @@ __device__ __forceinline__ void scale_table(const Grid &g, float m, double unit,
 template <class E>
 __device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan &p, const Grid &g, bool sums, int j0, int j1,
                                              u64 *sum, uint32_t *n, FilterSmem &s) {
-  const float hi = p.list ? INFINITY : p.t_hi;
-  auto list = [&](float l, int id) {
-    const uint32_t at = atomicAdd(&s.n_cand, 1u);
-    if (at < kCandMax) s.cand[at] = rank_word(l, id);
+  const float lo = p.t_lo, hi = p.list ? INFINITY : p.t_hi;
+  auto list = [&](const float (&v)[E::VE], int id) {
+#pragma unroll
+    for (int i = 0; i < E::VE; ++i) {
+      if (v[i] >= lo && v[i] < hi) {
+        const uint32_t at = atomicAdd(&s.n_cand, 1u);
+        if (at < kCandMax) s.cand[at] = rank_word(v[i], id + i);
+      }
+    }
+  };
+  auto any_listed = [&](const float (&v)[E::VE]) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < E::VE; ++i) any |= v[i] >= lo && v[i] < hi;
+    return __ballot(any) != 0;
   };
   if (sums && !p.list) {
-    wave_ids(r, j0, j1, [&](float l, int id) {
-      if (!(l >= p.t_lo)) return;
-      if (l < hi) {
-        list(l, id);
-      } else {
-        ++*n;
-        const double x = g.pos(l);
-        const uint32_t b = whole_part(x);
-        const double w = __builtin_fma(bin_weight(__builtin_amdgcn_fract(x)), s.scale[b < kGrid ? b : kGrid], 4503599627370496.0);
-        *sum += (u64)__double_as_longlong(w) & 0xfffffffffffffull;
+    uint32_t kept_n = 0;
+    u64 kept_w = 0;
+    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int id) {
+#pragma unroll
+      for (int i = 0; i < E::VE; ++i) {
+        const bool k = v[i] >= hi;
+        kept_n += __popcll(__ballot(k));
+        // An id that is not kept takes part as the lowest finite value, under the grid.
+        const double x = g.pos(k ? v[i] : -3.402823466e38f);
+        const uint32_t b = min(whole_part(x), (uint32_t)kGrid);
+        const double w = __builtin_fma(bin_weight(__builtin_amdgcn_fract(x)), s.scale[b], 4503599627370496.0);
+        kept_w += (u64)__double_as_longlong(w) & 0xfffffffffffffull;
       }
+      if (any_listed(v)) list(v, id);
     });
-  } else if (p.t_lo < hi) {
-    wave_ids(r, j0, j1, [&](float l, int id) {
-      if (l >= p.t_lo && l < hi) list(l, id);
+    *sum += kept_w;
+    *n += (threadIdx.x & 63) == 0 ? kept_n : 0;        // counted once a wave
+  } else if (lo < hi) {
+    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int id) {
+      if (any_listed(v)) list(v, id);
     });
   }
 }
