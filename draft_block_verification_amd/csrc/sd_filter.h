@@ -29,8 +29,9 @@ constexpr int kFilterWaves = kFilterThreads / kWave;
 constexpr int kGrid = 4096;          // bins of the first pass's histogram, half on each side
                                      // of its reference logit
 constexpr int kBins = 2048;          // bins of the narrowing path's histogram
-constexpr int kCandMax = 2048;       // ids that are ranked in LDS
-constexpr int kPerThread = kCandMax / kFilterThreads;
+constexpr int kCandMax = 1536;       // ids that are ranked in LDS (three workgroups a compute unit)
+constexpr int kCandPad = 2048;       // the same, up to a power of two
+constexpr int kPerThread = kCandPad / kFilterThreads;
 constexpr int kMaxShares = 64;       // parts a row's vectors are summed in
 constexpr int kFixBits = 46;         // most fraction bits of the summed weights
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // key of -inf (sort_key)
@@ -190,34 +191,44 @@ struct RowView {
 template <int N = 16, class E, class F>
 __device__ __forceinline__ void wave_vecs(const RowView<E> &r, int j0, int j1, F f) {
   const int lane = threadIdx.x & 63;
+  j0 = __builtin_amdgcn_readfirstlane(j0);
+  j1 = __builtin_amdgcn_readfirstlane(j1);
   constexpr int U = N > E::VE ? N / E::VE : 1;
   const bool head = j0 == 0 && j0 < j1 && !r.whole(0);
   const bool tail = j1 == r.nv && j0 < j1 && !r.whole(r.nv - 1) && !(head && r.nv == 1);
-  const int a = j0 + head, b = j1 - tail;
-  if (a < b) {
-    const typename E::S *base = r.p + r.off;
-    auto fetch = [&](int j) { return *reinterpret_cast<const u32x4 *>(base + (size_t)min(j, b - 1) * E::VE); };
-    u32x4 next[U];
+  const int a = j0 + head, n = j1 - tail - a;      // whole vectors
+  if (n > 0) {
+    // The wave's place in the row is one number for all its lanes: addresses are a scalar base
+    // and a lane's constant offset.
+    const char *base = reinterpret_cast<const char *>(r.p + r.off) + 16 * (size_t)a;
+    auto fetch = [&](int t, u32x4 (&q)[U]) {
+      const char *p = base + (size_t)t * (1024 * U);
+      if ((t + 1) * 64 * U <= n) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) next[u] = fetch(a + lane + 64 * u);
-    for (int j = a; j < b; j += 64 * U) {
+        for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const u32x4 *>(p + (u * 1024 + lane * 16));
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          q[u] = *reinterpret_cast<const u32x4 *>(base + 16 * (size_t)min(t * 64 * U + 64 * u + lane, n - 1));
+      }
+    };
+    u32x4 next[U];
+    fetch(0, next);
+    for (int t = 0; t * 64 * U < n; ++t) {
       u32x4 now[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) now[u] = next[u];
-      if (j + 64 * U < b) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = fetch(j + lane + 64 * (U + u));
-      }
-      if (j + 64 * U > b) {
+      if ((t + 1) * 64 * U < n) fetch(t + 1, next);
+      if ((t + 1) * 64 * U > n) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (j + lane + 64 * u >= b) now[u] = u32x4{E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
+          if (t * 64 * U + 64 * u + lane >= n) now[u] = u32x4{E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float v[E::VE];
         E::unpack(now[u], v);
-        f(v, r.id(j + lane + 64 * u, 0));
+        f(v, r.id(a + t * 64 * U + 64 * u + lane, 0));
       }
     }
   }
@@ -328,7 +339,7 @@ struct FilterSmem {
       u64 sub[kCandMax], sub_w[kCandMax];
     };
   };
-  u64 cand[kCandMax];
+  u64 cand[kCandPad];
   u64 red[kFilterWaves];
   u64 share[kMaxShares];   // weight of the kept ids by share of the row
   uint32_t n_cand, n_sub;
@@ -904,20 +915,25 @@ template <class E>
 __device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan &p, const Grid &g, bool sums, int j0, int j1,
                                              u64 *sum, uint32_t *n, FilterSmem &s) {
   const float lo = p.t_lo, hi = p.list ? INFINITY : p.t_hi;
+  // One counter update a wave and vector; the lanes' places follow from the ballots.
   auto list = [&](const float (&v)[E::VE], int id) {
+    u64 m[E::VE];
+    uint32_t count = 0;
 #pragma unroll
     for (int i = 0; i < E::VE; ++i) {
-      if (v[i] >= lo && v[i] < hi) {
-        const uint32_t at = atomicAdd(&s.n_cand, 1u);
-        if (at < kCandMax) s.cand[at] = rank_word(v[i], id + i);
-      }
+      m[i] = __ballot(v[i] >= lo && v[i] < hi);
+      count += __popcll(m[i]);
     }
-  };
-  auto any_listed = [&](const float (&v)[E::VE]) {
-    bool any = false;
+    if (count == 0) return;
+    uint32_t at = 0;
+    if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.n_cand, count);
+    at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
-    for (int i = 0; i < E::VE; ++i) any |= v[i] >= lo && v[i] < hi;
-    return __ballot(any) != 0;
+    for (int i = 0; i < E::VE; ++i) {
+      const uint32_t mine = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m[i], 0));
+      if (v[i] >= lo && v[i] < hi && mine < kCandMax) s.cand[mine] = rank_word(v[i], id + i);
+      at += __popcll(m[i]);
+    }
   };
   if (sums && !p.list) {
     uint32_t kept_n = 0;
@@ -933,14 +949,12 @@ __device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan 
         const double w = __builtin_fma(bin_weight(__builtin_amdgcn_fract(x)), s.scale[b], 4503599627370496.0);
         kept_w += (u64)__double_as_longlong(w) & 0xfffffffffffffull;
       }
-      if (any_listed(v)) list(v, id);
+      list(v, id);
     });
     *sum += kept_w;
     *n += (threadIdx.x & 63) == 0 ? kept_n : 0;        // counted once a wave
   } else if (lo < hi) {
-    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int id) {
-      if (any_listed(v)) list(v, id);
-    });
+    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int id) { list(v, id); });
   }
 }
 
@@ -980,6 +994,7 @@ __device__ __forceinline__ u64 pick(FilterSmem &s, int n, u64 need, Ord ord, Buc
   for (int i = tid; i < m; i += kFilterThreads) {
     const u64 x = s.sub[i], w = s.sub_w[i];
     u64 run = s.acc;
+#pragma unroll 8
     for (int j = 0; j < m; ++j) run += s.sub[j] > x ? s.sub_w[j] : 0;
     if (run < need && run + w >= need) { s.word = x; s.acc2 = run + w; }
   }
@@ -1171,6 +1186,7 @@ __device__ __forceinline__ u64 sum_shares(F f, int a, int b, int step, FilterSme
   if ((threadIdx.x & 63) == 0) s.share[wave] = m;
   __syncthreads();
   u64 total = 0;
+#pragma unroll
   for (int w = 0; w < kFilterWaves; ++w) total += s.share[w];
   return total;
 }
@@ -1191,12 +1207,13 @@ template <int VE, class F>
 __device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, u64 need, FilterSmem &s) {
   int a = 0, b = nv;
   for (;;) {
-    u64 before = 0, total = 0;
-    for (int i = 0; i < n; ++i) total += s.share[i];
+    // Every wave finds the share by itself, lane i holding share i.
+    const int lane = threadIdx.x & 63;
+    const u64 x = lane < n ? s.share[lane] : 0, incl = wave_incl_scan_u64(x), total = wave_sum_u64(x);
     need = need < total ? need : total;
-    int w = 0;
-    while (w < n - 1 && before + s.share[w] < need) before += s.share[w++];
-    need -= before;
+    const u64 m = __ballot(lane < n && incl >= need);
+    const int w = __builtin_amdgcn_readfirstlane(m ? __ffsll((long long)m) - 1 : n - 1);
+    need -= __shfl(incl - x, w);
     a += w * step;
     b = min(b, a + step);
     if (b - a <= 64) break;

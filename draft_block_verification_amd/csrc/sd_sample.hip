@@ -67,7 +67,7 @@ struct FilteredArgs {
   int64_t *counters;
   RowCut *cut_p;                 // [B][gamma + 1]
   RowCut *cut_q;                 // [B][gamma]
-  u64 *share;                    // [B][kMaxShares] sums of the draw's weights
+  u64 *share;                    // [B][kMaxShares][2] sums of the draw's weights
   WsHeader *ws;
 };
 
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
       if (tid < t.C) s.share[tid] = t.share[(size_t)row * kMaxShares + tid];
       __syncthreads();
       const bool sums = !Rows::kTotals && !o.plan.list;
-      if (sums) for (int i = 0; i < t.C; ++i) c.S += s.share[i];
+      if (sums) c.S = wave_sum_u64((tid & 63) < t.C ? s.share[tid & 63] : 0);
       else if (!o.plan.list) c.S = o.plan.above;
       last = cut_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s);
       if (sums) add_listed(r, set, c, nc, last, step, s);
@@ -359,38 +359,57 @@ __device__ __forceinline__ int first_rejection(const FilteredArgs &a, int r, int
 // sum over 2^21 ids is off by 2^-31 of a unit row at the very worst, 2^-42 for random roundings.
 constexpr double kResidualUnit = 2251799813685248.0;
 
-// Weights max(0, p' - q') of vector j of target row v in id order.
+// Weights of vector j of target row v in id order: max(0, p' - q'), and p' alone (wp), which is
+// drawn from when the former have no mass. All in kResidualUnit. has_q false: p' as both.
 struct Residual {
   RowView<ElemF32> v;
   const uint16_t *q;
   RowCut cp, cq;
   RowSettings set;
   double pp, pq;
-  __device__ Residual(const FilteredArgs &a, const RowView<ElemF32> &v_, int r, int acc, const RowCut &cp_,
+  __device__ Residual(const FilteredArgs &a, const RowView<ElemF32> &v_, int r, int acc, bool has_q, const RowCut &cp_,
                       const RowSettings &set_)
-      : v(v_), q(a.draft_logits + ((size_t)r * a.rm.gamma + acc) * a.V), cp(cp_),
-        cq(a.cut_q[(size_t)r * a.rm.gamma + acc]), set(set_) {
+      : v(v_), q(has_q ? a.draft_logits + ((size_t)r * a.rm.gamma + acc) * a.V : nullptr), cp(cp_), set(set_) {
     pp = per_weight(cp, set);
-    pq = per_weight(cq, set);
+    pq = 0.0;
+    if (q) {
+      cq = a.cut_q[(size_t)r * a.rm.gamma + acc];
+      pq = per_weight(cq, set);
+    }
   }
-  __device__ void operator()(int j, u64 (&w)[4]) const {
-    float l[4], lq[4];
-    v.load(j, l);
+  __device__ void raw_q(int j, uint2 &h) const {
     const int x0 = v.id(j, 0);
     if (v.whole(j) && (reinterpret_cast<uintptr_t>(q + x0) & 7) == 0) {
-      const uint2 h = *reinterpret_cast<const uint2 *>(q + x0);
-      lq[0] = __uint_as_float(h.x << 16); lq[1] = __uint_as_float(h.x & 0xffff0000u);
-      lq[2] = __uint_as_float(h.y << 16); lq[3] = __uint_as_float(h.y & 0xffff0000u);
+      h = *reinterpret_cast<const uint2 *>(q + x0);
     } else {
+      uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lq[i] = x0 + i >= 0 && x0 + i < v.V ? bf16_to_f32(q[x0 + i]) : 0.f;
+      for (int i = 0; i < 4; ++i) b[i] = x0 + i >= 0 && x0 + i < v.V ? q[x0 + i] : 0;
+      h = uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
     }
+  }
+  __device__ void weights(int j, const float (&l)[4], const uint2 &h, u64 (&w)[4], u64 (&wp)[4]) const {
+    const float lq[4] = {__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xffff0000u), __uint_as_float(h.y << 16),
+                         __uint_as_float(h.y & 0xffff0000u)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = 0;
-      const double p = prob(cp, pp, set, l[i], x0 + i);
-      if (p > 0.0) w[i] = to_fix(fmax(p - prob(cq, pq, set, canonical(lq[i]), x0 + i), 0.0), kResidualUnit);
+      w[i] = wp[i] = 0;
+      const double p = prob(cp, pp, set, l[i], v.id(j, i));
+      if (p > 0.0) {
+        w[i] = wp[i] = to_fix(p, kResidualUnit);
+        if (q) w[i] = to_fix(fmax(p - prob(cq, pq, set, canonical(lq[i]), v.id(j, i)), 0.0), kResidualUnit);
+      }
     }
+  }
+  __device__ void operator()(int j, bool only_p, u64 (&w)[4]) const {
+    float l[4];
+    uint2 h = {0u, 0u};
+    v.load(j, l);
+    if (q) raw_q(j, h);
+    u64 wp[4];
+    weights(j, l, h, w, wp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = only_p ? wp[i] : w[i];
   }
 };
 
@@ -416,11 +435,34 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_shares(FilteredArgs
   const RowView<ElemF32> v(a.logits + (size_t)(base + acc) * a.V, a.V);
   const RowCut cp = a.cut_p[(size_t)r * (g + 1) + acc];
   const int step = (v.nv + gridDim.y - 1) / gridDim.y, j0 = min(v.nv, part * step), j1 = min(v.nv, j0 + step);
-  const int per = (j1 - j0 + kFilterWaves - 1) / kFilterWaves;
-  u64 sum = 0;
-  if (acc < L) sum = sum_shares<4>(Residual(a, v, r, acc, cp, set), j0, j1, per, s);
-  else sum = sum_shares<4>([&](int j, u64 (&w)[4]) { kept_weights(v, cp, set, j, w); }, j0, j1, per, s);
-  if (tid == 0) a.share[(size_t)r * kMaxShares + part] = sum;
+  const Residual f(a, v, r, acc, acc < L, cp, set);
+  // Two vectors of both rows a lane are in flight.
+  u64 sum = 0, sum_p = 0;
+  for (int j = j0 + tid; j < j1; j += 2 * kFilterThreads) {
+    float l[2][4];
+    uint2 h[2] = {{0u, 0u}, {0u, 0u}};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int jj = min(j + u * kFilterThreads, j1 - 1);
+      v.load(jj, l[u]);
+      if (f.q) f.raw_q(jj, h[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (j + u * kFilterThreads < j1) {
+        u64 w[4], wp[4];
+        f.weights(j + u * kFilterThreads, l[u], h[u], w, wp);
+        sum += (w[0] + w[1]) + (w[2] + w[3]);
+        sum_p += (wp[0] + wp[1]) + (wp[2] + wp[3]);
+      }
+    }
+  }
+  sum = block_sum_u64(sum, s);
+  sum_p = block_sum_u64(sum_p, s);
+  if (tid == 0) {
+    a.share[((size_t)r * kMaxShares + part) * 2] = sum;
+    a.share[((size_t)r * kMaxShares + part) * 2 + 1] = sum_p;
+  }
 }
 
 __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a, int shares) {
@@ -434,24 +476,26 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
   const RowView<ElemF32> v(a.logits + (size_t)(base + acc) * a.V, a.V);
   RowCut cp = a.cut_p[(size_t)r * (g + 1) + acc];
   const float u = a.u_resample[(size_t)r * (g + 1) + acc];
-  if (tid < shares) s.share[tid] = a.share[(size_t)r * kMaxShares + tid];
+  u64 w = 0, wp = 0;
+  if ((tid & 63) < shares) {
+    w = a.share[((size_t)r * kMaxShares + (tid & 63)) * 2];
+    wp = a.share[((size_t)r * kMaxShares + (tid & 63)) * 2 + 1];
+  }
+  u64 S = wave_sum_u64(w);
+  const bool only_p = S == 0;        // no residual mass: the target's own distribution
+  if (only_p) {
+    S = wave_sum_u64(wp);
+    w = wp;
+  }
+  if (tid < shares) s.share[tid] = w;
   __syncthreads();
-  u64 S = 0;
-  for (int i = 0; i < shares; ++i) S += s.share[i];
-  const int step = (v.nv + shares - 1) / shares;
-  const bool residual = acc < L;
   int id = -1;
   if (S > 0) {
-    const u64 need = draw_need(u, S);
-    const int at = residual
-        ? draw_in_shares<4>(Residual(a, v, r, acc, cp, set), v.nv, shares, step, need, s)
-        : draw_in_shares<4>([&](int j, u64 (&w)[4]) { kept_weights(v, cp, set, j, w); }, v.nv, shares, step, need, s);
+    if (only_p && tid == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
+    const Residual f(a, v, r, acc, acc < L, cp, set);
+    const int at = draw_in_shares<4>([&](int j, u64 (&x)[4]) { f(j, only_p, x); }, v.nv, shares,
+                                     (v.nv + shares - 1) / shares, draw_need(u, S), s);
     if (at >= 0) id = v.off + at;
-  } else if (cp.n > 0) {
-    // No residual mass: the target's own distribution.
-    if (tid == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
-    float l;
-    id = row_draw(v, cp, set, kModeNone, 0, 0, 0, 0, u, &l, s);
   }
   if (tid == 0) {
     if (id < 0) raise_flag(a.ws, SD_FLAG_EMPTY_ROW);
@@ -474,7 +518,7 @@ struct FilteredLayout {
       : cut_p(sizeof(WsHeader)),
         cut_q(align_up(cut_p + (size_t)B * (gamma + 1) * sizeof(RowCut), 256)),
         share(align_up(cut_q + (size_t)B * gamma * sizeof(RowCut), 256)),
-        team(align_up(share + (size_t)B * kMaxShares * sizeof(u64), 256), B * (2 * gamma + 1), V) {}
+        team(align_up(share + (size_t)B * kMaxShares * 2 * sizeof(u64), 256), B * (2 * gamma + 1), V) {}
 };
 
 }  // namespace
