@@ -188,7 +188,7 @@ struct RowView {
 // no mask. The whole vectors go first, a round's loads issued before the round ahead of it is
 // used; then the row's first and last vector if it holds them and they lie in it in part, an
 // element a lane. N: ids a lane and round.
-template <int N = 16, class E, class F>
+template <int N = 8, class E, class F>
 __device__ __forceinline__ void wave_vecs(const RowView<E> &r, int j0, int j1, F f) {
   const int lane = threadIdx.x & 63;
   j0 = __builtin_amdgcn_readfirstlane(j0);
@@ -245,7 +245,7 @@ __device__ __forceinline__ void wave_vecs(const RowView<E> &r, int j0, int j1, F
 }
 
 // f(value, id) for their ids, canonical values above -inf only.
-template <int N = 16, class E, class F>
+template <int N = 8, class E, class F>
 __device__ __forceinline__ void wave_ids(const RowView<E> &r, int j0, int j1, F f) {
   wave_vecs<N>(r, j0, j1, [&](const float (&v)[E::VE], int id) {
 #pragma unroll
@@ -1054,7 +1054,8 @@ enum RowMode {
   kModeTop,      // at most one id, c.id
   kModeList,     // the words of s.cand[0 .. s.n_cand) from `last` up
   kModeShares,   // s.share, by share of the vectors
-  kModeNone      // not summed yet (c.S unset)
+  kModeNone,     // not summed yet (c.S unset)
+  kModeNarrow    // not cut: the narrowing path's
 };
 
 // Adds the kept listed ids' weights to the shares (of `step` vectors) they lie in.
@@ -1096,6 +1097,7 @@ __device__ __forceinline__ float row_reference(const RowView<E> &r, FilterSmem &
 //      summed by pass (collect_pass).
 //   4. The list is cut (cut_list).
 // totals: only the kept set and its weight are wanted; the bins give the weight above the cut.
+// A row that this leaves to the narrowing path is cut by row_cut_narrowing.
 template <class E>
 __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, bool totals, RowCut &c,
                                            u64 *last, FilterSmem &s) {
@@ -1126,10 +1128,7 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
   const Grid g(kind == kCutSum ? c.m : ref, set.T, kind == kCutCount);
   const CutPlan p = make_plan(set, kind, g, c.m, any, s);
   c.S = 0;
-  if (p.narrow) {
-    cut_narrowing(r, set, c, s);
-    return kModeNone;
-  }
+  if (p.narrow) return kModeNarrow;
   const bool sums = !totals && !p.list;
   __syncthreads();
   if (sums) scale_table(g, c.m, set.unit, s);
@@ -1154,6 +1153,17 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
   if (sums) add_listed(r, set, c, nc, *last, per, s);
   __syncthreads();
   return p.list ? kModeList : sums ? kModeShares : kModeNone;
+}
+
+// The cut of a row that row_cut leaves (c.S unset).
+template <class E>
+__device__ __forceinline__ void row_cut_narrowing(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
+  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves, j0 = min(r.nv, (int)(threadIdx.x >> 6) * per);
+  float m = -INFINITY;
+  wave_ids<4>(r, j0, min(r.nv, j0 + per), [&](float l, int) { m = fmaxf(m, l); });
+  c.m = word_value(block_max_u64(rank_word(m, 0), s));
+  c.S = 0;
+  cut_narrowing(r, set, c, s);
 }
 
 // ------------------------------------------------------------------ the draw

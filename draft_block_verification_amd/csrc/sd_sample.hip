@@ -109,16 +109,35 @@ struct AcceptRows {
 };
 
 // ------------------------------------------------------------------ one workgroup a row
+// todo[row] says whether the row is left to k_rows_narrow: its code would cost the others
+// registers, and with them one workgroup in three on each compute unit.
 template <class Rows>
-__global__ __launch_bounds__(kFilterThreads, 4) void k_rows(Rows rows) {
+__global__ __launch_bounds__(kFilterThreads, 6) void k_rows(Rows rows, uint32_t *todo) {
   __shared__ FilterSmem s;
   const int row = blockIdx.x;
+  if (threadIdx.x == 0) todo[row] = 0;
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     RowCut c;
     u64 last = 0;
     const RowMode mode = row_cut(r, set, Rows::kTotals, c, &last, s);
+    if (mode == kModeNarrow) {
+      if (threadIdx.x == 0) todo[row] = 1;
+      return;
+    }
     const int nc = min((int)s.n_cand, kCandMax);
     rows.finish(row, r, set, c, mode, kFilterWaves, (r.nv + kFilterWaves - 1) / kFilterWaves, nc, last, s);
+  });
+}
+
+template <class Rows>
+__global__ __launch_bounds__(kFilterThreads) void k_rows_narrow(Rows rows, const uint32_t *todo) {
+  __shared__ FilterSmem s;
+  const int row = blockIdx.x;
+  if (!todo[row]) return;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
+    RowCut c;
+    row_cut_narrowing(r, set, c, s);
+    rows.finish(row, r, set, c, kModeNone, 0, 0, 0, 0, s);
   });
 }
 
@@ -177,7 +196,7 @@ struct Part {
 };
 
 template <class Rows>
-__global__ __launch_bounds__(kFilterThreads, 4) void k_team_bins(Rows rows, Team t) {
+__global__ __launch_bounds__(kFilterThreads, 6) void k_team_bins(Rows rows, Team t) {
   __shared__ FilterSmem s;
   const int row = blockIdx.y, tid = threadIdx.x;
   rows.with(row, [&](const auto &r, const RowSettings &set) {
@@ -206,7 +225,7 @@ __global__ __launch_bounds__(kFilterThreads, 4) void k_team_bins(Rows rows, Team
 }
 
 template <class Rows>
-__global__ __launch_bounds__(kFilterThreads, 4) void k_team_collect(Rows rows, Team t) {
+__global__ __launch_bounds__(kFilterThreads, 6) void k_team_collect(Rows rows, Team t) {
   __shared__ FilterSmem s;
   const int row = blockIdx.y, tid = threadIdx.x;
   rows.with(row, [&](const auto &r, const RowSettings &set) {
@@ -287,9 +306,11 @@ int team_size(int rows, int V) {
   return c > V / 4096 ? (V / 4096 < kMaxShares ? V / 4096 : kMaxShares) : (c < kMaxShares ? c : kMaxShares);
 }
 
+// Workspace of the rows: a word each for one workgroup a row, else the team's state.
 struct TeamLayout {
   size_t row, grid, list, share, end;
-  TeamLayout(size_t start, int rows, int V) : row(start), grid(start), list(start), share(start), end(start) {
+  TeamLayout(size_t start, int rows, int V) : row(start), grid(start), list(start), share(start) {
+    end = align_up(start + 4 * (size_t)rows, 256);
     if (team_size(rows, V) < 2) return;
     grid = align_up(row + 128 * (size_t)rows, 256);
     list = grid + (size_t)rows * kGrid * sizeof(u64);
@@ -302,7 +323,11 @@ template <class Rows>
 hipError_t launch_rows(const Rows &rows, int n, int V, char *ws, const TeamLayout &l, hipStream_t stream) {
   const int C = team_size(n, V);
   if (C < 2) {
-    hipLaunchKernelGGL(k_rows<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows);
+    uint32_t *todo = reinterpret_cast<uint32_t *>(ws + l.row);
+    hipLaunchKernelGGL(k_rows<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows, todo);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_rows_narrow<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows, todo);
     return hipGetLastError();
   }
   const Team t{C, reinterpret_cast<TeamRow *>(ws + l.row), reinterpret_cast<u64 *>(ws + l.grid),
