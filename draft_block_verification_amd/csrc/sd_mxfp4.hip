@@ -28,6 +28,7 @@
 namespace sdv {
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -150,14 +151,16 @@ __device__ inline float e2m1_value(uint32_t c) {
   return (c & 8) ? -m : m;
 }
 
-__device__ inline uint16_t f32_to_bf16(float x) {
-  const uint32_t b = __float_as_uint(x);
-  if ((b & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((b >> 16) | 0x40);
-  return (uint16_t)((b + 0x7fffu + ((b >> 16) & 1u)) >> 16);
+// Rounded to nearest even, by the hardware's conversions.
+__device__ inline uint16_t pack16(float x, int32_t type) {
+  return type == SD_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)x) : __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
-__device__ inline uint16_t pack16(float x, int32_t type) {
-  return type == SD_BF16 ? f32_to_bf16(x) : __builtin_bit_cast(uint16_t, (_Float16)x);
+__device__ inline u32x2 pack4(const f32x4 &z, int32_t type) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+  return type == SD_BF16 ? __builtin_bit_cast(u32x2, __builtin_convertvector(z, bf16x4))
+                         : __builtin_bit_cast(u32x2, __builtin_convertvector(z, f16x4));
 }
 
 // x[row][8 c ..] from the codes, eight columns a thread; x is written to column d - 1.
@@ -206,7 +209,7 @@ struct MxGemmArgs {
   void *out;
   int32_t type;
   int64_t ld;               // elements from row to row
-  bool vec;                 // four-element stores allowed
+  bool vec, wide;           // four-element and 16-byte stores allowed
 };
 
 // D += A B^T over 128 columns of MXFP4: lane l holds row l % 16 of each operand at columns
@@ -252,14 +255,13 @@ __device__ inline void store4(const MxGemmArgs &a, int m, int v, const f32x4 &z)
     }
   } else {
     uint16_t *p = reinterpret_cast<uint16_t *>(a.out) + at;
-    uint16_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = pack16(z[i], a.type);
+    const u32x2 h = pack4(z, a.type);
     if (a.vec && v + 4 <= a.V) {
-      *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(h);
+      *reinterpret_cast<u32x2 *>(p) = h;
     } else {
+      const uint32_t w[2] = {h[0], h[1]};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) if (v + i < a.V) p[i] = h[i];
+      for (int i = 0; i < 4; ++i) if (v + i < a.V) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
   }
 }
@@ -380,6 +382,27 @@ __device__ __forceinline__ void mfma_mx_into(int sel_a, int sel_b, const u32x4 &
 
 __device__ __forceinline__ void settle() { asm volatile("s_nop 12"); }
 
+// n rows of W results of type T from a wave's part of LDS (rows ROW bytes apart) to rows m0 .. of
+// the output at column v0: 16 bytes a lane along the rows where they are aligned and whole, else
+// an element a lane.
+template <class T, int W, int ROW>
+__device__ __forceinline__ void store_rows(const MxGemmArgs &a, const LDSP uint8_t *part, int64_t m0, int n, int v0, int lane) {
+  constexpr int E = 16 / sizeof(T), LPR = W / E;     // elements a lane, lanes a row
+  static_assert(64 % LPR == 0, "whole rows a store");
+  const int rows = (int)min((int64_t)n, a.M - m0);
+  T *out = reinterpret_cast<T *>(a.out) + m0 * a.ld + v0;
+  if (a.wide && v0 + W <= a.V) {
+    for (int r = lane / LPR; r < rows; r += 64 / LPR) {
+      const u32x4 x = *(const LDSP u32x4 *)(part + r * ROW + (lane % LPR) * 16);
+      __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(out + r * a.ld + (lane % LPR) * E));
+    }
+  } else {
+    for (int r = 0; r < rows; ++r)
+      for (int v = lane; v < W && v0 + v < a.V; v += 64)
+        out[r * a.ld + v] = *(const LDSP T *)(part + r * ROW + v * (int)sizeof(T));
+  }
+}
+
 // A workgroup of four waves computes 64 GV ids by 64 GM hidden rows, each wave 16 TV by 16 TM
 // (WV by WM waves). A step's 128 columns of both operands come into one of NS LDS buffers by
 // direct loads, NS - 1 steps ahead. While a wave's matrix instructions consume step k from
@@ -477,17 +500,38 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int
     step(k + 1, f1, f0);
   }
   if (k < a.steps) multiply(f0);
-  wait_loads<0>();                     // the trailing loads land before LDS is given up
+  wait_loads<0>();                     // the trailing loads land before LDS is used again
+  raw_barrier();
+  // The results cross LDS so that a wave's stores run along the rows: out of the accumulators
+  // a store would touch 16 rows with 32 or 64 bytes each. Each wave has a part of LDS to
+  // itself, rows 16 bytes apart from a power of two so that neighbouring rows start on other
+  // banks; 16-bit results cross at once, 32-bit ones in two halves of the rows.
   const int col = lane & 15, blk = lane >> 4;
+  const int64_t m0 = (int64_t)mt * 64 * GM + wm * TM * 16;
+  const int v0 = vt * 64 * GV + wv * TV * 16;
+  constexpr int PART = NS * STAGE / 4 / 16 * 16;
+  LDSP uint8_t *part = (LDSP uint8_t *)S + wave * PART;
+  if (a.type == SD_F32) {
+    constexpr int ROW = TV * 16 * 4 + 16;
+    static_assert(ROW * TM * 8 <= PART, "half the rows in fp32");
 #pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    const int mm = mt * 64 * GM + (wm * TM + m) * 16 + col;
-    if (mm >= a.M) continue;
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-    for (int i = 0; i < TV; ++i) {
-      const int v = vt * 64 * GV + (wv * TV + i) * 16 + 4 * blk;
-      if (v < a.V) store4(a, mm, v, acc[i][m]);
+      for (int m = 0; m < TM / 2; ++m)
+#pragma unroll
+        for (int i = 0; i < TV; ++i)
+          *(LDSP f32x4 *)(part + (16 * m + col) * ROW + (16 * i + 4 * blk) * 4) = acc[i][half * TM / 2 + m];
+      store_rows<float, TV * 16, ROW>(a, part, m0 + half * TM * 8, TM * 8, v0, lane);
     }
+  } else {
+    constexpr int ROW = TV * 16 * 2 + 16;
+    static_assert(ROW * TM * 16 <= PART, "the rows in 16 bits");
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int i = 0; i < TV; ++i)
+        *(LDSP u32x2 *)(part + (16 * m + col) * ROW + (16 * i + 4 * blk) * 2) = pack4(acc[i][m], a.type);
+    store_rows<uint16_t, TV * 16, ROW>(a, part, m0, TM * 16, v0, lane);
   }
 }
 
@@ -555,7 +599,7 @@ hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int 
   hipError_t e = launch_mx_quantize(hidden, hidden_type, M, d, stride, h, h + hs, true, stream);
   if (e != hipSuccess) return e;
   const MxGemmArgs a{h, h + hs, head, head + ws, M, V, mx_padded(d) / 128, logits, type, ld,
-                     vec_rows(logits, type, ld, 4)};
+                     vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8)};
   if (M <= 64) {
     auto *k = M <= 16 ? &k_mx_skinny<1> : M <= 32 ? &k_mx_skinny<2> : &k_mx_skinny<4>;
     hipLaunchKernelGGL(k, dim3((V + 63) / 64), dim3(256), 0, stream, a);
