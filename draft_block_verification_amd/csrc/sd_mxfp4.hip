@@ -20,6 +20,8 @@
 // four fragments share the word, and the instruction's operand selects the byte.
 //   codes  [ceil(rows / 64)][kp / 128][4][64 lanes][16 bytes], then
 //   scales [ceil(rows / 64)][kp / 128][64 lanes][4 bytes]
+#include <utility>
+
 #include "sd_launch.h"
 
 #define LDSP __attribute__((address_space(3)))
@@ -341,6 +343,16 @@ __device__ inline void raw_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// f(0), f(1), .. f(N - 1) with each number a constant.
+template <class F, int... I>
+__device__ __forceinline__ void each_impl(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+  each_impl(f, std::make_integer_sequence<int, N>{});
+}
+
 // At most N of this wave's memory reads pending, no LDS read.
 template <int N>
 __device__ inline void wait_loads() {
@@ -355,7 +367,7 @@ __device__ inline void wait_loads() {
 #define SD_MX_INTO(SA0, SA1, SB0, SB1)                                                         \
   asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" #SA0       \
       "," #SB0 ",0] op_sel_hi:[" #SA1 "," #SB1 ",0] cbsz:4 blgp:4"                              \
-      : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb))
+      : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb) : "memory")
 
 __device__ __forceinline__ void mfma_mx_into(int sel_a, int sel_b, const u32x4 &a, int sa, const u32x4 &b, int sb,
                                              f32x4 &c) {
@@ -417,7 +429,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int
   constexpr int DPT = G + SPW;                // loads a wave and step
   static_assert(WV * WM == 4 && TV % 4 == 0 && TM % 4 == 0, "whole 64-row groups a wave");
   __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wv = wave / WM, wm = wave % WM;
   // Tiles go to the XCDs (workgroup id mod 8) in contiguous runs with the hidden tile
   // running fastest: an XCD's workgroups share LM-head tiles and hidden tiles in its L2.
@@ -425,81 +437,87 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int
   const int per = nb / 8, rem = nb % 8, xcd = hb % 8, pos = hb / 8;
   const int logical = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + pos;
   const int mt = logical % n_mt, vt = logical / n_mt;
-  // Source of each of this wave's loads at step 0; a step further is 4096 (codes) or 256
-  // (scales) bytes. Groups past the end repeat the last one; their results are not stored.
+  // Source of each of this wave's loads at step 0, the same address for all lanes; a step
+  // further is 4096 (codes) or 256 (scales) bytes. Groups past the end repeat the last one;
+  // their results are not stored.
   const int last_v = (a.V - 1) / 64, last_m = (a.M - 1) / 64;
   auto group = [&](int i, const uint8_t *w, const uint8_t *h, int64_t bytes) {
     return i < GV ? w + (int64_t)min(vt * GV + i, last_v) * a.steps * bytes
                   : h + (int64_t)min(mt * GM + i - GV, last_m) * a.steps * bytes;
   };
-  const uint8_t *src[G], *ssrc[SPW];
+  const uint8_t *src[DPT];
 #pragma unroll
-  for (int i = 0; i < G; ++i) src[i] = group(i, a.wc, a.hc, 4096) + wave * 1024 + lane * 16;
+  for (int i = 0; i < G; ++i) src[i] = group(i, a.wc, a.hc, 4096) + wave * 1024;
 #pragma unroll
-  for (int i = 0; i < SPW; ++i) ssrc[i] = group(min(wave + 4 * i, G - 1), a.ws, a.hs, 256) + lane * 4;
-  auto issue = [&](int k) {
-    const int64_t kk = min(k, a.steps - 1);        // past the end: the last step again, unused
+  for (int i = 0; i < SPW; ++i) src[G + i] = group(min(wave + 4 * i, G - 1), a.ws, a.hs, 256);
+  const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+  // Load i of the DPT that bring step k in; kk: the step itself, or the last one past the end.
+  auto issue = [&](int k, int kk, int i) __attribute__((always_inline)) {
     LDSP uint8_t *dst = (LDSP uint8_t *)S + (k % NS) * STAGE;
-#pragma unroll
-    for (int i = 0; i < G; ++i)
-      __builtin_amdgcn_global_load_lds((const GLBP void *)(src[i] + kk * 4096),
+    if (i < G)
+      __builtin_amdgcn_global_load_lds((const GLBP void *)(src[i] + (int64_t)kk * 4096 + lane16),
                                        (LDSP void *)(dst + i * 4096 + wave * 1024), 16, 0, 0);
-#pragma unroll
-    for (int i = 0; i < SPW; ++i)
-      __builtin_amdgcn_global_load_lds((const GLBP void *)(ssrc[i] + kk * 256),
-                                       (LDSP void *)(dst + G * 4096 + min(wave + 4 * i, G - 1) * 256), 4, 0, 0);
+    else
+      __builtin_amdgcn_global_load_lds((const GLBP void *)(src[i] + (int64_t)kk * 256 + lane4),
+                                       (LDSP void *)(dst + G * 4096 + min(wave + 4 * (i - G), G - 1) * 256), 4, 0, 0);
   };
   struct Frags {
     u32x4 w[TV], h[TM];
     int sw[TV / 4], sh[TM / 4];
   };
-  auto fetch = [&](int k, Frags &f) {
+  // Read j of the FETCHES that take a step's fragments out of LDS.
+  constexpr int FETCHES = TV + TM + TV / 4 + TM / 4;
+  auto fetch = [&](int k, int j, Frags &f) __attribute__((always_inline)) {
     const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE;
-    const LDSP uint8_t *wb = b + wv * TV * 1024 + lane * 16;
-    const LDSP uint8_t *hb = b + GV * 4096 + wm * TM * 1024 + lane * 16;
-    const LDSP uint8_t *sb = b + G * 4096 + lane * 4;
-#pragma unroll
-    for (int i = 0; i < TV / 4; ++i) f.sw[i] = *(const LDSP int *)(sb + (wv * TV / 4 + i) * 256);
-#pragma unroll
-    for (int i = 0; i < TM / 4; ++i) f.sh[i] = *(const LDSP int *)(sb + (GV + wm * TM / 4 + i) * 256);
-#pragma unroll
-    for (int i = 0; i < TV; ++i) f.w[i] = *(const LDSP u32x4 *)(wb + i * 1024);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) f.h[i] = *(const LDSP u32x4 *)(hb + i * 1024);
+    const LDSP uint8_t *sb = b + G * 4096 + lane4;
+    if (j < TV / 4) f.sw[j] = *(const LDSP int *)(sb + (wv * TV / 4 + j) * 256);
+    else if (j < TV / 4 + TM / 4) f.sh[j - TV / 4] = *(const LDSP int *)(sb + (GV + wm * TM / 4 + j - TV / 4) * 256);
+    else if ((j -= TV / 4 + TM / 4) < TM) f.h[j] = *(const LDSP u32x4 *)(b + GV * 4096 + wm * TM * 1024 + lane16 + j * 1024);
+    else f.w[j - TM] = *(const LDSP u32x4 *)(b + wv * TV * 1024 + lane16 + (j - TM) * 1024);
   };
   f32x4 acc[TV][TM];
 #pragma unroll
   for (int i = 0; i < TV; ++i)
 #pragma unroll
     for (int m = 0; m < TM; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const Frags &f) {
-#pragma unroll
-    for (int i = 0; i < TV; ++i)
-#pragma unroll
-      for (int m = 0; m < TM; ++m)
-        mfma_mx_into(i % 4, m % 4, f.w[i], f.sw[i / 4], f.h[m], f.sh[m / 4], acc[i][m]);
-    settle();
-  };
-  // Step k: its fragments are in `now`; the next step's go to `next`.
-  auto step = [&](int k, const Frags &now, Frags &next) {
+  // Step k: its fragments are in `now`; the next step's go to `next`. The reads and loads
+  // stand between the matrix instructions, where they are written: all at once, they would
+  // fill their queues and hold up the instructions behind them.
+  constexpr int MM = TV * TM;
+  static_assert(FETCHES <= MM && DPT <= MM, "at most one of each before a matrix instruction");
+  auto step = [&](int k, const Frags &now, Frags &next) __attribute__((always_inline)) {
     wait_loads<(NS - 2) * DPT>();      // step k + 1 has arrived
     raw_barrier();
-    issue(k + NS);
-    fetch(k + 1, next);
-    multiply(now);
+    const int kk = min(k + NS, a.steps - 1);
+    each<MM>([&](auto x) __attribute__((always_inline)) {
+      if constexpr (x * FETCHES % MM < FETCHES) fetch(k + 1, x * FETCHES / MM, next);
+      if constexpr (x * DPT % MM < DPT) issue(k + NS, kk, x * DPT / MM);
+      constexpr int i = x / TM, m = x % TM;
+      mfma_mx_into(i % 4, m % 4, now.w[i], now.sw[i / 4], now.h[m], now.sh[m / 4], acc[i][m]);
+    });
+    settle();
   };
 #pragma unroll
-  for (int k = 0; k < NS; ++k) issue(k);
+  for (int k = 0; k < NS; ++k)
+#pragma unroll
+    for (int i = 0; i < DPT; ++i) issue(k, min(k, a.steps - 1), i);
   wait_loads<(NS - 1) * DPT>();
   raw_barrier();
   Frags f0, f1;
-  fetch(0, f0);
+#pragma unroll
+  for (int j = 0; j < FETCHES; ++j) fetch(0, j, f0);
   int k = 0;
   for (; k + 1 < a.steps; k += 2) {
     step(k, f0, f1);
     step(k + 1, f1, f0);
   }
-  if (k < a.steps) multiply(f0);
+  if (k < a.steps) {
+    each<MM>([&](auto x) __attribute__((always_inline)) {
+      constexpr int i = x / TM, m = x % TM;
+      mfma_mx_into(i % 4, m % 4, f0.w[i], f0.sw[i / 4], f0.h[m], f0.sh[m / 4], acc[i][m]);
+    });
+    settle();
+  }
   wait_loads<0>();                     // the trailing loads land before LDS is used again
   raw_barrier();
   // The results cross LDS so that a wave's stores run along the rows: out of the accumulators
