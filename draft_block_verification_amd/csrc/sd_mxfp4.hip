@@ -273,7 +273,10 @@ __device__ inline void store4(const MxGemmArgs &a, int m, int v, const f32x4 &z)
 // waves take the 128-column steps in turn (wave w steps w, w + 4, ..), so a workgroup reads
 // one contiguous 17 KB run a round, straight into registers: each weight is used by one wave
 // only, so LDS would add a copy and share nothing. The hidden fragments are read by every
-// workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
+// workgroup and come from L2: at 64 rows as many bytes as weights, and slower than a tile
+// through LDS (129280 x 7168: 108 against 91 us; at 32 rows 86 against 89). The waves'
+// partial sums meet in LDS in wave order. 129280 x 7168 under 16 rows: 64 us where the head
+// is partly in the memory-side cache (repeated calls), 78 us = 6.3 TB/s from memory.
 template <int MT>
 __global__ __launch_bounds__(256) void k_mx_skinny(MxGemmArgs a) {
   constexpr int D = 3;                 // steps a wave has in flight
@@ -420,7 +423,10 @@ __device__ __forceinline__ void store_rows(const MxGemmArgs &a, const LDSP uint8
 // direct loads, NS - 1 steps ahead. While a wave's matrix instructions consume step k from
 // registers it reads step k + 1's fragments from LDS, so with one wave a SIMD the matrix
 // units still run back to back. One barrier a step: behind it every wave has read step k
-// out of LDS, so its buffer takes step k + NS.
+// out of LDS, so its buffer takes step k + NS. 256 x 256 tiles are bound by the matrix
+// instructions (their operands feed 128 products a byte): 2048 rows by 129280 ids at depth
+// 7168 take 1086 us (3.5 PFLOP/s; 4.1 at 32768 ids and depth 8192), 835 us of it the
+// instructions alone, which random operands slow to 6.2 - 7 PFLOP/s at the card's power.
 template <int WV, int WM, int TV, int TM, int NS>
 __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int n_vt) {
   constexpr int GV = WV * TV / 4, GM = WM * TM / 4, G = GV + GM;
@@ -563,6 +569,12 @@ hipError_t launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Rounds over 256 CUs of the workgroups of a tiling.
+double rounds(int M, int V, int ids, int rows) {
+  const int64_t n = (int64_t)((V + ids - 1) / ids) * ((M + rows - 1) / rows);
+  return (double)((n + 255) / 256);
+}
+
 bool vec_rows(const void *x, int32_t type, int64_t stride, int elems) {
   const int64_t size = type == SD_F32 ? 4 : 2, bytes = size * elems;
   return reinterpret_cast<uintptr_t>(x) % bytes == 0 && stride * size % bytes == 0;
@@ -618,13 +630,28 @@ hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int 
   if (e != hipSuccess) return e;
   const MxGemmArgs a{h, h + hs, head, head + ws, M, V, mx_padded(d) / 128, logits, type, ld,
                      vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8)};
-  if (M <= 64) {
-    auto *k = M <= 16 ? &k_mx_skinny<1> : M <= 32 ? &k_mx_skinny<2> : &k_mx_skinny<4>;
+  if (M <= 32) {
+    auto *k = M <= 16 ? &k_mx_skinny<1> : &k_mx_skinny<2>;
     hipLaunchKernelGGL(k, dim3((V + 63) / 64), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  if (M <= 128) return launch_tiled<2, 2, 8, 4, 4>(a, stream);
-  return launch_tiled<2, 2, 8, 8, 4>(a, stream);
+  // The tiling whose rounds over the 256 CUs cost least. Costs are times of a round at
+  // depth 7168 relative to 256 x 256 (61 us), from calls of many rounds; the 64-row and the
+  // 128 x 128 tilings run two workgroups a CU, at half a round each; 64 rows are for calls
+  // of no more, as every 64 rows would read the LM head again. Measured (us, ids x rows
+  // of a tile 256 x 256 / 256 x 128 / 128 x 128 / 256 x 64), V x depth, M:
+  //   129280 x 7168:  64: - / 95 / 97 / 91      128: 129 / 97 / 107 / -    300: 233 / 215 / 216 / -
+  //                  512: 245 / 285 / 295 / -
+  //    32000 x 4096: 128: 36 / 26 / 23 / -      256: 36 / 29 / 33 / -      512: 43 / 49 / 53 / -
+  //   151936 x 4096:  64: - / 78 / 68 / 68      128: 113 / 81 / 76 / -     512: 197 / 218 / 214 / -
+  const double cost[4] = {rounds(M, V, 256, 256), 0.58 * rounds(M, V, 256, 128), 0.32 * rounds(M, V, 128, 128),
+                          0.33 * rounds(M, V, 256, 64)};
+  int best = 0;
+  for (int i = 1; i < (M <= 64 ? 4 : 3); ++i) if (cost[i] < cost[best]) best = i;
+  if (best == 0) return launch_tiled<2, 2, 8, 8, 4>(a, stream);
+  if (best == 1) return launch_tiled<2, 2, 8, 4, 4>(a, stream);
+  if (best == 2) return launch_tiled<2, 2, 4, 4, 4>(a, stream);
+  return launch_tiled<4, 1, 4, 4, 3>(a, stream);
 }
 
 }  // namespace sdv

@@ -120,6 +120,15 @@ def test_logits(M, V, d, out):
     assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
 
 
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("M,V,d", [(40, 70001, 136), (64, 65600, 256), (130, 32000, 264), (100, 65700, 128),
+                                   (500, 32001, 256), (257, 40000, 384), (33, 300, 640), (1030, 140, 128)])
+def test_logits_many_ids(M, V, d, out):
+    """Sizes at which every tiling is taken, whole and cut at both edges."""
+    got, want, tol = logits_case(M, V, d, torch.bfloat16, out, 3)
+    assert bool(((got - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
 @pytest.mark.parametrize("M", [1, 20, 140])
 def test_logits_hidden_types(M, dtype):
