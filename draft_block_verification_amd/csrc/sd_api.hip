@@ -584,7 +584,7 @@ int32_t sd_mxfp4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d
   const int32_t st = check_mx(x, x_type, rows, d, x_stride, codes, scales);
   if (st != SD_OK) return st;
   return launch_status(launch_mx_quantize(x, x_type, rows, d, x_stride, codes, scales,
-                                          false, (hipStream_t)stream));
+                                          (hipStream_t)stream));
 }
 
 int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t d,

@@ -87,9 +87,9 @@ hipError_t launch_accept_rejection(const float *logits, const sd_row_stats *stat
 // MXFP4 rows: columns padded to one matrix instruction's depth.
 constexpr int mx_padded(int d) { return (d + 127) / 128 * 128; }
 
-// Codes and scales by row, or (tiled) in the product's tiles.
+// Codes and scales by row.
 hipError_t launch_mx_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride,
-                              uint8_t *codes, uint8_t *scales, bool tiled, hipStream_t stream);
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int d,
                                 void *x, int32_t type, int64_t stride, hipStream_t stream);
 // Bytes of the tiled form of [rows][d]; *scales: where its scales start.

@@ -32,40 +32,86 @@ namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// Eight consecutive values of a row as fp32, 0 past `left` of them. vec: 16-byte loads allowed.
-__device__ inline void load8(const void *x, int32_t type, int64_t at, int left, bool vec, float (&v)[8]) {
-  if (type == SD_F32) {
+// Eight consecutive values of a row as they are stored, 0 past `left` of them. vec: 16-byte
+// loads allowed.
+template <int T> struct Raw8 { u32x4 w; };
+template <> struct Raw8<SD_F32> { f32x4 a, b; };
+
+template <int T>
+__device__ __forceinline__ Raw8<T> load8(const void *x, int64_t at, int left, bool vec) {
+  Raw8<T> r;
+  if constexpr (T == SD_F32) {
     const float *p = reinterpret_cast<const float *>(x) + at;
     if (vec && left >= 8) {
-      const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+      r.a = *reinterpret_cast<const f32x4 *>(p);
+      r.b = *reinterpret_cast<const f32x4 *>(p + 4);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.f;
+      for (int i = 0; i < 4; ++i) { r.a[i] = i < left ? p[i] : 0.f; r.b[i] = 4 + i < left ? p[4 + i] : 0.f; }
     }
   } else {
     const uint16_t *p = reinterpret_cast<const uint16_t *>(x) + at;
-    uint16_t h[8];
     if (vec && left >= 8) {
-      *reinterpret_cast<u32x4 *>(h) = *reinterpret_cast<const u32x4 *>(p);
+      r.w = *reinterpret_cast<const u32x4 *>(p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = i < left ? p[i] : (uint16_t)0;
+      for (int i = 0; i < 4; ++i)
+        r.w[i] = (2 * i < left ? p[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)p[2 * i + 1] << 16 : 0u);
     }
+  }
+  return r;
+}
+
+// The bits as fp32 of the largest of the eight magnitudes; as integers magnitudes order like
+// the values, infinity and NaN on top.
+template <int T>
+__device__ __forceinline__ uint32_t top8(const Raw8<T> &r) {
+  if constexpr (T == SD_F32) {
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = type == SD_BF16 ? bf16_to_f32(h[i]) : (float)__builtin_bit_cast(_Float16, h[i]);
+    for (int i = 0; i < 4; ++i)
+      top = max(top, max(__float_as_uint(r.a[i]) & 0x7fffffffu, __float_as_uint(r.b[i]) & 0x7fffffffu));
+    return top;
+  } else {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(r.w[i] & 0x7fffu, (r.w[i] >> 16) & 0x7fffu));
+    if (T == SD_BF16) return top << 16;
+    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)top));
   }
 }
 
-// Code of x / 2^e (y = |x| / 2^e): the borders between neighbouring magnitudes lie midway,
-// and a value on a border goes to the even code.
-__device__ inline uint32_t e2m1(float x, float y) {
-  uint32_t c = (y > 0.25f) + (y >= 0.75f) + (y > 1.25f) + (y >= 1.75f) + (y > 2.5f) + (y >= 3.5f) + (y > 5.f);
-  return c | ((__float_as_uint(x) >> 31) << 3);
+// By value: a bit cast of a vector's element itself would take the first one.
+template <class P>
+__device__ __forceinline__ P pair(uint32_t w) { return __builtin_bit_cast(P, w); }
+
+// The eight codes, by the hardware's conversions: x / scale rounded to nearest, ties to the
+// even code, magnitudes over 6 to 6, for every scale from 2^-127 on and with denormals (each
+// 16-bit pattern and its scales tried against the rule, fp32 at the patterns around ties).
+template <int T>
+__device__ __forceinline__ uint32_t codes8(const Raw8<T> &r, float scale) {
+  uint32_t w = 0;
+  if constexpr (T == SD_F32) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.a[0], r.a[1], scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.a[2], r.a[3], scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.b[0], r.b[1], scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.b[2], r.b[3], scale, 3);
+  } else if constexpr (T == SD_BF16) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair<bf16x2>(r.w[0]), scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair<bf16x2>(r.w[1]), scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair<bf16x2>(r.w[2]), scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair<bf16x2>(r.w[3]), scale, 3);
+  } else {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, pair<f16x2>(r.w[0]), scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, pair<f16x2>(r.w[1]), scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, pair<f16x2>(r.w[2]), scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, pair<f16x2>(r.w[3]), scale, 3);
+  }
+  return w;
 }
 
 struct MxArgs {
@@ -74,57 +120,82 @@ struct MxArgs {
   int64_t rows, stride;    // elements from row to row
   int d, kp;
   bool vec;
-  bool tiled;              // codes and scales in tiles
   uint8_t *codes, *scales;
 };
 
-// Byte offsets in the tiled form of row `row`'s eight columns 8 c .. (codes) and of the scale
-// of their block.
-__device__ inline int64_t tiled_codes(int64_t row, int c, int steps) {
-  const int64_t tile = (row >> 6) * steps + (c >> 4);
-  return tile * 4096 + ((row >> 4) & 3) * 1024 + (((c >> 2) & 3) * 16 + (row & 15)) * 16 + (c & 3) * 4;
+// Scale byte (e + 127) of a block from its four threads' magnitudes, 255 for one that is not
+// finite; an all-zero block has 0, padding among them. word: the thread's eight codes.
+template <int T>
+__device__ __forceinline__ int quantize_block(const Raw8<T> &r, uint32_t &word) {
+  uint32_t top = top8<T>(r);
+  top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xb1, 0xf, 0xf, true));   // lane ^ 1
+  top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4e, 0xf, 0xf, true));   // lane ^ 2
+  const int field = (int)(top >> 23);          // floor(log2) + 127 of a normal number
+  const int byte = max(field - 2, 0);
+  word = field == 255 ? 0u : codes8<T>(r, __uint_as_float((uint32_t)byte << 23));
+  return field == 255 ? 255 : byte;
 }
 
-__device__ inline int64_t tiled_scale(int64_t row, int c, int steps) {
-  const int64_t tile = (row >> 6) * steps + (c >> 4);
-  return tile * 256 + (((c >> 2) & 3) * 16 + (row & 15)) * 4 + ((row >> 4) & 3);
+// Row and column group of item n: base (row, c) of the workgroup's first item, `per` a row.
+struct Item { int64_t row; int c; };
+__device__ __forceinline__ Item item_at(int64_t row0, int c0, int n, int per) {
+  const unsigned at = c0 + n, q = at / (unsigned)per;
+  return {row0 + q, (int)(at - q * per)};
 }
 
-// Eight columns a thread, four neighbouring threads a block: its largest magnitude comes
-// from two lane exchanges.
+// An item is eight columns; four neighbouring threads hold a block, whose largest magnitude
+// comes from two lane exchanges. A thread takes U items 256 apart, its loads issued together.
+template <int T, int U>
 __global__ __launch_bounds__(256) void k_mx_quantize(MxArgs a) {
-  const int per = a.kp / 8;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = t / per;
-  if (row >= a.rows) return;      // whole groups of four threads: per is a multiple of 16
-  const int c = (int)(t - row * per);
-  float v[8];
-  const int left = a.d - 8 * c;
-  if (left > 0) {
-    load8(a.x, a.type, row * a.stride + 8 * c, left, a.vec, v);
-  } else {
+  const int per = a.kp / 8;       // a multiple of 16: a block's items are all in or all out
+  const int64_t base = (int64_t)blockIdx.x * 256 * U, row0 = base / per;
+  const int c0 = (int)(base - row0 * per);
+  Item it[U];
+  Raw8<T> r[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  for (int u = 0; u < U; ++u) {
+    it[u] = item_at(row0, c0, threadIdx.x + 256 * u, per);
+    const int left = it[u].row < a.rows ? a.d - 8 * it[u].c : 0;
+    r[u] = Raw8<T>{};
+    if (left > 0) r[u] = load8<T>(a.x, it[u].row * a.stride + 8 * it[u].c, left, a.vec);
   }
-  // As integers the magnitudes order like the values, NaN and infinity on top.
-  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-  const int field = (int)(top >> 23);            // floor(log2) + 127 of a normal number
-  const bool bad = field == 255;
-  const int e = max(field - 127 - 2, -127);
-  uint32_t word = 0;
+  for (int u = 0; u < U; ++u) {
+    uint32_t word;
+    const int byte = quantize_block<T>(r[u], word);
+    const int64_t row = it[u].row;
+    const int c = it[u].c;
+    if (row >= a.rows) continue;
+    *reinterpret_cast<uint32_t *>(a.codes + row * (a.kp / 2) + 4 * c) = word;
+    if ((c & 3) == 0) a.scales[row * (a.kp / 32) + c / 4] = (uint8_t)byte;
+  }
+}
+
+// Rows quantised straight into tiles, one workgroup a tile: a wave takes 16 rows, four threads
+// a block, and its four blocks in turn, so that each store of the wave is a whole quarter of
+// its fragment. Rows past the last are left: their products are not stored.
+template <int T>
+__global__ __launch_bounds__(256) void k_mx_quantize_tiles(MxArgs a) {
+  const int steps = a.kp / 128, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t tile = blockIdx.x;
+  const int64_t group = tile / steps;
+  const int step = (int)(tile - group * steps), row16 = lane >> 2;
+  const int64_t row = 64 * group + 16 * wave + row16;
+  Raw8<T> r[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) word |= e2m1(v[i], ldexpf(fabsf(v[i]), -e)) << (4 * i);
-  if (bad) word = 0;
-  const int steps = a.kp / 128;
-  *reinterpret_cast<uint32_t *>(a.codes + (a.tiled ? tiled_codes(row, c, steps) : row * (a.kp / 2) + 4 * c)) = word;
-  // Padding keeps scale byte 0.
-  if ((c & 3) == 0)
-    a.scales[a.tiled ? tiled_scale(row, c, steps) : row * (a.kp / 32) + c / 4] =
-        bad ? 255 : (left > 0 ? (uint8_t)(e + 127) : 0);
+  for (int u = 0; u < 4; ++u) {
+    const int c = 128 * step + 32 * u + 8 * (lane & 3), left = row < a.rows ? a.d - c : 0;
+    r[u] = Raw8<T>{};
+    if (left > 0) r[u] = load8<T>(a.x, row * a.stride + c, left, a.vec);
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t word;
+    const int byte = quantize_block<T>(r[u], word);
+    if (row >= a.rows) continue;
+    *reinterpret_cast<uint32_t *>(a.codes + tile * 4096 + wave * 1024 + (16 * u + row16) * 16 + (lane & 3) * 4) = word;
+    if ((lane & 3) == 0) a.scales[tile * 256 + (16 * u + row16) * 4 + wave] = (uint8_t)byte;
+  }
 }
 
 // The tiled form of codes and scales stored by row: one workgroup a tile, thread t moves the
@@ -146,18 +217,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const uint8_t *codes, const uin
   out_scales[tile * 256 + lane * 4 + (t >> 6)] = s;
 }
 
-__device__ inline float e2m1_value(uint32_t c) {
-  // Magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 in halves: 0 1 2 3 4 6 8 12.
-  const uint32_t h = (0xc8643210u >> (4 * (c & 7))) & 15u;
-  const float m = 0.5f * (float)h;
-  return (c & 8) ? -m : m;
-}
-
 // Rounded to nearest even, by the hardware's conversions.
-__device__ inline uint16_t pack16(float x, int32_t type) {
-  return type == SD_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)x) : __builtin_bit_cast(uint16_t, (_Float16)x);
-}
-
 __device__ inline u32x2 pack4(const f32x4 &z, int32_t type) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -165,40 +225,55 @@ __device__ inline u32x2 pack4(const f32x4 &z, int32_t type) {
                          : __builtin_bit_cast(u32x2, __builtin_convertvector(z, f16x4));
 }
 
-// x[row][8 c ..] from the codes, eight columns a thread; x is written to column d - 1.
+// x[row][8 c ..] from the codes; x is written to column d - 1. Items as in k_mx_quantize.
+// The hardware's conversion gives the fp32 value of code and scale exactly (each pair tried).
+template <int T, int U>
 __global__ __launch_bounds__(256) void k_mx_dequantize(MxArgs a, void *x) {
   const int per = (a.d + 7) / 8;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = t / per;
-  if (row >= a.rows) return;
-  const int c = (int)(t - row * per), left = a.d - 8 * c;
-  const uint32_t word = *reinterpret_cast<const uint32_t *>(a.codes + row * (a.kp / 2) + 4 * c);
-  const int s = a.scales[row * (a.kp / 32) + c / 4];
-  float v[8];
+  const int64_t base = (int64_t)blockIdx.x * 256 * U, row0 = base / per;
+  const int c0 = (int)(base - row0 * per);
+  Item it[U];
+  uint32_t word[U];
+  int s[U];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = s == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(e2m1_value((word >> (4 * i)) & 15u), s - 127);
-  }
-  const int64_t at = row * a.stride + 8 * c;
-  if (a.type == SD_F32) {
-    float *p = reinterpret_cast<float *>(x) + at;
-    if (a.vec && left >= 8) {
-      *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) if (i < left) p[i] = v[i];
+  for (int u = 0; u < U; ++u) {
+    it[u] = item_at(row0, c0, threadIdx.x + 256 * u, per);
+    if (it[u].row < a.rows) {
+      word[u] = *reinterpret_cast<const uint32_t *>(a.codes + it[u].row * (a.kp / 2) + 4 * it[u].c);
+      s[u] = a.scales[it[u].row * (a.kp / 32) + it[u].c / 4];
     }
-  } else {
-    uint16_t *p = reinterpret_cast<uint16_t *>(x) + at;
-    uint16_t h[8];
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = pack16(v[i], a.type);
-    if (a.vec && left >= 8) {
-      *reinterpret_cast<u32x4 *>(p) = *reinterpret_cast<u32x4 *>(h);
+  for (int u = 0; u < U; ++u) {
+    if (it[u].row >= a.rows) continue;
+    const float scale = __uint_as_float((uint32_t)s[u] << 23);
+    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word[u], scale, 0);
+    const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word[u], scale, 1);
+    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word[u], scale, 2);
+    const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word[u], scale, 3);
+    f32x4 lo = {p0[0], p0[1], p1[0], p1[1]}, hi = {p2[0], p2[1], p3[0], p3[1]};
+    if (s[u] == 255) lo = hi = f32x4{1.f, 1.f, 1.f, 1.f} * __uint_as_float(0x7fc00000u);
+    const int64_t at = it[u].row * a.stride + 8 * it[u].c;
+    const int left = a.d - 8 * it[u].c;
+    if constexpr (T == SD_F32) {
+      float *p = reinterpret_cast<float *>(x) + at;
+      if (a.vec && left >= 8) {
+        *reinterpret_cast<f32x4 *>(p) = lo;
+        *reinterpret_cast<f32x4 *>(p + 4) = hi;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) if (i < left) p[i] = i < 4 ? lo[i] : hi[i - 4];
+      }
     } else {
+      uint16_t *p = reinterpret_cast<uint16_t *>(x) + at;
+      const u32x2 a2 = pack4(lo, T), b2 = pack4(hi, T);
+      const u32x4 h = {a2[0], a2[1], b2[0], b2[1]};
+      if (a.vec && left >= 8) {
+        *reinterpret_cast<u32x4 *>(p) = h;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) if (i < left) p[i] = h[i];
+        for (int i = 0; i < 8; ++i) if (i < left) p[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
+      }
     }
   }
 }
@@ -559,7 +634,23 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int
   }
 }
 
-int64_t blocks_of(int64_t threads) { return (threads + 255) / 256; }
+template <class F>
+void by_type(int32_t type, F f) {
+  if (type == SD_F32) f(std::integral_constant<int, SD_F32>{});
+  else if (type == SD_BF16) f(std::integral_constant<int, SD_BF16>{});
+  else f(std::integral_constant<int, SD_F16>{});
+}
+
+// launch(type, items a thread, grid) for items of eight columns: four a thread where that
+// still gives every CU several workgroups.
+template <class F>
+hipError_t by_items(int32_t type, int64_t items, F launch) {
+  by_type(type, [&](auto T) {
+    if (items >= 1 << 20) launch(T, std::integral_constant<int, 4>{}, dim3((unsigned)((items + 1023) / 1024)));
+    else launch(T, std::integral_constant<int, 1>{}, dim3((unsigned)((items + 255) / 256)));
+  });
+  return hipGetLastError();
+}
 
 template <int WV, int WM, int TV, int TM, int NS>
 hipError_t launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
@@ -583,21 +674,22 @@ bool vec_rows(const void *x, int32_t type, int64_t stride, int elems) {
 }  // namespace
 
 hipError_t launch_mx_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride,
-                              uint8_t *codes, uint8_t *scales, bool tiled, hipStream_t stream) {
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream) {
   const bool vec = vec_rows(x, type, stride, type == SD_F32 ? 4 : 8);
-  const MxArgs a{x, type, rows, stride, d, mx_padded(d), vec, tiled, codes, scales};
-  hipLaunchKernelGGL(k_mx_quantize, dim3((unsigned)blocks_of(rows * (a.kp / 8))), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  const MxArgs a{x, type, rows, stride, d, mx_padded(d), vec, codes, scales};
+  return by_items(type, rows * (a.kp / 8), [&](auto T, auto U, dim3 grid) {
+    hipLaunchKernelGGL((k_mx_quantize<T, U>), grid, dim3(256), 0, stream, a);
+  });
 }
 
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int d,
                                 void *x, int32_t type, int64_t stride, hipStream_t stream) {
   const bool vec = vec_rows(x, type, stride, type == SD_F32 ? 4 : 8);
-  const MxArgs a{nullptr, type, rows, stride, d, mx_padded(d), vec, false, const_cast<uint8_t *>(codes),
+  const MxArgs a{nullptr, type, rows, stride, d, mx_padded(d), vec, const_cast<uint8_t *>(codes),
                  const_cast<uint8_t *>(scales)};
-  hipLaunchKernelGGL(k_mx_dequantize, dim3((unsigned)blocks_of(rows * ((d + 7) / 8))), dim3(256), 0,
-                     stream, a, x);
-  return hipGetLastError();
+  return by_items(type, rows * ((d + 7) / 8), [&](auto T, auto U, dim3 grid) {
+    hipLaunchKernelGGL((k_mx_dequantize<T, U>), grid, dim3(256), 0, stream, a, x);
+  });
 }
 
 size_t mx_tiled_bytes(int64_t rows, int d, size_t *scales) {
@@ -626,7 +718,12 @@ hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int 
   mx_tiled_bytes(M, d, &hs);
   mx_tiled_bytes(V, d, &ws);
   uint8_t *h = reinterpret_cast<uint8_t *>(workspace) + sizeof(WsHeader);
-  hipError_t e = launch_mx_quantize(hidden, hidden_type, M, d, stride, h, h + hs, true, stream);
+  const MxArgs q{hidden, hidden_type, M, stride, d, mx_padded(d),
+                 vec_rows(hidden, hidden_type, stride, hidden_type == SD_F32 ? 4 : 8), h, h + hs};
+  by_type(hidden_type, [&](auto T) {
+    hipLaunchKernelGGL((k_mx_quantize_tiles<T>), dim3((unsigned)(hs / 4096)), dim3(256), 0, stream, q);
+  });
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const MxGemmArgs a{h, h + hs, head, head + ws, M, V, mx_padded(d) / 128, logits, type, ld,
                      vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8)};
