@@ -8,6 +8,7 @@ importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -115,7 +116,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # The current stream's handle without a Stream object around it: 0.3 us, not 3.
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -677,6 +679,29 @@ def _call(name: str, dev: torch.device, stream, *args) -> None:
         _check(name, getattr(_lib, name)(*args, _stream(stream)))
 
 
+def _current(stream, dev: torch.device):
+    """`stream` as torch's current stream, or the one that is."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`: taken on that stream, so that neither an earlier user of
+    it is still at work nor a later one begins before the call is over."""
+    with _current(stream, dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(nbytes: int, dev: torch.device, stream) -> torch.Tensor:
+    ws = _empty(max(nbytes, 256), torch.uint8, dev, stream)
+    _call("sd_workspace_init", dev, stream, _ptr(ws), ws.numel())
+    return ws
+
+
 def mxfp4_columns(d: int) -> int:
     """Stored columns of an MXFP4 row: d rounded up to a multiple of 128."""
     kp = int(_lib.sd_mxfp4_columns(d))
@@ -705,9 +730,9 @@ def sd_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     rows, d = x.shape
     kp = mxfp4_columns(d)
     if codes is None:
-        codes = torch.empty((rows, kp // 2), dtype=torch.uint8, device=x.device)
+        codes = _empty((rows, kp // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((rows, kp // 32), dtype=torch.uint8, device=x.device)
+        scales = _empty((rows, kp // 32), torch.uint8, x.device, stream)
     _need(codes, "codes", torch.uint8, (rows, kp // 2))
     _need(scales, "scales", torch.uint8, (rows, kp // 32))
     _same_device(x.device, codes=codes, scales=scales)
@@ -726,7 +751,7 @@ def sd_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
     _need(codes, "codes", torch.uint8, (rows, kp // 2))
     _need(scales, "scales", torch.uint8, (rows, kp // 32))
     if out is None:
-        out = torch.empty((rows, d), dtype=dtype, device=codes.device)
+        out = _empty((rows, d), dtype, codes.device, stream)
     _rows(out, "out")
     if tuple(out.shape) != (rows, d):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, d)}")
@@ -748,8 +773,9 @@ class Mxfp4Weights:
         V = codes.shape[0]
         if d % 32 == 0 and kp != d and tuple(codes.shape) == (V, d // 2):
             _need(scales, "scales", torch.uint8, (V, d // 32))
-            codes = torch.nn.functional.pad(codes, (0, (kp - d) // 2))
-            scales = torch.nn.functional.pad(scales, (0, (kp - d) // 32))
+            with _current(stream, codes.device):
+                codes = torch.nn.functional.pad(codes, (0, (kp - d) // 2))
+                scales = torch.nn.functional.pad(scales, (0, (kp - d) // 32))
         _need(codes, "codes", torch.uint8, (V, kp // 2))
         _need(scales, "scales", torch.uint8, (V, kp // 32))
         _same_device(codes.device, scales=scales)
@@ -758,7 +784,7 @@ class Mxfp4Weights:
             raise ValueError(f"no MXFP4 LM head of [{V}][{d}]")
         self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
         self.nbytes = nbytes
-        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        self.buf = _empty(nbytes, torch.uint8, codes.device, stream)
         _call("sd_mxfp4_head", codes.device, stream, _ptr(codes), _ptr(scales), self.V, self.d,
               _ptr(self.buf), nbytes)
 
@@ -781,12 +807,12 @@ def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
         raise ValueError("lm_head must be [V][d] with the hidden size of `hidden`")
     dev = hidden.device
     if logits is None:
-        logits = torch.empty((M, lm_head.V), dtype=dtype, device=dev)
+        logits = _empty((M, lm_head.V), dtype, dev, stream)
     _rows(logits, "logits")
     if tuple(logits.shape) != (M, lm_head.V):
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected {(M, lm_head.V)}")
     if workspace is None:
-        workspace = new_workspace(mxfp4_logits_workspace_bytes(M, d), dev, stream)
+        workspace = _workspace(mxfp4_logits_workspace_bytes(M, d), dev, stream)
     _same_device(dev, lm_head=lm_head, logits=logits, workspace=workspace)
     _call("sd_mxfp4_logits", dev, stream, _ptr(hidden), _TYPE_CODES[hidden.dtype], M, d,
           _row_stride(hidden), _ptr(lm_head.buf), lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
@@ -878,16 +904,16 @@ def sd_sample(logits: torch.Tensor, u: torch.Tensor, params: SamplingParams,
     if R % params.n != 0:
         raise ValueError(f"{R} rows cannot share the settings of {params.n} requests")
     if tokens is None:
-        tokens = torch.empty(R, dtype=torch.int32, device=dev)
+        tokens = _empty(R, torch.int32, dev, stream)
     if kept is None:
-        kept = torch.empty(R, dtype=torch.int32, device=dev)
+        kept = _empty(R, torch.int32, dev, stream)
     if logprob is None:
-        logprob = torch.empty(R, dtype=torch.float32, device=dev)
+        logprob = _empty(R, torch.float32, dev, stream)
     _vector(tokens, "tokens", torch.int32, R)
     _need(kept, "kept", torch.int32, (R,))
     _need(logprob, "logprob", torch.float32, (R,))
     if workspace is None:
-        workspace = new_workspace(sample_workspace_bytes(R, V), dev, stream)
+        workspace = _workspace(sample_workspace_bytes(R, V), dev, stream)
     _same_device(dev, u=u, params=params, tokens=tokens, kept=kept, logprob=logprob,
                  workspace=workspace)
     _call("sd_sample", dev, stream, _ptr(logits), _TYPE_CODES[logits.dtype], _row_stride(logits), R,
@@ -923,14 +949,14 @@ def sd_accept_filtered(logits: torch.Tensor, draft_logits: torch.Tensor,
         raise TypeError("params must be SamplingParams")
     if params.n != B:
         raise ValueError(f"params holds the settings of {params.n} requests, expected {B}")
-    accept_len = torch.empty(B, dtype=torch.int32, device=dev) if accept_len is None else accept_len
-    next_token = torch.empty(B, dtype=torch.int32, device=dev) if next_token is None else next_token
+    accept_len = _empty(B, torch.int32, dev, stream) if accept_len is None else accept_len
+    next_token = _empty(B, torch.int32, dev, stream) if next_token is None else next_token
     _need(accept_len, "accept_len", torch.int32, (B,))
     _need(next_token, "next_token", torch.int32, (B,))
     if counters is not None:
         _need(counters, "counters", torch.int64, (2,))
     if workspace is None:
-        workspace = new_workspace(accept_filtered_workspace_bytes(B, g, V), dev, stream)
+        workspace = _workspace(accept_filtered_workspace_bytes(B, g, V), dev, stream)
     _same_device(dev, logits=logits, draft_logits=draft_logits, verify_len=verify_len,
                  row_offsets=row_offsets, u_accept=u_accept, u_resample=u_resample, params=params,
                  accept_len=accept_len, next_token=next_token, counters=counters,

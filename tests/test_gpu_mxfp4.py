@@ -200,3 +200,34 @@ def test_logits_repeat_and_graph(M):
         assert torch.equal(out, eager[i])
         assert torch.equal(sd.sd_mxfp4_logits(hs[i], head), eager[i])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_given_stream(handle):
+    """Everything a call makes for itself (padding, codes, workspace, results) is made on the
+    stream it is given, behind work that is still on it."""
+    d, V, M = 160, 3000, 70
+    w = rand(V, d, torch.bfloat16, 1, spread=False).cuda()
+    h = rand(M, d, torch.bfloat16, 2, spread=False).cuda()
+    codes, scales = sd.sd_mxfp4_quantize(w)
+    want = sd.sd_mxfp4_logits(h, sd.Mxfp4Weights(codes, scales, d))
+    back = sd.sd_mxfp4_dequantize(codes, scales, d)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    s = st.cuda_stream if handle else st
+    big = torch.randn(4096, 4096, device="cuda")
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(st):
+            late = torch.zeros_like(w)
+            for _ in range(4):
+                big @ big
+            late.copy_(w)
+        c, e = sd.sd_mxfp4_quantize(late, stream=s)
+        head = sd.Mxfp4Weights(c, e, d, stream=s)
+        got = sd.sd_mxfp4_logits(h, head, stream=s)
+        val = sd.sd_mxfp4_dequantize(c, e, d, stream=s)
+        junk = [torch.full((V, d), 9.0, device="cuda") for _ in range(4)]
+        st.synchronize()
+        assert torch.equal(got, want) and torch.equal(val, back)
+        del junk
