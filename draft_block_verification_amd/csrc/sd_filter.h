@@ -32,7 +32,7 @@ constexpr int kBins = 2048;          // bins of the narrowing path's histogram
 constexpr int kCandMax = 1536;       // ids that are ranked in LDS (three workgroups a compute unit)
 constexpr int kCandPad = 2048;       // the same, up to a power of two
 constexpr int kPerThread = kCandPad / kFilterThreads;
-constexpr int kMaxShares = 64;       // parts a row's vectors are summed in
+constexpr int kMaxShares = 256;      // parts a row's vectors are summed in
 constexpr int kFixBits = 46;         // most fraction bits of the summed weights
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // key of -inf (sort_key)
 
@@ -733,11 +733,15 @@ __device__ inline double bin_weight(double y) {
 __device__ inline double bin_unit(const RowSettings &set) { return set.unit * 0.25; }
 
 // Smallest value (not -inf) for which `ok`, which holds from some value on; +inf has to be
-// one. Each wave searches by itself, 64 probes a step.
+// one. Each wave searches by itself, 64 probes a step: first those around a guess, which is
+// nearly always within a few steps of fp32 of the border.
 template <class F>
-__device__ __forceinline__ float smallest(F ok) {
+__device__ __forceinline__ float smallest(double guess, F ok) {
   const int lane = threadIdx.x & 63;
   uint32_t lo = kKeyNegInf + 1, hi = 0xff800000u;   // keys of the lowest finite value and +inf
+  const uint32_t mid = min(max(sort_key(canonical((float)guess)), lo + 64), hi - 64);
+  const u64 near = __ballot(ok(key_value(mid - 32 + lane)));
+  if (near && !(near & 1)) return key_value(mid - 32 + (__ffsll((long long)near) - 1));
   while (hi > lo) {
     const uint32_t step = (hi - lo + 63) / 64;
     const uint32_t probe = (uint32_t)lane * step < hi - lo ? lo + (uint32_t)lane * step : hi;
@@ -750,6 +754,11 @@ __device__ __forceinline__ float smallest(F ok) {
     hi = at;
   }
   return key_value(hi);
+}
+
+// Smallest value at or above the lower end of bin b.
+__device__ __forceinline__ float bin_floor(const Grid &g, int b) {
+  return smallest(((double)b - g.c) / g.k, [&](float l) { return g.pos(l) >= (double)b; });
 }
 
 // Lane's part of the first pass over vectors j0 .. j1 - 1: the largest logit (best), and by
@@ -820,6 +829,7 @@ struct CutPlan {
   bool narrow;     // left to the narrowing path
   u64 need;        // weight at which the top-p run of a kCutMass row ends, 0 without one
   u64 above;       // kCutMass: weight of the ids from t_hi up, by the bins
+  u64 in_bin;      // kCutMass: weight of the ids in the bin of the cut
 };
 
 // The plan of a row with largest logit m (above -inf) and `any` ids above -inf (kCutCount),
@@ -831,10 +841,12 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
                                              FilterSmem &s) {
   const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
   const float lowest = key_value(kKeyNegInf + 1);
-  CutPlan p{lowest, lowest, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), 0, 0};
+  CutPlan p{lowest, lowest, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), 0, 0, 0};
   const bool min_p = set.min_p > 0.0;
   if (p.narrow) return p;
-  const float t_m = min_p ? smallest([&](float l) { return l >= m || weight_finite(l, m, set.sl) >= set.min_p; }) : lowest;
+  const float t_m = min_p ? smallest((double)m + log2((double)set.min_p) / set.sl,
+                                     [&](float l) { return l >= m || weight_finite(l, m, set.sl) >= set.min_p; })
+                          : lowest;
   if (kind == kCutSum) {
     p.t_lo = p.t_hi = t_m;
     return p;
@@ -872,7 +884,7 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
     p.list = true;
     const u64 upto = cb < 0 ? all : s.acc2;
     p.narrow = upto > kCandMax || (cb < 0 && all != any);   // fewer than k in the grid
-    if (cb >= 0) p.t_lo = smallest([&](float l) { return g.pos(l) >= (double)cb; });
+    if (cb >= 0) p.t_lo = bin_floor(g, cb);
     p.t_lo = fmaxf(p.t_lo, t_m);
     return p;
   }
@@ -884,19 +896,23 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
   // No bin holds more ids than its weights say: each is at least 1 (to 2e-14).
   const double per_id = 1.001 / bin_unit(set);
   u64 above = 0, ids = 0;
+  if (tid == 0) s.acc2 = 0;
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPlan; ++i) {
     if (b0 - i > cb) above += total[i];
+    if (b0 - i == cb) s.acc2 = total[i];
     if (b0 - i >= cb) ids += (u64)((double)raw[i] * per_id);
   }
   p.above = block_sum_u64(above, s);
+  p.in_bin = s.acc2;
   if (cb >= 0) {
     ids = block_sum_u64(ids, s);
     const u64 in_bin = (u64)((double)s.grid[cb] * per_id);
     p.narrow = in_bin > kCandMax;
     p.list = ids <= kCandMax;
-    p.t_lo = fmaxf(smallest([&](float l) { return g.pos(l) >= (double)cb; }), t_m);
-    p.t_hi = smallest([&](float l) { return g.pos(l) >= (double)(cb + 1); });
+    p.t_lo = fmaxf(bin_floor(g, cb), t_m);
+    p.t_hi = bin_floor(g, cb + 1);
   }
   return p;
 }
@@ -911,7 +927,7 @@ __device__ __forceinline__ void scale_table(const Grid &g, float m, double unit,
 // Second pass over vectors j0 .. j1 - 1: lists ids in s.cand (s.n_cand counts them) and, with
 // `sums` (s.scale set), adds up the rest of the kept ones: a weight is its bin's scale times
 // its weight inside the bin, half the work of an exponential.
-template <class E>
+template <int N = 8, class E>
 __device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan &p, const Grid &g, bool sums, int j0, int j1,
                                              u64 *sum, uint32_t *n, FilterSmem &s) {
   const float lo = p.t_lo, hi = p.list ? INFINITY : p.t_hi;
@@ -954,7 +970,7 @@ __device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan 
     *sum += kept_w;
     *n += (threadIdx.x & 63) == 0 ? kept_n : 0;        // counted once a wave
   } else if (lo < hi) {
-    wave_vecs(r, j0, j1, [&](const float (&v)[E::VE], int id) { list(v, id); });
+    wave_vecs<N>(r, j0, j1, [&](const float (&v)[E::VE], int id) { list(v, id); });
   }
 }
 
@@ -1091,20 +1107,27 @@ __device__ __forceinline__ float row_reference(const RowView<E> &r, FilterSmem &
 //   1. One pass bins the row (bin_pass), around a reference taken from a few thousand of its
 //      logits; a row whose largest logit lies past the grid is passed again around that.
 //   2. The bin that holds the cut, and the smallest logits of it and of the bin above, follow
-//      from the bins' totals (make_plan).
+//      from the bins' totals (make_plan). Both steps: row_plan.
 //   3. A second pass lists the ids in that bin and, where a draw follows, sums the weights of
 //      those above it by wave; when all kept ids are few they are listed and nothing is
 //      summed by pass (collect_pass).
-//   4. The list is cut (cut_list).
+//   4. The list is cut (cut_list). Both steps: row_rest.
 // totals: only the kept set and its weight are wanted; the bins give the weight above the cut.
 // A row that this leaves to the narrowing path is cut by row_cut_narrowing.
+struct RowPlan {
+  CutKind kind;
+  float ref;       // the grid's reference
+  CutPlan plan;
+};
+
+// kModeTop: c is the cut; kModeNarrow; else c.m is set and row_rest comes next.
 template <class E>
-__device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, bool totals, RowCut &c,
-                                           u64 *last, FilterSmem &s) {
+__device__ __forceinline__ RowMode row_plan(const RowView<E> &r, const RowSettings &set, bool totals, RowPlan &o, RowCut &c,
+                                            FilterSmem &s) {
   const int tid = threadIdx.x, wave = tid >> 6;
   const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
   const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
-  const CutKind kind = cut_kind(set, r.V, totals);
+  const CutKind kind = o.kind = cut_kind(set, r.V, totals);
   const bool binned = kind == kCutCount || kind == kCutMass;
   float ref = binned ? row_reference(r, s) : 0.f;
   u64 any = 0, top;
@@ -1125,10 +1148,20 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
   }
   if (!top || kind == kCutOne) return cut_top(set, top, c);
   __syncthreads();
-  const Grid g(kind == kCutSum ? c.m : ref, set.T, kind == kCutCount);
-  const CutPlan p = make_plan(set, kind, g, c.m, any, s);
+  o.ref = kind == kCutSum ? c.m : ref;
+  o.plan = make_plan(set, kind, Grid(o.ref, set.T, kind == kCutCount), c.m, any, s);
+  return o.plan.narrow ? kModeNarrow : kModeNone;
+}
+
+template <int N = 8, class E>
+__device__ __forceinline__ RowMode row_rest(const RowView<E> &r, const RowSettings &set, bool totals, const RowPlan &o,
+                                            RowCut &c, u64 *last, FilterSmem &s) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves;
+  const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
+  const CutPlan &p = o.plan;
+  const Grid g(o.ref, set.T, o.kind == kCutCount);
   c.S = 0;
-  if (p.narrow) return kModeNarrow;
   const bool sums = !totals && !p.list;
   __syncthreads();
   if (sums) scale_table(g, c.m, set.unit, s);
@@ -1136,7 +1169,7 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
   __syncthreads();
   u64 sum = 0;
   uint32_t n_sum = 0;
-  collect_pass(r, p, g, sums, j0, j1, &sum, &n_sum, s);
+  collect_pass<N>(r, p, g, sums, j0, j1, &sum, &n_sum, s);
   if (totals && !p.list) {
     c.S = p.above;
     n_sum = 1;                     // some
@@ -1149,10 +1182,17 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
     for (int w = 0; w < kFilterWaves; ++w) c.S += s.share[w];
   }
   const int nc = min((int)s.n_cand, kCandMax);
-  *last = cut_list(set, kind, p, nc, n_sum, c, s);
+  *last = cut_list(set, o.kind, p, nc, n_sum, c, s);
   if (sums) add_listed(r, set, c, nc, *last, per, s);
   __syncthreads();
   return p.list ? kModeList : sums ? kModeShares : kModeNone;
+}
+
+template <class E>
+__device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSettings &set, RowCut &c, u64 *last, FilterSmem &s) {
+  RowPlan o;
+  const RowMode mode = row_plan(r, set, false, o, c, s);
+  return mode == kModeNone ? row_rest(r, set, false, o, c, last, s) : mode;
 }
 
 // The cut of a row that row_cut leaves (c.S unset).
@@ -1178,27 +1218,29 @@ __device__ inline void kept_weights(const RowView<E> &r, const RowCut &c, const 
     w[i] = v[i] > -INFINITY && kept(c, v[i], r.id(j, i)) ? to_fix(weight(v[i], c.m, set.sl), set.unit) : 0;
 }
 
-// Weights f(j, w) of vectors a .. b - 1 summed over the waves' contiguous shares of `step`
-// vectors: s.share afterwards, and the total.
+// Weights f(j, w) of vectors a .. b - 1 summed by shares of *step vectors, a multiple of 64:
+// s.share[0 .. *n) afterwards, and their total.
 template <int VE, class F>
-__device__ __forceinline__ u64 sum_shares(F f, int a, int b, int step, FilterSmem &s) {
-  const int wave = threadIdx.x >> 6, w0 = a + wave * step, w1 = min(b, w0 + step);
-  u64 m = 0;
-#pragma unroll 2
-  for (int j = w0 + (int)(threadIdx.x & 63); j < w1; j += 64) {
-    u64 w[VE];
-    f(j, w);
+__device__ __forceinline__ u64 sum_shares(F f, int a, int b, int *n, int *step, FilterSmem &s) {
+  const int per = 64 * ((b - a + 64 * kMaxShares - 1) / (64 * kMaxShares)), count = (b - a + per - 1) / per;
+  u64 own = 0;
+  __syncthreads();
+  for (int w = threadIdx.x >> 6; w < count; w += kFilterWaves) {
+    u64 m = 0;
+    const int j0 = a + w * per, j1 = min(b, j0 + per);
+    for (int j = j0 + (int)(threadIdx.x & 63); j < j1; j += 64) {
+      u64 x[VE];
+      f(j, x);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) m += w[i];
+      for (int i = 0; i < VE; ++i) m += x[i];
+    }
+    own += m;
+    m = wave_sum_u64(m);
+    if ((threadIdx.x & 63) == 0) s.share[w] = m;
   }
-  m = wave_sum_u64(m);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.share[wave] = m;
-  __syncthreads();
-  u64 total = 0;
-#pragma unroll
-  for (int w = 0; w < kFilterWaves; ++w) total += s.share[w];
-  return total;
+  *n = count;
+  *step = per;
+  return block_sum_u64(own, s);
 }
 
 // The running total that a draw for uniform u of total S > 0 has to reach: the least whole
@@ -1210,45 +1252,47 @@ __device__ inline u64 draw_need(float u, u64 S) {
 
 // Position (vector VE + element) of the first weight at which the running sum reaches need,
 // given the sums of n contiguous shares of `step` of all nv vectors in s.share: the share that
-// holds the crossing is split again, a part to each wave, until one wave load covers it. The
-// shares may come from another form of the weights, units apart: a need past the sum of the
-// parts is taken as that sum. -1 when nothing there has weight.
+// holds the crossing is split again until a vector a thread covers it. The shares may come
+// from another form of the weights, units apart: a need past the sum of the parts is taken as
+// that sum. -1 when nothing there has weight.
 template <int VE, class F>
 __device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, u64 need, FilterSmem &s) {
+  const int tid = threadIdx.x;
   int a = 0, b = nv;
+  // The running sums over the threads' x: whether this thread's holds the crossing.
+  auto crosses = [&](u64 x, u64 *before) __attribute__((always_inline)) {
+    *before = block_excl_scan_u64(x, s);
+    u64 total = 0;
+#pragma unroll
+    for (int w = 0; w < kFilterWaves; ++w) total += s.red[w];
+    need = need < total ? need : total;
+    return *before < need && *before + x >= need;
+  };
+  u64 before;
   for (;;) {
-    // Every wave finds the share by itself, lane i holding share i.
-    const int lane = threadIdx.x & 63;
-    const u64 x = lane < n ? s.share[lane] : 0, incl = wave_incl_scan_u64(x), total = wave_sum_u64(x);
-    need = need < total ? need : total;
-    const u64 m = __ballot(lane < n && incl >= need);
-    const int w = __builtin_amdgcn_readfirstlane(m ? __ffsll((long long)m) - 1 : n - 1);
-    need -= __shfl(incl - x, w);
-    a += w * step;
+    if (tid == 0) s.hit = -1;
+    if (crosses(tid < n ? s.share[tid] : 0, &before)) { s.hit = tid; s.acc = before; }
+    __syncthreads();
+    if (s.hit < 0) return -1;
+    need -= s.acc;
+    a += s.hit * step;
     b = min(b, a + step);
-    if (b - a <= 64) break;
-    n = kFilterWaves;
-    step = (b - a + n - 1) / n;
-    sum_shares<VE>(f, a, b, step, s);
+    if (b - a <= kFilterThreads) break;
+    sum_shares<VE>(f, a, b, &n, &step, s);
   }
-  if (threadIdx.x < 64) {
-    const int j = a + threadIdx.x;
-    u64 w[VE], own = 0;
+  u64 w[VE], own = 0;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) w[i] = 0;
-    if (j < b) f(j, w);
+  for (int i = 0; i < VE; ++i) w[i] = 0;
+  if (a + tid < b) f(a + tid, w);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) own += w[i];
-    const u64 incl = wave_incl_scan_u64(own), total = wave_sum_u64(own);
-    need = need < total ? need : total;
-    if (threadIdx.x == 0) s.id = -1;
-    u64 run = incl - own;
-    if (run < need && incl >= need) {
+  for (int i = 0; i < VE; ++i) own += w[i];
+  if (tid == 0) s.id = -1;
+  if (crosses(own, &before)) {
+    u64 run = before;
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        if (run < need && run + w[i] >= need) s.id = j * VE + i;
-        run += w[i];
-      }
+    for (int i = 0; i < VE; ++i) {
+      if (run < need && run + w[i] >= need) s.id = (a + tid) * VE + i;
+      run += w[i];
     }
   }
   __syncthreads();
@@ -1261,8 +1305,8 @@ __device__ __forceinline__ int draw_in_shares(F f, int nv, int n, int step, u64 
 template <class E>
 __device__ __forceinline__ void row_total(const RowView<E> &r, RowCut &c, const RowSettings &set, FilterSmem &s) {
   if (c.n == 0 || c.S > 0) return;
-  c.S = sum_shares<E::VE>([&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); }, 0, r.nv,
-                          (r.nv + kFilterWaves - 1) / kFilterWaves, s);
+  int n, step;
+  c.S = sum_shares<E::VE>([&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); }, 0, r.nv, &n, &step, s);
 }
 
 // The row's draw for uniform u: the smallest kept id whose running weight, in id order, passes
@@ -1283,11 +1327,7 @@ __device__ __forceinline__ int row_draw(const RowView<E> &r, RowCut &c, const Ro
     return word_id(swap_halves(x));
   }
   auto f = [&](int j, u64 (&w)[E::VE]) { kept_weights(r, c, set, j, w); };
-  if (mode == kModeNone) {
-    n = kFilterWaves;
-    step = (r.nv + n - 1) / n;
-    c.S = sum_shares<E::VE>(f, 0, r.nv, step, s);
-  }
+  if (mode == kModeNone) c.S = sum_shares<E::VE>(f, 0, r.nv, &n, &step, s);
   if (c.n == 0 || c.S == 0) return -1;
   const int at = draw_in_shares<E::VE>(f, r.nv, n, step, draw_need(u, c.S), s);
   if (at < 0) return -1;

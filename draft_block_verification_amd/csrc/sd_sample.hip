@@ -54,6 +54,17 @@ struct SampleRows {
   }
 };
 
+// A row after the first of its two passes: its weight S lies in [s_lo, s_hi] (in
+// RowSettings::unit), ids from plan.t_hi up are kept and ids under plan.t_lo are not.
+struct RowBound {
+  CutPlan plan;
+  float m, ref;
+  double s_lo, s_hi;
+  uint32_t open;        // 0: the cut itself is known
+  uint32_t pad;
+};
+static_assert(sizeof(RowBound) == 72, "row bounds are 72 bytes");
+
 struct FilteredArgs {
   const float *logits;           // [cap][V]
   const uint16_t *draft_logits;  // bf16 [B][gamma][V]
@@ -67,6 +78,8 @@ struct FilteredArgs {
   int64_t *counters;
   RowCut *cut_p;                 // [B][gamma + 1]
   RowCut *cut_q;                 // [B][gamma]
+  RowBound *bound;               // [B (2 gamma + 1)], or null: every cut is exact
+  uint32_t *todo;                // rows to be cut: their number, then from word 64 on the rows
   u64 *share;                    // [B][kMaxShares][2] sums of the draw's weights
   WsHeader *ws;
 };
@@ -75,7 +88,7 @@ struct FilteredArgs {
 __device__ inline int first_row(const RowMap &rm, int r, int L, WsHeader *ws) {
   const int cap = rm.B * (rm.gamma + 1);
   const int base = rm.row_offsets ? rm.row_offsets[r] : r * (rm.gamma + 1);
-  if (base < 0 || base + L >= cap) {
+  if (base < 0 || base >= cap - L) {
     raise_flag(ws, SD_FLAG_ROW_OFFSETS);
     return -1;
   }
@@ -119,7 +132,7 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_rows(Rows rows, uint32_t 
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     RowCut c;
     u64 last = 0;
-    const RowMode mode = row_cut(r, set, Rows::kTotals, c, &last, s);
+    const RowMode mode = row_cut(r, set, c, &last, s);
     if (mode == kModeNarrow) {
       if (threadIdx.x == 0) todo[row] = 1;
       return;
@@ -149,7 +162,7 @@ struct TeamRow {
   u64 top, any;
   uint32_t n_list, n_above;
   float ref;
-  uint32_t pad;
+  uint32_t done;     // workgroups whose bins are in
   CutPlan plan;
 };
 static_assert(sizeof(TeamRow) <= 128, "team rows are 128 bytes");
@@ -177,24 +190,42 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_start(Rows rows, Team t
     if (threadIdx.x == 0) {
       TeamRow &o = t.at(row);
       o.top = o.any = 0;
-      o.n_list = o.n_above = 0;
+      o.n_list = o.n_above = o.done = 0;
       o.ref = ref;
     }
   });
 }
 
-// Vectors of this workgroup's share and of the calling wave in it.
+// Vectors of the calling wave in workgroup x of the C that a row's vectors are dealt to: share
+// 8 x + wave of 8 C.
 struct Part {
-  int step, j0, j1;
-  __device__ Part(int nv, int C) {
-    step = (nv + C - 1) / C;
-    const int a = min(nv, (int)blockIdx.x * step), b = min(nv, a + step);
-    const int per = (b - a + kFilterWaves - 1) / kFilterWaves;
-    j0 = min(b, a + (int)(threadIdx.x >> 6) * per);
-    j1 = min(b, j0 + per);
+  int step, j0, j1, share;
+  __device__ Part(int nv, int C, int x) {
+    step = part_step(nv, C);
+    share = x * kFilterWaves + (int)(threadIdx.x >> 6);
+    j0 = min(nv, share * step);
+    j1 = min(nv, j0 + step);
   }
+  __device__ static int part_step(int nv, int C) { return (nv + C * kFilterWaves - 1) / (C * kFilterWaves); }
 };
 
+// Lowest bin that can hold the end of a top-k run, by this workgroup's own counts alone: where
+// they reach k from above, the row's do.
+__device__ __forceinline__ int lowest_bin(u64 k, FilterSmem &s) {
+  const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
+  u64 own = 0;
+#pragma unroll
+  for (int i = 0; i < kPlan; ++i) own += (uint32_t)s.grid[b0 - i];
+  if (tid == 0) s.hit = 0;
+  const u64 before = block_excl_scan_u64(own, s);
+  if (before < k && before + own >= k) s.hit = b0 - kPlan + 1;
+  __syncthreads();
+  return s.hit;
+}
+
+// Bins by workgroup, then in the workspace. The row's last workgroup to arrive makes the plan:
+// everything it takes from the others went through atomics that were over before they
+// counted themselves in.
 template <class Rows>
 __global__ __launch_bounds__(kFilterThreads, 6) void k_team_bins(Rows rows, Team t) {
   __shared__ FilterSmem s;
@@ -208,19 +239,38 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_bins(Rows rows, Team
       for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
       __syncthreads();
     }
-    const Part part(r.nv, t.C);
+    const Part part(r.nv, t.C, blockIdx.x);
     PassOut out;
     bin_pass(r, g, kind, bin_unit(set), part.j0, part.j1, out, s);
-    const u64 top = block_max_u64(rank_word(out.best, out.at), s);
-    const u64 any = kind == kCutCount ? block_sum_u64(out.any, s) : 0;
+    u64 top = block_max_u64(rank_word(out.best, out.at), s);
+    u64 any = kind == kCutCount ? block_sum_u64(out.any, s) : 0;
     __syncthreads();
-    if (binned)
-      for (int b = tid; b < kGrid; b += kFilterThreads)
-        if (s.grid[b]) atomicAdd(&t.grid[(size_t)row * kGrid + b], s.grid[b]);
+    u64 *grid = t.grid + (size_t)row * kGrid;
+    if (binned) {
+      const int low = kind == kCutCount ? lowest_bin((u64)set.k, s) : 0;
+      for (int b = low + tid; b < kGrid; b += kFilterThreads)
+        if (s.grid[b]) atomicAdd(&grid[b], s.grid[b]);
+    }
     if (tid == 0) {
       atomicMax(&o.top, top);
       if (any) atomicAdd(&o.any, any);
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) s.n_sub = atomicAdd(&o.done, 1u);
+    __syncthreads();
+    if (s.n_sub != (uint32_t)t.C - 1) return;
+    top = __hip_atomic_load(&o.top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    any = __hip_atomic_load(&o.any, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (!top || kind == kCutOne) return;
+    if (binned) {
+      for (int b = tid; b < kGrid; b += kFilterThreads)
+        s.grid[b] = __hip_atomic_load(&grid[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+    }
+    const float m = word_value(top);
+    const CutPlan p = make_plan(set, kind, Grid(kind == kCutSum ? m : o.ref, set.T, kind == kCutCount), m, any, s);
+    if (tid == 0) o.plan = p;
   });
 }
 
@@ -233,31 +283,26 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_collect(Rows rows, T
     TeamRow &o = t.at(row);
     const u64 top = o.top;
     if (!top || kind == kCutOne) return;
-    const float m = word_value(top);
-    if (kind != kCutSum) {
-      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = t.grid[(size_t)row * kGrid + b];
-      __syncthreads();
-    }
-    const Grid g(kind == kCutSum ? m : o.ref, set.T, kind == kCutCount);
-    const CutPlan p = make_plan(set, kind, g, m, o.any, s);
-    if (blockIdx.x == 0 && tid == 0) o.plan = p;
+    const CutPlan p = o.plan;
     if (p.narrow) return;
-    __syncthreads();
-    if (!Rows::kTotals && !p.list) scale_table(g, m, set.unit, s);
+    const float m = word_value(top);
+    const Grid g(kind == kCutSum ? m : o.ref, set.T, kind == kCutCount);
+    const bool sums = !Rows::kTotals && !p.list;
+    if (sums) scale_table(g, m, set.unit, s);
     if (tid == 0) s.n_cand = 0;
     __syncthreads();
-    const Part part(r.nv, t.C);
+    const Part part(r.nv, t.C, blockIdx.x);
     u64 sum = 0;
     uint32_t n = 0;
-    collect_pass(r, p, g, !Rows::kTotals && !p.list, part.j0, part.j1, &sum, &n, s);
-    sum = block_sum_u64(sum, s);
-    n = (uint32_t)block_sum_u64(n, s);
-    const uint32_t nc = min(s.n_cand, (uint32_t)kCandMax);
-    if (tid == 0) {
-      t.share[(size_t)row * kMaxShares + blockIdx.x] = sum;
-      if (n) atomicAdd(&o.n_above, n);
-      s.key = nc ? atomicAdd(&o.n_list, nc) : 0;
+    collect_pass(r, p, g, sums, part.j0, part.j1, &sum, &n, s);
+    if (sums) {
+      sum = wave_sum_u64(sum);
+      if ((tid & 63) == 0) t.share[(size_t)row * kMaxShares + part.share] = sum;
+      if (n) atomicAdd(&o.n_above, n);       // one lane a wave
     }
+    __syncthreads();
+    const uint32_t nc = min(s.n_cand, (uint32_t)kCandMax);
+    if (tid == 0) s.key = nc ? atomicAdd(&o.n_list, nc) : 0;
     __syncthreads();
     for (uint32_t i = tid; i < nc; i += kFilterThreads)
       if (s.key + i < (uint32_t)kCandMax) t.list[(size_t)row * kCandMax + s.key + i] = s.cand[i];
@@ -271,7 +316,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
     const TeamRow o = t.at(row);
-    const int step = (r.nv + t.C - 1) / t.C;
+    const int step = Part::part_step(r.nv, t.C), shares = t.C * kFilterWaves;
     RowCut c;
     RowMode mode;
     u64 last = 0;
@@ -285,25 +330,27 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
       mode = kModeNone;
     } else {
       for (int i = tid; i < nc; i += kFilterThreads) s.cand[i] = t.list[(size_t)row * kCandMax + i];
-      if (tid < t.C) s.share[tid] = t.share[(size_t)row * kMaxShares + tid];
-      __syncthreads();
       const bool sums = !Rows::kTotals && !o.plan.list;
-      if (sums) c.S = wave_sum_u64((tid & 63) < t.C ? s.share[tid & 63] : 0);
+      const u64 share = sums && tid < shares ? t.share[(size_t)row * kMaxShares + tid] : 0;
+      if (tid < shares) s.share[tid] = share;
+      if (sums) c.S = block_sum_u64(share, s);
       else if (!o.plan.list) c.S = o.plan.above;
+      __syncthreads();
       last = cut_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s);
       if (sums) add_listed(r, set, c, nc, last, step, s);
       __syncthreads();
       mode = o.plan.list ? kModeList : sums ? kModeShares : kModeNone;
     }
-    rows.finish(row, r, set, c, mode, t.C, step, nc, last, s);
+    rows.finish(row, r, set, c, mode, shares, step, nc, last, s);
   });
 }
 
 // Workgroups a row's vectors are dealt to: enough for about two on every compute unit, each
 // with at least 4096 ids; 1: the row is one workgroup's.
 int team_size(int rows, int V) {
-  const int c = rows < 1024 ? 1024 / rows : 0;
-  return c > V / 4096 ? (V / 4096 < kMaxShares ? V / 4096 : kMaxShares) : (c < kMaxShares ? c : kMaxShares);
+  int c = rows < 1024 ? 1024 / rows : 0;
+  if (c > V / 10240) c = V / 10240;
+  return c < kMaxShares / kFilterWaves ? c : kMaxShares / kFilterWaves;
 }
 
 // Workspace of the rows: a word each for one workgroup a row, else the team's state.
@@ -320,16 +367,8 @@ struct TeamLayout {
 };
 
 template <class Rows>
-hipError_t launch_rows(const Rows &rows, int n, int V, char *ws, const TeamLayout &l, hipStream_t stream) {
+hipError_t launch_team(const Rows &rows, int n, int V, char *ws, const TeamLayout &l, hipStream_t stream) {
   const int C = team_size(n, V);
-  if (C < 2) {
-    uint32_t *todo = reinterpret_cast<uint32_t *>(ws + l.row);
-    hipLaunchKernelGGL(k_rows<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows, todo);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_rows_narrow<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows, todo);
-    return hipGetLastError();
-  }
   const Team t{C, reinterpret_cast<TeamRow *>(ws + l.row), reinterpret_cast<u64 *>(ws + l.grid),
                reinterpret_cast<u64 *>(ws + l.list), reinterpret_cast<u64 *>(ws + l.share)};
   hipLaunchKernelGGL(k_team_start<Rows>, dim3(1, n), dim3(kFilterThreads), 0, stream, rows, t);
@@ -340,6 +379,17 @@ hipError_t launch_rows(const Rows &rows, int n, int V, char *ws, const TeamLayou
   hipLaunchKernelGGL(k_team_collect<Rows>, dim3(C, n), dim3(kFilterThreads), 0, stream, rows, t);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(k_team_finish<Rows>, dim3(1, n), dim3(kFilterThreads), 0, stream, rows, t);
+  return hipGetLastError();
+}
+
+template <class Rows>
+hipError_t launch_rows(const Rows &rows, int n, int V, char *ws, const TeamLayout &l, hipStream_t stream) {
+  if (team_size(n, V) >= 2) return launch_team(rows, n, V, ws, l, stream);
+  uint32_t *todo = reinterpret_cast<uint32_t *>(ws + l.row);
+  hipLaunchKernelGGL(k_rows<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows, todo);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_rows_narrow<Rows>, dim3(n), dim3(kFilterThreads), 0, stream, rows, todo);
   return hipGetLastError();
 }
 
@@ -360,24 +410,136 @@ __device__ inline double per_weight(const RowCut &c, const RowSettings &set) {
   return c.n > 0 ? set.unit / (double)c.S : 0.0;
 }
 
-// a_r of request r by one wave, lane j deciding position j.
-__device__ __forceinline__ int first_rejection(const FilteredArgs &a, int r, int L, int base, const RowSettings &set) {
-  const int lane = threadIdx.x & 63, g = a.rm.gamma;
-  bool miss = false;
-  if (lane < L) {
-    const size_t rj = (size_t)r * g + lane;
-    const int x = a.draft_tokens[rj];
-    miss = true;
-    if (x >= 0 && x < a.V) {
-      const RowCut cp = a.cut_p[rj + r], cq = a.cut_q[rj];
-      const double p = prob(cp, per_weight(cp, set), set, canonical(a.logits[(size_t)(base + lane) * a.V + x]), x);
-      const double q = prob(cq, per_weight(cq, set), set, canonical(bf16_to_f32(a.draft_logits[rj * a.V + x])), x);
-      // A token that the target does not keep is rejected, whatever the drafter's.
-      miss = !((double)a.u_accept[rj] < (p >= q ? (p > 0.0 ? 1.0 : 0.0) : p / q));
-    }
+// The probability as far as it is known. An open row's bounds are taken 1e-9 wider than the
+// sums they come from, which are good to 1e-12.
+struct Between { double lo, hi; };
+__device__ inline Between prob_between(const RowCut &c, const RowBound *b, const RowSettings &set, float l, int x) {
+  if (!b || !b->open) {
+    const double p = prob(c, per_weight(c, set), set, l, x);
+    return {p, p};
   }
-  const u64 m = __ballot(miss);
+  if (b->plan.narrow) return {0.0, INFINITY};
+  if (l < b->plan.t_lo) return {0.0, 0.0};
+  const double w = weight(l, b->m, set.sl) * set.unit;
+  return {l >= b->plan.t_hi ? w / b->s_hi : 0.0, w / b->s_lo};
+}
+
+// Acceptance probability of a token of probabilities p and q: one that the target does not
+// keep is rejected, whatever the drafter's. It rises with p and falls with q.
+__device__ inline double accept_prob(double p, double q) { return p >= q ? (p > 0.0 ? 1.0 : 0.0) : p / q; }
+
+enum Verdict { kAccept, kReject, kUnsure };
+
+// Position `lane` of request r, whose token is drawn against u.
+__device__ __forceinline__ Verdict judge(const FilteredArgs &a, int r, int base, const RowSettings &set) {
+  const int lane = threadIdx.x & 63, g = a.rm.gamma;
+  const size_t rj = (size_t)r * g + lane;
+  const int x = a.draft_tokens[rj];
+  if (x < 0 || x >= a.V) return kReject;
+  const RowBound *bp = a.bound ? a.bound + rj + r : nullptr;
+  const RowBound *bq = a.bound ? a.bound + (size_t)a.rm.B * (g + 1) + rj : nullptr;
+  const Between p = prob_between(a.cut_p[rj + r], bp, set, canonical(a.logits[(size_t)(base + lane) * a.V + x]), x);
+  const Between q = prob_between(a.cut_q[rj], bq, set, canonical(bf16_to_f32(a.draft_logits[rj * a.V + x])), x);
+  const double u = (double)a.u_accept[rj];
+  return u < accept_prob(p.lo, q.hi) ? kAccept : !(u < accept_prob(p.hi, q.lo)) ? kReject : kUnsure;
+}
+
+// a_r of request r by one wave, lane j deciding position j. Positions up to a_r are sure
+// (k_filtered_need); those behind it may say anything.
+__device__ __forceinline__ int first_rejection(const FilteredArgs &a, int r, int L, int base, const RowSettings &set) {
+  const u64 m = __ballot((int)(threadIdx.x & 63) < L && judge(a, r, base, set) == kReject);
   return m ? __ffsll((long long)m) - 1 : L;
+}
+
+// Many rows: two passes over all of them cost twice the bytes, and the second one is needed of
+// few. The first pass leaves bounds (k_filtered_bounds) that decide nearly every position: the
+// weight of a top-p run is its needed weight and less than one id more, so only a token in the
+// bin of the cut or a uniform within some 1e-5 of the border stays open. Rows of open
+// positions up to the first sure rejection, and of that one (or the bonus row), whose
+// distribution is drawn from, are listed (k_filtered_need) and cut (k_filtered_cut).
+__global__ __launch_bounds__(kFilterThreads, 6) void k_filtered_bounds(AcceptRows rows) {
+  __shared__ FilterSmem s;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const FilteredArgs &a = rows.a;
+  if (row == 0 && tid == 0) a.todo[0] = 0;
+  rows.with(row, [&](const auto &r, const RowSettings &set) {
+    RowCut c;
+    RowPlan o;
+    const RowMode mode = row_plan(r, set, true, o, c, s);
+    // A count's second pass is needed for its weight; without a cut nothing is left to pass.
+    const bool open = mode == kModeNarrow || (mode == kModeNone && o.kind == kCutMass && o.plan.t_lo < o.plan.t_hi);
+    if (tid == 0) {
+      RowBound b;
+      b.open = open;
+      if (open) {
+        b.plan = o.plan;
+        b.m = c.m;
+        b.ref = o.ref;
+        // A top-p run weighs what it needs, unless min-p ends it earlier, and less than its
+        // last id more; any kept set holds the largest logit and what lies above the bin.
+        const CutPlan &p = o.plan;
+        const double above = fmax((double)p.above, set.unit), need = (double)p.need;
+        const double one = weight(p.t_hi, fmaxf(c.m, p.t_hi), set.sl) * set.unit;
+        b.s_lo = (p.need && set.min_p == 0.0 ? need : above) * (1.0 - 1e-9);
+        b.s_hi = (p.need ? need + one : above + (double)p.in_bin) * (1.0 + 1e-9);
+      }
+      a.bound[row] = b;
+    }
+    if (open) return;
+    u64 last = 0;
+    const RowMode m = mode == kModeNone ? row_rest(r, set, true, o, c, &last, s) : mode;
+    rows.finish(row, r, set, c, m, 0, 0, 0, last, s);
+  });
+}
+
+// Position `lane` of request `blockIdx.x`.
+__global__ __launch_bounds__(kWave) void k_filtered_need(FilteredArgs a) {
+  const int r = blockIdx.x, g = a.rm.gamma, lane = threadIdx.x;
+  const int L = clamp_len(a.verify_len, r, g, nullptr);
+  const int base = first_row(a.rm, r, L, nullptr);
+  if (base < 0) return;
+  const RowSettings set = load_settings(a.set, r, a.V, nullptr);
+  const Verdict v = lane < L ? judge(a, r, base, set) : kAccept;
+  const u64 rejects = __ballot(v == kReject);
+  const int stop = rejects ? __ffsll((long long)rejects) - 1 : L;
+  const bool need = lane < L && (lane == stop || (lane < stop && v == kUnsure));
+  const uint32_t target = (uint32_t)(r * (g + 1) + lane), draft = (uint32_t)(a.rm.B * (g + 1) + r * g + lane);
+  const bool t = need && a.bound[target].open, d = need && a.bound[draft].open;
+  const u64 tm = __ballot(t), dm = __ballot(d);
+  const uint32_t nt = __popcll(tm), nd = __popcll(dm), bonus = (uint32_t)(r * (g + 1) + L);
+  const bool with_bonus = stop == L && a.bound[bonus].open;
+  uint32_t at = 0;
+  if (lane == 0 && nt + nd + with_bonus) {
+    at = atomicAdd(&a.todo[0], nt + nd + with_bonus);
+    if (with_bonus) a.todo[64 + at + nt + nd] = bonus;
+  }
+  at = __builtin_amdgcn_readfirstlane(at);
+  const u64 below = (1ull << lane) - 1;
+  if (t) a.todo[64 + at + __popcll(tm & below)] = target;
+  if (d) a.todo[64 + at + nt + __popcll(dm & below)] = draft;
+}
+
+__global__ __launch_bounds__(kFilterThreads, 4) void k_filtered_cut(AcceptRows rows) {
+  __shared__ FilterSmem s;
+  const uint32_t n = rows.a.todo[0];
+  for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const int row = (int)rows.a.todo[64 + i];
+    rows.with(row, [&](const auto &r, const RowSettings &set) {
+      RowBound &b = rows.a.bound[row];
+      RowCut c;
+      u64 last = 0;
+      if (b.plan.narrow) {
+        row_cut_narrowing(r, set, c, s);
+      } else {
+        c.m = b.m;
+        const RowPlan o{kCutMass, b.ref, b.plan};
+        row_rest<32>(r, set, true, o, c, &last, s);
+      }
+      rows.finish(row, r, set, c, kModeNone, 0, 0, 0, last, s);
+      __syncthreads();
+      if (threadIdx.x == 0) b.open = 0;
+    });
+  }
 }
 
 // Residual weights are summed in units of 2^-51: they add up to at most 1 (and a little), so a
@@ -438,8 +600,7 @@ struct Residual {
   }
 };
 
-__global__ __launch_bounds__(kFilterThreads) void k_filtered_shares(FilteredArgs a) {
-  __shared__ FilterSmem s;
+__global__ __launch_bounds__(kFilterThreads, 6) void k_filtered_shares(FilteredArgs a) {
   const int r = blockIdx.x, part = blockIdx.y, g = a.rm.gamma, tid = threadIdx.x;
   WsHeader *ws = part == 0 && tid == 0 ? a.ws : nullptr;
   const int L = clamp_len(a.verify_len, r, g, ws);
@@ -459,34 +620,34 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_shares(FilteredArgs
   }
   const RowView<ElemF32> v(a.logits + (size_t)(base + acc) * a.V, a.V);
   const RowCut cp = a.cut_p[(size_t)r * (g + 1) + acc];
-  const int step = (v.nv + gridDim.y - 1) / gridDim.y, j0 = min(v.nv, part * step), j1 = min(v.nv, j0 + step);
+  const Part mine(v.nv, gridDim.y, part);
   const Residual f(a, v, r, acc, acc < L, cp, set);
   // Two vectors of both rows a lane are in flight.
   u64 sum = 0, sum_p = 0;
-  for (int j = j0 + tid; j < j1; j += 2 * kFilterThreads) {
+  for (int j = mine.j0 + (tid & 63); j < mine.j1; j += 2 * kWave) {
     float l[2][4];
     uint2 h[2] = {{0u, 0u}, {0u, 0u}};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int jj = min(j + u * kFilterThreads, j1 - 1);
+      const int jj = min(j + u * kWave, mine.j1 - 1);
       v.load(jj, l[u]);
       if (f.q) f.raw_q(jj, h[u]);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      if (j + u * kFilterThreads < j1) {
+      if (j + u * kWave < mine.j1) {
         u64 w[4], wp[4];
-        f.weights(j + u * kFilterThreads, l[u], h[u], w, wp);
+        f.weights(j + u * kWave, l[u], h[u], w, wp);
         sum += (w[0] + w[1]) + (w[2] + w[3]);
         sum_p += (wp[0] + wp[1]) + (wp[2] + wp[3]);
       }
     }
   }
-  sum = block_sum_u64(sum, s);
-  sum_p = block_sum_u64(sum_p, s);
-  if (tid == 0) {
-    a.share[((size_t)r * kMaxShares + part) * 2] = sum;
-    a.share[((size_t)r * kMaxShares + part) * 2 + 1] = sum_p;
+  sum = wave_sum_u64(sum);
+  sum_p = wave_sum_u64(sum_p);
+  if ((tid & 63) == 0) {
+    a.share[((size_t)r * kMaxShares + mine.share) * 2] = sum;
+    a.share[((size_t)r * kMaxShares + mine.share) * 2 + 1] = sum_p;
   }
 }
 
@@ -502,14 +663,14 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
   RowCut cp = a.cut_p[(size_t)r * (g + 1) + acc];
   const float u = a.u_resample[(size_t)r * (g + 1) + acc];
   u64 w = 0, wp = 0;
-  if ((tid & 63) < shares) {
-    w = a.share[((size_t)r * kMaxShares + (tid & 63)) * 2];
-    wp = a.share[((size_t)r * kMaxShares + (tid & 63)) * 2 + 1];
+  if (tid < shares) {
+    w = a.share[((size_t)r * kMaxShares + tid) * 2];
+    wp = a.share[((size_t)r * kMaxShares + tid) * 2 + 1];
   }
-  u64 S = wave_sum_u64(w);
+  u64 S = block_sum_u64(w, s);
   const bool only_p = S == 0;        // no residual mass: the target's own distribution
   if (only_p) {
-    S = wave_sum_u64(wp);
+    S = block_sum_u64(wp, s);
     w = wp;
   }
   if (tid < shares) s.share[tid] = w;
@@ -519,7 +680,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
     if (only_p && tid == 0) raise_flag(a.ws, SD_FLAG_NO_RESIDUAL);
     const Residual f(a, v, r, acc, acc < L, cp, set);
     const int at = draw_in_shares<4>([&](int j, u64 (&x)[4]) { f(j, only_p, x); }, v.nv, shares,
-                                     (v.nv + shares - 1) / shares, draw_need(u, S), s);
+                                     Part::part_step(v.nv, shares / kFilterWaves), draw_need(u, S), s);
     if (at >= 0) id = v.off + at;
   }
   if (tid == 0) {
@@ -533,17 +694,24 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
 int draw_shares(int B, int V) {
   int c = B < 1024 ? 1024 / B : 1;
   if (c > V / 2048) c = V / 2048;
-  return c < 1 ? 1 : (c > kMaxShares ? kMaxShares : c);
+  return c < 1 ? 1 : (c > kMaxShares / kFilterWaves ? kMaxShares / kFilterWaves : c);
 }
 
 struct FilteredLayout {
   size_t cut_p, cut_q, share;
   TeamLayout team;
+  size_t bound, todo, end;
   FilteredLayout(int B, int gamma, int V)
       : cut_p(sizeof(WsHeader)),
         cut_q(align_up(cut_p + (size_t)B * (gamma + 1) * sizeof(RowCut), 256)),
         share(align_up(cut_q + (size_t)B * gamma * sizeof(RowCut), 256)),
-        team(align_up(share + (size_t)B * kMaxShares * 2 * sizeof(u64), 256), B * (2 * gamma + 1), V) {}
+        team(align_up(share + (size_t)B * kMaxShares * 2 * sizeof(u64), 256), B * (2 * gamma + 1), V),
+        bound(team.row), todo(team.row), end(team.end) {
+    const size_t rows = (size_t)B * (2 * gamma + 1);
+    if (team_size((int)rows, V) >= 2) return;
+    todo = align_up(bound + rows * sizeof(RowBound), 256);
+    end = align_up(todo + (64 + rows) * sizeof(uint32_t), 256);
+  }
 };
 
 }  // namespace
@@ -563,7 +731,7 @@ hipError_t launch_sample(const void *logits, int32_t type, int64_t stride, int R
   return launch_rows(SampleRows<ElemF16>{a}, R, V, ws, l, stream);
 }
 
-size_t accept_filtered_workspace_layout(int B, int gamma, int V) { return FilteredLayout(B, gamma, V).team.end; }
+size_t accept_filtered_workspace_layout(int B, int gamma, int V) { return FilteredLayout(B, gamma, V).end; }
 
 hipError_t launch_accept_filtered(const float *logits, const uint16_t *draft_logits,
                                   const int32_t *draft_tokens, const int32_t *verify_len,
@@ -573,16 +741,29 @@ hipError_t launch_accept_filtered(const float *logits, const uint16_t *draft_log
                                   void *workspace, hipStream_t stream) {
   const FilteredLayout l(rm.B, rm.gamma, V);
   char *w = reinterpret_cast<char *>(workspace);
+  const int rows = rm.B * (2 * rm.gamma + 1);
+  const bool team = team_size(rows, V) >= 2;
   const FilteredArgs a{logits, draft_logits, draft_tokens, verify_len, rm, u_accept, u_resample, set, V,
                        accept_len, next_token, counters, reinterpret_cast<RowCut *>(w + l.cut_p),
-                       reinterpret_cast<RowCut *>(w + l.cut_q), reinterpret_cast<u64 *>(w + l.share),
+                       reinterpret_cast<RowCut *>(w + l.cut_q), team ? nullptr : reinterpret_cast<RowBound *>(w + l.bound),
+                       reinterpret_cast<uint32_t *>(w + l.todo), reinterpret_cast<u64 *>(w + l.share),
                        reinterpret_cast<WsHeader *>(workspace)};
-  hipError_t e = launch_rows(AcceptRows{a}, rm.B * (2 * rm.gamma + 1), V, w, l.team, stream);
+  hipError_t e;
+  if (team) {
+    e = launch_team(AcceptRows{a}, rows, V, w, l.team, stream);
+  } else {
+    hipLaunchKernelGGL(k_filtered_bounds, dim3(rows), dim3(kFilterThreads), 0, stream, AcceptRows{a});
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(k_filtered_need, dim3(rm.B), dim3(kWave), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(k_filtered_cut, dim3(rows < 512 ? rows : 512), dim3(kFilterThreads), 0, stream, AcceptRows{a});
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return e;
   const int shares = draw_shares(rm.B, V);
   hipLaunchKernelGGL(k_filtered_shares, dim3(rm.B, shares), dim3(kFilterThreads), 0, stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(k_filtered_pick, dim3(rm.B), dim3(kFilterThreads), 0, stream, a, shares);
+  hipLaunchKernelGGL(k_filtered_pick, dim3(rm.B), dim3(kFilterThreads), 0, stream, a, shares * kFilterWaves);
   return hipGetLastError();
 }
 
