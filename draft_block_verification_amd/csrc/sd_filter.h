@@ -830,7 +830,14 @@ struct CutPlan {
   u64 need;        // weight at which the top-p run of a kCutMass row ends, 0 without one
   u64 above;       // kCutMass: weight of the ids from t_hi up, by the bins
   u64 in_bin;      // kCutMass: weight of the ids in the bin of the cut
+  bool listed;     // the first pass has listed the ids already (some of them under t_lo)
 };
+
+// Smallest logit that min-p keeps under maximum m.
+__device__ __forceinline__ float min_p_floor(const RowSettings &set, float m) {
+  return smallest((double)m + log2((double)set.min_p) / set.sl,
+                  [&](float l) { return l >= m || weight_finite(l, m, set.sl) >= set.min_p; });
+}
 
 // The plan of a row with largest logit m (above -inf) and `any` ids above -inf (kCutCount),
 // from the grid in LDS. Every thread gets it. Thread t holds the kPlan bins from kGrid - 1 -
@@ -841,12 +848,10 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
                                              FilterSmem &s) {
   const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
   const float lowest = key_value(kKeyNegInf + 1);
-  CutPlan p{lowest, lowest, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), 0, 0, 0};
+  CutPlan p{lowest, lowest, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), 0, 0, 0, false};
   const bool min_p = set.min_p > 0.0;
   if (p.narrow) return p;
-  const float t_m = min_p ? smallest((double)m + log2((double)set.min_p) / set.sl,
-                                     [&](float l) { return l >= m || weight_finite(l, m, set.sl) >= set.min_p; })
-                          : lowest;
+  const float t_m = min_p ? min_p_floor(set, m) : lowest;
   if (kind == kCutSum) {
     p.t_lo = p.t_hi = t_m;
     return p;
@@ -924,6 +929,29 @@ __device__ __forceinline__ void scale_table(const Grid &g, float m, double unit,
     s.scale[b] = b < kGrid && (double)b <= xm ? unit * exp2_f64(((double)b - xm) * kBinOctaves) : 0.0;
 }
 
+// Lists the ids id + i whose values v[i] `take` names. One counter update a wave and vector;
+// the lanes' places follow from the ballots.
+template <int VE, class F>
+__device__ __forceinline__ void list_ids(const float (&v)[VE], int id, F take, FilterSmem &s) {
+  u64 m[VE];
+  uint32_t count = 0;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) {
+    m[i] = __ballot(take(v[i]));
+    count += __popcll(m[i]);
+  }
+  if (count == 0) return;
+  uint32_t at = 0;
+  if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.n_cand, count);
+  at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+  for (int i = 0; i < VE; ++i) {
+    const uint32_t mine = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m[i], 0));
+    if (take(v[i]) && mine < kCandMax) s.cand[mine] = rank_word(v[i], id + i);
+    at += __popcll(m[i]);
+  }
+}
+
 // Second pass over vectors j0 .. j1 - 1: lists ids in s.cand (s.n_cand counts them) and, with
 // `sums` (s.scale set), adds up the rest of the kept ones: a weight is its bin's scale times
 // its weight inside the bin, half the work of an exponential.
@@ -931,25 +959,8 @@ template <int N = 8, class E>
 __device__ __forceinline__ void collect_pass(const RowView<E> &r, const CutPlan &p, const Grid &g, bool sums, int j0, int j1,
                                              u64 *sum, uint32_t *n, FilterSmem &s) {
   const float lo = p.t_lo, hi = p.list ? INFINITY : p.t_hi;
-  // One counter update a wave and vector; the lanes' places follow from the ballots.
   auto list = [&](const float (&v)[E::VE], int id) {
-    u64 m[E::VE];
-    uint32_t count = 0;
-#pragma unroll
-    for (int i = 0; i < E::VE; ++i) {
-      m[i] = __ballot(v[i] >= lo && v[i] < hi);
-      count += __popcll(m[i]);
-    }
-    if (count == 0) return;
-    uint32_t at = 0;
-    if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.n_cand, count);
-    at = __builtin_amdgcn_readfirstlane(at);
-#pragma unroll
-    for (int i = 0; i < E::VE; ++i) {
-      const uint32_t mine = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m[i], 0));
-      if (v[i] >= lo && v[i] < hi && mine < kCandMax) s.cand[mine] = rank_word(v[i], id + i);
-      at += __popcll(m[i]);
-    }
+    list_ids<E::VE>(v, id, [&](float l) { return l >= lo && l < hi; }, s);
   };
   if (sums && !p.list) {
     uint32_t kept_n = 0;
@@ -1094,18 +1105,114 @@ __device__ inline RowMode cut_top(const RowSettings &set, u64 top, RowCut &c) {
   return kModeTop;
 }
 
-// Reference of a row's grid: the largest of some of its first logits in each wave's share.
+// First bin from above at which the running count of s.grid reaches need, 0 when none does.
+__device__ __forceinline__ int bin_of_count(u64 need, FilterSmem &s) {
+  const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
+  u64 own = 0;
+#pragma unroll
+  for (int i = 0; i < kPlan; ++i) own += b0 - i > 0 ? (uint32_t)s.grid[b0 - i] : 0;
+  if (tid == 0) s.hit = 0;
+  u64 run = block_excl_scan_u64(own, s);
+  if (run < need && run + own >= need) {
+#pragma unroll
+    for (int i = 0; i < kPlan; ++i) {
+      const u64 n = b0 - i > 0 ? (uint32_t)s.grid[b0 - i] : 0;
+      if (run < need && run + n >= need) s.hit = b0 - i;
+      run += n;
+    }
+  }
+  __syncthreads();
+  return s.hit;
+}
+
+// From a sample of the row, 128 runs of eight vectors spread evenly: the largest logit, which
+// the grid is laid around, and for a top-k of few ids a logit that somewhat more than k ids of
+// the row reach (`guess`; NaN without one). With F the sampled fraction, the sample's rank k F
+// + 4 sqrt(k F) + 8 is wanted: then less than k ids reach the guess about as often as a
+// normal variable lies 4 deviations out, and more than can be listed seldom (both are
+// noticed, and cost a second look at the row).
 template <class E>
-__device__ __forceinline__ float row_reference(const RowView<E> &r, FilterSmem &s) {
-  const int per = (r.nv + kFilterWaves - 1) / kFilterWaves, j0 = min(r.nv, (int)(threadIdx.x >> 6) * per);
-  float ref = -INFINITY;
-  wave_ids(r, j0, min(min(r.nv, j0 + per), j0 + 128), [&](float l, int) { ref = fmaxf(ref, l); });
-  return word_value(block_max_u64(rank_word(ref, 0), s));
+__device__ __forceinline__ float row_sample(const RowView<E> &r, const RowSettings &set, CutKind kind, float *guess,
+                                            FilterSmem &s) {
+  constexpr int U = 1024 / kFilterThreads;
+  float v[U][E::VE], ref = -INFINITY;
+  const int taken = min(r.nv, 1024);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = threadIdx.x + u * kFilterThreads;
+    const int j = r.nv <= 1024 ? i : (int)((int64_t)(i >> 3) * (r.nv - 8) / 127) + (i & 7);
+#pragma unroll
+    for (int e = 0; e < E::VE; ++e) v[u][e] = -INFINITY;
+    if (i < taken) r.load(j, v[u]);
+#pragma unroll
+    for (int e = 0; e < E::VE; ++e) ref = fmaxf(ref, v[u][e]);
+  }
+  ref = word_value(block_max_u64(rank_word(ref, 0), s));
+  *guess = NAN;
+  if (kind != kCutCount) return ref;
+  const double share = (double)taken / (double)r.nv, kf = (double)set.k * share;
+  const double rank = taken == r.nv ? (double)set.k : kf + 4.0 * sqrt(kf) + 8.0;
+  if (rank / share * (1.0 + (taken == r.nv ? 0.0 : 1.5 / sqrt(rank))) > (double)kCandMax) return ref;
+  const Grid g(ref, set.T, true);
+  if (ref == -INFINITY || ref == INFINITY || !g.fine) return ref;
+  for (int b = threadIdx.x; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < E::VE; ++e) {
+      const uint32_t b = whole_part(g.pos(v[u][e]));
+      if (b > 0 && b < kGrid) atomicAdd(reinterpret_cast<uint32_t *>(&s.grid[b]), 1u);
+    }
+  __syncthreads();
+  const int bin = bin_of_count(at_least(rank), s);
+  *guess = bin > 0 ? bin_floor(g, bin) : key_value(kKeyNegInf + 1);
+  return ref;
+}
+
+// Lists the ids of vectors j0 .. j1 - 1 from `lo` up in s.cand (s.n_cand counts them).
+template <int N = 8, class E>
+__device__ __forceinline__ void list_pass(const RowView<E> &r, float lo, int j0, int j1, FilterSmem &s) {
+  wave_vecs<N>(r, j0, j1, [&](const float (&v)[E::VE], int id) {
+    list_ids<E::VE>(v, id, [&](float l) { return l >= lo; }, s);
+  });
+}
+
+// Whether n ids from `guess` up hold the first k and fit the list.
+__device__ inline bool guess_holds(const RowSettings &set, float guess, u64 n) {
+  return n <= kCandMax && (n >= (u64)set.k || guess == key_value(kKeyNegInf + 1));
+}
+
+// Plan of a row whose ids from `guess` up are listed.
+__device__ __forceinline__ CutPlan listed_plan(const RowSettings &set, float guess, float m) {
+  CutPlan p{guess, guess, true, m == INFINITY, 0, 0, 0, true};
+  if (set.min_p > 0.0 && !p.narrow) p.t_lo = fmaxf(guess, min_p_floor(set, m));
+  return p;
+}
+
+// Drops the listed ids under lo; every thread gets the rest's number.
+__device__ __forceinline__ int drop_under(float lo, int n, FilterSmem &s) {
+  u64 x[kPerThread];
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int at = threadIdx.x + i * kFilterThreads;
+    x[i] = at < n ? s.cand[at] : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.n_cand = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i)
+    if (x[i] && word_value(x[i]) >= lo) s.cand[atomicAdd(&s.n_cand, 1u)] = x[i];
+  __syncthreads();
+  return (int)s.n_cand;
 }
 
 // The cut of one row by one workgroup and the weight of what it keeps; every thread gets both.
-//   1. One pass bins the row (bin_pass), around a reference taken from a few thousand of its
-//      logits; a row whose largest logit lies past the grid is passed again around that.
+//   1. One pass bins the row (bin_pass), around a reference taken from a sample; a row whose
+//      largest logit lies past the grid is passed again around that. For a top-k of few ids
+//      the sample also gives a logit that slightly more than k ids reach: one pass lists
+//      those (list_pass), and if it got them all the row is not passed again.
 //   2. The bin that holds the cut, and the smallest logits of it and of the bin above, follow
 //      from the bins' totals (make_plan). Both steps: row_plan.
 //   3. A second pass lists the ids in that bin and, where a draw follows, sums the weights of
@@ -1129,7 +1236,25 @@ __device__ __forceinline__ RowMode row_plan(const RowView<E> &r, const RowSettin
   const int j0 = min(r.nv, wave * per), j1 = min(r.nv, j0 + per);
   const CutKind kind = o.kind = cut_kind(set, r.V, totals);
   const bool binned = kind == kCutCount || kind == kCutMass;
-  float ref = binned ? row_reference(r, s) : 0.f;
+  float guess = NAN, ref = binned ? row_sample(r, set, kind, &guess, s) : 0.f;
+  if (kind == kCutCount && guess == guess) {
+    if (tid == 0) s.n_cand = 0;
+    __syncthreads();
+    list_pass(r, guess, j0, j1, s);
+    __syncthreads();
+    const uint32_t n = s.n_cand;
+    if (guess_holds(set, guess, n)) {
+      u64 top = 0;
+      for (uint32_t i = tid; i < n; i += kFilterThreads) top = s.cand[i] > top ? s.cand[i] : top;
+      top = block_max_u64(top, s);
+      if (!top) return cut_top(set, top, c);
+      c.m = word_value(top);
+      o.ref = ref;
+      o.plan = listed_plan(set, guess, c.m);
+      return o.plan.narrow ? kModeNarrow : kModeNone;
+    }
+    __syncthreads();
+  }
   u64 any = 0, top;
   for (int attempt = 0;; ++attempt) {
     const Grid g(ref, set.T, kind == kCutCount);
@@ -1165,11 +1290,15 @@ __device__ __forceinline__ RowMode row_rest(const RowView<E> &r, const RowSettin
   const bool sums = !totals && !p.list;
   __syncthreads();
   if (sums) scale_table(g, c.m, set.unit, s);
-  if (tid == 0) s.n_cand = 0;
-  __syncthreads();
   u64 sum = 0;
   uint32_t n_sum = 0;
-  collect_pass<N>(r, p, g, sums, j0, j1, &sum, &n_sum, s);
+  if (p.listed) {
+    if (set.min_p > 0.0) drop_under(p.t_lo, (int)s.n_cand, s);
+  } else {
+    if (tid == 0) s.n_cand = 0;
+    __syncthreads();
+    collect_pass<N>(r, p, g, sums, j0, j1, &sum, &n_sum, s);
+  }
   if (totals && !p.list) {
     c.S = p.above;
     n_sum = 1;                     // some

@@ -63,7 +63,7 @@ struct RowBound {
   uint32_t open;        // 0: the cut itself is known
   uint32_t pad;
 };
-static_assert(sizeof(RowBound) == 72, "row bounds are 72 bytes");
+static_assert(sizeof(RowBound) == 80, "row bounds are 80 bytes");
 
 struct FilteredArgs {
   const float *logits;           // [cap][V]
@@ -161,8 +161,9 @@ __global__ __launch_bounds__(kFilterThreads) void k_rows_narrow(Rows rows, const
 struct TeamRow {
   u64 top, any;
   uint32_t n_list, n_above;
-  float ref;
+  float ref, guess;
   uint32_t done;     // workgroups whose bins are in
+  uint32_t pad;
   CutPlan plan;
 };
 static_assert(sizeof(TeamRow) <= 128, "team rows are 128 bytes");
@@ -184,14 +185,16 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_start(Rows rows, Team t
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
     const bool binned = kind == kCutCount || kind == kCutMass;
-    const float ref = binned ? row_reference(r, s) : 0.f;
-    if (binned)
+    float guess = NAN;
+    const float ref = binned ? row_sample(r, set, kind, &guess, s) : 0.f;
+    if (binned && guess != guess)
       for (int b = threadIdx.x; b < kGrid; b += kFilterThreads) t.grid[(size_t)row * kGrid + b] = 0;
     if (threadIdx.x == 0) {
       TeamRow &o = t.at(row);
       o.top = o.any = 0;
       o.n_list = o.n_above = o.done = 0;
       o.ref = ref;
+      o.guess = guess;
     }
   });
 }
@@ -209,18 +212,12 @@ struct Part {
   __device__ static int part_step(int nv, int C) { return (nv + C * kFilterWaves - 1) / (C * kFilterWaves); }
 };
 
-// Lowest bin that can hold the end of a top-k run, by this workgroup's own counts alone: where
-// they reach k from above, the row's do.
-__device__ __forceinline__ int lowest_bin(u64 k, FilterSmem &s) {
-  const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
-  u64 own = 0;
-#pragma unroll
-  for (int i = 0; i < kPlan; ++i) own += (uint32_t)s.grid[b0 - i];
-  if (tid == 0) s.hit = 0;
-  const u64 before = block_excl_scan_u64(own, s);
-  if (before < k && before + own >= k) s.hit = b0 - kPlan + 1;
+// Adds s.cand[0 .. nc) to the row's list.
+__device__ __forceinline__ void append_list(const Team &t, int row, TeamRow &o, uint32_t nc, FilterSmem &s) {
+  if (threadIdx.x == 0) s.key = nc ? atomicAdd(&o.n_list, nc) : 0;
   __syncthreads();
-  return s.hit;
+  for (uint32_t i = threadIdx.x; i < nc; i += kFilterThreads)
+    if (s.key + i < (uint32_t)kCandMax) t.list[(size_t)row * kCandMax + s.key + i] = s.cand[i];
 }
 
 // Bins by workgroup, then in the workspace. The row's last workgroup to arrive makes the plan:
@@ -232,24 +229,40 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_bins(Rows rows, Team
   const int row = blockIdx.y, tid = threadIdx.x;
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     const CutKind kind = cut_kind(set, r.V, Rows::kTotals);
-    const bool binned = kind == kCutCount || kind == kCutMass;
     TeamRow &o = t.at(row);
-    const Grid g(o.ref, set.T, kind == kCutCount);
-    if (binned) {
-      for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
-      __syncthreads();
-    }
     const Part part(r.nv, t.C, blockIdx.x);
-    PassOut out;
-    bin_pass(r, g, kind, bin_unit(set), part.j0, part.j1, out, s);
-    u64 top = block_max_u64(rank_word(out.best, out.at), s);
-    u64 any = kind == kCutCount ? block_sum_u64(out.any, s) : 0;
-    __syncthreads();
+    const float guess = o.guess;
+    const bool listed = kind == kCutCount && guess == guess, binned = !listed && (kind == kCutCount || kind == kCutMass);
     u64 *grid = t.grid + (size_t)row * kGrid;
-    if (binned) {
-      const int low = kind == kCutCount ? lowest_bin((u64)set.k, s) : 0;
-      for (int b = low + tid; b < kGrid; b += kFilterThreads)
-        if (s.grid[b]) atomicAdd(&grid[b], s.grid[b]);
+    u64 top = 0, any = 0;
+    if (listed) {
+      if (tid == 0) s.n_cand = 0;
+      __syncthreads();
+      list_pass(r, guess, part.j0, part.j1, s);
+      __syncthreads();
+      any = s.n_cand;
+      const uint32_t nc = min((uint32_t)any, (uint32_t)kCandMax);
+      for (uint32_t i = tid; i < nc; i += kFilterThreads) top = s.cand[i] > top ? s.cand[i] : top;
+      top = block_max_u64(top, s);
+      append_list(t, row, o, nc, s);
+    } else {
+      const Grid g(o.ref, set.T, kind == kCutCount);
+      if (binned) {
+        for (int b = tid; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
+        __syncthreads();
+      }
+      PassOut out;
+      bin_pass(r, g, kind, bin_unit(set), part.j0, part.j1, out, s);
+      top = block_max_u64(rank_word(out.best, out.at), s);
+      any = kind == kCutCount ? block_sum_u64(out.any, s) : 0;
+      __syncthreads();
+      if (binned) {
+        // Where this workgroup's own counts reach k from above, the row's do: the bins below
+        // cannot hold the end of the run.
+        const int low = kind == kCutCount ? bin_of_count((u64)set.k, s) : 0;
+        for (int b = low + tid; b < kGrid; b += kFilterThreads)
+          if (s.grid[b]) atomicAdd(&grid[b], s.grid[b]);
+      }
     }
     if (tid == 0) {
       atomicMax(&o.top, top);
@@ -263,6 +276,12 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_bins(Rows rows, Team
     top = __hip_atomic_load(&o.top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     any = __hip_atomic_load(&o.any, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (!top || kind == kCutOne) return;
+    if (listed) {
+      CutPlan p = listed_plan(set, guess, word_value(top));
+      p.narrow = p.narrow || !guess_holds(set, guess, any);
+      if (tid == 0) o.plan = p;
+      return;
+    }
     if (binned) {
       for (int b = tid; b < kGrid; b += kFilterThreads)
         s.grid[b] = __hip_atomic_load(&grid[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -284,7 +303,7 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_collect(Rows rows, T
     const u64 top = o.top;
     if (!top || kind == kCutOne) return;
     const CutPlan p = o.plan;
-    if (p.narrow) return;
+    if (p.narrow || p.listed) return;
     const float m = word_value(top);
     const Grid g(kind == kCutSum ? m : o.ref, set.T, kind == kCutCount);
     const bool sums = !Rows::kTotals && !p.list;
@@ -301,11 +320,7 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_collect(Rows rows, T
       if (n) atomicAdd(&o.n_above, n);       // one lane a wave
     }
     __syncthreads();
-    const uint32_t nc = min(s.n_cand, (uint32_t)kCandMax);
-    if (tid == 0) s.key = nc ? atomicAdd(&o.n_list, nc) : 0;
-    __syncthreads();
-    for (uint32_t i = tid; i < nc; i += kFilterThreads)
-      if (s.key + i < (uint32_t)kCandMax) t.list[(size_t)row * kCandMax + s.key + i] = s.cand[i];
+    append_list(t, row, o, min(s.n_cand, (uint32_t)kCandMax), s);
   });
 }
 
@@ -320,13 +335,13 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
     RowCut c;
     RowMode mode;
     u64 last = 0;
-    const int nc = min(o.n_list, (uint32_t)kCandMax);
+    int nc = min(o.n_list, (uint32_t)kCandMax);
     c.S = 0;
     c.m = word_value(o.top);
     if (!o.top || kind == kCutOne) {
       mode = cut_top(set, o.top, c);
     } else if (o.plan.narrow) {
-      cut_narrowing(r, set, c, s);
+      row_cut_narrowing(r, set, c, s);
       mode = kModeNone;
     } else {
       for (int i = tid; i < nc; i += kFilterThreads) s.cand[i] = t.list[(size_t)row * kCandMax + i];
@@ -336,6 +351,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
       if (sums) c.S = block_sum_u64(share, s);
       else if (!o.plan.list) c.S = o.plan.above;
       __syncthreads();
+      if (o.plan.listed && set.min_p > 0.0) nc = drop_under(o.plan.t_lo, nc, s);
       last = cut_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s);
       if (sums) add_listed(r, set, c, nc, last, step, s);
       __syncthreads();
