@@ -373,3 +373,138 @@ def test_drafter_step_verify_and_accept_together():
         want = expect()
         assert np.array_equal(vr.accept_len.cpu().numpy(), want[0])
         assert np.array_equal(vr.next_token.cpu().numpy(), want[1])
+
+
+def test_sample_many_rows():
+    """More rows than are dealt to several workgroups, each with settings of its own."""
+    rows, V = 520, 20611
+    z = head_logits(rows, V, 1)
+    z[7] = -np.inf
+    z[8, 1:] = -np.inf
+    z[9] = np.round(z[9])
+    z[10] = 0.0
+    u = np.random.default_rng(2).random(rows, dtype=np.float32)
+    settings = [f32(list(SETTINGS.values())[r % len(SETTINGS)]) for r in range(rows)]
+    col = lambda i, dt: torch.tensor([s[i] for s in settings], dtype=dt, device="cuda")
+    params = sd.SamplingParams(col(0, torch.float32), col(1, torch.int32), col(2, torch.float32), col(3, torch.float32))
+    check_rows(z, u, settings, params)
+
+
+@pytest.mark.parametrize("name", ["top_k", "usual", "all", "top_p", "min_p"])
+@pytest.mark.parametrize("V", [9001, 40009])
+def test_sample_misleading_rows(V, name):
+    """Rows of which a part says little about the rest: sorted, a likely block, likely (or
+    unlikely) ids at evenly spread places alone, ties, a few ids in one place."""
+    g = np.random.default_rng(V)
+    rows = 9
+    z = (1.5 * g.standard_normal((rows, V))).astype(np.float32)
+    z[0] = np.linspace(0, -20, V)
+    z[1] = np.linspace(-20, 0, V)
+    z[2, :V // 256] += 9
+    for r, up in ((3, 12.0), (4, -12.0)):
+        head = (-(r * V)) % 4
+        off = head - 4 if head else 0
+        nv = (V - off + 3) // 4
+        for c in range(128):
+            a = off + 4 * (c * (nv - 8) // 127)
+            z[r, max(a, 0):max(a + 32, 0)] += up
+    z[5] = 1.25
+    z[6] = -np.inf
+    z[6, V // 2 + 40:V // 2 + 100] = g.standard_normal(60)
+    z[7] = -np.inf
+    z[7, V - 1] = -3.0
+    z[8, ::2] = -np.inf
+    u = g.random(rows, dtype=np.float32)
+    s = SETTINGS[name]
+    check_rows(z, u, [f32(s)] * rows, sd.SamplingParams(**s))
+
+
+@pytest.mark.parametrize("mix", range(len(MIXES)))
+@pytest.mark.parametrize("B,g,V", [(1, 5, 70003), (3, 2, 30011), (37, 7, 20603)])
+def test_accept_filtered_long_rows(B, g, V, mix):
+    s = f32(MIXES[mix])
+    lens = [min(g, b % (g + 1)) for b in range(B)] if B > 1 else None
+    z, zq, lens, offs, ua, ur = accept_case(B, g, V, 10 * mix + V, lens=lens)
+    zqd = zq.double().numpy()
+    x = draft_by_sampling(zqd, [s] * B, mix)
+    want = F.accept(z.astype(np.float64), zqd, x, lens, offs, ua, ur, [s] * B)
+    c = lambda a: torch.from_numpy(a).cuda()
+    a, t = sd.sd_accept_filtered(c(z), zq.cuda(), c(x), c(lens), c(offs), c(ua), c(ur),
+                                 sd.SamplingParams(**MIXES[mix], n=B))
+    assert np.array_equal(a.cpu().numpy(), want[0])
+    assert np.array_equal(t.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("mix", [dict(top_p=0.9), dict(top_p=0.7, min_p=0.01), dict(top_k=30, top_p=0.95), dict(min_p=0.02)])
+@pytest.mark.parametrize("B,g,V", [(3, 64, 700), (2, 6, 24001)])
+def test_accept_filtered_tokens_at_the_border(B, g, V, mix):
+    """Equal target and drafter rows: the last kept id is accepted whatever the uniform, up to
+    a whole block of 64 and the bonus row; the next id in rank is rejected."""
+    s = f32(mix)
+    z, zq, lens, offs, ua, ur = accept_case(B, g, V, 4)
+    z = z.reshape(B, g + 1, V)
+    z[:, :g] = zq.float().numpy()
+    z = z.reshape(B * (g + 1), V)
+    zqd = zq.double().numpy()
+    x = np.zeros((B, g), dtype=np.int32)
+    for b in range(B):
+        for j in range(g):
+            n = F.filtered(zqd[b, j], *s)[1]
+            order = np.lexsort((np.arange(V), -zqd[b, j]))
+            x[b, j] = order[n - 1 if b < B - 1 or j != g // 2 else n]
+    want = F.accept(z.astype(np.float64), zqd, x, lens, offs, ua, ur, [s] * B)
+    assert want[0].tolist() == [g] * (B - 1) + [g // 2]
+    c = lambda a: torch.from_numpy(a).cuda()
+    a, t = sd.sd_accept_filtered(c(z), zq.cuda(), c(x), None, None, c(ua), c(ur), sd.SamplingParams(**mix, n=B))
+    assert np.array_equal(a.cpu().numpy(), want[0])
+    assert np.array_equal(t.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("B,g,V", [(1, 3, 30000), (4, 5, 3000), (40, 7, 20600)])
+def test_accept_filtered_graph_and_two_streams(B, g, V):
+    """A captured call replayed with new inputs between eager ones, and two calls at once on
+    streams and workspaces of their own."""
+    params = sd.SamplingParams(top_p=0.9, temperature=0.9, n=B)
+    cases = []
+    for seed in (1, 2, 3):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        z = 1.5 * torch.randn((B * (g + 1), V), device="cuda", generator=gen)
+        zq = (z.view(B, g + 1, V)[:, :g] + 0.3 * torch.randn((B, g, V), device="cuda", generator=gen)).to(torch.bfloat16).contiguous()
+        x = torch.randint(0, V, (B, g), device="cuda", generator=gen, dtype=torch.int32)
+        x[:, :g // 2] = z.view(B, g + 1, V)[:, :g // 2].argmax(2).int()
+        ua = 0.1 * torch.rand((B, g), device="cuda", generator=gen)
+        ur = torch.rand((B, g + 1), device="cuda", generator=gen)
+        cases.append((z, zq, x, ua, ur))
+    call = lambda s, **k: sd.sd_accept_filtered(s[0], s[1], s[2], None, None, s[3], s[4], params, **k)
+    eager = [[t.clone() for t in call(s)] for s in cases]
+    nbytes = sd.accept_filtered_workspace_bytes(B, g, V)
+    live = [t.clone() for t in cases[0]]
+    ws = sd.new_workspace(nbytes, "cuda")
+    out = (torch.empty(B, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda"))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        call(live, accept_len=out[0], next_token=out[1], workspace=ws)
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(live, accept_len=out[0], next_token=out[1], workspace=ws)
+    for i in (1, 2, 0, 2):
+        for a, b in zip(live, cases[i]):
+            a.copy_(b)
+        graph.replay()
+        assert torch.equal(out[0], eager[i][0]) and torch.equal(out[1], eager[i][1])
+        again = call(cases[i])
+        assert torch.equal(again[0], eager[i][0]) and torch.equal(again[1], eager[i][1])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [sd.new_workspace(nbytes, "cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got.append(call(cases[k], workspace=spaces[k]))
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert torch.equal(got[k][0], eager[k][0]) and torch.equal(got[k][1], eager[k][1])
