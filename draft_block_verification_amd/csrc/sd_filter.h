@@ -346,7 +346,6 @@ struct FilterSmem {
   int hit;
   uint32_t key;
   int32_t id;
-  float val;
   u64 acc, acc2, word;
 };
 
@@ -825,12 +824,13 @@ __device__ __forceinline__ u64 block_max_u64(u64 k, FilterSmem &s) {
 // it is listed (with `list` every id from t_lo up is).
 struct CutPlan {
   float t_lo, t_hi;
+  float t_m;       // smallest logit that min-p keeps, -inf when it is off
   bool list;
   bool narrow;     // left to the narrowing path
+  bool listed;     // the first pass has listed the ids already
   u64 need;        // weight at which the top-p run of a kCutMass row ends, 0 without one
   u64 above;       // kCutMass: weight of the ids from t_hi up, by the bins
   u64 in_bin;      // kCutMass: weight of the ids in the bin of the cut
-  bool listed;     // the first pass has listed the ids already (some of them under t_lo)
 };
 
 // Smallest logit that min-p keeps under maximum m.
@@ -848,10 +848,11 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
                                              FilterSmem &s) {
   const int tid = threadIdx.x, b0 = kGrid - 1 - kPlan * tid;
   const float lowest = key_value(kKeyNegInf + 1);
-  CutPlan p{lowest, lowest, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), 0, 0, 0, false};
+  CutPlan p{lowest, lowest, -INFINITY, false, m == INFINITY || !g.fine || !(g.pos(m) < (double)kGrid), false, 0, 0, 0};
   const bool min_p = set.min_p > 0.0;
   if (p.narrow) return p;
   const float t_m = min_p ? min_p_floor(set, m) : lowest;
+  if (min_p) p.t_m = t_m;
   if (kind == kCutSum) {
     p.t_lo = p.t_hi = t_m;
     return p;
@@ -890,7 +891,6 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
     const u64 upto = cb < 0 ? all : s.acc2;
     p.narrow = upto > kCandMax || (cb < 0 && all != any);   // fewer than k in the grid
     if (cb >= 0) p.t_lo = bin_floor(g, cb);
-    p.t_lo = fmaxf(p.t_lo, t_m);
     return p;
   }
   // That of top-p, or of min-p's bound if it is higher.
@@ -1042,34 +1042,45 @@ __device__ __forceinline__ u64 cut_list(const RowSettings &set, CutKind kind, co
   c.val = p.t_hi; c.id = 0x7fffffff;
   c.n = (int)n_above;
   if (nc == 0) return 0;
-  const float hi = p.list ? c.m : p.t_hi, per = (float)(kFilterThreads - 1) / (hi - p.t_lo);
+  float lo = p.t_lo;
+  if (lo == key_value(kKeyNegInf + 1)) {                 // every finite id is listed
+    u64 low = 0;
+    for (int i = tid; i < nc; i += kFilterThreads) low = ~s.cand[i] > low ? ~s.cand[i] : low;
+    lo = word_value(~block_max_u64(low, s));
+  }
+  const float hi = p.list ? c.m : p.t_hi, per = (float)(kFilterThreads - 1) / (hi - lo);
   auto ord = [](u64 x) { return x; };
   auto bucket = [&](u64 x) { return (int)fminf(fmaxf((hi - word_value(x)) * per, 0.f), (float)(kFilterThreads - 1)); };
   auto mass = [&](u64 x) { return to_fix(weight_finite(word_value(x), c.m, set.sl), set.unit); };
-  u64 last = 0, upto;
-  int n = nc;
-  if (kind == kCutCount && nc > set.k) {
-    last = pick(s, nc, (u64)set.k, ord, bucket, [](u64) { return 1ull; }, &upto);
-    n = set.k;
-  }
-  u64 total = 0;
-  for (int i = tid; i < nc; i += kFilterThreads)
-    if (s.cand[i] >= last) total += mass(s.cand[i]);
-  total = block_sum_u64(total, s);
-  u64 need = 0;
+  // Weight and number of the listed words from x up.
+  auto totals = [&](u64 x, u64 *n) __attribute__((always_inline)) {
+    u64 w = 0, m = 0;
+    for (int i = tid; i < nc; i += kFilterThreads) {
+      if (s.cand[i] < x) continue;
+      w += mass(s.cand[i]);
+      ++m;
+    }
+    *n = block_sum_u64(m, s);
+    return block_sum_u64(w, s);
+  };
+  u64 last = 0, upto, n;
+  if (kind == kCutCount && nc > set.k) last = pick(s, nc, (u64)set.k, ord, bucket, [](u64) { return 1ull; }, &upto);
+  u64 total = totals(last, &n), need = 0;
   if (kind == kCutCount && set.p < 1.0) need = at_least(set.p * (double)total);
   if (kind == kCutMass && p.need > 0) {
     if (p.need <= mass_above) return ~0ull;              // nothing of the list
     need = p.need - mass_above < total ? p.need - mass_above : total;
   }
-  if (need > 0) {
-    const u64 k = last;
-    last = pick(s, nc, need, ord, bucket, [&](u64 x) { return x >= k ? mass(x) : 0ull; }, &total);
-    u64 at = 0;
-    for (int i = tid; i < nc; i += kFilterThreads) at += s.cand[i] >= last;
-    n = (int)block_sum_u64(at, s);
+  const u64 first = last;
+  if (need > 0) last = pick(s, nc, need, ord, bucket, [&](u64 x) { return x >= first ? mass(x) : 0ull; }, &upto);
+  // Min-p's own run, where the list does not end with it already: the top-p share is one of
+  // the whole top-k run.
+  if (kind == kCutCount && p.t_m > -INFINITY) {
+    const u64 floor = ((u64)sort_key(p.t_m) << 32) | (uint32_t)~0x7fffffff;
+    last = floor > last ? floor : last;
   }
-  c.n = (int)n_above + n;
+  if (last != first) total = totals(last, &n);
+  c.n = (int)n_above + (int)n;
   c.S = mass_above + total;
   if (last) { c.val = word_value(last); c.id = word_id(last); }
   else { c.val = p.t_lo; c.id = 0x7fffffff; }
@@ -1185,27 +1196,8 @@ __device__ inline bool guess_holds(const RowSettings &set, float guess, u64 n) {
 
 // Plan of a row whose ids from `guess` up are listed.
 __device__ __forceinline__ CutPlan listed_plan(const RowSettings &set, float guess, float m) {
-  CutPlan p{guess, guess, true, m == INFINITY, 0, 0, 0, true};
-  if (set.min_p > 0.0 && !p.narrow) p.t_lo = fmaxf(guess, min_p_floor(set, m));
-  return p;
-}
-
-// Drops the listed ids under lo; every thread gets the rest's number.
-__device__ __forceinline__ int drop_under(float lo, int n, FilterSmem &s) {
-  u64 x[kPerThread];
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int at = threadIdx.x + i * kFilterThreads;
-    x[i] = at < n ? s.cand[at] : 0;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) s.n_cand = 0;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i)
-    if (x[i] && word_value(x[i]) >= lo) s.cand[atomicAdd(&s.n_cand, 1u)] = x[i];
-  __syncthreads();
-  return (int)s.n_cand;
+  const bool narrow = m == INFINITY;
+  return {guess, guess, set.min_p > 0.0 && !narrow ? min_p_floor(set, m) : -INFINITY, true, narrow, true, 0, 0, 0};
 }
 
 // The cut of one row by one workgroup and the weight of what it keeps; every thread gets both.
@@ -1292,9 +1284,7 @@ __device__ __forceinline__ RowMode row_rest(const RowView<E> &r, const RowSettin
   if (sums) scale_table(g, c.m, set.unit, s);
   u64 sum = 0;
   uint32_t n_sum = 0;
-  if (p.listed) {
-    if (set.min_p > 0.0) drop_under(p.t_lo, (int)s.n_cand, s);
-  } else {
+  if (!p.listed) {
     if (tid == 0) s.n_cand = 0;
     __syncthreads();
     collect_pass<N>(r, p, g, sums, j0, j1, &sum, &n_sum, s);

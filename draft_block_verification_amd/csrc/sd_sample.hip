@@ -63,7 +63,7 @@ struct RowBound {
   uint32_t open;        // 0: the cut itself is known
   uint32_t pad;
 };
-static_assert(sizeof(RowBound) == 80, "row bounds are 80 bytes");
+static_assert(sizeof(RowBound) == 72, "row bounds are 72 bytes");
 
 struct FilteredArgs {
   const float *logits;           // [cap][V]
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
     RowCut c;
     RowMode mode;
     u64 last = 0;
-    int nc = min(o.n_list, (uint32_t)kCandMax);
+    const int nc = min(o.n_list, (uint32_t)kCandMax);
     c.S = 0;
     c.m = word_value(o.top);
     if (!o.top || kind == kCutOne) {
@@ -351,7 +351,6 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
       if (sums) c.S = block_sum_u64(share, s);
       else if (!o.plan.list) c.S = o.plan.above;
       __syncthreads();
-      if (o.plan.listed && set.min_p > 0.0) nc = drop_under(o.plan.t_lo, nc, s);
       last = cut_list(set, kind, o.plan, nc, sums || o.plan.list ? o.n_above : 1, c, s);
       if (sums) add_listed(r, set, c, nc, last, step, s);
       __syncthreads();

@@ -508,3 +508,33 @@ def test_accept_filtered_graph_and_two_streams(B, g, V):
         torch.cuda.synchronize()
         for k in range(2):
             assert torch.equal(got[k][0], eager[k][0]) and torch.equal(got[k][1], eager[k][1])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,rows", [(1000, 24), (40009, 24), (20611, 560)])
+def test_sample_three_filters(V, rows, dtype):
+    """Top-k, top-p and min-p together, each of them the shortest run in some rows: the share of
+    top-p is one of the top-k run, whatever min-p leaves of it."""
+    g = np.random.default_rng(rows + V)
+    z = head_logits(rows, V, rows)
+    z[::4, g.random(V) < 0.98] = -np.inf
+    settings = [(float(np.float32(t)), int(k), float(np.float32(p)), float(np.float32(m)))
+                for t, k, p, m in zip(g.choice([0.6, 0.8, 1.1], rows), g.choice([15, 80, 320], rows),
+                                      g.choice([0.8, 0.9, 0.95], rows), g.choice([0.01, 0.03, 0.07], rows))]
+    col = lambda i, dt: torch.tensor([s[i] for s in settings], dtype=dt, device="cuda")
+    params = sd.SamplingParams(col(0, torch.float32), col(1, torch.int32), col(2, torch.float32), col(3, torch.float32))
+    check_rows(z, g.random(rows, dtype=np.float32), settings, params, TYPES[dtype])
+
+
+@pytest.mark.parametrize("B,g,V", [(3, 5, 2000), (2, 4, 30011)])
+def test_accept_filtered_three_filters(B, g, V):
+    mix = dict(temperature=0.8, top_k=90, top_p=0.9, min_p=0.04)
+    s = f32(mix)
+    z, zq, lens, offs, ua, ur = accept_case(B, g, V, 21)
+    zqd = zq.double().numpy()
+    x = draft_by_sampling(zqd, [s] * B, 2)
+    want = F.accept(z.astype(np.float64), zqd, x, lens, offs, ua, ur, [s] * B)
+    c = lambda a: torch.from_numpy(a).cuda()
+    a, t = sd.sd_accept_filtered(c(z), zq.cuda(), c(x), None, None, c(ua), c(ur), sd.SamplingParams(**mix, n=B))
+    assert np.array_equal(a.cpu().numpy(), want[0])
+    assert np.array_equal(t.cpu().numpy(), want[1])
