@@ -1073,10 +1073,10 @@ __device__ __forceinline__ u64 cut_list(const RowSettings &set, CutKind kind, co
   }
   const u64 first = last;
   if (need > 0) last = pick(s, nc, need, ord, bucket, [&](u64 x) { return x >= first ? mass(x) : 0ull; }, &upto);
-  // Min-p's own run, where the list does not end with it already: the top-p share is one of
-  // the whole top-k run.
+  // Min-p's own run if it ends earlier, not before top-p's share is taken: that is one of the
+  // whole top-k run. Nothing under the list is kept, whatever min-p says.
   if (kind == kCutCount && p.t_m > -INFINITY) {
-    const u64 floor = ((u64)sort_key(p.t_m) << 32) | (uint32_t)~0x7fffffff;
+    const u64 floor = ((u64)sort_key(fmaxf(p.t_m, p.t_lo)) << 32) | (uint32_t)~0x7fffffff;
     last = floor > last ? floor : last;
   }
   if (last != first) total = totals(last, &n);

@@ -538,3 +538,24 @@ def test_accept_filtered_three_filters(B, g, V):
     a, t = sd.sd_accept_filtered(c(z), zq.cuda(), c(x), None, None, c(ua), c(ur), sd.SamplingParams(**mix, n=B))
     assert np.array_equal(a.cpu().numpy(), want[0])
     assert np.array_equal(t.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("B,g,V", [(60, 3, 1200), (60, 2, 21000)])
+def test_accept_filtered_short_runs(B, g, V):
+    """Top-k runs that end before min-p's: what min-p alone would keep has no probability."""
+    r = np.random.default_rng(V)
+    settings = [(float(np.float32(0.8 + 0.4 * r.random())), int(r.integers(2, 9)), 1.0,
+                 float(np.float32(0.002 + 0.02 * r.random()))) for _ in range(B)]
+    z, zq, lens, offs, ua, ur = accept_case(B, g, V, 8)
+    zqd = zq.double().numpy()
+    r2 = np.random.default_rng(1)
+    x = np.array([[F.draw(F.filtered(zqd[b, j], *settings[b])[0], r2.random()) for j in range(g)] for b in range(B)], dtype=np.int32)
+    col = lambda i, dt: torch.tensor([s[i] for s in settings], dtype=dt, device="cuda")
+    params = sd.SamplingParams(col(0, torch.float32), col(1, torch.int32), col(2, torch.float32), col(3, torch.float32))
+    c = lambda a: torch.from_numpy(a).cuda()
+    for seed in range(4):
+        ur = np.random.default_rng(seed).random((B, g + 1), dtype=np.float32)
+        want = F.accept(z.astype(np.float64), zqd, x, lens, offs, ua, ur, settings)
+        a, t = sd.sd_accept_filtered(c(z), zq.cuda(), c(x), None, None, c(ua), c(ur), params)
+        assert np.array_equal(a.cpu().numpy(), want[0])
+        assert np.array_equal(t.cpu().numpy(), want[1])
