@@ -34,6 +34,15 @@ int32_t check_sizes(int32_t B, int32_t gamma, int32_t d, int32_t V) {
   return SD_OK;
 }
 
+// Rows that one call of the filtered samplers takes: a workgroup of 512 threads each.
+constexpr int64_t kMaxFilterRows = 1 << 22;
+
+int32_t check_filtered(int32_t B, int32_t gamma, int32_t V) {
+  const int32_t st = check_sizes(B, gamma, 8, V);
+  if (st != SD_OK) return st;
+  return (int64_t)B * (2 * gamma + 1) > kMaxFilterRows ? SD_ESHAPE : SD_OK;
+}
+
 bool known_type(int32_t t) { return t == SD_F32 || t == SD_BF16 || t == SD_F16; }
 
 size_t type_size(int32_t t) { return t == SD_F32 ? 4 : 2; }
@@ -639,7 +648,7 @@ int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int3
 }
 
 size_t sd_sample_workspace_bytes(int32_t R, int32_t V) {
-  if (R < 1 || V < 1 || V > kMaxVocab) return 0;
+  if (R < 1 || R > kMaxFilterRows || V < 1 || V > kMaxVocab) return 0;
   return sample_workspace_layout(R, V);
 }
 
@@ -648,7 +657,7 @@ int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits_stride
                   int32_t *tokens, int64_t token_stride, int32_t *kept, float *logprob,
                   void *workspace, size_t workspace_bytes, void *stream) {
   if (!logits || !u || !sampling || !tokens || !known_type(logits_type)) return SD_EINVAL;
-  if (R < 1 || V < 1 || V > kMaxVocab || rows_per_request < 1 || logits_stride < V ||
+  if (R < 1 || R > kMaxFilterRows || V < 1 || V > kMaxVocab || rows_per_request < 1 || logits_stride < V ||
       logits_stride > ((int64_t)1 << 40) || token_stride < 1 || token_stride > ((int64_t)1 << 30))
     return SD_ESHAPE;
   if (!aligned(logits, type_size(logits_type)) || !aligned(u, 4) || !aligned(tokens, 4) ||
@@ -662,7 +671,7 @@ int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits_stride
 }
 
 size_t sd_accept_filtered_workspace_bytes(int32_t B, int32_t gamma, int32_t V) {
-  if (check_sizes(B, gamma, 8, V) != SD_OK) return 0;
+  if (check_filtered(B, gamma, V) != SD_OK) return 0;
   return accept_filtered_workspace_layout(B, gamma, V);
 }
 
@@ -677,7 +686,7 @@ int32_t sd_accept_filtered(const float *logits, const uint16_t *draft_logits,
       !accept_len || !next_token)
     return SD_EINVAL;
   if ((verify_len == nullptr) != (row_offsets == nullptr)) return SD_EINVAL;
-  if (check_sizes(B, gamma, 8, V) != SD_OK) return SD_ESHAPE;
+  if (check_filtered(B, gamma, V) != SD_OK) return SD_ESHAPE;
   if (!aligned(logits, 16) || !aligned(draft_logits, 16) || !aligned(draft_tokens, 4) ||
       !aligned(u_accept, 4) || !aligned(u_resample, 4) || !aligned(accept_len, 4) ||
       !aligned(next_token, 4) || (counters && !aligned(counters, 8)) || !aligned_settings(*sampling) ||

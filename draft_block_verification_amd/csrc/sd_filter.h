@@ -24,7 +24,8 @@
 
 namespace sdv {
 
-constexpr int kFilterThreads = 512;
+constexpr int kFilterThreads = 512;    // three workgroups a compute unit in 80 registers a
+                                     // lane; 1024 threads or fewer workgroups were no faster
 constexpr int kFilterWaves = kFilterThreads / kWave;
 constexpr int kGrid = 4096;          // bins of the first pass's histogram, half on each side
                                      // of its reference logit

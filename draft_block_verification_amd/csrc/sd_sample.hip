@@ -122,6 +122,10 @@ struct AcceptRows {
 };
 
 // ------------------------------------------------------------------ one workgroup a row
+// 1088 rows of 151936 fp32 ids under top-p (662 MB): 360 - 380 us. The first pass takes 151 of
+// them (134 without its bins: the rate at which rows arrive), the second, which also forms the
+// weights of what is kept and lists the bin of the cut, the rest (100 for the rows alone, as
+// more rows are in work than the memory-side cache holds).
 // todo[row] says whether the row is left to k_rows_narrow: its code would cost the others
 // registers, and with them one workgroup in three on each compute unit.
 template <class Rows>
@@ -155,7 +159,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_rows_narrow(Rows rows, const
 }
 
 // ------------------------------------------------------------------ several workgroups a row
-// For few rows: the steps of row_cut as launches, a row's vectors dealt to C workgroups in
+// For few rows: the steps of row_plan and row_rest as launches, a row's vectors dealt to C workgroups in
 // contiguous shares. Bins and lists meet in the workspace through integer atomics, whose
 // order does not change a sum; the list is ranked before it is used.
 struct TeamRow {
@@ -360,8 +364,12 @@ __global__ __launch_bounds__(kFilterThreads) void k_team_finish(Rows rows, Team 
   });
 }
 
-// Workgroups a row's vectors are dealt to: enough for about two on every compute unit, each
-// with at least 4096 ids; 1: the row is one workgroup's.
+// Workgroups a row's vectors are dealt to: 1024 in all, each with at least 10240 ids (its bins
+// cost it the same whatever their number); 1: the row is one workgroup's. Measured (us):
+//   128 bf16 rows of 129280 ids, workgroups in all: 512 85, 768 78, 1024 76, 2048 81
+//   33 rows of 151936 ids (a block of 16), ids a workgroup: 4096 58, 10240 47, 24576 47
+//   one row of 151936 ids: 4096 28.2, 10240 28.6, 24576 31.5
+//   1088 rows of 151936 ids: one workgroup 362, two 370 - 377
 int team_size(int rows, int V) {
   int c = rows < 1024 ? 1024 / rows : 0;
   if (c > V / 10240) c = V / 10240;
@@ -469,7 +477,10 @@ __device__ __forceinline__ int first_rejection(const FilteredArgs &a, int r, int
 // Many rows: two passes over all of them cost twice the bytes, and the second one is needed of
 // few. The first pass leaves bounds (k_filtered_bounds) that decide nearly every position: the
 // weight of a top-p run is its needed weight and less than one id more, so only a token in the
-// bin of the cut or a uniform within some 1e-5 of the border stays open. Rows of open
+// bin of the cut or a uniform within some 1e-5 of the border stays open. 128 ragged requests
+// of up to 16 drafts, 129280 ids, top-p (some 1800 rows in use, 687 MB): 257 us for the bounds,
+// 8 to decide, 42 for the rows that are cut, 70 + 8 for the draws; cutting every row took
+// 395 - 440 in place of the first three. Rows of open
 // positions up to the first sure rejection, and of that one (or the bonus row), whose
 // distribution is drawn from, are listed (k_filtered_need) and cut (k_filtered_cut).
 __global__ __launch_bounds__(kFilterThreads, 6) void k_filtered_bounds(AcceptRows rows) {
@@ -704,8 +715,8 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
   }
 }
 
-// Shares of the draw's row: about two workgroups on every compute unit over all requests, at
-// least 2048 ids each.
+// Workgroups that sum the draw's row of a request, at least 2048 ids each, 1024 in all: one
+// request of 151936 ids 7.7 us, 128 requests of 129280 70 us.
 int draw_shares(int B, int V) {
   int c = B < 1024 ? 1024 / B : 1;
   if (c > V / 2048) c = V / 2048;

@@ -603,8 +603,8 @@ typedef struct sd_sampling {
  *   workspace sd_sample_workspace_bytes(R, V) bytes
  * Weights are formed in fp64 and summed exactly in units of about 2^-46 of the largest: an id
  * whose weight is below half a unit is never drawn.
- * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (R < 1, V outside [1, 2^21],
- * rows_per_request < 1, short strides), SD_EALIGN (an array not aligned to its elements),
+ * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (R outside [1, 2^22], V outside
+ * [1, 2^21], rows_per_request < 1, short strides), SD_EALIGN (an array not aligned to its elements),
  * SD_EWORKSPACE, SD_EDEVICE.
  */
 SD_API size_t sd_sample_workspace_bytes(int32_t R, int32_t V);
@@ -631,7 +631,7 @@ SD_API int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits
  *   sampling  settings of each request (temperature 0: both sides keep their likeliest id)
  *   workspace sd_accept_filtered_workspace_bytes(B, gamma, V) bytes
  * A target row without any logit above -inf emits -1 and raises SD_FLAG_EMPTY_ROW.
- * Errors: as for sd_accept_rejection.
+ * Errors: as for sd_accept_rejection; SD_ESHAPE also for B (2 gamma + 1) over 2^22.
  */
 SD_API size_t sd_accept_filtered_workspace_bytes(int32_t B, int32_t gamma, int32_t V);
 SD_API int32_t sd_accept_filtered(const float *logits, const uint16_t *draft_logits,

@@ -185,3 +185,18 @@ def test_statement_acceptance_is_lossless():
         res = res / res.sum() if res.sum() > 0 else pp
         emitted = qq * keep + (qq * (1 - keep)).sum() * res
         assert np.allclose(emitted, pp, atol=1e-15)
+
+
+def test_row_limits():
+    """One call of the filtered samplers takes up to 2^22 rows."""
+    assert sd.sample_workspace_bytes(1 << 22, 10) > 0 and sd.sample_workspace_bytes((1 << 22) + 1, 10) == 0
+    assert sd.accept_filtered_workspace_bytes(1 << 15, 63, 10) > 0
+    assert sd.accept_filtered_workspace_bytes(1 << 15, 64, 10) == 0
+    assert sd.accept_filtered_workspace_bytes(1 << 24, 60, 10) == 0
+    s = Four(None, None, None, None)
+    args = [FAKE, 0, i64(10), (1 << 22) + 1, 10, FAKE, ctypes.byref(s), 1, FAKE, i64(1), None, None, FAKE,
+            sz(1 << 40), None]
+    assert lib.sd_sample(*args) == 2
+    args = [FAKE] * 3 + [None, None, FAKE, FAKE, ctypes.byref(s), 1 << 15, 64, 10, FAKE, FAKE, None, FAKE,
+                         sz(1 << 40), None]
+    assert lib.sd_accept_filtered(*args) == 2
