@@ -302,15 +302,10 @@ __device__ inline f32x4 mfma_mx(const u32x4 &a, int sa, const u32x4 &b, int sb, 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aa, bb, c, 4, 4, SA, sa, SB, sb);
 }
 
-// The byte selectors are immediates: a call per (tile % 4, tile % 4) pair.
+// The byte selectors are immediates: a call per (id fragment, row fragment) pair.
 template <int SA>
 __device__ inline f32x4 mfma_mx_b(int sel_b, const u32x4 &a, int sa, const u32x4 &b, int sb, f32x4 c) {
-  switch (sel_b) {
-    case 0: return mfma_mx<SA, 0>(a, sa, b, sb, c);
-    case 1: return mfma_mx<SA, 1>(a, sa, b, sb, c);
-    case 2: return mfma_mx<SA, 2>(a, sa, b, sb, c);
-    default: return mfma_mx<SA, 3>(a, sa, b, sb, c);
-  }
+  return sel_b == 0 ? mfma_mx<SA, 0>(a, sa, b, sb, c) : mfma_mx<SA, 1>(a, sa, b, sb, c);
 }
 
 __device__ inline f32x4 mfma_mx_sel(int sel_a, int sel_b, const u32x4 &a, int sa, const u32x4 &b, int sb, f32x4 c) {
@@ -346,7 +341,7 @@ __device__ inline void store4(const MxGemmArgs &a, int m, int v, const f32x4 &z)
 }
 
 // ---------------------------------------------------------- few hidden rows
-// Up to 16 MT rows: the LM head's bytes bound the call. One workgroup per 64 ids; its four
+// Up to 16 MT rows, MT at most 2: the LM head's bytes bound the call. One workgroup per 64 ids; its four
 // waves take the 128-column steps in turn (wave w steps w, w + 4, ..), so a workgroup reads
 // one contiguous 17 KB run a round, straight into registers: each weight is used by one wave
 // only, so LDS would add a copy and share nothing. The hidden fragments are read by every
@@ -356,6 +351,7 @@ __device__ inline void store4(const MxGemmArgs &a, int m, int v, const f32x4 &z)
 // is partly in the memory-side cache (repeated calls), 78 us = 6.3 TB/s from memory.
 template <int MT>
 __global__ __launch_bounds__(256) void k_mx_skinny(MxGemmArgs a) {
+  static_assert(MT <= 2, "selectors of two row fragments");
   constexpr int D = 3;                 // steps a wave has in flight
   constexpr int LDR = 68;              // floats from row to row in LDS: rows start on other banks
   __shared__ float red[4][16 * MT * LDR];
