@@ -692,6 +692,8 @@ def _current(stream, dev: torch.device):
 def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
     """Memory for a call on `stream`: taken on that stream, so that neither an earlier user of
     it is still at work nor a later one begins before the call is over."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     with _current(stream, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
 
@@ -729,14 +731,18 @@ def sd_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     _rows(x, "x")
     rows, d = x.shape
     kp = mxfp4_columns(d)
+    dev = x.device
     if codes is None:
-        codes = _empty((rows, kp // 2), torch.uint8, x.device, stream)
+        codes = _empty((rows, kp // 2), torch.uint8, dev, stream)
+    else:
+        _need(codes, "codes", torch.uint8, (rows, kp // 2))
+        _same_device(dev, codes=codes)
     if scales is None:
-        scales = _empty((rows, kp // 32), torch.uint8, x.device, stream)
-    _need(codes, "codes", torch.uint8, (rows, kp // 2))
-    _need(scales, "scales", torch.uint8, (rows, kp // 32))
-    _same_device(x.device, codes=codes, scales=scales)
-    _call("sd_mxfp4_quantize", x.device, stream, _ptr(x), _TYPE_CODES[x.dtype], rows, d,
+        scales = _empty((rows, kp // 32), torch.uint8, dev, stream)
+    else:
+        _need(scales, "scales", torch.uint8, (rows, kp // 32))
+        _same_device(dev, scales=scales)
+    _call("sd_mxfp4_quantize", dev, stream, _ptr(x), _TYPE_CODES[x.dtype], rows, d,
           _row_stride(x), _ptr(codes), _ptr(scales))
     return codes, scales
 
@@ -751,10 +757,13 @@ def sd_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
     _need(codes, "codes", torch.uint8, (rows, kp // 2))
     _need(scales, "scales", torch.uint8, (rows, kp // 32))
     if out is None:
+        if dtype not in _TYPE_CODES:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
         out = _empty((rows, d), dtype, codes.device, stream)
-    _rows(out, "out")
-    if tuple(out.shape) != (rows, d):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, d)}")
+    else:
+        _rows(out, "out")
+        if tuple(out.shape) != (rows, d):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, d)}")
     _same_device(codes.device, scales=scales, out=out)
     _call("sd_mxfp4_dequantize", codes.device, stream, _ptr(codes), _ptr(scales), rows, d,
           _ptr(out), _TYPE_CODES[out.dtype], _row_stride(out))
@@ -807,10 +816,13 @@ def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
         raise ValueError("lm_head must be [V][d] with the hidden size of `hidden`")
     dev = hidden.device
     if logits is None:
+        if dtype not in _TYPE_CODES:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
         logits = _empty((M, lm_head.V), dtype, dev, stream)
-    _rows(logits, "logits")
-    if tuple(logits.shape) != (M, lm_head.V):
-        raise ValueError(f"logits has shape {tuple(logits.shape)}, expected {(M, lm_head.V)}")
+    else:
+        _rows(logits, "logits")
+        if tuple(logits.shape) != (M, lm_head.V):
+            raise ValueError(f"logits has shape {tuple(logits.shape)}, expected {(M, lm_head.V)}")
     if workspace is None:
         workspace = _workspace(mxfp4_logits_workspace_bytes(M, d), dev, stream)
     _same_device(dev, lm_head=lm_head, logits=logits, workspace=workspace)
@@ -905,13 +917,16 @@ def sd_sample(logits: torch.Tensor, u: torch.Tensor, params: SamplingParams,
         raise ValueError(f"{R} rows cannot share the settings of {params.n} requests")
     if tokens is None:
         tokens = _empty(R, torch.int32, dev, stream)
+    else:
+        _vector(tokens, "tokens", torch.int32, R)
     if kept is None:
         kept = _empty(R, torch.int32, dev, stream)
+    else:
+        _need(kept, "kept", torch.int32, (R,))
     if logprob is None:
         logprob = _empty(R, torch.float32, dev, stream)
-    _vector(tokens, "tokens", torch.int32, R)
-    _need(kept, "kept", torch.int32, (R,))
-    _need(logprob, "logprob", torch.float32, (R,))
+    else:
+        _need(logprob, "logprob", torch.float32, (R,))
     if workspace is None:
         workspace = _workspace(sample_workspace_bytes(R, V), dev, stream)
     _same_device(dev, u=u, params=params, tokens=tokens, kept=kept, logprob=logprob,
