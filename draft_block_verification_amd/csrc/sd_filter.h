@@ -1139,10 +1139,10 @@ __device__ __forceinline__ int bin_of_count(u64 need, FilterSmem &s) {
 
 // From a sample of the row, 128 runs of eight vectors spread evenly: the largest logit, which
 // the grid is laid around, and for a top-k of few ids a logit that somewhat more than k ids of
-// the row reach (`guess`; NaN without one). With F the sampled fraction, the sample's rank k F
-// + 4 sqrt(k F) + 8 is wanted: then less than k ids reach the guess about as often as a
-// normal variable lies 4 deviations out, and more than can be listed seldom (both are
-// noticed, and cost a second look at the row).
+// the row reach (`guess`; NaN without one). With F the sampled fraction, the sample's rank
+// k F + 4 sqrt(k F) + 6 is taken: less than k ids reach it, or more than can be listed, about
+// as seldom as a normal variable lies 4 deviations out. Both are noticed; they cost a second
+// look at the row, and a row of several workgroups the narrowing path (some 200 us).
 template <class E>
 __device__ __forceinline__ float row_sample(const RowView<E> &r, const RowSettings &set, CutKind kind, float *guess,
                                             FilterSmem &s) {
@@ -1163,8 +1163,8 @@ __device__ __forceinline__ float row_sample(const RowView<E> &r, const RowSettin
   *guess = NAN;
   if (kind != kCutCount) return ref;
   const double share = (double)taken / (double)r.nv, kf = (double)set.k * share;
-  const double rank = taken == r.nv ? (double)set.k : kf + 4.0 * sqrt(kf) + 8.0;
-  if (rank / share * (1.0 + (taken == r.nv ? 0.0 : 1.5 / sqrt(rank))) > (double)kCandMax) return ref;
+  const double rank = taken == r.nv ? (double)set.k : kf + 4.0 * sqrt(kf) + 6.0;
+  if (rank / share * (1.0 + (taken == r.nv ? 0.0 : 4.0 / sqrt(rank))) > (double)kCandMax) return ref;
   const Grid g(ref, set.T, true);
   if (ref == -INFINITY || ref == INFINITY || !g.fine) return ref;
   for (int b = threadIdx.x; b < kGrid; b += kFilterThreads) s.grid[b] = 0;
