@@ -410,13 +410,14 @@ __device__ __forceinline__ void sort_desc(FilterSmem &s, int n) {
 // ------------------------------------------------------------------ the narrowing path
 // Bins of the mass histogram: equal steps of (m - l), which falls as the rank rises, over
 // max(33 T, 16). A logit past that range weighs under 2^-47 (33 T are 47.6 octaves), so its
-// summed weight is 0 and no filter but the count of top-k can reach it: those ids are
-// counted, not binned. Equal steps spread a row's logits over many bins, so that lanes
-// seldom meet on one LDS counter and a bin holds few ids to rank.
+// summed weight is 0 and no filter but the count of top-k can end among those ids: the last
+// bin stands for them, without weight. Equal steps spread a row's logits over many bins, so
+// that lanes seldom meet on one LDS counter and a bin holds few ids to rank; the last bin's
+// ids are counted in registers.
 struct BinScale {
   float m, scale;
   __device__ BinScale(float m_, float T) : m(m_), scale((float)(kBins - 1) / fmaxf(33.f * T, 16.f)) {}
-  // Bin of a logit, kBins - 1 and up: past the range.
+  // Bin of a logit, kBins - 1 past the range.
   __device__ int of(float l) const {
     const float d = l == m ? 0.f : (m - l) * scale;
     return d < (float)(kBins - 1) ? (int)d : kBins - 1;
@@ -599,8 +600,12 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
 
 // The narrowing path: the cut of a row whose largest logit c.m is known, for every row that the single-pass path leaves: more ids at the cut than are ranked
 // in LDS, a top-k past them, logits too large for the grid's arithmetic, or +inf among them.
+// totals (as for row_plan): probabilities are taken from the cut, and an id past the range has
+// one as long as it is kept. A draw sums such weights to 0, so it does without the last member
+// of a top-k run that ends there: c.n is right, and ids behind that run are not told apart.
 template <class E>
-__device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
+__device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSettings &set, bool totals, RowCut &c,
+                                              FilterSmem &s) {
   const int tid = threadIdx.x, wave = tid >> 6;
   c.val = -INFINITY;
   c.id = -1;
@@ -639,12 +644,12 @@ __device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSett
     total = block_sum_u64(total, s);
     in_bins = block_sum_u64(in_bins, s);
     CutAt at{kKeyNegInf, -1, in_bins + past, total};
-    // A top-k run that ends among ids without weight: they count, and cannot be drawn.
-    if ((u64)set.k >= in_bins && (u64)set.k < at.n) at.n = set.k;
+    const u64 rankable = totals ? at.n : in_bins;
+    if ((u64)set.k >= rankable && (u64)set.k < at.n) at.n = set.k;
     // First the end of the top-k run, then that of the top-p run inside it.
 #pragma unroll 1
     for (int by_mass = 0; by_mass < 2; ++by_mass) {
-      if (by_mass ? !(set.p < 1.0) : !((u64)set.k < in_bins)) continue;
+      if (by_mass ? !(set.p < 1.0) : !((u64)set.k < rankable)) continue;
       const u64 need = by_mass ? at_least(set.p * (double)at.mass) : (u64)set.k;
       // The histogram again: narrowing the top-k run may have overwritten it.
       __syncthreads();
@@ -657,6 +662,7 @@ __device__ __forceinline__ void cut_narrowing(const RowView<E> &r, const RowSett
         atomicAdd(&s.cnt[b], 1u);
         atomicAdd(&s.mass[b], to_fix(weight(l, c.m, set.sl), set.unit));
       });
+      if (tid == 0) s.cnt[kBins - 1] = past;
       __syncthreads();
       u64 before, n_before = 0, mass_before = 0;
       const int bin = find_bin(s, need, [&](int b) { return by_mass ? s.mass[b] : (u64)s.cnt[b]; }, &before);
@@ -1317,13 +1323,14 @@ __device__ __forceinline__ RowMode row_cut(const RowView<E> &r, const RowSetting
 
 // The cut of a row that row_cut leaves (c.S unset).
 template <class E>
-__device__ __forceinline__ void row_cut_narrowing(const RowView<E> &r, const RowSettings &set, RowCut &c, FilterSmem &s) {
+__device__ __forceinline__ void row_cut_narrowing(const RowView<E> &r, const RowSettings &set, bool totals, RowCut &c,
+                                                  FilterSmem &s) {
   const int per = (r.nv + kFilterWaves - 1) / kFilterWaves, j0 = min(r.nv, (int)(threadIdx.x >> 6) * per);
   float m = -INFINITY;
   wave_ids<4>(r, j0, min(r.nv, j0 + per), [&](float l, int) { m = fmaxf(m, l); });
   c.m = word_value(block_max_u64(rank_word(m, 0), s));
   c.S = 0;
-  cut_narrowing(r, set, c, s);
+  cut_narrowing(r, set, totals, c, s);
 }
 
 // ------------------------------------------------------------------ the draw

@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_rows_narrow(Rows rows, const
   if (!todo[row]) return;
   rows.with(row, [&](const auto &r, const RowSettings &set) {
     RowCut c;
-    row_cut_narrowing(r, set, c, s);
+    row_cut_narrowing(r, set, Rows::kTotals, c, s);
     rows.finish(row, r, set, c, kModeNone, 0, 0, 0, 0, s);
   });
 }
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(kFilterThreads, 6) void k_team_cut(Rows rows, Team 
     if (one) {
       mode = cut_top(set, top, c);
     } else if (p.narrow) {
-      row_cut_narrowing(r, set, c, s);
+      row_cut_narrowing(r, set, Rows::kTotals, c, s);
     } else {
       nc = min(from_all(&o.n_list), (uint32_t)kCandMax);
       for (int i = tid; i < nc; i += kFilterThreads) s.cand[i] = from_all(&t.list[(size_t)row * kCandMax + i]);
@@ -561,7 +561,7 @@ __global__ __launch_bounds__(kFilterThreads, 4) void k_filtered_cut(AcceptRows r
       RowCut c;
       u64 last = 0;
       if (b.plan.narrow) {
-        row_cut_narrowing(r, set, c, s);
+        row_cut_narrowing(r, set, true, c, s);
       } else {
         c.m = b.m;
         const RowPlan o{kCutMass, b.ref, b.plan};
