@@ -900,10 +900,12 @@ __device__ __forceinline__ CutPlan make_plan(const RowSettings &set, CutKind kin
     if (cb >= 0) p.t_lo = bin_floor(g, cb);
     return p;
   }
-  // That of top-p, or of min-p's bound if it is higher.
+  // That of top-p, or of min-p's bound if it is higher. A bound under bin 1 (bin 0 is not read)
+  // parts ids without weight: the bins name no cut, min_p_floor's value alone states the run.
+  p.t_lo = p.t_hi = t_m;
   if (min_p) {
-    const int mb = max(0, (int)g.pos(t_m));
-    if (mb > cb) { cb = mb; p.need = 0; }
+    const int mb = (int)whole_part(g.pos(t_m));
+    if (mb > max(cb, 0)) { cb = mb; p.need = 0; }
   }
   // No bin holds more ids than its weights say: each is at least 1 (to 2e-14).
   const double per_id = 1.001 / bin_unit(set);

@@ -1,5 +1,5 @@
 """Filtered sampling and acceptance at the ends of their ranges, on the GPU against the 64-bit
-statement: runs that end among ids of next to no weight.
+statement: runs that end among ids of next to no weight, thresholds under the binned range.
 
 Decisions are whole numbers and must be equal. Every drafted token and uniform here is chosen
 so that the statement's decision holds by a wide margin (stated in each test), far over the
@@ -95,3 +95,34 @@ def test_top_k_ends_far_below_the_maximum(V, bulk, T):
             assert got[1][b] == want[1][b] == 7
         else:
             assert F.filtered(z[b, want[0][b]].astype(np.float64), *settings[b])[0][got[1][b]] > 0
+
+
+@pytest.mark.parametrize("V,B", [(4001, 2), (24001, 2)])
+def test_min_p_under_the_binned_range(V, B):
+    """A min-p border more than 33 temperatures below the maximum, many ids there: the row's
+    weight is that of its 1400 equal likely ids, p' = 1 / 1400, against a q' of 1 / 700 (the
+    acceptance probability is a half, to 1e-11): accepted at 0.4, rejected at 0.6."""
+    g, n = 3, 1400
+    r = np.random.default_rng(V)
+    low = -33.0 + 0.5 * 33.0 / 2048          # the lowest bin's middle
+    z = np.full((B, g + 1, V), -60.0, dtype=np.float32)
+    zq = np.full((B, g, V), -60.0, dtype=np.float32)
+    x = np.zeros((B, g), dtype=np.int32)
+    for b in range(B):
+        for j in range(g + 1):
+            ids = r.permutation(V)
+            z[b, j, ids[:n]] = 0.0
+            z[b, j, ids[n:2 * n]] = low
+            if j < g:
+                zq[b, j, ids[:n // 2]] = 0.0
+                x[b, j] = ids[r.integers(n // 2)]
+    ua = np.full((B, g), 0.4, dtype=np.float32)
+    for b in range(B):
+        ua[b, 1 + b % 2] = 0.6
+    settings = [(1.0, 0, 1.0, float(np.float32(1e-15)))] * B
+    # the residual's 700 equal ids: uniforms in the middle of one's share
+    ur = ((np.floor(r.random((B, g + 1)) * 600) + 0.5) / 700).astype(np.float32)
+    got, want = accept(z, zq, x, ua, ur, settings)
+    assert want[0] == [1 + b % 2 for b in range(B)]
+    assert got[0] == want[0]
+    assert got[1] == want[1]
