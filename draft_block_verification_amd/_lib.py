@@ -293,6 +293,20 @@ def w12_encode(W_bits: np.ndarray):
     return codes, corr, int(cap.value), int(b2.value), V
 
 
+class _Handle:
+    """Attributes that are fixed once made: calls read device memory at the addresses and sizes
+    that were checked then."""
+
+    def __setattr__(self, name, value):
+        if "_made" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: write into its tensors, "
+                                 "or make another")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed")
+
+
 class W12Weights:
     """A W12 LM head in device memory: 12-byte groups, correction slots, window start.
     Pass it as `lm_head` to sd_verify_logits / sd_verify_greedy / VerifyRound."""
@@ -837,12 +851,13 @@ class _SdSampling(ctypes.Structure):
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
 
 
-class SamplingParams:
+class SamplingParams(_Handle):
     """Sampling settings of n requests in device memory, for sd_sample, sd_accept_filtered and
     VerifyRound. Each of temperature (default 1; 0 is greedy), top_k (< 1: off), top_p
     (>= 1: off) and min_p (<= 0: off) is None (its filter is off), one number for every
     request, a sequence of n numbers, or a device tensor of n values that is used as it is
-    (float32; int32 for top_k), so that writing to it changes later calls."""
+    (float32; int32 for top_k), so that writing to it changes later calls. The attributes
+    themselves are fixed: calls read the tensors at the addresses they were made with."""
 
     def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None,
                  n: Optional[int] = None, device="cuda"):
@@ -868,6 +883,7 @@ class SamplingParams:
         _same_device(self.device, **{k: getattr(self, k) for k in given})
         self._desc = _SdSampling(*[None if t is None else t.data_ptr() for t in self._arrays()])
         self._ref = ctypes.byref(self._desc)
+        self._made = True
 
     def _arrays(self):
         return (self.temperature, self.top_k, self.top_p, self.min_p)

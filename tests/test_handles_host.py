@@ -1,0 +1,32 @@
+"""Handles that hold device addresses (sampling settings, LM heads), on the host: what they
+were made from cannot be taken away under a later call."""
+import copy
+
+import pytest
+import torch
+
+import draft_block_verification_amd as sd
+
+
+def test_sampling_params_are_fixed():
+    """The descriptor that calls read holds the tensors' addresses: another tensor in an
+    attribute would leave it pointing at freed memory, another n would read past the arrays."""
+    p = sd.SamplingParams([0.5, 0.9], [3, 4], [0.7, 0.8], 0.1, device="cpu")
+    was = bytes(p._desc)
+    for name in ("temperature", "top_k", "top_p", "min_p", "n", "device"):
+        old = getattr(p, name)
+        with pytest.raises(AttributeError):
+            setattr(p, name, None if name == "device" else 4 if name == "n" else torch.ones(2))
+        with pytest.raises(AttributeError):
+            delattr(p, name)
+        assert getattr(p, name) is old
+    with pytest.raises(AttributeError):
+        p.min_q = 0.1                               # a slip of the pen is not kept either
+    q = copy.copy(p)
+    with pytest.raises(AttributeError):
+        q.top_p = None
+    assert bytes(p._desc) == was == bytes(q._desc)
+    assert [p._desc.temperature, p._desc.top_k, p._desc.top_p, p._desc.min_p] == [
+        t.data_ptr() for t in (p.temperature, p.top_k, p.top_p, p.min_p)]
+    p.top_p.fill_(0.25)                             # writing into them is how settings change
+    assert p.top_p.tolist() == [0.25] * 2
