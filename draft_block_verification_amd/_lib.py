@@ -319,14 +319,14 @@ class W12Weights:
         self.corr = torch.from_numpy(np.ascontiguousarray(corr).view(np.int32)).to(device)
         self.shape = (self.V, self.d)
         self.nbytes = self.codes.numel() + 4 * self.corr.numel()
-        self._desc = _SdW12(self.codes.data_ptr(), self.corr.data_ptr(), self.cap, self.b2)
 
     @classmethod
     def from_bf16(cls, W_bits: np.ndarray, device="cuda") -> "W12Weights":
         return cls(*w12_encode(W_bits), device=device)
 
     def descriptor(self):
-        return ctypes.byref(self._desc)
+        # From the tensors as they are: a kept address would outlive one that is replaced.
+        return ctypes.byref(_SdW12(self.codes.data_ptr(), self.corr.data_ptr(), self.cap, self.b2))
 
 
 def sd_verify_logits_w12(hidden, lm_head: W12Weights, *args, **kwargs):

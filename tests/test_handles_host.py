@@ -2,6 +2,7 @@
 were made from cannot be taken away under a later call."""
 import copy
 
+import numpy as np
 import pytest
 import torch
 
@@ -30,3 +31,13 @@ def test_sampling_params_are_fixed():
         t.data_ptr() for t in (p.temperature, p.top_k, p.top_p, p.min_p)]
     p.top_p.fill_(0.25)                             # writing into them is how settings change
     assert p.top_p.tolist() == [0.25] * 2
+
+
+def test_w12_descriptor_follows_its_tensors():
+    """A W12 LM head whose tensors are replaced (moved, say) is read where they are now."""
+    w = sd.W12Weights.from_bf16(np.full((4, 256), 0x3f80, dtype=np.uint16), device="cpu")
+    for name in ("codes", "corr"):
+        setattr(w, name, torch.cat([getattr(w, name)]))
+    d = w.descriptor()._obj
+    assert (d.codes, d.corr) == (w.codes.data_ptr(), w.corr.data_ptr())
+    assert (d.cap, d.b2) == (w.cap, w.b2)
