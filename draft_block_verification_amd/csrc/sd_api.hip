@@ -49,12 +49,22 @@ size_t type_size(int32_t t) { return t == SD_F32 ? 4 : 2; }
 
 constexpr int kMaxMxColumns = 1 << 20;
 
+// A launch has under 2^32 threads along x. Rows by row: four items of eight columns a thread,
+// 256 threads a workgroup. Rows in tiles of 64 x 128: 256 threads a tile.
+bool mx_rows_fit(int32_t rows, int32_t d) {
+  return (int64_t)rows * (mx_padded(d) / 8) <= ((int64_t)1 << 34) - 1024;
+}
+
+bool mx_tiles_fit(int32_t rows, int32_t d) {
+  return ((int64_t)rows + 63) / 64 * (mx_padded(d) / 128) < 1 << 24;
+}
+
 // Shared checks of the MXFP4 calls: [rows][d] of `type` beside its codes and scales.
 int32_t check_mx(const void *x, int32_t type, int32_t rows, int32_t d, int64_t stride,
                  const uint8_t *codes, const uint8_t *scales) {
   if (!x || !codes || !scales || !known_type(type)) return SD_EINVAL;
   if (rows < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns || stride < d ||
-      stride > ((int64_t)1 << 40) || (int64_t)rows * mx_padded(d) > ((int64_t)1 << 38))
+      stride > ((int64_t)1 << 40) || !mx_rows_fit(rows, d))
     return SD_ESHAPE;
   if (!aligned(x, type_size(type)) || !aligned(codes, 16) || !aligned(scales, 4)) return SD_EALIGN;
   return SD_OK;
@@ -605,9 +615,7 @@ int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t
 }
 
 size_t sd_mxfp4_head_bytes(int32_t V, int32_t d) {
-  if (V < 1 || V > kMaxVocab || d < 8 || d % 8 != 0 || d > kMaxMxColumns ||
-      (int64_t)V * mx_padded(d) > ((int64_t)1 << 38))
-    return 0;
+  if (V < 1 || V > kMaxVocab || d < 8 || d % 8 != 0 || d > kMaxMxColumns || !mx_tiles_fit(V, d)) return 0;
   return mx_tiled_bytes(V, d, nullptr);
 }
 
@@ -622,9 +630,7 @@ int32_t sd_mxfp4_head(const uint8_t *codes, const uint8_t *scales, int32_t V, in
 }
 
 size_t sd_mxfp4_logits_workspace_bytes(int32_t M, int32_t d) {
-  if (M < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns ||
-      (int64_t)M * mx_padded(d) > ((int64_t)1 << 38))
-    return 0;
+  if (M < 1 || d < 8 || d % 8 != 0 || d > kMaxMxColumns || !mx_tiles_fit(M, d)) return 0;
   return mx_logits_workspace_bytes(M, d);
 }
 
@@ -637,8 +643,8 @@ int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int3
   if (need == 0 || sd_mxfp4_head_bytes(V, d) == 0 || hidden_stride < d || hidden_stride > ((int64_t)1 << 40) ||
       logits_stride < V || logits_stride > ((int64_t)1 << 40))
     return SD_ESHAPE;
-  // One workgroup per output tile of 64 x 64 at least; the grid counts them in 32 bits.
-  if ((int64_t)((M + 63) / 64) * ((V + 63) / 64) > ((int64_t)1 << 30)) return SD_ESHAPE;
+  // The smallest output tile of a call of more than 64 rows is 128 x 128, by 256 threads.
+  if (((int64_t)M + 127) / 128 * (((int64_t)V + 127) / 128) >= 1 << 24) return SD_ESHAPE;
   if (!aligned(hidden, type_size(hidden_type)) || !aligned(head, 256) || !aligned(logits, type_size(logits_type)))
     return SD_EALIGN;
   if (!workspace || workspace_bytes < need) return SD_EWORKSPACE;

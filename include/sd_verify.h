@@ -521,7 +521,7 @@ SD_API int32_t sd_mxfp4_columns(int32_t d);
  * Quantise rows of x, and the values back.
  *   x       [rows][d] of type x_type (SD_F32, SD_BF16, SD_F16), row stride x_stride elements
  *           (>= d; any alignment of the element type, 16-byte aligned rows are fastest)
- *   rows    >= 1; d a positive multiple of 8
+ *   rows    >= 1; d a positive multiple of 8, at most 2^20; rows * kp at most 2^37 - 2^13
  *   codes, scales  as above, 16-byte and 4-byte aligned
  * sd_mxfp4_dequantize writes x rounded once to x_type (exact in fp32 and, unless the scale
  * leaves its normal range, in bf16); nothing between row ends and strides is written.
@@ -536,7 +536,8 @@ SD_API int32_t sd_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, 
 /*
  * The form of an MXFP4 LM head that sd_mxfp4_logits reads: the codes and scales above, re-laid
  * once into tiles of 64 rows by 128 columns (rows past V zero), in one device buffer.
- * sd_mxfp4_head_bytes: its size (0 unless V is in [1, 2^21] and d is a positive multiple of 8).
+ * sd_mxfp4_head_bytes: its size (0 unless V is in [1, 2^21], d is a positive multiple of 8 up to
+ * 2^20, and there are fewer than 2^24 tiles).
  * sd_mxfp4_head: writes it on `stream`.
  *   codes, scales  as above, [V] rows
  *   head           sd_mxfp4_head_bytes(V, d) bytes, 256-byte aligned, apart from the inputs
@@ -560,7 +561,8 @@ SD_API int32_t sd_mxfp4_head(const uint8_t *codes, const uint8_t *scales, int32_
  * logits[m][v] = sum over blocks of 2^(eh + ew) sum of the code products, accumulated in
  * fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives NaN.
  * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (M < 1, d not a positive multiple
- * of 8, V outside [1, 2^21], short strides), SD_EALIGN, SD_EWORKSPACE, SD_EDEVICE.
+ * of 8 up to 2^20, V outside [1, 2^21], 2^24 or more tiles of hidden rows, of the LM head or, at
+ * 128 x 128, of logits, short strides), SD_EALIGN, SD_EWORKSPACE, SD_EDEVICE.
  */
 SD_API size_t sd_mxfp4_logits_workspace_bytes(int32_t M, int32_t d);
 SD_API int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d,
