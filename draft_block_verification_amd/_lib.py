@@ -657,6 +657,7 @@ def sd_verify_rejection(hidden: torch.Tensor, lm_head, draft_tokens: torch.Tenso
 
 # --------------------------------------------------------------- MXFP4 and sampling
 
+_F32_MAX = torch.finfo(torch.float32).max
 _TYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -900,9 +901,9 @@ class SamplingParams(_Handle):
         v = [v] * self.n if isinstance(v, (int, float)) else list(v)
         for x in v:
             if name == "top_k":
-                if int(x) != x or not -2**31 <= x < 2**31:
+                if not -2**31 <= x < 2**31 or int(x) != x:
                     raise ValueError(f"top_k must be whole 32-bit numbers, got {x}")
-            elif x != x or (name == "temperature" and not 0 <= x < float("inf")):
+            elif x != x or (name == "temperature" and not 0 <= x <= _F32_MAX):
                 raise ValueError(f"{name} cannot be {x}")
         return torch.tensor([int(x) if name == "top_k" else float(x) for x in v], dtype=dtype,
                             device=self.device)

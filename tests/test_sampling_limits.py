@@ -33,3 +33,17 @@ def test_mxfp4_tiles_past_a_launch():
                                               sz(1 << 62), None)
     assert logits(1 << 17, 1 << 21) == 2     # 2^10 by 2^14 output tiles
     assert logits(2 ** 31 - 1, 1 << 21) == 2
+
+
+@pytest.mark.parametrize("bad", [dict(temperature=1e39), dict(temperature=[1.0, 3.5e38]), dict(top_k=float("inf")),
+                                 dict(top_k=[1, float("-inf")]), dict(temperature=torch.tensor([1e300], dtype=torch.float64))])
+def test_settings_past_their_type(bad):
+    """A finite temperature that fp32 holds as infinity would count as 0, the greedy choice."""
+    with pytest.raises(ValueError):
+        sd.SamplingParams(device="cpu", **bad)
+
+
+def test_settings_at_the_end_of_their_type():
+    big = torch.finfo(torch.float32).max
+    p = sd.SamplingParams(big, 2 ** 31 - 1, float("inf"), float("inf"), device="cpu")
+    assert p.temperature.tolist() == [big] and p.top_k.tolist() == [2 ** 31 - 1]
