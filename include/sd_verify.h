@@ -118,8 +118,12 @@ SD_API size_t sd_accept_workspace_bytes(int32_t B, int32_t gamma, int32_t V);
 /* Prepare a freshly allocated workspace: clears its 256-byte header (flag word and
  * counters) and, in a workspace of at least 256 + 1049600 bytes (every verify workspace),
  * sets the 1049600-byte publication area that follows the header to all ones bytes (the
- * state sd_verify_greedy's in-launch decision expects; every later call leaves it so).
- * Must be called once per workspace before its first use; enqueued on `stream`. */
+ * state sd_verify_greedy's in-launch decision expects; every later verify call leaves it so).
+ * Must be called once per workspace before its first use; enqueued on `stream`.
+ * Calls in turn may share a workspace of the largest size among them, calls at the same time
+ * may not. A workspace serves the verify calls or the others (acceptance, sampling, MXFP4
+ * logits): those keep scratch in that area, so it becomes a verify workspace only by being
+ * prepared again. */
 SD_API int32_t sd_workspace_init(void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, copy the sticky flag word of `workspace` to *flags (host) and,
