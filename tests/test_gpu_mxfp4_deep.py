@@ -52,3 +52,17 @@ def test_many_steps(M, V, d, out):
     if out != torch.float32:
         tol = tol + (want.abs() + tol) * torch.finfo(out).eps / 2
     assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_every_code_and_scale_back(dtype):
+    """All 16 codes under all 256 scales: the value rounded once to the type, subnormal and past
+    its largest (infinite) included; a scale byte of 255 is NaN."""
+    codes = np.tile(np.array([(2 * i + 1) << 4 | 2 * i for i in range(8)], dtype=np.uint8), (256, 8))
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 4, axis=1)
+    got = sd.sd_mxfp4_dequantize(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 128, dtype).cpu()
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(F.mx_values(codes, scales, 128)).to(dtype)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and bool(torch.isnan(got[255]).all())
+    assert torch.equal(got[:255], want[:255])
+    assert torch.equal(torch.signbit(got[:255]), torch.signbit(want[:255]))
