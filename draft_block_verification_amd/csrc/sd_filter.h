@@ -8,11 +8,13 @@
 // The kept set is then stated by its last member alone: the pair (key, id) of a RowCut.
 //
 // Weights are formed in fp64 (relative error 4e-14) and summed as 64-bit integers in
-// units of 2^-b: integer sums do not depend on order, so results are the same whatever
-// the split over lanes, waves and workgroups, and every running sum is exact in those
-// units. b is 46, less for rows of more than 2^17 ids so that V 2^b stays under 2^63. One
-// weight's rounding is at most 2^-(b+1) of the row's largest, a few 1e-12 of the total
-// over a whole row, and a weight under 2^-47 counts as 0.
+// units of 2^-b: integer sums do not depend on order, so a call repeated gives the same
+// bytes, and running sums of the same weights are exact in those units. b is 46, less for
+// rows of more than 2^17 ids (45 up to 2^18, .. 42 at 2^21) so that V 2^b stays under 2^63.
+// One weight's rounding is at most 2^-(b+1) of the row's largest, V 2^-(b+1) of it over a
+// whole row, and a weight under 2^-(b+1) counts as 0. Where a row is passed in shares, the
+// share that holds a draw is found by weights scaled from their bin, the id in it by single
+// exponentials: a border may lie a few units elsewhere than under another split.
 //
 // The functions that hold workgroup barriers are forced inline: as calls they spill and read
 // LDS through flat addresses.
@@ -598,8 +600,14 @@ __device__ __forceinline__ CutAt cut_in_bin(const RowView<E> &r, FilterSmem &s, 
   return c;
 }
 
-// The narrowing path: the cut of a row whose largest logit c.m is known, for every row that the single-pass path leaves: more ids at the cut than are ranked
-// in LDS, a top-k past them, logits too large for the grid's arithmetic, or +inf among them.
+// The narrowing path: the cut of a row whose largest logit c.m is known, for every row that the
+// single-pass path leaves: more ids at the cut than are ranked in LDS, a top-k past them, a
+// top-k that ends under the grid, logits too large for the grid's arithmetic, +inf among them,
+// and of the rows dealt to several workgroups those whose largest logit lies past the grid
+// that their sample gave (under it: a mask that left the sample nothing). One row of 151936
+// fp32 ids: 10 ids allowed 125 us, those 10 with the others at fp32's lowest value 200, an
+// unsampled peak 15 over the rest at T = 0.3 under top-p 198, top-k 2000 265, T = 3 under
+// top-p 0.85 393, against 28 for top-k 50 and 40 for top-p 0.9 on the single-pass path.
 // totals (as for row_plan): probabilities are taken from the cut, and an id past the range has
 // one as long as it is kept. A draw sums such weights to 0, so it does without the last member
 // of a top-k run that ends there: c.n is right, and ids behind that run are not told apart.
@@ -1150,7 +1158,7 @@ __device__ __forceinline__ int bin_of_count(u64 need, FilterSmem &s) {
 // the row reach (`guess`; NaN without one). With F the sampled fraction, the sample's rank
 // k F + 4 sqrt(k F) + 6 is taken: less than k ids reach it, or more than can be listed, about
 // as seldom as a normal variable lies 4 deviations out. Both are noticed; they cost a second
-// look at the row, and a row of several workgroups the narrowing path (some 200 us).
+// look at the row, and a row of several workgroups the narrowing path.
 template <class E>
 __device__ __forceinline__ float row_sample(const RowView<E> &r, const RowSettings &set, CutKind kind, float *guess,
                                             FilterSmem &s) {

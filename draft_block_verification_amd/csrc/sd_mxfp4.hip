@@ -496,10 +496,12 @@ __device__ __forceinline__ void store_rows(const MxGemmArgs &a, const LDSP uint8
 // direct loads, NS - 1 steps ahead. While a wave's matrix instructions consume step k from
 // registers it reads step k + 1's fragments from LDS, so with one wave a SIMD the matrix
 // units still run back to back. One barrier a step: behind it every wave has read step k
-// out of LDS, so its buffer takes step k + NS. 256 x 256 tiles are bound by the matrix
-// instructions (their operands feed 128 products a byte): 2048 rows by 129280 ids at depth
-// 7168 take 1086 us (3.5 PFLOP/s; 4.1 at 32768 ids and depth 8192), 835 us of it the
-// instructions alone, which random operands slow to 6.2 - 7 PFLOP/s at the card's power.
+// out of LDS, so its buffer takes step k + NS. 2048 rows by 129280 ids at depth 7168 in 256 x
+// 256 tiles take 930 us (4.1 PFLOP/s). With the loads left out (copies of the kernel, for
+// timing) it is 743 us, with the LDS reads left out too 642 us: 5.9 PFLOP/s, near the 6.0 -
+// 6.8 of the bare instruction on random operands in registers (8.6 on zeros: the card's power
+// sets its clock). So 290 us of feeding are not hidden behind the instructions; what holds
+// them up is not known.
 template <int WV, int WM, int TV, int TM, int NS>
 __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int n_vt) {
   constexpr int GV = WV * TV / 4, GM = WM * TM / 4, G = GV + GM;

@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_rows_narrow(Rows rows, const
 // workgroups in contiguous shares. Bins and lists meet in the workspace through integer
 // atomics, whose order does not change a sum; the list is ranked before it is used. No
 // workgroup waits for another: the last of a row to arrive goes on with it. One row of 151936
-// ids under top-k 50 and top-p: 24.5 us, 6 to sample it, 8 to list, 10 to cut and draw; a
+// ids under top-k 50 and top-p: 24.6 us, 6 to sample it, 7 to list, 10 to cut and draw; a
 // launch for the cut alone, in place of the last workgroup, made it 25.9.
 struct TeamRow {
   u64 top, any;
@@ -484,11 +484,11 @@ __device__ __forceinline__ int first_rejection(const FilteredArgs &a, int r, int
 // few. The first pass leaves bounds (k_filtered_bounds) that decide nearly every position: the
 // weight of a top-p run is its needed weight and less than one id more, so only a token in the
 // bin of the cut or a uniform within some 1e-5 of the border stays open. 128 ragged requests
-// of up to 16 drafts, 129280 ids, top-p (some 1800 rows in use, 687 MB): 257 us for the bounds,
-// 8 to decide, 42 for the rows that are cut, 70 + 8 for the draws; cutting every row took
-// 395 - 440 in place of the first three. Rows of open
-// positions up to the first sure rejection, and of that one (or the bonus row), whose
-// distribution is drawn from, are listed (k_filtered_need) and cut (k_filtered_cut).
+// of up to 16 drafts, 129280 ids, top-p (some 1800 rows in use, 687 MB): 241 us for the bounds,
+// 8 to decide, 42 for the rows that are cut, 66 + 8 for the draws; cutting every row took
+// 395 - 440 in place of the first three. Rows of open positions up to the first sure
+// rejection, and of that one (or the bonus row), whose distribution is drawn from, are listed
+// (k_filtered_need) and cut (k_filtered_cut).
 __global__ __launch_bounds__(kFilterThreads, 6) void k_filtered_bounds(AcceptRows rows) {
   __shared__ FilterSmem s;
   const int row = blockIdx.x, tid = threadIdx.x;
@@ -722,7 +722,7 @@ __global__ __launch_bounds__(kFilterThreads) void k_filtered_pick(FilteredArgs a
 }
 
 // Workgroups that sum the draw's row of a request, at least 2048 ids each, 1024 in all: one
-// request of 151936 ids 7.7 us, 128 requests of 129280 70 us.
+// request of 151936 ids 9 us, 128 requests of 129280 66 us.
 int draw_shares(int B, int V) {
   int c = B < 1024 ? 1024 / B : 1;
   if (c > V / 2048) c = V / 2048;

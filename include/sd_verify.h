@@ -528,7 +528,9 @@ SD_API int32_t sd_mxfp4_columns(int32_t d);
  *   rows    >= 1; d a positive multiple of 8, at most 2^20; rows * kp at most 2^37 - 2^13
  *   codes, scales  as above, 16-byte and 4-byte aligned
  * sd_mxfp4_dequantize writes x rounded once to x_type (exact in fp32 and, unless the scale
- * leaves its normal range, in bf16); nothing between row ends and strides is written.
+ * leaves its normal range, in bf16; scale bytes over 252, which quantisation never gives, can
+ * pass the largest fp32 number and then give an infinity); nothing between row ends and
+ * strides is written.
  * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE, SD_EALIGN, SD_EDEVICE.
  */
 SD_API int32_t sd_mxfp4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d,
@@ -607,8 +609,9 @@ typedef struct sd_sampling {
  *   kept      int32 [R] or NULL: out, size of the kept set
  *   logprob   fp32 [R] or NULL: out, log of the token's filtered probability (-inf with -1)
  *   workspace sd_sample_workspace_bytes(R, V) bytes
- * Weights are formed in fp64 and summed exactly in units of about 2^-46 of the largest: an id
- * whose weight is below half a unit is never drawn.
+ * Weights are formed in fp64 and summed exactly in units of 2^-46 of the largest (V over 2^17:
+ * 2^(ceil(log2 V) - 63), 2^-42 at 2^21): an id whose weight is below half a unit is never drawn,
+ * and a border of top-p or of the draw is met to V / 2 units.
  * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (R outside [1, 2^22], V outside
  * [1, 2^21], rows_per_request < 1, short strides), SD_EALIGN (an array not aligned to its elements),
  * SD_EWORKSPACE, SD_EDEVICE.
@@ -629,8 +632,11 @@ SD_API int32_t sd_sample(const void *logits, int32_t logits_type, int64_t logits
  *   with p' = 0 never does);
  *   a_r = first failing j, else L_r;
  *   if a_r < L_r the token is drawn from norm(max(0, p'_a - q'_a)) (from p'_a, raising
- *   SD_FLAG_NO_RESIDUAL, when that has no mass), else from p'_{L_r}; draws as in sd_sample.
- * Lossless: the emitted tokens follow p'.
+ *   SD_FLAG_NO_RESIDUAL, when that has no mass), else from p'_{L_r}; draws as in sd_sample,
+ *   probabilities in units of 2^-51: a residual under half of that at every id has no mass.
+ * Lossless: the emitted tokens follow p', where the drafts were drawn from the very values of
+ * draft_logits (drawn from finer logits that were rounded to bf16 afterwards, they follow
+ * another q').
  *   logits    fp32 [B * (gamma + 1)][V] written by sd_verify_logits (any temperature)
  *   draft_logits bf16 [B][gamma][V], draft_tokens, verify_len, row_offsets, u_accept,
  *   u_resample, accept_len, next_token, counters   as for sd_accept_rejection
