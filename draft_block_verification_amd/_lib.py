@@ -785,7 +785,7 @@ def sd_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
     return out
 
 
-class Mxfp4Weights:
+class Mxfp4Weights(_Handle):
     """An MXFP4 LM head in the form sd_mxfp4_logits reads (sd_mxfp4_head), made once from codes
     uint8 [V][kp / 2] and scales uint8 [V][kp / 32], kp = mxfp4_columns(d), or from rows
     without the padding, [V][d / 2] and [V][d / 32] for d a multiple of 32."""
@@ -811,6 +811,7 @@ class Mxfp4Weights:
         self.buf = _empty(nbytes, torch.uint8, codes.device, stream)
         _call("sd_mxfp4_head", codes.device, stream, _ptr(codes), _ptr(scales), self.V, self.d,
               _ptr(self.buf), nbytes)
+        self._made = True
 
     @classmethod
     def from_tensor(cls, lm_head: torch.Tensor, stream=None) -> "Mxfp4Weights":

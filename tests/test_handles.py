@@ -1,5 +1,5 @@
-"""Handles that hold device addresses (sampling settings, LM heads), on the host: what they
-were made from cannot be taken away under a later call."""
+"""Handles that hold device addresses (sampling settings, LM heads): what they were made from
+cannot be taken away under a later call."""
 import copy
 
 import numpy as np
@@ -41,3 +41,17 @@ def test_w12_descriptor_follows_its_tensors():
     d = w.descriptor()._obj
     assert (d.codes, d.corr) == (w.codes.data_ptr(), w.corr.data_ptr())
     assert (d.cap, d.b2) == (w.cap, w.b2)
+
+
+@pytest.mark.gpu
+def test_mxfp4_weights_are_fixed():
+    """The product reads V ids of d columns from buf: a shorter buffer, or larger sizes, would be
+    read past the end."""
+    head = sd.Mxfp4Weights.from_tensor(torch.ones((70, 256), dtype=torch.bfloat16, device="cuda"))
+    for name in ("buf", "V", "d", "shape", "nbytes", "device"):
+        old = getattr(head, name)
+        with pytest.raises(AttributeError):
+            setattr(head, name, old[:1] if name == "buf" else 1 << 20)
+        assert getattr(head, name) is old
+    h = torch.ones((2, 256), dtype=torch.bfloat16, device="cuda")
+    assert bool((sd.sd_mxfp4_logits(h, copy.copy(head)) == 256).all())
