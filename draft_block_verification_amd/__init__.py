@@ -17,7 +17,11 @@ from ._lib import (EXPORTED, FLAG_WAIT, FLAG_NO_RESIDUAL, FLAG_ROW_OFFSETS, FLAG
                    FLAG_EMPTY_ROW, FLAG_SAMPLING, Mxfp4Weights, SamplingParams,
                    accept_filtered_workspace_bytes, mxfp4_columns,
                    mxfp4_logits_workspace_bytes, sample_workspace_bytes, sd_accept_filtered,
-                   sd_mxfp4_dequantize, sd_mxfp4_logits, sd_mxfp4_quantize, sd_sample)
+                   sd_mxfp4_dequantize, sd_mxfp4_logits, sd_mxfp4_quantize, sd_sample,
+                   Mxfp8Weights, RmsNorm, W4Weights, mxfp8_logits_workspace_bytes,
+                   sd_mxfp8_dequantize, sd_mxfp8_logits, sd_mxfp8_quantize, sd_rms_norm,
+                   sd_rms_norm_mxfp8, sd_w4_dequantize, sd_w4_logits, sd_w4_quantize,
+                   w4_logits_workspace_bytes)
 
 __all__ = ["EXPORTED", "FLAG_WAIT", "FLAG_NO_RESIDUAL", "FLAG_ROW_OFFSETS", "FLAG_VERIFY_LEN", "LIB_PATH",
            "LM_HEAD_BLOCKED", "LM_HEAD_ROWS", "LM_HEAD_W12", "sd_verify_rejection",
@@ -33,4 +37,8 @@ __all__ = ["EXPORTED", "FLAG_WAIT", "FLAG_NO_RESIDUAL", "FLAG_ROW_OFFSETS", "FLA
            "FLAG_EMPTY_ROW", "FLAG_SAMPLING", "Mxfp4Weights", "SamplingParams",
            "accept_filtered_workspace_bytes", "mxfp4_columns", "mxfp4_logits_workspace_bytes",
            "sample_workspace_bytes", "sd_accept_filtered", "sd_mxfp4_dequantize",
-           "sd_mxfp4_logits", "sd_mxfp4_quantize", "sd_sample"]
+           "sd_mxfp4_logits", "sd_mxfp4_quantize", "sd_sample",
+           "Mxfp8Weights", "RmsNorm", "W4Weights", "mxfp8_logits_workspace_bytes",
+           "sd_mxfp8_dequantize", "sd_mxfp8_logits", "sd_mxfp8_quantize", "sd_rms_norm",
+           "sd_rms_norm_mxfp8", "sd_w4_dequantize", "sd_w4_logits", "sd_w4_quantize",
+           "w4_logits_workspace_bytes"]

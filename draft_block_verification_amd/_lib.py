@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -75,6 +76,24 @@ _SIGS = {
     "sd_mxfp4_logits_workspace_bytes": (_sz, [_i32, _i32]),
     "sd_mxfp4_logits": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _vp, _sz,
                                _vp]),
+    "sd_rms_norm": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i32, _f32, _f32, _i32, _i32, _vp,
+                           _i64, _vp, _i32, _i64, _vp]),
+    "sd_rms_norm_mxfp8": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i32, _f32, _f32, _i32, _i32,
+                                 _vp, _i64, _vp, _vp, _vp]),
+    "sd_mxfp8_quantize": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
+    "sd_mxfp8_dequantize": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp]),
+    "sd_mxfp8_head_bytes": (_sz, [_i32, _i32]),
+    "sd_mxfp8_head": (_i32, [_vp, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "sd_mxfp8_logits_workspace_bytes": (_sz, [_i32, _i32]),
+    "sd_mxfp8_logits": (_i32, [_vp, _i32, _vp, _i32, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _vp,
+                               _sz, _vp]),
+    "sd_w4_quantize": (_i32, [_vp, _i32, _i32, _i32, _i64, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "sd_w4_dequantize": (_i32, [_vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _vp]),
+    "sd_w4_head_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "sd_w4_head": (_i32, [_vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "sd_w4_logits_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "sd_w4_logits": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _vp, _i32,
+                            _i64, _vp, _sz, _vp]),
     "sd_sample_workspace_bytes": (_sz, [_i32, _i32]),
     "sd_sample": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp,
                          _sz, _vp]),
@@ -848,6 +867,329 @@ def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
     return logits
 
 
+# ------------------------------------------- the final norm, 8-bit and 4-bit LM heads
+
+_MXFP8 = 3      # hidden rows that are MXFP8 already
+
+
+def _output(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev, stream):
+    """`t` as a matrix of this shape, or a new one of `dtype`."""
+    if t is None:
+        if dtype not in _TYPE_CODES:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        return _empty(shape, dtype, dev, stream)
+    _rows(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _same_device(dev, **{name: t})
+    return t
+
+
+def _bytes(t: Optional[torch.Tensor], name: str, shape, dev, stream, dtype=torch.uint8):
+    """`t` as a contiguous tensor of this shape and type, or a new one."""
+    if t is None:
+        return _empty(shape, dtype, dev, stream)
+    _need(t, name, dtype, shape)
+    _same_device(dev, **{name: t})
+    return t
+
+
+def _norm_inputs(x, weight, residual, eps, weight_offset, total):
+    """The arguments of the norms up to `sum`, checked."""
+    _rows(x, "x")
+    rows, d = x.shape
+    if residual is not None:
+        _rows(residual, "residual")
+        if tuple(residual.shape) != (rows, d):
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(rows, d)}")
+        if residual.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"residual must be {x.dtype} or float32, got {residual.dtype}")
+    if weight is not None:
+        _need(weight, "weight", weight.dtype if isinstance(weight, torch.Tensor)
+              and weight.dtype in _TYPE_CODES else x.dtype, (d,))
+    if total is not None:
+        if residual is None:
+            raise ValueError("total is the sum with a residual, and there is none")
+        _rows(total, "total", residual.dtype)
+        if tuple(total.shape) != (rows, d):
+            raise ValueError(f"total has shape {tuple(total.shape)}, expected {(rows, d)}")
+    _same_device(x.device, residual=residual, weight=weight, total=total)
+    kind = 0 if residual is None else _TYPE_CODES[residual.dtype]
+    return (_ptr(x), _TYPE_CODES[x.dtype], _row_stride(x), _ptr(residual), kind,
+            0 if residual is None else _row_stride(residual), _ptr(weight),
+            0 if weight is None else _TYPE_CODES[weight.dtype], float(weight_offset), float(eps),
+            rows, d, _ptr(total), 0 if total is None else _row_stride(total))
+
+
+def sd_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                weight_offset: float = 0.0, out: Optional[torch.Tensor] = None,
+                dtype: Optional[torch.dtype] = None, total: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """RMS norm of the rows of x + residual (any row strides), times weight_offset + weight: a
+    matrix of `dtype` (default: x's), or `out`. residual: x's type or float32; total: takes the sum
+    in the residual's type (may be residual itself, or x where the types agree)."""
+    args = _norm_inputs(x, weight, residual, eps, weight_offset, total)
+    out = _output(out, "out", tuple(x.shape), x.dtype if dtype is None else dtype, x.device, stream)
+    _call("sd_rms_norm", x.device, stream, *args, _ptr(out), _TYPE_CODES[out.dtype],
+          _row_stride(out))
+    return out
+
+
+def sd_rms_norm_mxfp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      weight_offset: float = 0.0, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None,
+                      total: Optional[torch.Tensor] = None, stream=None):
+    """sd_rms_norm with the result as MXFP8 rows: (codes uint8 [rows][kp], scales uint8
+    [rows][kp / 32]), kp = mxfp4_columns(d)."""
+    args = _norm_inputs(x, weight, residual, eps, weight_offset, total)
+    kp = mxfp4_columns(x.shape[1])
+    codes = _bytes(codes, "codes", (x.shape[0], kp), x.device, stream)
+    scales = _bytes(scales, "scales", (x.shape[0], kp // 32), x.device, stream)
+    _call("sd_rms_norm_mxfp8", x.device, stream, *args, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+class RmsNorm(_Handle):
+    """A final norm for VerifyRound: weight [d] (float32, bfloat16 or float16; None: no factor),
+    eps and the offset that is added to the weight."""
+
+    def __init__(self, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 weight_offset: float = 0.0):
+        if weight is not None:
+            if not isinstance(weight, torch.Tensor) or weight.dtype not in _TYPE_CODES:
+                raise TypeError("weight must be a float32, bfloat16 or float16 tensor")
+            _need(weight, "weight", weight.dtype)
+            if weight.dim() != 1:
+                raise ValueError(f"weight must be a vector, got shape {tuple(weight.shape)}")
+        if not (math.isfinite(eps) and eps >= 0 and math.isfinite(weight_offset)):
+            raise ValueError("eps must be finite and >= 0, weight_offset finite")
+        self.weight, self.eps, self.weight_offset = weight, float(eps), float(weight_offset)
+        self._made = True
+
+
+def sd_mxfp8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, stream=None):
+    """MXFP8 form of the rows of x (float32, bfloat16 or float16, any row stride): returns
+    (codes uint8 [rows][kp], scales uint8 [rows][kp / 32]), kp = mxfp4_columns(d)."""
+    _rows(x, "x")
+    rows, d = x.shape
+    kp = mxfp4_columns(d)
+    codes = _bytes(codes, "codes", (rows, kp), x.device, stream)
+    scales = _bytes(scales, "scales", (rows, kp // 32), x.device, stream)
+    _call("sd_mxfp8_quantize", x.device, stream, _ptr(x), _TYPE_CODES[x.dtype], rows, d,
+          _row_stride(x), _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def sd_mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
+                        dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """The values that MXFP8 rows stand for, [rows][d] of `dtype` (or into out)."""
+    kp = mxfp4_columns(d)
+    _need(codes, "codes", torch.uint8)
+    rows = codes.shape[0]
+    _need(codes, "codes", torch.uint8, (rows, kp))
+    _need(scales, "scales", torch.uint8, (rows, kp // 32))
+    _same_device(codes.device, scales=scales)
+    out = _output(out, "out", (rows, d), dtype, codes.device, stream)
+    _call("sd_mxfp8_dequantize", codes.device, stream, _ptr(codes), _ptr(scales), rows, d,
+          _ptr(out), _TYPE_CODES[out.dtype], _row_stride(out))
+    return out
+
+
+class Mxfp8Weights(_Handle):
+    """An MXFP8 LM head in the form sd_mxfp8_logits reads (sd_mxfp8_head), made once from codes
+    uint8 [V][kp] and scales uint8 [V][kp / 32], kp = mxfp4_columns(d), or from rows without the
+    padding, [V][d] and [V][d / 32] for d a multiple of 32."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d: int, stream=None):
+        kp = mxfp4_columns(d)
+        _need(codes, "codes", torch.uint8)
+        _need(scales, "scales", torch.uint8)
+        V = codes.shape[0]
+        if d % 32 == 0 and kp != d and tuple(codes.shape) == (V, d):
+            _need(scales, "scales", torch.uint8, (V, d // 32))
+            with _current(stream, codes.device):
+                codes = torch.nn.functional.pad(codes, (0, kp - d))
+                scales = torch.nn.functional.pad(scales, (0, (kp - d) // 32))
+        _need(codes, "codes", torch.uint8, (V, kp))
+        _need(scales, "scales", torch.uint8, (V, kp // 32))
+        _same_device(codes.device, scales=scales)
+        nbytes = int(_lib.sd_mxfp8_head_bytes(V, d))
+        if nbytes == 0:
+            raise ValueError(f"no MXFP8 LM head of [{V}][{d}]")
+        self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
+        self.nbytes = nbytes
+        self.buf = _empty(nbytes, torch.uint8, codes.device, stream)
+        _call("sd_mxfp8_head", codes.device, stream, _ptr(codes), _ptr(scales), self.V, self.d,
+              _ptr(self.buf), nbytes)
+        self._made = True
+
+    @classmethod
+    def from_tensor(cls, lm_head: torch.Tensor, stream=None) -> "Mxfp8Weights":
+        """Quantise a [V][d] LM head (float32, bfloat16 or float16)."""
+        return cls(*sd_mxfp8_quantize(lm_head, stream=stream), lm_head.shape[1], stream=stream)
+
+
+def mxfp8_logits_workspace_bytes(rows: int, d: int) -> int:
+    return int(_lib.sd_mxfp8_logits_workspace_bytes(rows, d))
+
+
+def w4_logits_workspace_bytes(rows: int, d: int, group: int) -> int:
+    return int(_lib.sd_w4_logits_workspace_bytes(rows, d, group))
+
+
+def sd_mxfp8_logits(hidden, lm_head: Mxfp8Weights, logits: Optional[torch.Tensor] = None,
+                    dtype: torch.dtype = torch.float32,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Logits [M][V] of hidden rows under an MXFP8 LM head, as `dtype` or into `logits` (any row
+    stride). hidden: [M][d] (float32, bfloat16 or float16, any row stride; quantised in the call)
+    or MXFP8 rows, the pair (codes, scales) of sd_rms_norm_mxfp8 or sd_mxfp8_quantize."""
+    if not isinstance(lm_head, Mxfp8Weights):
+        raise TypeError("lm_head must be Mxfp8Weights")
+    scales = None
+    if isinstance(hidden, (tuple, list)):
+        hidden, scales = hidden
+        kp = mxfp4_columns(lm_head.d)
+        _need(hidden, "hidden codes", torch.uint8)
+        M, d = hidden.shape[0], lm_head.d
+        _need(hidden, "hidden codes", torch.uint8, (M, kp))
+        _need(scales, "hidden scales", torch.uint8, (M, kp // 32))
+        kind, stride = _MXFP8, kp
+    else:
+        _rows(hidden, "hidden")
+        M, d = hidden.shape
+        if d != lm_head.d:
+            raise ValueError("lm_head must be [V][d] with the hidden size of `hidden`")
+        kind, stride = _TYPE_CODES[hidden.dtype], _row_stride(hidden)
+    dev = hidden.device
+    logits = _output(logits, "logits", (M, lm_head.V), dtype, dev, stream)
+    if workspace is None:
+        workspace = _empty(max(mxfp8_logits_workspace_bytes(M, d), 256), torch.uint8, dev, stream)
+    _same_device(dev, lm_head=lm_head, scales=scales, workspace=workspace)
+    _call("sd_mxfp8_logits", dev, stream, _ptr(hidden), kind, _ptr(scales), M, d, stride,
+          _ptr(lm_head.buf), lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
+          _row_stride(logits), _ptr(workspace), workspace.numel())
+    return logits
+
+
+def _w4_form(codes, scales, zeros, d) -> int:
+    """Group size of a 4-bit form, its tensors checked."""
+    _need(codes, "codes", torch.uint8)
+    _need(scales, "scales", scales.dtype if isinstance(scales, torch.Tensor)
+          and scales.dtype == torch.float16 else torch.bfloat16)
+    rows = codes.shape[0]
+    if scales.dim() != 2 or scales.shape[1] < 1 or d % scales.shape[1] != 0:
+        raise ValueError(f"scales must be [rows][d / group], got shape {tuple(scales.shape)}")
+    group = d // scales.shape[1]
+    if group not in (32, 64, 128):
+        raise ValueError(f"groups of 32, 64 or 128 columns, got {group}")
+    _need(codes, "codes", torch.uint8, (rows, d // 2))
+    _need(scales, "scales", scales.dtype, (rows, d // group))
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, (rows, d // group))
+    _same_device(codes.device, scales=scales, zeros=zeros)
+    return group
+
+
+def sd_w4_quantize(x: torch.Tensor, group: int = 128, symmetric: bool = False,
+                   scale_dtype: Optional[torch.dtype] = None,
+                   codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                   zeros: Optional[torch.Tensor] = None, stream=None):
+    """4-bit form of the rows of x (float32, bfloat16 or float16, any row stride) in groups of 32,
+    64 or 128 columns: (codes uint8 [rows][d / 2], scales [rows][d / group] of scale_dtype, zeros
+    uint8 [rows][d / group], or None where symmetric). scale_dtype: bfloat16 or float16 (default:
+    x's, bfloat16 for float32)."""
+    _rows(x, "x")
+    rows, d = x.shape
+    if group not in (32, 64, 128) or d % group != 0:
+        raise ValueError(f"groups of 32, 64 or 128 columns that divide d = {d}, got {group}")
+    if scales is not None and scale_dtype is None and isinstance(scales, torch.Tensor):
+        scale_dtype = scales.dtype
+    if scale_dtype is None:
+        scale_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
+    if scale_dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"scale_dtype must be bfloat16 or float16, got {scale_dtype}")
+    if symmetric and zeros is not None:
+        raise ValueError("the symmetric form has no zeros")
+    dev = x.device
+    codes = _bytes(codes, "codes", (rows, d // 2), dev, stream)
+    scales = _bytes(scales, "scales", (rows, d // group), dev, stream, scale_dtype)
+    zeros = None if symmetric else _bytes(zeros, "zeros", (rows, d // group), dev, stream)
+    _call("sd_w4_quantize", dev, stream, _ptr(x), _TYPE_CODES[x.dtype], rows, d, _row_stride(x),
+          group, _ptr(codes), _ptr(scales), _TYPE_CODES[scale_dtype], _ptr(zeros))
+    return codes, scales, zeros
+
+
+def sd_w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor],
+                     d: int, dtype: torch.dtype = torch.float32,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values (code - zero) * scale of 4-bit rows, [rows][d] of `dtype` (or into out)."""
+    group = _w4_form(codes, scales, zeros, d)
+    rows = codes.shape[0]
+    out = _output(out, "out", (rows, d), dtype, codes.device, stream)
+    _call("sd_w4_dequantize", codes.device, stream, _ptr(codes), _ptr(scales),
+          _TYPE_CODES[scales.dtype], _ptr(zeros), rows, d, group, _ptr(out),
+          _TYPE_CODES[out.dtype], _row_stride(out))
+    return out
+
+
+class W4Weights(_Handle):
+    """An LM head of 4-bit integers with group scales in the form sd_w4_logits reads (sd_w4_head),
+    made once from codes uint8 [V][d / 2] (column 2 i in the low half of byte i), scales
+    [V][d / group] (bfloat16 or float16) and zeros uint8 [V][d / group] (None: 8 everywhere)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor],
+                 d: int, stream=None):
+        group = _w4_form(codes, scales, zeros, d)
+        V = codes.shape[0]
+        nbytes = int(_lib.sd_w4_head_bytes(V, d, group, int(zeros is not None)))
+        if nbytes == 0:
+            raise ValueError(f"no 4-bit LM head of [{V}][{d}] in groups of {group}")
+        self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
+        self.group, self.scale_dtype, self.has_zeros = group, scales.dtype, zeros is not None
+        self.nbytes = nbytes
+        self.buf = _empty(nbytes, torch.uint8, codes.device, stream)
+        _call("sd_w4_head", codes.device, stream, _ptr(codes), _ptr(scales),
+              _TYPE_CODES[scales.dtype], _ptr(zeros), self.V, self.d, group, _ptr(self.buf), nbytes)
+        self._made = True
+
+    @classmethod
+    def from_tensor(cls, lm_head: torch.Tensor, group: int = 128, symmetric: bool = False,
+                    scale_dtype: Optional[torch.dtype] = None, stream=None) -> "W4Weights":
+        """Quantise a [V][d] LM head (float32, bfloat16 or float16)."""
+        return cls(*sd_w4_quantize(lm_head, group, symmetric, scale_dtype, stream=stream),
+                   lm_head.shape[1], stream=stream)
+
+
+def sd_w4_logits(hidden: torch.Tensor, lm_head: W4Weights, logits: Optional[torch.Tensor] = None,
+                 dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Logits [M][V] of hidden rows [M][d] (bfloat16 or float16, any row stride) under an LM head
+    of 4-bit integers with group scales, as `dtype` or into `logits` (any row stride)."""
+    _rows(hidden, "hidden")
+    if hidden.dtype == torch.float32:
+        raise TypeError("hidden must be bfloat16 or float16, got torch.float32")
+    if not isinstance(lm_head, W4Weights):
+        raise TypeError("lm_head must be W4Weights")
+    M, d = hidden.shape
+    if d != lm_head.d:
+        raise ValueError("lm_head must be [V][d] with the hidden size of `hidden`")
+    dev = hidden.device
+    logits = _output(logits, "logits", (M, lm_head.V), dtype, dev, stream)
+    if workspace is None:
+        workspace = _empty(max(w4_logits_workspace_bytes(M, d, lm_head.group), 256), torch.uint8,
+                           dev, stream)
+    _same_device(dev, lm_head=lm_head, workspace=workspace)
+    _call("sd_w4_logits", dev, stream, _ptr(hidden), _TYPE_CODES[hidden.dtype], M, d,
+          _row_stride(hidden), _ptr(lm_head.buf), lm_head.V, lm_head.group,
+          _TYPE_CODES[lm_head.scale_dtype], int(lm_head.has_zeros), _ptr(logits),
+          _TYPE_CODES[logits.dtype], _row_stride(logits), _ptr(workspace), workspace.numel())
+    return logits
+
+
 class _SdSampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
@@ -1012,14 +1354,20 @@ class VerifyRound:
     launches, for every LM-head format); fused=False keeps the separate sd_verify_logits
     + sd_accept_* calls. With `sampling` (SamplingParams of B requests) the accept step is
     sd_accept_filtered under those settings, after sd_verify_logits at `temperature`.
+    With `norm` (an RmsNorm) run() is given the last layer's output instead of hidden rows, and
+    its residual if there is one, [B][gamma + 1][d] each: sd_rms_norm makes the hidden rows first.
     """
 
     def __init__(self, B: int, gamma: int, d: int, V: int, temperature: float,
                  truncate: bool, threshold: float = 0.3, device="cuda", stream=None,
                  fused: bool = True, accept_rate: bool = False, scheduler: Optional[int] = None,
                  sps: Optional[torch.Tensor] = None,
-                 sampling: Optional[SamplingParams] = None):
+                 sampling: Optional[SamplingParams] = None, norm: Optional[RmsNorm] = None):
         self.B, self.gamma, self.d, self.V = B, gamma, d, V
+        if norm is not None and (not isinstance(norm, RmsNorm) or norm.weight is not None
+                                 and norm.weight.shape[0] != d):
+            raise ValueError(f"norm must be an RmsNorm of {d} columns")
+        self.norm = norm
         self.sampling = sampling
         if sampling is not None and (not isinstance(sampling, SamplingParams) or sampling.n != B):
             raise ValueError("sampling must be SamplingParams of B requests")
@@ -1050,9 +1398,25 @@ class VerifyRound:
         # Analytic acceptance rate per verified draft position (rejection rounds only).
         self.accept_rate = (torch.empty((B, gamma), dtype=torch.float64, device=dev)
                             if accept_rate and self.T > 0 else None)
+        self.hidden = (torch.empty((B, gamma + 1, d), dtype=torch.bfloat16, device=dev)
+                       if norm is not None else None)
 
     def run(self, hidden, lm_head, draft_tokens, conf=None, draft_logits=None, u_accept=None,
-            u_resample=None, stream=None, conf_stale=None):
+            u_resample=None, stream=None, conf_stale=None, residual=None):
+        if self.norm is not None:
+            shape = (self.B, self.gamma + 1, self.d)
+            for name, t in (("hidden", hidden), ("residual", residual)):
+                if t is not None and tuple(t.shape) != shape:
+                    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+            _need(hidden, "hidden", hidden.dtype)
+            if residual is not None:
+                _need(residual, "residual", residual.dtype)
+                residual = residual.view(-1, self.d)
+            sd_rms_norm(hidden.view(-1, self.d), self.norm.weight, residual, self.norm.eps,
+                        self.norm.weight_offset, out=self.hidden.view(-1, self.d), stream=stream)
+            hidden = self.hidden
+        elif residual is not None:
+            raise ValueError("a residual needs norm=RmsNorm(...)")
         if self.truncate and self.scheduler is not None:
             sd_schedule_prefix(conf, self.sps, self.scheduler,
                                conf_stale if self.scheduler == SCHED_TOP_K else None,

@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdverify.so")
 SOURCES = ["sd_api.hip", "sd_gemm.hip", "sd_accept.hip", "sd_sched.hip", "sd_w12.hip",
-           "sd_mxfp4.hip", "sd_sample.hip"]
+           "sd_mxfp4.hip", "sd_sample.hip", "sd_norm.hip", "sd_mxfp8.hip", "sd_w4.hip",
+           "sd_narrow.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "sd_launch.h"
@@ -68,6 +69,45 @@ int32_t check_mx(const void *x, int32_t type, int32_t rows, int32_t d, int64_t s
     return SD_ESHAPE;
   if (!aligned(x, type_size(type)) || !aligned(codes, 16) || !aligned(scales, 4)) return SD_EALIGN;
   return SD_OK;
+}
+
+bool stride_fits(int64_t stride, int64_t columns) { return stride >= columns && stride <= (int64_t)1 << 40; }
+
+// Shared checks of the norms.
+int32_t check_norm(const NormArgs &a) {
+  if (!a.x || !known_type(a.x_type) || (a.w && !known_type(a.w_type)) || !(a.eps >= 0.f) ||
+      !std::isfinite(a.eps) || !std::isfinite(a.offset) || (a.sum && !a.r))
+    return SD_EINVAL;
+  if (a.r && a.r_type != a.x_type && a.r_type != SD_F32) return SD_EINVAL;
+  if (a.rows < 1 || a.d < 1 || a.d > kMaxMxColumns || !stride_fits(a.x_stride, a.d) ||
+      (a.r && !stride_fits(a.r_stride, a.d)) || (a.sum && !stride_fits(a.sum_stride, a.d)))
+    return SD_ESHAPE;
+  if (!aligned(a.x, type_size(a.x_type)) || (a.r && !aligned(a.r, type_size(a.r_type))) ||
+      (a.sum && !aligned(a.sum, type_size(a.r_type))) || (a.w && !aligned(a.w, type_size(a.w_type))))
+    return SD_EALIGN;
+  return SD_OK;
+}
+
+bool w4_group(int32_t d, int32_t group) {
+  return (group == 32 || group == 64 || group == 128) && d >= group && d % group == 0 && d <= kMaxMxColumns;
+}
+
+bool w4_scale_type(int32_t t) { return t == SD_BF16 || t == SD_F16; }
+
+// Shared checks of the 4-bit integer calls over rows.
+int32_t check_w4(const void *x, int32_t type, int32_t rows, int32_t d, int64_t stride, int32_t group,
+                 const uint8_t *codes, const void *scales, int32_t scale_type, const uint8_t *zeros) {
+  if (!x || !codes || !scales || !known_type(type) || !w4_scale_type(scale_type)) return SD_EINVAL;
+  if (rows < 1 || !w4_group(d, group) || !stride_fits(stride, d) || !mx_rows_fit(rows, d)) return SD_ESHAPE;
+  if (!aligned(x, type_size(type)) || !aligned(codes, 16) || !aligned(scales, 4) || (zeros && !aligned(zeros, 4)))
+    return SD_EALIGN;
+  return SD_OK;
+}
+
+// The smallest output tile of the products' large calls is 128 x 128, by 256 threads; their small
+// calls have a workgroup for 64 ids and 32 rows at least, or 64 rows and more at a time.
+bool logits_fit(int32_t M, int32_t V) {
+  return ((int64_t)M + 127) / 128 * (((int64_t)V + 127) / 128) < 1 << 24;
 }
 
 SampleSettings settings(const sd_sampling &s) {
@@ -651,6 +691,146 @@ int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t M, int3
   if (!aligned(workspace, 256)) return SD_EALIGN;
   return launch_status(launch_mx_logits(hidden, hidden_type, M, d, hidden_stride, head, V, logits,
                                         logits_type, logits_stride, workspace, (hipStream_t)stream));
+}
+
+int32_t sd_rms_norm(const void *x, int32_t x_type, int64_t x_stride, const void *residual,
+                    int32_t residual_type, int64_t residual_stride, const void *weight,
+                    int32_t weight_type, float weight_offset, float eps, int32_t rows, int32_t d, void *sum,
+                    int64_t sum_stride, void *y, int32_t y_type, int64_t y_stride, void *stream) {
+  const NormArgs a{x, x_type, x_stride, residual, residual_type, residual_stride, weight, weight_type,
+                   weight_offset, eps, rows, d, sum, sum_stride, y, y_type, y_stride, nullptr, nullptr};
+  if (!y || !known_type(y_type)) return SD_EINVAL;
+  const int32_t st = check_norm(a);
+  if (st != SD_OK) return st;
+  if (!stride_fits(y_stride, d)) return SD_ESHAPE;
+  if (!aligned(y, type_size(y_type))) return SD_EALIGN;
+  return launch_status(launch_norm(a, (hipStream_t)stream));
+}
+
+int32_t sd_rms_norm_mxfp8(const void *x, int32_t x_type, int64_t x_stride, const void *residual,
+                          int32_t residual_type, int64_t residual_stride, const void *weight,
+                          int32_t weight_type, float weight_offset, float eps, int32_t rows, int32_t d,
+                          void *sum, int64_t sum_stride, uint8_t *codes, uint8_t *scales, void *stream) {
+  const NormArgs a{x, x_type, x_stride, residual, residual_type, residual_stride, weight, weight_type,
+                   weight_offset, eps, rows, d, sum, sum_stride, nullptr, SD_F32, 0, codes, scales};
+  if (!codes || !scales) return SD_EINVAL;
+  const int32_t st = check_norm(a);
+  if (st != SD_OK) return st;
+  if (d % 8 != 0) return SD_ESHAPE;
+  if (!aligned(codes, 16) || !aligned(scales, 4)) return SD_EALIGN;
+  return launch_status(launch_norm(a, (hipStream_t)stream));
+}
+
+int32_t sd_mxfp8_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d, int64_t x_stride,
+                          uint8_t *codes, uint8_t *scales, void *stream) {
+  const int32_t st = check_mx(x, x_type, rows, d, x_stride, codes, scales);
+  if (st != SD_OK) return st;
+  return launch_status(launch_mx8_quantize(x, x_type, rows, d, x_stride, codes, scales, (hipStream_t)stream));
+}
+
+int32_t sd_mxfp8_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t d,
+                            void *x, int32_t x_type, int64_t x_stride, void *stream) {
+  const int32_t st = check_mx(x, x_type, rows, d, x_stride, codes, scales);
+  if (st != SD_OK) return st;
+  return launch_status(launch_mx8_dequantize(codes, scales, rows, d, x, x_type, x_stride, (hipStream_t)stream));
+}
+
+size_t sd_mxfp8_head_bytes(int32_t V, int32_t d) {
+  return sd_mxfp4_head_bytes(V, d) == 0 ? 0 : mx8_head_bytes(V, d);
+}
+
+int32_t sd_mxfp8_head(const uint8_t *codes, const uint8_t *scales, int32_t V, int32_t d, uint8_t *head,
+                      size_t head_bytes, void *stream) {
+  if (!codes || !scales || !head) return SD_EINVAL;
+  const size_t need = sd_mxfp8_head_bytes(V, d);
+  if (need == 0) return SD_ESHAPE;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(head, 256)) return SD_EALIGN;
+  if (head_bytes < need) return SD_EWORKSPACE;
+  return launch_status(launch_mx8_head(codes, scales, V, d, head, (hipStream_t)stream));
+}
+
+size_t sd_mxfp8_logits_workspace_bytes(int32_t M, int32_t d) {
+  return sd_mxfp4_logits_workspace_bytes(M, d) == 0 ? 0 : mx8_logits_workspace_bytes(M, d);
+}
+
+int32_t sd_mxfp8_logits(const void *hidden, int32_t hidden_type, const uint8_t *hidden_scales, int32_t M,
+                        int32_t d, int64_t hidden_stride, const uint8_t *head, int32_t V, void *logits,
+                        int32_t logits_type, int64_t logits_stride, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+  const bool coded = hidden_type == SD_MXFP8;
+  if (!hidden || !head || !logits || (!coded && !known_type(hidden_type)) || !known_type(logits_type) ||
+      coded != (hidden_scales != nullptr))
+    return SD_EINVAL;
+  const size_t need = sd_mxfp8_logits_workspace_bytes(M, d);
+  if (need == 0 || sd_mxfp8_head_bytes(V, d) == 0 || !logits_fit(M, V) || !stride_fits(logits_stride, V) ||
+      (coded ? hidden_stride != mx_padded(d) : !stride_fits(hidden_stride, d)))
+    return SD_ESHAPE;
+  if (!aligned(hidden, coded ? 16 : type_size(hidden_type)) || (coded && !aligned(hidden_scales, 4)) ||
+      !aligned(head, 256) || !aligned(logits, type_size(logits_type)))
+    return SD_EALIGN;
+  if (!workspace || workspace_bytes < need) return SD_EWORKSPACE;
+  if (!aligned(workspace, 256)) return SD_EALIGN;
+  return launch_status(launch_mx8_logits(hidden, hidden_type, hidden_scales, M, d, hidden_stride, head, V, logits,
+                                         logits_type, logits_stride, workspace, (hipStream_t)stream));
+}
+
+int32_t sd_w4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d, int64_t x_stride, int32_t group,
+                       uint8_t *codes, void *scales, int32_t scale_type, uint8_t *zeros, void *stream) {
+  const int32_t st = check_w4(x, x_type, rows, d, x_stride, group, codes, scales, scale_type, zeros);
+  if (st != SD_OK) return st;
+  return launch_status(launch_w4_quantize(x, x_type, rows, d, x_stride, group, codes,
+                                          reinterpret_cast<uint16_t *>(scales), scale_type, zeros,
+                                          (hipStream_t)stream));
+}
+
+int32_t sd_w4_dequantize(const uint8_t *codes, const void *scales, int32_t scale_type, const uint8_t *zeros,
+                         int32_t rows, int32_t d, int32_t group, void *x, int32_t x_type, int64_t x_stride,
+                         void *stream) {
+  const int32_t st = check_w4(x, x_type, rows, d, x_stride, group, codes, scales, scale_type, zeros);
+  if (st != SD_OK) return st;
+  return launch_status(launch_w4_dequantize(codes, reinterpret_cast<const uint16_t *>(scales), scale_type, zeros,
+                                            rows, d, group, x, x_type, x_stride, (hipStream_t)stream));
+}
+
+size_t sd_w4_head_bytes(int32_t V, int32_t d, int32_t group, int32_t has_zeros) {
+  if (V < 1 || V > kMaxVocab || !w4_group(d, group) || has_zeros < 0 || has_zeros > 1 || !mx_tiles_fit(V, d)) return 0;
+  return w4_head_bytes(V, d, group, has_zeros == 1);
+}
+
+int32_t sd_w4_head(const uint8_t *codes, const void *scales, int32_t scale_type, const uint8_t *zeros, int32_t V,
+                   int32_t d, int32_t group, uint8_t *head, size_t head_bytes, void *stream) {
+  if (!codes || !scales || !head || !w4_scale_type(scale_type)) return SD_EINVAL;
+  const size_t need = sd_w4_head_bytes(V, d, group, zeros != nullptr);
+  if (need == 0) return SD_ESHAPE;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || (zeros && !aligned(zeros, 4)) || !aligned(head, 256))
+    return SD_EALIGN;
+  if (head_bytes < need) return SD_EWORKSPACE;
+  return launch_status(launch_w4_head(codes, reinterpret_cast<const uint16_t *>(scales), zeros, V, d, group, head,
+                                      (hipStream_t)stream));
+}
+
+size_t sd_w4_logits_workspace_bytes(int32_t M, int32_t d, int32_t group) {
+  if (M < 1 || !w4_group(d, group) || !mx_tiles_fit(M, d)) return 0;
+  return w4_logits_workspace_bytes(M, d);
+}
+
+int32_t sd_w4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d, int64_t hidden_stride,
+                     const uint8_t *head, int32_t V, int32_t group, int32_t scale_type, int32_t has_zeros,
+                     void *logits, int32_t logits_type, int64_t logits_stride, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  if (!hidden || !head || !logits || (hidden_type != SD_BF16 && hidden_type != SD_F16) ||
+      !known_type(logits_type) || !w4_scale_type(scale_type) || has_zeros < 0 || has_zeros > 1)
+    return SD_EINVAL;
+  const size_t need = sd_w4_logits_workspace_bytes(M, d, group);
+  if (need == 0 || sd_w4_head_bytes(V, d, group, has_zeros) == 0 || !logits_fit(M, V) ||
+      !stride_fits(hidden_stride, d) || !stride_fits(logits_stride, V))
+    return SD_ESHAPE;
+  if (!aligned(hidden, 2) || !aligned(head, 256) || !aligned(logits, type_size(logits_type))) return SD_EALIGN;
+  if (!workspace || workspace_bytes < need) return SD_EWORKSPACE;
+  if (!aligned(workspace, 256)) return SD_EALIGN;
+  return launch_status(launch_w4_logits(hidden, hidden_type, M, d, hidden_stride, head, V, group, scale_type,
+                                        has_zeros == 1, logits, logits_type, logits_stride, workspace,
+                                        (hipStream_t)stream));
 }
 
 size_t sd_sample_workspace_bytes(int32_t R, int32_t V) {

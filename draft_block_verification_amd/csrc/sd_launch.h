@@ -1,6 +1,7 @@
 // Host-side launchers and workspace layouts of the HIP library (defined in sd_gemm.hip,
-// sd_accept.hip, sd_sched.hip, sd_sample.hip and sd_mxfp4.hip; called by sd_api.hip). Each launcher enqueues its
-// kernels on `stream` and returns the hipError_t of the launch.
+// sd_accept.hip, sd_sched.hip, sd_sample.hip, sd_mxfp4.hip, sd_norm.hip, sd_mxfp8.hip, sd_w4.hip and
+// sd_narrow.hip; called by sd_api.hip). Each launcher enqueues its kernels on `stream` and returns the
+// hipError_t of the launch.
 #pragma once
 
 #include "sd_internal.h"
@@ -102,6 +103,57 @@ size_t mx_logits_workspace_bytes(int M, int d);
 hipError_t launch_mx_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
                             const uint8_t *head, int V, void *logits, int32_t type, int64_t ld,
                             void *workspace, hipStream_t stream);
+
+// RMS norm of rows; r (the residual) and sum may be null, w too; the output goes to y or, where
+// codes is not null, to MXFP8 rows.
+struct NormArgs {
+  const void *x;
+  int32_t x_type;
+  int64_t x_stride;
+  const void *r;
+  int32_t r_type;           // of r and sum: x_type or SD_F32
+  int64_t r_stride;
+  const void *w;
+  int32_t w_type;
+  float offset, eps;
+  int64_t rows;
+  int d;
+  void *sum;
+  int64_t sum_stride;
+  void *y;
+  int32_t y_type;
+  int64_t y_stride;
+  uint8_t *codes, *scales;
+};
+hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
+
+// MXFP8 rows, an LM head of them re-laid into tiles, and logits under it.
+hipError_t launch_mx8_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride,
+                               uint8_t *codes, uint8_t *scales, hipStream_t stream);
+hipError_t launch_mx8_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int d,
+                                 void *x, int32_t type, int64_t stride, hipStream_t stream);
+size_t mx8_head_bytes(int64_t V, int d);
+hipError_t launch_mx8_head(const uint8_t *codes, const uint8_t *scales, int V, int d, uint8_t *head,
+                           hipStream_t stream);
+size_t mx8_logits_workspace_bytes(int M, int d);
+hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint8_t *hidden_scales, int M, int d,
+                             int64_t stride, const uint8_t *head, int V, void *logits, int32_t type, int64_t ld,
+                             void *workspace, hipStream_t stream);
+
+// 4-bit integer weights with group scales (zeros null: symmetric), likewise.
+hipError_t launch_w4_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride, int group,
+                              uint8_t *codes, uint16_t *scales, int32_t scale_type, uint8_t *zeros,
+                              hipStream_t stream);
+hipError_t launch_w4_dequantize(const uint8_t *codes, const uint16_t *scales, int32_t scale_type,
+                                const uint8_t *zeros, int64_t rows, int d, int group, void *x, int32_t type,
+                                int64_t stride, hipStream_t stream);
+size_t w4_head_bytes(int64_t V, int d, int group, bool zeros);
+hipError_t launch_w4_head(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int V, int d,
+                          int group, uint8_t *head, hipStream_t stream);
+size_t w4_logits_workspace_bytes(int M, int d);
+hipError_t launch_w4_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
+                            const uint8_t *head, int V, int group, int32_t scale_type, bool zeros, void *logits,
+                            int32_t type, int64_t ld, void *workspace, hipStream_t stream);
 
 // Filtered sampling and acceptance.
 hipError_t launch_sample(const void *logits, int32_t type, int64_t stride, int R, int V,

@@ -20,74 +20,11 @@
 // four fragments share the word, and the instruction's operand selects the byte.
 //   codes  [ceil(rows / 64)][kp / 128][4][64 lanes][16 bytes], then
 //   scales [ceil(rows / 64)][kp / 128][64 lanes][4 bytes]
-#include <utility>
-
 #include "sd_launch.h"
-
-#define LDSP __attribute__((address_space(3)))
-#define GLBP __attribute__((address_space(1)))
+#include "sd_rows.h"
 
 namespace sdv {
 namespace {
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// Eight consecutive values of a row as they are stored, 0 past `left` of them. vec: 16-byte
-// loads allowed.
-template <int T> struct Raw8 { u32x4 w; };
-template <> struct Raw8<SD_F32> { f32x4 a, b; };
-
-template <int T>
-__device__ __forceinline__ Raw8<T> load8(const void *x, int64_t at, int left, bool vec) {
-  Raw8<T> r;
-  if constexpr (T == SD_F32) {
-    const float *p = reinterpret_cast<const float *>(x) + at;
-    if (vec && left >= 8) {
-      r.a = *reinterpret_cast<const f32x4 *>(p);
-      r.b = *reinterpret_cast<const f32x4 *>(p + 4);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { r.a[i] = i < left ? p[i] : 0.f; r.b[i] = 4 + i < left ? p[4 + i] : 0.f; }
-    }
-  } else {
-    const uint16_t *p = reinterpret_cast<const uint16_t *>(x) + at;
-    if (vec && left >= 8) {
-      r.w = *reinterpret_cast<const u32x4 *>(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r.w[i] = (2 * i < left ? p[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-    }
-  }
-  return r;
-}
-
-// The bits as fp32 of the largest of the eight magnitudes; as integers magnitudes order like
-// the values, infinity and NaN on top.
-template <int T>
-__device__ __forceinline__ uint32_t top8(const Raw8<T> &r) {
-  if constexpr (T == SD_F32) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      top = max(top, max(__float_as_uint(r.a[i]) & 0x7fffffffu, __float_as_uint(r.b[i]) & 0x7fffffffu));
-    return top;
-  } else {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(r.w[i] & 0x7fffu, (r.w[i] >> 16) & 0x7fffu));
-    if (T == SD_BF16) return top << 16;
-    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)top));
-  }
-}
-
-// By value: a bit cast of a vector's element itself would take the first one.
-template <class P>
-__device__ __forceinline__ P pair(uint32_t w) { return __builtin_bit_cast(P, w); }
 
 // The eight codes, by the hardware's conversions: x / scale rounded to nearest, ties to the
 // even code, magnitudes over 6 to 6, for every scale from 2^-127 on and with denormals (each
@@ -134,13 +71,6 @@ __device__ __forceinline__ int quantize_block(const Raw8<T> &r, uint32_t &word) 
   const int byte = max(field - 2, 0);
   word = field == 255 ? 0u : codes8<T>(r, __uint_as_float((uint32_t)byte << 23));
   return field == 255 ? 255 : byte;
-}
-
-// Row and column group of item n: base (row, c) of the workgroup's first item, `per` a row.
-struct Item { int64_t row; int c; };
-__device__ __forceinline__ Item item_at(int64_t row0, int c0, int n, int per) {
-  const unsigned at = c0 + n, q = at / (unsigned)per;
-  return {row0 + q, (int)(at - q * per)};
 }
 
 // An item is eight columns; four neighbouring threads hold a block, whose largest magnitude
@@ -217,14 +147,6 @@ __global__ __launch_bounds__(256) void k_mx_tile(const uint8_t *codes, const uin
   }
   *reinterpret_cast<u32x4 *>(out_codes + tile * 4096 + t * 16) = w;
   out_scales[tile * 256 + lane * 4 + (t >> 6)] = s;
-}
-
-// Rounded to nearest even, by the hardware's conversions.
-__device__ inline u32x2 pack4(const f32x4 &z, int32_t type) {
-  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-  typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-  return type == SD_BF16 ? __builtin_bit_cast(u32x2, __builtin_convertvector(z, bf16x4))
-                         : __builtin_bit_cast(u32x2, __builtin_convertvector(z, f16x4));
 }
 
 // x[row][8 c ..] from the codes; x is written to column d - 1. Items as in k_mx_quantize.
@@ -413,28 +335,6 @@ __global__ __launch_bounds__(256) void k_mx_skinny(MxGemmArgs a) {
 }
 
 // ------------------------------------------------------------- many hidden rows
-__device__ inline void raw_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// f(0), f(1), .. f(N - 1) with each number a constant.
-template <class F, int... I>
-__device__ __forceinline__ void each_impl(F f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void each(F f) {
-  each_impl(f, std::make_integer_sequence<int, N>{});
-}
-
-// At most N of this wave's memory reads pending, no LDS read.
-template <int N>
-__device__ inline void wait_loads() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | (((N >> 4) & 3) << 14) | (0x7 << 4));
-}
-
 // The matrix instruction with its accumulator as both operand and result, in accumulation
 // registers: left to itself the compiler gives this instruction another result register and
 // moves accumulators about, some 200 moves for 64 instructions. It also knows no hazards of
@@ -634,25 +534,6 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiled(MxGemmArgs a, int n_mt, int
   }
 }
 
-template <class F>
-void by_type(int32_t type, F f) {
-  if (type == SD_F32) f(std::integral_constant<int, SD_F32>{});
-  else if (type == SD_BF16) f(std::integral_constant<int, SD_BF16>{});
-  else f(std::integral_constant<int, SD_F16>{});
-}
-
-// launch(type, items a thread, grid) for items of eight columns. Four a thread once every CU
-// has several workgroups of them. bf16, us for one / four a thread (quantise; back):
-//   2^16 items 3.5 / 4.1; 3.5 / 4.2   2^21 items 9.5 / 8.5; 9.6 / 9.2   2^25 items 125 / 122; 138 / 115
-template <class F>
-hipError_t by_items(int32_t type, int64_t items, F launch) {
-  by_type(type, [&](auto T) {
-    if (items >= 1 << 21) launch(T, std::integral_constant<int, 4>{}, dim3((unsigned)((items + 1023) / 1024)));
-    else launch(T, std::integral_constant<int, 1>{}, dim3((unsigned)((items + 255) / 256)));
-  });
-  return hipGetLastError();
-}
-
 template <int WV, int WM, int TV, int TM, int NS>
 hipError_t launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
   const int n_mt = (a.M + 16 * WM * TM - 1) / (16 * WM * TM), n_vt = (a.V + 16 * WV * TV - 1) / (16 * WV * TV);
@@ -665,11 +546,6 @@ hipError_t launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
 double rounds(int M, int V, int ids, int rows) {
   const int64_t n = (int64_t)((V + ids - 1) / ids) * ((M + rows - 1) / rows);
   return (double)((n + 255) / 256);
-}
-
-bool vec_rows(const void *x, int32_t type, int64_t stride, int elems) {
-  const int64_t size = type == SD_F32 ? 4 : 2, bytes = size * elems;
-  return reinterpret_cast<uintptr_t>(x) % bytes == 0 && stride * size % bytes == 0;
 }
 
 }  // namespace

@@ -1,0 +1,190 @@
+// 4-bit integer weights with a scale per group of columns: quantisation and the values back
+// (gfx950).
+//
+// A group of G (32, 64 or 128) consecutive columns of a row shares a 16-bit scale s and, in
+// the asymmetric form, a zero z in 0 .. 15 (z = 8 in the symmetric form); a value is
+// (c - z) s for its code c in 0 .. 15.
+//   asymmetric  s = (max(x, 0) - min(x, 0)) / 15 rounded to fp32 and to its type,
+//               z = -min(x, 0) / s rounded and held to 0 .. 15
+//   symmetric   s = max |x| / 7 in fp32, rounded to its type
+//   c = x / s rounded, plus z, held to 0 .. 15
+// Quotients are rounded to fp32, then to the nearest integer, ties to even. A scale under the
+// smallest normal fp32 number is 0 and its codes are z = 0 (8); a group that holds a NaN or an
+// infinity, or whose scale passes its type, has a NaN scale.
+#include "sd_launch.h"
+#include "sd_rows.h"
+
+namespace sdv {
+namespace {
+
+struct W4Args {
+  const void *x;
+  int64_t rows, stride;    // elements from row to row
+  int d;
+  bool vec, symmetric;
+  int32_t scale_type;
+  uint8_t *codes;          // [rows][d / 2]
+  uint16_t *scales;        // [rows][d / G]
+  uint8_t *zeros;          // [rows][d / G], null in the symmetric form
+};
+
+// f over the G / 8 neighbouring threads of a group: quads, halves of 16 lanes, 16 lanes.
+template <int G, class F>
+__device__ __forceinline__ uint32_t over_group(uint32_t v, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));                    // lane ^ 1
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));                    // lane ^ 2
+  if (G >= 64) v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));      // 7 - lane of 8
+  if (G >= 128) v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));     // 15 - lane of 16
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  return __uint_as_float(over_group<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+
+// x / s rounded to nearest, r being 1 / s rounded: the quotient's error is taken from x by one
+// fused operation (exact but near the ends of fp32's range) and corrected by another.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+
+__device__ __forceinline__ float scale_value(uint16_t bits, int32_t type) {
+  return type == SD_BF16 ? __uint_as_float((uint32_t)bits << 16) : (float)__builtin_bit_cast(_Float16, bits);
+}
+
+// An item is eight columns, G / 8 neighbouring threads hold a group; a thread takes U items 256
+// apart, its loads issued together.
+template <int T, int U, int G>
+__global__ __launch_bounds__(256) void k_w4_quantize(W4Args a) {
+  const int per = a.d / 8;        // a multiple of G / 8: a group's items are all in or all out
+  const int64_t base = (int64_t)blockIdx.x * 256 * U, row0 = base / per;
+  const int c0 = (int)(base - row0 * per);
+  Item it[U];
+  Raw8<T> raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    it[u] = item_at(row0, c0, threadIdx.x + 256 * u, per);
+    raw[u] = Raw8<T>{};
+    if (it[u].row < a.rows) raw[u] = load8<T>(a.x, it[u].row * a.stride + 8 * it[u].c, 8, a.vec);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    f32x4 lo, hi;
+    widen8<T>(raw[u], lo, hi);
+    const uint32_t top = over_group<G>(top8<T>(raw[u]), [](uint32_t p, uint32_t q) { return max(p, q); });
+    float s, most = 0.f, least = 0.f;
+    if (a.symmetric) {
+      s = __uint_as_float(top) / 7.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        most = fmaxf(most, fmaxf(lo[i], hi[i]));
+        least = fmaxf(least, fmaxf(-lo[i], -hi[i]));
+      }
+      most = group_max<G>(most);
+      least = group_max<G>(least);
+      // The sum over 15, corrected as quotient() is.
+      const double w = (double)most + (double)least, q = w * (1.0 / 15);
+      s = (float)fma(fma(-15.0, q, w), 1.0 / 15, q);
+    }
+    const u32x2 packed = pack4(f32x4{s, s, s, s}, a.scale_type);
+    uint16_t bits = (uint16_t)packed[0];
+    s = scale_value(bits, a.scale_type);
+    const bool bad = top >= 0x7f800000u || s > 3.4028234e38f, none = s < 1.17549435e-38f;
+    if (bad) bits = a.scale_type == SD_BF16 ? 0x7fc0 : 0x7e00;
+    else if (none) bits = 0;
+    const float r = 1.f / s;
+    float z = a.symmetric ? 8.f : fminf(rintf(quotient(least, s, r)), 15.f);
+    if (!a.symmetric && (bad || none)) z = 0.f;
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float c = rintf(quotient(i < 4 ? lo[i & 3] : hi[i & 3], s, r)) + z;
+      c = bad || none ? z : __builtin_amdgcn_fmed3f(c, 0.f, 15.f);
+      word |= (uint32_t)c << (4 * i);
+    }
+    const int64_t row = it[u].row;
+    const int c = it[u].c;
+    if (row >= a.rows) continue;
+    *reinterpret_cast<uint32_t *>(a.codes + row * (a.d / 2) + 4 * c) = word;
+    if (c % (G / 8) == 0) {
+      const int64_t g = row * (a.d / G) + c / (G / 8);
+      a.scales[g] = bits;
+      if (!a.symmetric) a.zeros[g] = (uint8_t)z;
+    }
+  }
+}
+
+// x[row][8 c ..]: (code - zero) scale, exact in fp32, rounded once.
+template <int T, int U, int G>
+__global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a, void *x) {
+  const int per = a.d / 8;
+  const int64_t base = (int64_t)blockIdx.x * 256 * U, row0 = base / per;
+  const int c0 = (int)(base - row0 * per);
+  Item it[U];
+  uint32_t word[U];
+  uint16_t s[U];
+  uint8_t z[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    it[u] = item_at(row0, c0, threadIdx.x + 256 * u, per);
+    if (it[u].row < a.rows) {
+      const int64_t g = it[u].row * (a.d / G) + it[u].c / (G / 8);
+      word[u] = *reinterpret_cast<const uint32_t *>(a.codes + it[u].row * (a.d / 2) + 4 * it[u].c);
+      s[u] = a.scales[g];
+      z[u] = a.symmetric ? 8 : a.zeros[g];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (it[u].row >= a.rows) continue;
+    const float scale = scale_value(s[u], a.scale_type);
+    f32x4 lo, hi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = (float)((int)(word[u] >> (4 * i) & 15) - z[u]) * scale;
+      hi[i] = (float)((int)(word[u] >> (16 + 4 * i) & 15) - z[u]) * scale;
+    }
+    store8<T>(x, it[u].row * a.stride + 8 * it[u].c, 8, a.vec, lo, hi);
+  }
+}
+
+template <class F>
+hipError_t by_group(int group, F f) {
+  if (group == 32) return f(std::integral_constant<int, 32>{});
+  if (group == 64) return f(std::integral_constant<int, 64>{});
+  return f(std::integral_constant<int, 128>{});
+}
+
+}  // namespace
+
+hipError_t launch_w4_quantize(const void *x, int32_t type, int64_t rows, int d, int64_t stride, int group,
+                              uint8_t *codes, uint16_t *scales, int32_t scale_type, uint8_t *zeros,
+                              hipStream_t stream) {
+  const W4Args a{x, rows, stride, d, vec_rows(x, type, stride, type == SD_F32 ? 4 : 8), zeros == nullptr,
+                 scale_type, codes, scales, zeros};
+  return by_group(group, [&](auto G) {
+    return by_items(type, rows * (d / 8), [&](auto T, auto U, dim3 grid) {
+      hipLaunchKernelGGL((k_w4_quantize<T, U, G>), grid, dim3(256), 0, stream, a);
+    });
+  });
+}
+
+hipError_t launch_w4_dequantize(const uint8_t *codes, const uint16_t *scales, int32_t scale_type,
+                                const uint8_t *zeros, int64_t rows, int d, int group, void *x, int32_t type,
+                                int64_t stride, hipStream_t stream) {
+  const W4Args a{nullptr, rows, stride, d, vec_rows(x, type, stride, type == SD_F32 ? 4 : 8), zeros == nullptr,
+                 scale_type, const_cast<uint8_t *>(codes), const_cast<uint16_t *>(scales),
+                 const_cast<uint8_t *>(zeros)};
+  return by_group(group, [&](auto G) {
+    return by_items(type, rows * (d / 8), [&](auto T, auto U, dim3 grid) {
+      hipLaunchKernelGGL((k_w4_dequantize<T, U, G>), grid, dim3(256), 0, stream, a, x);
+    });
+  });
+}
+
+}  // namespace sdv

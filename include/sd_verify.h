@@ -9,8 +9,12 @@
  *   3. sd_accept_greedy           greedy prefix acceptance + correction/bonus token
  *      sd_accept_rejection        rejection-sampling acceptance + residual/bonus draw
  *      sd_accept_filtered         the same under top-k, top-p and min-p
+ * before it
+ *      sd_rms_norm                the last residual addition and norm, which make the hidden rows
  * and, on the drafter's side:
  *      sd_mxfp4_logits            logits under a 4-bit copy of the LM head
+ *      sd_mxfp8_logits            the same under an 8-bit copy
+ *      sd_w4_logits               the same under 4-bit integer weights with group scales
  *      sd_sample                  draws under temperature, top-k, top-p and min-p
  *
  * Conventions shared by every call
@@ -504,7 +508,8 @@ SD_API int32_t sd_verify_rejection(const uint16_t *hidden, const void *lm_head,
 enum {
     SD_F32 = 0,
     SD_BF16 = 1,
-    SD_F16 = 2
+    SD_F16 = 2,
+    SD_MXFP8 = 3   /* hidden rows of sd_mxfp8_logits only */
 };
 
 /*
@@ -575,6 +580,153 @@ SD_API int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t 
                                int64_t hidden_stride, const uint8_t *head, int32_t V,
                                void *logits, int32_t logits_type, int64_t logits_stride,
                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * RMS norm of rows with the residual's addition (DSpark summary, "Production deployment": the
+ * LM head maps the hidden state to logits; this is the step that makes that hidden state):
+ *   s = x + residual, added in fp32 and rounded to the residual's type (s = x without one)
+ *   y = s / sqrt(mean(s^2) + eps) * (weight_offset + weight)
+ * with the mean, the root and the product in fp64 and y rounded to fp32, then to its type.
+ *   x         [rows][d] of type x_type, row stride x_stride elements (>= d)
+ *   residual  [rows][d] of type residual_type (x_type or SD_F32), or NULL
+ *   weight    [d] of type weight_type, or NULL: no factor (weight_offset is not used then)
+ *   eps       finite and >= 0 (a row of zeros under eps 0 gives NaN)
+ *   sum       [rows][d] of residual_type or NULL: out, s; only with a residual
+ *   sd_rms_norm:        y [rows][d] of type y_type: out
+ *   sd_rms_norm_mxfp8:  codes, scales: out, y as MXFP8 rows (below; y's fp32 value is what is
+ *                       quantised), d a multiple of 8
+ * A row is read before any of it is written: sum or y may be x or the residual itself (same
+ * address, type and stride), not the same one both; no other overlap is allowed. Any alignment of
+ * the element types; 16-byte aligned rows are fastest. No workspace.
+ * A NaN makes its row NaN. In a row with an infinity that column is NaN and the finite ones 0;
+ * as MXFP8, where a block that holds a NaN reads as NaN, the other blocks 0.
+ * Errors: SD_EINVAL (null pointer, unknown type, eps or weight_offset not finite, eps < 0, a sum
+ * without a residual), SD_ESHAPE (rows < 1, d outside [1, 2^20], d % 8 != 0 for MXFP8, short
+ * strides), SD_EALIGN (an array not aligned to its elements; codes 16 bytes, scales 4), SD_EDEVICE.
+ */
+SD_API int32_t sd_rms_norm(const void *x, int32_t x_type, int64_t x_stride, const void *residual,
+                           int32_t residual_type, int64_t residual_stride, const void *weight,
+                           int32_t weight_type, float weight_offset, float eps, int32_t rows,
+                           int32_t d, void *sum, int64_t sum_stride, void *y, int32_t y_type,
+                           int64_t y_stride, void *stream);
+SD_API int32_t sd_rms_norm_mxfp8(const void *x, int32_t x_type, int64_t x_stride,
+                                 const void *residual, int32_t residual_type,
+                                 int64_t residual_stride, const void *weight, int32_t weight_type,
+                                 float weight_offset, float eps, int32_t rows, int32_t d, void *sum,
+                                 int64_t sum_stride, uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * MXFP8 (OCP Microscaling Formats, e4m3): as MXFP4 with a byte a value, kp = sd_mxfp4_columns(d):
+ *   codes   uint8 [rows][kp]       e4m3
+ *   scales  uint8 [rows][kp / 32]  e + 127; 255: the block's values are NaN
+ * Columns d .. kp - 1 hold code 0, whole blocks of them under scale byte 0.
+ * Quantisation: a = the block's largest magnitude, e = max(floor(log2 a) - 8, -127), code =
+ * x / 2^e rounded to the nearest e4m3 number, ties to the even code, over 448 to 448. A block that
+ * holds a NaN or an infinity gets scale byte 255 and code 0.
+ * Arguments and errors as for the MXFP4 calls. sd_mxfp8_dequantize rounds once to x_type (exact in
+ * fp32 and bf16 unless the scale leaves their normal range; scale bytes over 246, which
+ * quantisation never gives, can pass the largest fp32 number and then give an infinity).
+ */
+SD_API int32_t sd_mxfp8_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d,
+                                 int64_t x_stride, uint8_t *codes, uint8_t *scales, void *stream);
+SD_API int32_t sd_mxfp8_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows,
+                                   int32_t d, void *x, int32_t x_type, int64_t x_stride,
+                                   void *stream);
+
+/*
+ * The form of an MXFP8 LM head that sd_mxfp8_logits reads, made once: tiles of 64 rows by 128
+ * columns in the order the matrix instructions take them. Arguments, limits and errors as for
+ * sd_mxfp4_head_bytes and sd_mxfp4_head.
+ */
+SD_API size_t sd_mxfp8_head_bytes(int32_t V, int32_t d);
+SD_API int32_t sd_mxfp8_head(const uint8_t *codes, const uint8_t *scales, int32_t V, int32_t d,
+                             uint8_t *head, size_t head_bytes, void *stream);
+
+/*
+ * Logits of hidden rows under an MXFP8 LM head (a drafter's copy that is coarser than bf16 and
+ * finer than MXFP4).
+ *   hidden   hidden_type SD_F32, SD_BF16, SD_F16: [M][d], row stride hidden_stride elements,
+ *            quantised to MXFP8 in the call; hidden_scales NULL
+ *            hidden_type SD_MXFP8: codes [M][kp] as sd_rms_norm_mxfp8 or sd_mxfp8_quantize wrote
+ *            them, 16-byte aligned, with hidden_scales [M][kp / 32], 4-byte aligned;
+ *            hidden_stride kp
+ *   head     the [V][d] LM head as sd_mxfp8_head wrote it
+ *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
+ *   workspace  sd_mxfp8_logits_workspace_bytes(M, d) bytes
+ * logits[m][v] = the sum of the products of the values, every product exact, accumulated in
+ * fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives NaN.
+ * Errors: as for sd_mxfp4_logits; SD_EINVAL also for hidden_scales that do not go with hidden_type.
+ */
+SD_API size_t sd_mxfp8_logits_workspace_bytes(int32_t M, int32_t d);
+SD_API int32_t sd_mxfp8_logits(const void *hidden, int32_t hidden_type,
+                               const uint8_t *hidden_scales, int32_t M, int32_t d,
+                               int64_t hidden_stride, const uint8_t *head, int32_t V, void *logits,
+                               int32_t logits_type, int64_t logits_stride, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * 4-bit integer weights with group scales: `group` (32, 64 or 128) consecutive columns of a row
+ * share a scale and, in the asymmetric form, a zero; a value is (code - zero) * scale.
+ *   codes   uint8 [rows][d / 2]      codes 0 .. 15, column 2 i in the low half of byte i
+ *   scales  [rows][d / group]        of scale_type SD_BF16 or SD_F16
+ *   zeros   uint8 [rows][d / group]  0 .. 15, or NULL: the symmetric form, every zero is 8
+ * Quantisation:
+ *   asymmetric  scale = (max(x, 0) - min(x, 0)) / 15, rounded to fp32 and to scale_type,
+ *               zero = -min(x, 0) / scale, rounded and held to 15
+ *   symmetric   scale = max |x| / 7 in fp32, rounded to scale_type
+ *   code = x / scale rounded, plus zero, held to 0 .. 15
+ * quotients in fp32, rounded to the nearest integer, ties to even. A scale under the smallest
+ * normal fp32 number (2^-126) becomes 0, its zero 0 (8) and its codes that zero. A group that
+ * holds a NaN or an infinity, or whose scale passes scale_type's largest number, has a NaN scale.
+ *   x       [rows][d] of type x_type, row stride x_stride elements (any alignment of the element
+ *           type, 16-byte aligned rows are fastest); rows >= 1, d a positive multiple of group, at
+ *           most 2^20; rows * d at most 2^37 - 2^13
+ *   codes, scales, zeros  16-, 4- and 4-byte aligned
+ * sd_w4_dequantize writes the values, rounded once to x_type (products are exact in fp32).
+ * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (also a group not among the three),
+ * SD_EALIGN, SD_EDEVICE.
+ */
+SD_API int32_t sd_w4_quantize(const void *x, int32_t x_type, int32_t rows, int32_t d,
+                              int64_t x_stride, int32_t group, uint8_t *codes, void *scales,
+                              int32_t scale_type, uint8_t *zeros, void *stream);
+SD_API int32_t sd_w4_dequantize(const uint8_t *codes, const void *scales, int32_t scale_type,
+                                const uint8_t *zeros, int32_t rows, int32_t d, int32_t group,
+                                void *x, int32_t x_type, int64_t x_stride, void *stream);
+
+/*
+ * The form of such an LM head that sd_w4_logits reads, made once from any such codes, scales and
+ * zeros: tiles of 64 rows by 128 columns in the order the matrix instructions take them.
+ * sd_w4_head_bytes: its size (has_zeros: 1 with zeros, 0 without; 0 unless V is in [1, 2^21], d is
+ * a positive multiple of group up to 2^20, group is 32, 64 or 128, and there are fewer than 2^24
+ * tiles).
+ * sd_w4_head: writes it on `stream`; head 256-byte aligned, apart from the inputs.
+ *   Errors: SD_EINVAL (null pointer, unknown scale_type), SD_ESHAPE, SD_EALIGN, SD_EWORKSPACE
+ *   (head_bytes too small), SD_EDEVICE.
+ */
+SD_API size_t sd_w4_head_bytes(int32_t V, int32_t d, int32_t group, int32_t has_zeros);
+SD_API int32_t sd_w4_head(const uint8_t *codes, const void *scales, int32_t scale_type,
+                          const uint8_t *zeros, int32_t V, int32_t d, int32_t group, uint8_t *head,
+                          size_t head_bytes, void *stream);
+
+/*
+ * Logits of hidden rows under a 4-bit LM head with group scales; the hidden rows are not rounded.
+ *   hidden   [M][d] of hidden_type SD_BF16 or SD_F16, row stride hidden_stride elements
+ *   head, V, d, group, scale_type, has_zeros   as sd_w4_head wrote it
+ *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
+ *   workspace  sd_w4_logits_workspace_bytes(M, d, group) bytes
+ * logits[m][v] = sum over groups of scale * (sum code * hidden - zero * sum hidden), products
+ * exact, sums in fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives
+ * NaN, and so may one whose sum of 15 |hidden| over a group passes the largest fp32 number.
+ * Errors: SD_EINVAL (null pointer, unknown type), SD_ESHAPE (M < 1, V, d or group as above, 2^24
+ * or more tiles of hidden rows, of the LM head or, at 128 x 128, of logits, short strides),
+ * SD_EALIGN, SD_EWORKSPACE, SD_EDEVICE.
+ */
+SD_API size_t sd_w4_logits_workspace_bytes(int32_t M, int32_t d, int32_t group);
+SD_API int32_t sd_w4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d,
+                            int64_t hidden_stride, const uint8_t *head, int32_t V, int32_t group,
+                            int32_t scale_type, int32_t has_zeros, void *logits,
+                            int32_t logits_type, int64_t logits_stride, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 /*
  * Sampling settings (host struct of device pointers, each may be NULL: that filter is off,

@@ -1,0 +1,312 @@
+"""MXFP8 on the GPU against the 64-bit statement: codes and scales exactly, logits within the
+fp32 accumulation's rounding.
+
+Logit tolerance: a product of two MXFP8 values is exact in fp32, and the sum of d of them in
+fp32, in any order, is off by at most (d - 1) 2^-24 sum |terms|; an output rounded once to bf16
+or fp16 adds half a step (eps / 2 relative)."""
+import numpy as np
+import pytest
+import torch
+
+import _narrow as N
+import draft_block_verification_amd as sd
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def need_gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a visible MI355X")
+    yield
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,d", [(1, 8), (3, 32), (2, 40), (5, 96), (7, 136), (1, 256), (130, 2048), (33, 7168)])
+def test_quantise_and_back(rows, d, dtype):
+    x = N.rand(rows, d, dtype, rows * d, spread=True)
+    codes, scales = sd.sd_mxfp8_quantize(x.cuda())
+    rc, rs = N.mx8_quantize(x.double().numpy())
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    assert np.array_equal(codes.cpu().numpy(), rc)
+    for out in TYPES:
+        got = sd.sd_mxfp8_dequantize(codes, scales, d, out).cpu()
+        assert torch.equal(got, torch.from_numpy(N.mx8_values(rc, rs, d)).to(out)), out
+
+
+def test_many_items_a_thread():
+    """Sizes at which a thread takes several items, cut at the end."""
+    x = N.rand(4099, 4104, torch.bfloat16, 1, spread=True)
+    codes, scales = sd.sd_mxfp8_quantize(x.cuda())
+    rc, rs = N.mx8_quantize(x.double().numpy())
+    assert np.array_equal(scales.cpu().numpy(), rs) and np.array_equal(codes.cpu().numpy(), rc)
+    got = sd.sd_mxfp8_dequantize(codes, scales, 4104, torch.bfloat16).cpu()
+    assert torch.equal(got, torch.from_numpy(N.mx8_values(rc, rs, 4104)).to(torch.bfloat16))
+
+
+def test_borders_zeros_and_extremes():
+    """Every tie between neighbouring magnitudes and its neighbours, the range between 448 and 512,
+    zeros of both signs, the smallest and the largest scales, subnormal blocks."""
+    ties = (N.E4M3[1:] + N.E4M3[:-1]) / 2
+    around = [np.nextafter(np.float32(t), np.float32(s)) for t in ties for s in (0, 1000)]
+    vals = np.concatenate([ties, around, [448, 449, 463.9, 464, 480, 511.9, 0.0, -0.0]]).astype(np.float32)
+    vals = np.concatenate([vals, -vals])
+    blocks = np.zeros((-(-len(vals) // 31), 32), dtype=np.float32)
+    blocks[:, 31] = 256                        # every block's exponent is 0
+    for i in range(len(blocks)):
+        part = vals[31 * i:31 * i + 31]
+        blocks[i, :len(part)] = part
+    rows = [blocks * np.float32(2.0 ** e) for e in (0, 1, -3, 60, -100, 118)]
+    rows.append(np.zeros((1, 32), dtype=np.float32))
+    rows.append(np.full((1, 32), -0.0, dtype=np.float32))
+    for v in (np.finfo(np.float32).max, np.finfo(np.float32).tiny, 1e-42, 2.0 ** -149):
+        rows.append(np.full((1, 32), v, dtype=np.float32))
+    x = np.concatenate(rows)
+    codes, scales = sd.sd_mxfp8_quantize(torch.from_numpy(x).cuda())
+    rc, rs = N.mx8_quantize(x.astype(np.float64))
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    assert np.array_equal(codes.cpu().numpy(), rc)
+    got = sd.sd_mxfp8_dequantize(codes, scales, 32).cpu().numpy()
+    assert np.array_equal(got, N.mx8_values(rc, rs, 32).astype(np.float32))
+
+
+def test_every_code_under_every_scale_back():
+    codes = np.tile(np.arange(256, dtype=np.uint8), (256, 1))
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 8, axis=1)
+    with np.errstate(all="ignore"):
+        v = N.mx8_values(codes, scales, 256)
+    for out in TYPES:
+        got = sd.sd_mxfp8_dequantize(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), 256, out).cpu()
+        want = torch.from_numpy(v).float().to(out)
+        assert bool(((got == want) | (torch.isnan(got) & torch.isnan(want))).all()), out
+
+
+def test_not_finite_blocks():
+    x = N.rand(4, 128, torch.float32, 3)
+    x[0, 5], x[1, 40], x[2, 127] = float("nan"), float("inf"), float("-inf")
+    codes, scales = sd.sd_mxfp8_quantize(x.cuda())
+    rc, rs = N.mx8_quantize(x.double().numpy())
+    assert np.array_equal(scales.cpu().numpy(), rs) and (rs == 255).sum() == 3
+    assert np.array_equal(codes.cpu().numpy(), rc)
+    got = sd.sd_mxfp8_dequantize(codes, scales, 128).cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.repeat(rs == 255, 32, axis=1))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strided_rows(dtype):
+    """Rows of a wider tensor at an odd offset, into rows of a wider one, neighbours untouched."""
+    d = 136
+    x = N.rand(6, 160, dtype, 9).cuda()[::2, 3:3 + d]
+    codes, scales = sd.sd_mxfp8_quantize(x)
+    c2, s2 = sd.sd_mxfp8_quantize(x.contiguous())
+    assert torch.equal(codes, c2) and torch.equal(scales, s2)
+    out = torch.full((3, 200), 77.0, dtype=dtype, device="cuda")
+    sd.sd_mxfp8_dequantize(codes, scales, d, out=out[:, 5:5 + d])
+    assert torch.equal(out[:, 5:5 + d], sd.sd_mxfp8_dequantize(codes, scales, d, dtype))
+    assert bool((out[:, :5] == 77).all()) and bool((out[:, 5 + d:] == 77).all())
+
+
+def logits_case(M, V, d, dtype, out, seed, hidden=None, coded=False, spread=False):
+    h = N.rand(M, d, dtype, seed, spread) if hidden is None else hidden
+    w = N.rand(V, d, torch.bfloat16, seed + 1, spread)
+    head = sd.Mxfp8Weights.from_tensor(w.cuda())
+    given = sd.sd_mxfp8_quantize(h.cuda()) if coded else h.cuda()
+    got = sd.sd_mxfp8_logits(given, head, dtype=out).cpu().double()
+    hv = torch.from_numpy(N.mx8_values(*N.mx8_quantize(h.double().numpy()), d))
+    wv = torch.from_numpy(N.mx8_values(*N.mx8_quantize(w.double().numpy()), d))
+    want, size = hv @ wv.t(), hv.abs() @ wv.abs().t()
+    tol = d * 2.0 ** -24 * size
+    if out != torch.float32:
+        tol = tol + (want.abs() + tol) * torch.finfo(out).eps / 2
+    return got, want, tol
+
+
+SHAPES = [(1, 1, 8), (1, 15, 32), (2, 17, 128), (3, 64, 136), (16, 100, 256), (17, 1000, 512), (5, 257, 2048),
+          (33, 515, 640), (64, 1023, 384), (65, 300, 1152), (129, 777, 1024), (256, 1536, 512), (300, 2049, 768),
+          (1, 5003, 4096)]
+
+
+@pytest.mark.parametrize("coded", [False, True])
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("M,V,d", SHAPES)
+def test_logits(M, V, d, out, coded):
+    got, want, tol = logits_case(M, V, d, torch.bfloat16, out, 7 * M + V + d, coded=coded)
+    assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V,d", [(40, 70001, 136), (64, 65600, 256), (130, 32000, 264), (100, 65700, 128),
+                                   (500, 32001, 256), (257, 40000, 384), (33, 300, 640), (1030, 140, 128)])
+def test_logits_many_ids(M, V, d, out):
+    got, want, tol = logits_case(M, V, d, torch.bfloat16, out, 3)
+    assert bool(((got - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("M", [2, 20, 70, 140])
+def test_logits_scales_apart(M):
+    """Blocks of very different scales on both sides: each is applied to its own."""
+    got, want, tol = logits_case(M, 333, 640, torch.float32, torch.float32, 8, spread=True)
+    assert bool(((got - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("M", [1, 20, 140])
+def test_logits_hidden_types(M, dtype):
+    got, want, tol = logits_case(M, 333, 256, dtype, torch.float32, 5)
+    assert bool(((got - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("M", [4, 40, 200])
+@pytest.mark.parametrize("coded", [False, True])
+def test_logits_not_finite_row(M, coded):
+    """A hidden row with a NaN or an infinity gives NaN in that row alone."""
+    h = N.rand(M, 256, torch.bfloat16, 1)
+    h[1, 200], h[2, 3] = float("nan"), float("inf")
+    got, want, tol = logits_case(M, 130, 256, torch.bfloat16, torch.float32, 1, hidden=h, coded=coded)
+    assert bool(torch.isnan(got[1:3]).all())
+    rest = [0] + list(range(3, M))
+    assert bool(((got - want)[rest].abs() <= tol[rest]).all())
+
+
+@pytest.mark.parametrize("M", [1, 20, 100])
+def test_logits_nan_blocks_of_any_codes(M):
+    """A block under scale byte 255 reads as NaN whatever its codes, in the LM head and in hidden
+    rows; NaN codes do under any scale."""
+    V, d = 100, 256
+    hc, hs = sd.sd_mxfp8_quantize(N.rand(M, d, torch.bfloat16, 1).cuda())
+    wc, ws = sd.sd_mxfp8_quantize(N.rand(V, d, torch.bfloat16, 2).cuda())
+    ws[70, 3], wc[71, 5], wc[72, 255] = 255, 0x7f, 0xff
+    got = sd.sd_mxfp8_logits((hc, hs), sd.Mxfp8Weights(wc, ws, d))
+    bad = torch.isnan(got)
+    assert bool(bad[:, 70:73].all()) and int(bad.sum()) == 3 * M
+    hs[M - 1, 6] = 255
+    got = sd.sd_mxfp8_logits((hc, hs), sd.Mxfp8Weights(wc, ws, d))
+    assert bool(torch.isnan(got[M - 1]).all()) and int(torch.isnan(got).sum()) == 3 * (M - 1) + V
+
+
+@pytest.mark.parametrize("d", [32, 160, 992])
+def test_unpadded_weights(d):
+    """Codes and scales as checkpoints hold them, d no multiple of 128."""
+    w = N.rand(77, d, torch.bfloat16, d)
+    rc, rs = N.mx8_quantize(w.double().numpy())
+    h = N.rand(3, d, torch.bfloat16, d + 1).cuda()
+    head = sd.Mxfp8Weights(torch.from_numpy(rc[:, :d].copy()).cuda(), torch.from_numpy(rs[:, :d // 32].copy()).cuda(), d)
+    assert torch.equal(sd.sd_mxfp8_logits(h, head), sd.sd_mxfp8_logits(h, sd.Mxfp8Weights.from_tensor(w.cuda())))
+
+
+@pytest.mark.parametrize("M", [1, 6, 40, 100])
+@pytest.mark.parametrize("out", TYPES)
+def test_logits_into_strided_columns(M, out):
+    """Position j of every request's block of logits, rows gamma V apart, at an odd vocabulary; the
+    other positions stay, and so do rows behind the last."""
+    g, V, d = 3, 203, 256
+    h = N.rand(2 * M, d, torch.bfloat16, 4).cuda()
+    head = sd.Mxfp8Weights.from_tensor(N.rand(V, d, torch.bfloat16, 5).cuda())
+    plain = sd.sd_mxfp8_logits(h[::2].contiguous(), head, dtype=out)
+    block = torch.full((M + 2, g, V), 7.0, dtype=out, device="cuda")
+    sd.sd_mxfp8_logits(h[::2], head, block[:M, 1])
+    assert torch.equal(block[:M, 1], plain)
+    assert bool((block[:, 0] == 7).all()) and bool((block[:, 2] == 7).all()) and bool((block[M:] == 7).all())
+
+
+@pytest.mark.parametrize("M", [1, 48, 272])
+def test_logits_repeat_and_graph(M):
+    """The same bytes from call to call, and from two captured graphs that share a workspace,
+    replayed in turn with eager work and new inputs in between."""
+    V, d = 1500, 512
+    head = sd.Mxfp8Weights.from_tensor(N.rand(V, d, torch.bfloat16, 2).cuda())
+    hs = [N.rand(M, d, torch.bfloat16, 20 + i).cuda() for i in range(3)]
+    eager = [sd.sd_mxfp8_logits(h, head) for h in hs]
+    h = hs[0].clone()
+    outs = [torch.empty((M, V), device="cuda") for _ in range(2)]
+    ws = sd.new_workspace(sd.mxfp8_logits_workspace_bytes(M, d), "cuda")
+    codes = torch.empty((M, 512), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((M, 16), dtype=torch.uint8, device="cuda")
+
+    def one(i):
+        if i == 0:
+            sd.sd_mxfp8_logits(h, head, outs[0], workspace=ws)
+        else:
+            sd.sd_mxfp8_quantize(h, codes, scales)
+            sd.sd_mxfp8_logits((codes, scales), head, outs[1], workspace=ws)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        one(0), one(1)
+    torch.cuda.current_stream().wait_stream(st)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            one(i)
+    for i in (1, 2, 0, 1):
+        h.copy_(hs[i])
+        for k in (0, 1):
+            outs[k].zero_()
+            graphs[k].replay()
+            assert torch.equal(outs[k], eager[i])
+        assert torch.equal(sd.sd_mxfp8_logits(hs[i], head), eager[i])
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_given_stream(handle):
+    """Everything a call makes for itself (padding, codes, workspace, results) is made on the
+    stream it is given, behind work that is still on it."""
+    d, V, M = 160, 3000, 70
+    w = N.rand(V, d, torch.bfloat16, 1).cuda()
+    h = N.rand(M, d, torch.bfloat16, 2).cuda()
+    codes, scales = sd.sd_mxfp8_quantize(w)
+    want = sd.sd_mxfp8_logits(h, sd.Mxfp8Weights(codes, scales, d))
+    back = sd.sd_mxfp8_dequantize(codes, scales, d)
+    normed = sd.sd_rms_norm(w)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    s = st.cuda_stream if handle else st
+    big = torch.randn(4096, 4096, device="cuda")
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(st):
+            late = torch.zeros_like(w)
+            for _ in range(4):
+                big @ big
+            late.copy_(w)
+        c, e = sd.sd_mxfp8_quantize(late, stream=s)
+        head = sd.Mxfp8Weights(c, e, d, stream=s)
+        got = sd.sd_mxfp8_logits(h, head, stream=s)
+        val = sd.sd_mxfp8_dequantize(c, e, d, stream=s)
+        nrm = sd.sd_rms_norm(late, stream=s)
+        junk = [torch.full((V, d), 9.0, device="cuda") for _ in range(4)]
+        st.synchronize()
+        assert torch.equal(got, want) and torch.equal(val, back) and torch.equal(nrm, normed)
+        del junk
+
+
+def test_norm_logits_sample_together():
+    """A drafter's last steps as they run: residual and norm into MXFP8 rows, logits under the
+    8-bit LM head, one token a row; and the same rows under the 4-bit heads."""
+    M, d, V = 24, 512, 4000
+    x = N.rand(M, d, torch.bfloat16, 1)
+    res, w = N.rand(M, d, torch.bfloat16, 2), N.rand(1, d, torch.bfloat16, 3)[0]
+    lm = N.rand(V, d, torch.bfloat16, 4) * 0.1
+    head8 = sd.Mxfp8Weights.from_tensor(lm.cuda())
+    r = res.cuda()
+    rows = sd.sd_rms_norm_mxfp8(x.cuda(), w.cuda(), r, total=r)
+    z = sd.sd_mxfp8_logits(rows, head8)
+    s, y = N.norm(x, w, res)
+    assert torch.equal(r.cpu(), s)
+    hv = torch.from_numpy(N.mx8_values(*N.mx8_quantize(y.astype(np.float32).astype(np.float64)), d))
+    wv = torch.from_numpy(N.mx8_values(*N.mx8_quantize(lm.double().numpy()), d))
+    want, tol = hv @ wv.t(), d * 2.0 ** -24 * (hv.abs() @ wv.abs().t())
+    assert bool(((z.double().cpu() - want).abs() <= tol).all())
+    # tokens: greedy ones are the argmax of the very logits, drawn ones lie in the kept set
+    greedy = sd.SamplingParams([0.0] * M, None, None, None)
+    u = torch.rand(M, generator=torch.Generator().manual_seed(5)).cuda()
+    assert torch.equal(sd.sd_sample(z, u, greedy)[0].long(), z.argmax(1))
+    head4 = sd.W4Weights.from_tensor(lm.cuda(), 64)
+    hidden = sd.sd_rms_norm(x.cuda(), w.cuda(), res.cuda())
+    z4 = sd.sd_w4_logits(hidden, head4)
+    top = z4.topk(8, dim=1)[1]
+    drawn = sd.sd_sample(z4, u, sd.SamplingParams([0.9] * M, [8] * M, None, None))[0].long()
+    assert bool((top == drawn[:, None]).any(1).all())
