@@ -811,7 +811,7 @@ int32_t sd_w4_head(const uint8_t *codes, const void *scales, int32_t scale_type,
 
 size_t sd_w4_logits_workspace_bytes(int32_t M, int32_t d, int32_t group) {
   if (M < 1 || !w4_group(d, group) || !mx_tiles_fit(M, d)) return 0;
-  return w4_logits_workspace_bytes(M, d);
+  return w4_logits_workspace_bytes(M, d, group);
 }
 
 int32_t sd_w4_logits(const void *hidden, int32_t hidden_type, int32_t M, int32_t d, int64_t hidden_stride,

@@ -150,7 +150,7 @@ hipError_t launch_w4_dequantize(const uint8_t *codes, const uint16_t *scales, in
 size_t w4_head_bytes(int64_t V, int d, int group, bool zeros);
 hipError_t launch_w4_head(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int V, int d,
                           int group, uint8_t *head, hipStream_t stream);
-size_t w4_logits_workspace_bytes(int M, int d);
+size_t w4_logits_workspace_bytes(int M, int d, int group);
 hipError_t launch_w4_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
                             const uint8_t *head, int V, int group, int32_t scale_type, bool zeros, void *logits,
                             int32_t type, int64_t ld, void *workspace, hipStream_t stream);

@@ -370,27 +370,6 @@ __device__ __forceinline__ void mfma_mx_into(int sel_a, int sel_b, const u32x4 &
 
 __device__ __forceinline__ void settle() { asm volatile("s_nop 12"); }
 
-// n rows of W results of type T from a wave's part of LDS (rows ROW bytes apart) to rows m0 .. of
-// the output at column v0: 16 bytes a lane along the rows where they are aligned and whole, else
-// an element a lane.
-template <class T, int W, int ROW>
-__device__ __forceinline__ void store_rows(const MxGemmArgs &a, const LDSP uint8_t *part, int64_t m0, int n, int v0, int lane) {
-  constexpr int E = 16 / sizeof(T), LPR = W / E;     // elements a lane, lanes a row
-  static_assert(64 % LPR == 0, "whole rows a store");
-  const int rows = (int)min((int64_t)n, a.M - m0);
-  T *out = reinterpret_cast<T *>(a.out) + m0 * a.ld + v0;
-  if (a.wide && v0 + W <= a.V) {
-    for (int r = lane / LPR; r < rows; r += 64 / LPR) {
-      const u32x4 x = *(const LDSP u32x4 *)(part + r * ROW + (lane % LPR) * 16);
-      __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(out + r * a.ld + (lane % LPR) * E));
-    }
-  } else {
-    for (int r = 0; r < rows; ++r)
-      for (int v = lane; v < W && v0 + v < a.V; v += 64)
-        out[r * a.ld + v] = *(const LDSP T *)(part + r * ROW + v * (int)sizeof(T));
-  }
-}
-
 // A workgroup of four waves computes 64 GV ids by 64 GM hidden rows, each wave 16 TV by 16 TM
 // (WV by WM waves). A step's 128 columns of both operands come into one of NS LDS buffers by
 // direct loads, NS - 1 steps ahead. While a wave's matrix instructions consume step k from

@@ -122,8 +122,11 @@ __device__ __forceinline__ float byte_scale(uint32_t word, int i) {
   return __uint_as_float((word >> (8 * i) & 255) << 23);
 }
 
-__device__ __forceinline__ float wide_scale(uint32_t bits, bool f16) {
-  return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __uint_as_float(bits << 16);
+// A 16-bit scale; f16: all ones for fp16, 0 for bf16 (bits, as a choice between the two would be
+// a branch around every use).
+__device__ __forceinline__ float wide_scale(uint32_t bits, uint32_t f16) {
+  const uint32_t h = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)bits));
+  return __uint_as_float((h & f16) | (bits << 16 & ~f16));
 }
 
 struct NarrowArgs {
@@ -133,12 +136,13 @@ struct NarrowArgs {
   const uint8_t *codes;     // LM head, tiled
   const uint8_t *scales;
   const uint8_t *zeros;
-  bool scale_f16;           // scales of the 4-bit form in fp16, else bf16
+  uint32_t scale_f16;       // scales of the 4-bit form: ~0 in fp16, 0 in bf16
   int M, V, steps;          // steps: 128-column steps
   void *out;
   int32_t type;
   int64_t ld;
   bool vec, wide;           // four-element and 16-byte stores allowed
+  const float *sums;        // tiled kernel, 4-bit form: see k_w4_rows
 };
 
 __device__ inline void store4(const NarrowArgs &a, int m, int v, const f32x4 &z) {
@@ -175,7 +179,7 @@ struct Mx8 {
     uint32_t hs[MT];
   };
   template <int TV, int MT>
-  static __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int row0, int k, int lane,
+  static __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int k, int lane,
                                               Step<TV, MT> &st) {
     const int q = lane >> 4;
 #pragma unroll
@@ -193,7 +197,7 @@ struct Mx8 {
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int64_t row = min(row0 + 16 * m + (lane & 15), a.M - 1);
+      const int64_t row = min(16 * m + (lane & 15), a.M - 1);
       const uint8_t *p = reinterpret_cast<const uint8_t *>(a.hidden) + row * a.hstride + 128 * k + 16 * q;
       st.h[m][0] = *reinterpret_cast<const u32x4 *>(p);
       st.h[m][1] = *reinterpret_cast<const u32x4 *>(p + 64);
@@ -238,7 +242,7 @@ struct W4 {
     u32x4 h[MT][4];
   };
   template <int TV, int MT>
-  static __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int row0, int k, int lane,
+  static __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int k, int lane,
                                               Step<TV, MT> &st) {
 #pragma unroll
     for (int i = 0; i < TV; ++i) {
@@ -256,7 +260,7 @@ struct W4 {
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int64_t row = min(row0 + 16 * m + (lane & 15), a.M - 1);
+      const int64_t row = min(16 * m + (lane & 15), a.M - 1);
       const uint16_t *p = reinterpret_cast<const uint16_t *>(a.hidden) + row * a.hstride + 128 * k + 8 * (lane >> 4);
 #pragma unroll
       for (int t = 0; t < 4; ++t) st.h[m][t] = *reinterpret_cast<const u32x4 *>(p + 32 * t);
@@ -300,7 +304,7 @@ struct W4 {
 };
 
 // ---------------------------------------------------------------- few hidden rows
-// Up to 16 MT rows (and more by blockIdx.y): the LM head's bytes bound the call. One workgroup
+// Up to 16 MT rows: the LM head's bytes bound the call. One workgroup
 // per 16 TV ids; its NW waves take the 128-column steps in turn, straight into registers: each
 // weight is used by one wave only, so LDS would add a copy and share nothing. The hidden rows are
 // read by every workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
@@ -310,25 +314,31 @@ __global__ __launch_bounds__(64 * NW) void k_narrow_skinny(NarrowArgs a) {
   __shared__ float red[NW][16 * MT * LDR];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t group = (int64_t)blockIdx.x * (TV / 4);
-  const int row0 = 16 * MT * blockIdx.y;
   f32x4 acc[TV][MT];
 #pragma unroll
   for (int i = 0; i < TV; ++i)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
   typename F::template Step<TV, MT> st[D];
+  const int n = (a.steps - wave + NW - 1) / NW;       // steps of this wave; past its end the last one, unused
+  auto load = [&](int j, typename F::template Step<TV, MT> &to) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    F::template load<TV, MT>(a, group, min(wave + NW * j, a.steps - 1), lane, to);
+    __builtin_amdgcn_sched_barrier(0);       // whole sets of loads, in the order of their use
+  };
 #pragma unroll
-  for (int x = 0; x < D; ++x) F::template load<TV, MT>(a, group, row0, min(wave + NW * x, a.steps - 1), lane, st[x]);
-  for (int k = wave; k < a.steps; k += NW * D) {
+  for (int x = 0; x < D; ++x) load(x, st[x]);
+  int j = 0;
+  for (; j + D <= n; j += D) {
 #pragma unroll
     for (int x = 0; x < D; ++x) {
-      if (k + NW * x < a.steps) {
-        F::template use<TV, MT>(a, st[x], lane, acc);
-        // past the end: the last step again, unused
-        F::template load<TV, MT>(a, group, row0, min(k + NW * (x + D), a.steps - 1), lane, st[x]);
-      }
+      F::template use<TV, MT>(a, st[x], lane, acc);
+      load(j + x + D, st[x]);
     }
   }
+#pragma unroll
+  for (int x = 0; x < D - 1; ++x)
+    if (j + x < n) F::template use<TV, MT>(a, st[x], lane, acc);
   const int col = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -339,7 +349,7 @@ __global__ __launch_bounds__(64 * NW) void k_narrow_skinny(NarrowArgs a) {
   __syncthreads();
   for (int t = threadIdx.x; t < 16 * MT * IDS / 4; t += 64 * NW) {
     const int m = t / (IDS / 4), v = 4 * (t % (IDS / 4));
-    if (row0 + m >= a.M) break;
+    if (m >= a.M) break;
     f32x4 z = *reinterpret_cast<const f32x4 *>(&red[0][m * LDR + v]);
 #pragma unroll
     for (int w = 1; w < NW; ++w) {
@@ -347,45 +357,361 @@ __global__ __launch_bounds__(64 * NW) void k_narrow_skinny(NarrowArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) z[e] += o[e];
     }
-    store4(a, row0 + m, IDS * (int)blockIdx.x + v, z);
+    store4(a, m, IDS * (int)blockIdx.x + v, z);
+  }
+}
+
+// ---------------------------------------------------------------- many hidden rows
+// What a wave of the tiled kernel keeps of one step's weights (a tile of 64 ids), and what it
+// does with them and the hidden rows' fragments (frag(m, t)). chunk(): which 16 bytes of the 256 that
+// a step takes of a hidden row instruction t reads for the lanes of q.
+struct Mx8Tile {
+  static constexpr int kSums = 0;
+  u32x4 w[4][2];
+  uint32_t s[2];
+  __device__ __forceinline__ void load(const NarrowArgs &a, int64_t tile, int lane) {
+    const u32x4 *c = reinterpret_cast<const u32x4 *>(a.codes + tile * kMx8Tile) + lane;
+    const uint32_t *p = reinterpret_cast<const uint32_t *>(a.scales + tile * kMx8Scales) + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[i][h] = c[128 * i + 64 * h];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = p[16 * (2 * h + (lane >> 5))];
+  }
+  // Reads every register that load() fills: the compiler waits for them here.
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(w[i][0]), "+v"(w[i][1]));
+    asm volatile("" : "+v"(s[0]), "+v"(s[1]));
+  }
+  static __device__ __forceinline__ int chunk(int t, int q) { return 2 * q + (t & 1) + 8 * (t >> 1); }
+  template <int TM, class Frag, class Sum>
+  __device__ __forceinline__ void use(const NarrowArgs &, Frag frag, Sum, f32x4 (&acc)[4][TM]) const {
+    u32x4 h[2][TM];
+#pragma unroll
+    for (int m = 0; m < TM; ++m) h[0][m] = frag(m, 0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t < 3)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) h[(t + 1) & 1][m] = frag(m, t + 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x4 x = decode8(w[i][t / 2][t % 2 * 2], w[i][t / 2][t % 2 * 2 + 1], byte_scale(s[t / 2], i));
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[i][m] = mfma16<SD_BF16>(h[t & 1][m], x, acc[i][m]);
+      }
+    }
+  }
+};
+
+// The products of a group start from -zero times the row's sum over the group (sum(g, m): the
+// four rows of fragment m, times -8 already in the symmetric form).
+template <int H, int NG, bool ASYM>
+struct W4Tile {
+  static constexpr int kSums = NG;
+  u32x4 w[4];
+  u32x2 s[NG];
+  uint32_t z[NG];
+  __device__ __forceinline__ void load(const NarrowArgs &a, int64_t tile, int lane) {
+    const u32x4 *c = reinterpret_cast<const u32x4 *>(a.codes + tile * kW4Tile) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = c[64 * i];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int64_t at = (tile * NG + g) * 16 + (lane & 15);
+      s[g] = reinterpret_cast<const u32x2 *>(a.scales)[at];
+      if (ASYM) z[g] = reinterpret_cast<const uint32_t *>(a.zeros)[at];
+    }
+  }
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(w[i]));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      asm volatile("" : "+v"(s[g]));
+      if (ASYM) asm volatile("" : "+v"(z[g]));
+    }
+  }
+  static __device__ __forceinline__ int chunk(int t, int q) { return 4 * t + q; }
+  template <int TM, class Frag, class Sum>
+  __device__ __forceinline__ void use(const NarrowArgs &a, Frag frag, Sum sum, f32x4 (&acc)[4][TM]) const {
+    constexpr int KS = 4 / NG;
+    u32x4 h[2][TM];
+    f32x4 part[4][TM];
+#pragma unroll
+    for (int m = 0; m < TM; ++m) h[0][m] = frag(m, 0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t < 3)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) h[(t + 1) & 1][m] = frag(m, t + 1);
+      const int g = t / KS;
+      if (t % KS == 0) {
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+          const f32x4 c = sum(g, m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if constexpr (ASYM) {
+              const float zero = (float)(z[g] >> (8 * i) & 255);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) part[i][m][e] = zero * c[e];
+            } else {
+              part[i][m] = c;
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x4 x = decode4<H>(w[i][t]);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) part[i][m] = mfma16<H>(h[t & 1][m], x, part[i][m]);
+      }
+      if (t % KS == KS - 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float sc = wide_scale(s[g][i / 2] >> (16 * (i % 2)) & 0xffff, a.scale_f16);
+#pragma unroll
+          for (int m = 0; m < TM; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][m][e] = fmaf(sc, part[i][m][e], acc[i][m][e]);
+        }
+      }
+    }
+  }
+};
+
+// 16 or 4 bytes a lane from base + lane_at + at to LDS, lane after lane from dst on. Through a
+// buffer descriptor: behind a direct load with plain addresses the compiler lets no other load be
+// awaited alone.
+__device__ __forceinline__ void to_lds16(const void *base, int lane_at, int at, LDSP uint8_t *dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, -1, 0x00020000),
+                                           (LDSP void *)dst, 16, lane_at, at, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, LDSP uint8_t *dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, -1, 0x00020000),
+                                           (LDSP void *)dst, 4, lane_at, at, 0, 0);
+}
+
+// A workgroup of four waves computes 256 ids by 16 TM hidden rows, each wave 64 ids by all of
+// them. A step's 128 columns of the hidden rows (and the rows' sums of its groups) come into one
+// of three LDS buffers by direct loads, two steps ahead; chunk c of row r lies at place
+// c ^ (r % 16), so that the 16 rows of a fragment are read without bank conflicts. Each weight is
+// used by one wave alone: it comes from memory into that wave's registers, two steps ahead,
+// and is decoded there. Every wave issues the same loads every step, past the end the last
+// step's again: a step's weights are issued behind its hidden rows, so when the former have
+// arrived the latter have, and behind the barrier those of all waves.
+template <class F, int TM>
+__global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt, int n_vt) {
+  constexpr int NS = 3, ROWS = 16 * TM, STAGE = ROWS * 256 + F::kSums * ROWS * 4;
+  constexpr int LOADS = ROWS / 16;                 // of four rows, by each wave
+  static_assert(F::kSums == 0 || ROWS == 64, "a wave's load of a group's sums is 64 rows");
+  __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  // Tiles go to the XCDs (workgroup id mod 8) in contiguous runs with the hidden tile running
+  // fastest: an XCD's workgroups share LM-head tiles and hidden tiles in its L2.
+  const int nb = n_mt * n_vt, hb = blockIdx.x;
+  const int per = nb / 8, rem = nb % 8, xcd = hb % 8, pos = hb / 8;
+  const int logical = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + pos;
+  const int mt = logical % n_mt, vt = logical / n_mt;
+  const int64_t row0 = (int64_t)mt * ROWS;
+  const int64_t tile0 = min((int64_t)vt * 4 + wave, (int64_t)(a.V - 1) / 64) * a.steps;
+  const uint8_t *rows = reinterpret_cast<const uint8_t *>(a.hidden) + row0 * a.hstride * 2;
+  int src[LOADS];
+#pragma unroll
+  for (int n = 0; n < LOADS; ++n) {
+    const int at = 4 * (wave * LOADS + n) + q;       // row of the tile
+    src[n] = (int)(min((int64_t)at, a.M - 1 - row0) * a.hstride * 2) + ((r ^ (at & 15)) * 16);
+  }
+  const float *sums = a.sums + (int64_t)mt * a.steps * F::kSums * ROWS;
+  auto issue = [&](int k) __attribute__((always_inline)) {
+    LDSP uint8_t *dst = (LDSP uint8_t *)S + (k % NS) * STAGE;
+    const int kk = min(k, a.steps - 1);
+#pragma unroll
+    for (int n = 0; n < LOADS; ++n)
+      to_lds16(rows, src[n], kk * 256, dst + (wave * LOADS + n) * 1024);
+    if constexpr (F::kSums > 0)
+      to_lds4(sums, lane * 4, (kk * F::kSums + wave % F::kSums) * ROWS * 4,
+              dst + ROWS * 256 + (wave % F::kSums) * ROWS * 4);
+    asm volatile("" ::: "memory");
+  };
+  f32x4 acc[4][TM];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  F st[2];
+  auto step = [&](int k, F &now) __attribute__((always_inline)) {
+    now.arrived();
+    raw_barrier();                     // and every wave has read step k - 1 out of LDS
+    issue(k + NS - 1);
+    const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE;
+    auto frag = [&](int m, int t) __attribute__((always_inline)) {
+      return *(const LDSP u32x4 *)(b + (16 * m + r) * 256 + ((F::chunk(t, q) ^ r) * 16));
+    };
+    auto sum = [&](int g, int m) __attribute__((always_inline)) {
+      return *(const LDSP f32x4 *)(b + ROWS * 256 + (g * ROWS + 16 * m + 4 * q) * 4);
+    };
+    now.template use<TM>(a, frag, sum, acc);
+    now.load(a, tile0 + min(k + 2, a.steps - 1), lane);
+  };
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    issue(k);
+    st[k].load(a, tile0 + min(k, a.steps - 1), lane);
+    asm volatile("" ::: "memory");
+  }
+  int k = 0;
+  for (; k + 1 < a.steps; k += 2) {
+    step(k, st[0]);
+    step(k + 1, st[1]);
+  }
+  if (k < a.steps) step(k, st[0]);
+  wait_loads<0>();                     // the trailing loads land before LDS is used again
+  raw_barrier();
+  // The results cross LDS so that stores run along the rows: a lane holds one id of four rows.
+  const int64_t m0 = row0;
+  const int v0 = vt * 256 + wave * 64;
+  constexpr int PART = NS * STAGE / 4 / 16 * 16;
+  LDSP uint8_t *part = (LDSP uint8_t *)S + wave * PART;
+  if (a.type == SD_F32) {
+    constexpr int ROW = 64 * 4 + 16;
+    static_assert(ROW * ROWS / 2 <= PART, "half the rows in fp32");
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int m = 0; m < TM / 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *(LDSP float *)(part + (16 * m + 4 * q + e) * ROW + (16 * i + r) * 4) = acc[i][half * TM / 2 + m][e];
+      store_rows<float, 64, ROW>(a, part, m0 + half * ROWS / 2, ROWS / 2, v0, lane);
+    }
+  } else {
+    constexpr int ROW = 64 * 2 + 16;
+    static_assert(ROW * ROWS <= PART, "the rows in 16 bits");
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x2 h = pack4(acc[i][m], a.type);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *(LDSP uint16_t *)(part + (16 * m + 4 * q + e) * ROW + (16 * i + r) * 2) = (uint16_t)(h[e / 2] >> (16 * (e & 1)));
+      }
+    store_rows<uint16_t, 64, ROW>(a, part, m0, ROWS, v0, lane);
   }
 }
 
 // ---------------------------------------------------------------- hidden rows made ready
-// 16-bit rows copied to whole 128-column steps, zeros behind column d.
-__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t *x, int64_t rows, int64_t stride, int d, int kp,
-                                                  bool vec, uint16_t *out) {
+// Whole 128-column steps of 16-bit rows, zeros behind column d (out null: not stored), and each
+// group's sum of a row times `factor` (sums null: not formed): [ceil(rows / 64)][kp / G][64], rows
+// past the last left. An item is eight columns.
+template <int H, int G>
+__global__ __launch_bounds__(256) void k_w4_rows(const uint16_t *x, int64_t rows, int64_t stride, int d, int kp,
+                                                 bool vec, uint16_t *out, float *sums, float factor) {
   const int per = kp / 8;
   const int64_t base = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256, row0 = base / per;
   const Item it = item_at(row0, (int)(base - row0 * per), threadIdx.x, per);
-  if (it.row >= rows) return;
-  const int left = d - 8 * it.c;
-  u32x4 w = {0u, 0u, 0u, 0u};
-  if (left > 0) w = load8<SD_BF16>(x, it.row * stride + 8 * it.c, left, vec).w;
-  *reinterpret_cast<u32x4 *>(out + it.row * kp + 8 * it.c) = w;
+  const int left = it.row < rows ? d - 8 * it.c : 0;
+  Raw8<H> raw{};
+  if (left > 0) raw = load8<H>(x, it.row * stride + 8 * it.c, left, vec);
+  if (out && it.row < rows) *reinterpret_cast<u32x4 *>(out + it.row * kp + 8 * it.c) = raw.w;
+  if (!sums) return;
+  f32x4 lo, hi;
+  widen8<H>(raw, lo, hi);
+  float s = ((lo[0] + lo[1]) + (lo[2] + lo[3])) + ((hi[0] + hi[1]) + (hi[2] + hi[3]));
+  s = __uint_as_float(over_group<G>(__float_as_uint(s), [](uint32_t p, uint32_t q) {
+    return __float_as_uint(__uint_as_float(p) + __uint_as_float(q));
+  }));
+  if (it.row < rows && it.c % (G / 8) == 0)
+    sums[(it.row / 64 * (kp / G) + it.c / (G / 8)) * 64 + it.row % 64] = factor * s;
 }
+
+// Hidden rows of any type as the bf16 numbers of their MXFP8 form, [M][kp].
+template <int T>
+__global__ __launch_bounds__(256) void k_mx8_rows(const void *x, int64_t rows, int64_t stride, int d, int kp, bool vec,
+                                                  uint16_t *out) {
+  const int per = kp / 8;
+  const int64_t base = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256, row0 = base / per;
+  const Item it = item_at(row0, (int)(base - row0 * per), threadIdx.x, per);
+  const int left = it.row < rows ? d - 8 * it.c : 0;
+  Raw8<T> raw{};
+  if (left > 0) raw = load8<T>(x, it.row * stride + 8 * it.c, left, vec);
+  f32x4 lo, hi;
+  widen8<T>(raw, lo, hi);
+  const int byte = mx8_scale(block_top(top8<T>(raw)));
+  const u32x2 w = byte == 255 ? u32x2{0u, 0u} : mx8_codes(lo, hi, byte);
+  mx8_values(w, byte, lo, hi);
+  if (it.row < rows) store8<SD_BF16>(out, it.row * kp + 8 * it.c, 8, true, lo, hi);
+}
+
+// The same from codes and scales.
+__global__ __launch_bounds__(256) void k_mx8_decode(const uint8_t *codes, const uint8_t *scales, int64_t rows, int kp,
+                                                    uint16_t *out) {
+  const int64_t at = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (at >= rows * kp) return;
+  f32x4 lo, hi;
+  mx8_values(*reinterpret_cast<const u32x2 *>(codes + at), scales[at / 32], lo, hi);
+  store8<SD_BF16>(out, at, 8, true, lo, hi);
+}
+
+// A launch of n items of 256 threads a workgroup has under 2^32 threads along x.
+dim3 item_groups(int64_t items) {
+  const int64_t n = (items + 255) / 256, x = n < 1 << 20 ? n : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
+constexpr int kFewRows = 32;      // rows from which on the tiled kernel runs
 
 template <class F, int TV, int NW, int D>
 hipError_t launch_skinny(const NarrowArgs &a, hipStream_t stream) {
   const unsigned n = (unsigned)((a.V + 16 * TV - 1) / (16 * TV));
-  if (a.M <= 16)
-    hipLaunchKernelGGL((k_narrow_skinny<F, TV, 1, NW, D>), dim3(n), dim3(64 * NW), 0, stream, a);
-  else
-    hipLaunchKernelGGL((k_narrow_skinny<F, TV, 2, NW, D>), dim3(n, (a.M + 31) / 32), dim3(64 * NW), 0, stream, a);
+  auto *k = a.M <= 16 ? &k_narrow_skinny<F, TV, 1, NW, D> : &k_narrow_skinny<F, TV, 2, NW, D>;
+  hipLaunchKernelGGL(k, dim3(n), dim3(64 * NW), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class F, int TM>
+hipError_t launch_tiled(const NarrowArgs &a, hipStream_t stream) {
+  const int n_mt = (a.M + 16 * TM - 1) / (16 * TM), n_vt = (a.V + 255) / 256;
+  hipLaunchKernelGGL((k_narrow_tiled<F, TM>), dim3((unsigned)((int64_t)n_mt * n_vt)), dim3(256), 0, stream, a, n_mt, n_vt);
   return hipGetLastError();
 }
 
 template <int H, int NG>
 hipError_t launch_w4_of(const NarrowArgs &a, hipStream_t stream) {
+  if (a.M > kFewRows)
+    return a.zeros ? launch_tiled<W4Tile<H, NG, true>, 4>(a, stream) : launch_tiled<W4Tile<H, NG, false>, 4>(a, stream);
   return a.zeros ? launch_skinny<W4<H, NG, true>, 8, 4, 2>(a, stream)
                  : launch_skinny<W4<H, NG, false>, 8, 4, 2>(a, stream);
 }
 
-template <int H>
-hipError_t launch_w4_group(const NarrowArgs &a, int group, hipStream_t stream) {
-  if (group == 128) return launch_w4_of<H, 1>(a, stream);
-  if (group == 64) return launch_w4_of<H, 2>(a, stream);
-  return launch_w4_of<H, 4>(a, stream);
+// The rows of a call made ready, its group sums among them where the tiled kernel runs, and the call.
+template <int H, int G>
+hipError_t launch_w4_group(NarrowArgs a, int d, uint16_t *copy, float *sums, hipStream_t stream) {
+  const int kp = a.steps * 128;
+  const bool vec = vec_rows(a.hidden, H, a.hstride, 8);
+  // 64 rows of a tile are addressed by 32 bits
+  if (vec && kp == d && a.hstride < 1 << 24) copy = nullptr;
+  if (a.M <= kFewRows) sums = nullptr;
+  if (copy || sums) {
+    hipLaunchKernelGGL((k_w4_rows<H, G>), item_groups((int64_t)a.M * (kp / 8)), dim3(256), 0, stream,
+                       reinterpret_cast<const uint16_t *>(a.hidden), (int64_t)a.M, a.hstride, d, kp, vec, copy, sums,
+                       a.zeros ? -1.f : -8.f);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (copy) {
+    a.hidden = copy;
+    a.hstride = kp;
+  }
+  a.sums = sums;
+  return launch_w4_of<H, 128 / G>(a, stream);
 }
 
 int64_t tiles_of(int64_t rows, int d) { return (rows + 63) / 64 * (mx_padded(d) / 128); }
@@ -415,53 +741,73 @@ hipError_t launch_w4_head(const uint8_t *codes, const uint16_t *scales, const ui
   return hipGetLastError();
 }
 
+// Codes and scales of few rows, or many rows in bf16.
 size_t mx8_logits_workspace_bytes(int M, int d) {
   const size_t kp = mx_padded(d);
-  return align_up(sizeof(WsHeader) + M * kp + M * (kp / 32), 256);
+  return align_up(sizeof(WsHeader) + (M <= kFewRows ? M * kp + M * (kp / 32) : 2 * M * kp), 256);
 }
 
 hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint8_t *hidden_scales, int M, int d,
                              int64_t stride, const uint8_t *head, int V, void *logits, int32_t type, int64_t ld,
                              void *workspace, hipStream_t stream) {
   const int kp = mx_padded(d);
-  const uint8_t *h = reinterpret_cast<const uint8_t *>(hidden), *hs = hidden_scales;
-  if (hidden_type != SD_MXFP8) {
-    uint8_t *q = reinterpret_cast<uint8_t *>(workspace) + sizeof(WsHeader), *qs = q + (size_t)M * kp;
-    const hipError_t e = launch_mx8_quantize(hidden, hidden_type, M, d, stride, q, qs, stream);
-    if (e != hipSuccess) return e;
-    h = q;
-    hs = qs;
+  uint8_t *ws = reinterpret_cast<uint8_t *>(workspace) + sizeof(WsHeader);
+  NarrowArgs a{hidden, hidden_scales, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, 0, M, V, kp / 128,
+               logits, type, ld, vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8),
+               nullptr};
+  const bool coded = hidden_type == SD_MXFP8;
+  hipError_t e = hipSuccess;
+  if (M <= kFewRows) {
+    if (!coded) {
+      uint8_t *scales = ws + (size_t)M * kp;
+      e = launch_mx8_quantize(hidden, hidden_type, M, d, stride, ws, scales, stream);
+      a.hidden = ws;
+      a.hscales = scales;
+    }
+    return e != hipSuccess ? e : launch_skinny<Mx8, 4, 4, 2>(a, stream);
   }
-  const NarrowArgs a{h, hs, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, false, M, V, kp / 128, logits, type, ld,
-                     vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8)};
-  return launch_skinny<Mx8, 4, 4, 2>(a, stream);
+  uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
+  const dim3 grid = item_groups((int64_t)M * (kp / 8));
+  if (coded)
+    hipLaunchKernelGGL(k_mx8_decode, grid, dim3(256), 0, stream, reinterpret_cast<const uint8_t *>(hidden), hidden_scales,
+                       (int64_t)M, kp, rows);
+  else
+    by_type(hidden_type, [&](auto T) {
+      hipLaunchKernelGGL((k_mx8_rows<T>), grid, dim3(256), 0, stream, hidden, (int64_t)M, stride, d, kp,
+                         vec_rows(hidden, hidden_type, stride, hidden_type == SD_F32 ? 4 : 8), rows);
+    });
+  e = hipGetLastError();
+  a.hidden = rows;
+  return e != hipSuccess ? e : launch_tiled<Mx8Tile, 4>(a, stream);
 }
 
-size_t w4_logits_workspace_bytes(int M, int d) {
-  return align_up(sizeof(WsHeader) + (size_t)M * mx_padded(d) * 2, 256);
+// Where the group sums of many rows lie behind a copy of the rows.
+size_t w4_sums_at(int M, int d) { return align_up(sizeof(WsHeader) + (size_t)M * mx_padded(d) * 2, 256); }
+
+size_t w4_logits_workspace_bytes(int M, int d, int group) {
+  const size_t at = w4_sums_at(M, d);
+  return M <= kFewRows ? at : at + (size_t)((M + 63) / 64) * (mx_padded(d) / group) * 64 * 4;
 }
 
 hipError_t launch_w4_logits(const void *hidden, int32_t hidden_type, int M, int d, int64_t stride,
                             const uint8_t *head, int V, int group, int32_t scale_type, bool zeros, void *logits,
                             int32_t type, int64_t ld, void *workspace, hipStream_t stream) {
-  const int kp = mx_padded(d);
   const int64_t n = tiles_of(V, d);
-  const bool vec = vec_rows(hidden, hidden_type, stride, 8);
-  if (!vec || kp != d) {
-    uint16_t *copy = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(workspace) + sizeof(WsHeader));
-    const int64_t n = ((int64_t)M * (kp / 8) + 255) / 256, x = n < 1 << 20 ? n : 1 << 20;
-    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)x, (unsigned)((n + x - 1) / x)), dim3(256), 0, stream,
-                       reinterpret_cast<const uint16_t *>(hidden), (int64_t)M, stride, d, kp, vec, copy);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hidden = copy;
-    stride = kp;
-  }
   const uint8_t *s = head + n * kW4Tile;
+  uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+  float *sums = reinterpret_cast<float *>(ws + w4_sums_at(M, d));
+  uint16_t *copy = reinterpret_cast<uint16_t *>(ws + sizeof(WsHeader));
   const NarrowArgs a{hidden, nullptr, stride, head, s, zeros ? s + n * (128 / group) * 128 : nullptr,
-                     scale_type == SD_F16, M, V, kp / 128,
-                     logits, type, ld, vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8)};
-  return hidden_type == SD_BF16 ? launch_w4_group<SD_BF16>(a, group, stream) : launch_w4_group<SD_F16>(a, group, stream);
+                     scale_type == SD_F16 ? ~0u : 0u, M, V, mx_padded(d) / 128, logits, type, ld, vec_rows(logits, type, ld, 4),
+                     vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8), nullptr};
+  if (hidden_type == SD_BF16) {
+    if (group == 128) return launch_w4_group<SD_BF16, 128>(a, d, copy, sums, stream);
+    if (group == 64) return launch_w4_group<SD_BF16, 64>(a, d, copy, sums, stream);
+    return launch_w4_group<SD_BF16, 32>(a, d, copy, sums, stream);
+  }
+  if (group == 128) return launch_w4_group<SD_F16, 128>(a, d, copy, sums, stream);
+  if (group == 64) return launch_w4_group<SD_F16, 64>(a, d, copy, sums, stream);
+  return launch_w4_group<SD_F16, 32>(a, d, copy, sums, stream);
 }
 
 }  // namespace sdv

@@ -158,6 +158,37 @@ __device__ inline void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (((N >> 4) & 3) << 14) | (0x7 << 4));
 }
 
+// f over the G / 8 neighbouring threads of a group: quads, halves of 16 lanes, 16 lanes.
+template <int G, class F>
+__device__ __forceinline__ uint32_t over_group(uint32_t v, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));                    // lane ^ 1
+  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));                    // lane ^ 2
+  if (G >= 64) v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));      // 7 - lane of 8
+  if (G >= 128) v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));     // 15 - lane of 16
+  return v;
+}
+
+// n rows of W results of type T from a wave's part of LDS (rows ROW bytes apart) to rows m0 .. of
+// the output at column v0: 16 bytes a lane along the rows where they are aligned and whole, else
+// an element a lane.
+template <class T, int W, int ROW, class Args>
+__device__ __forceinline__ void store_rows(const Args &a, const LDSP uint8_t *part, int64_t m0, int n, int v0, int lane) {
+  constexpr int E = 16 / sizeof(T), LPR = W / E;     // elements a lane, lanes a row
+  static_assert(64 % LPR == 0, "whole rows a store");
+  const int rows = (int)min((int64_t)n, a.M - m0);
+  T *out = reinterpret_cast<T *>(a.out) + m0 * a.ld + v0;
+  if (a.wide && v0 + W <= a.V) {
+    for (int r = lane / LPR; r < rows; r += 64 / LPR) {
+      const u32x4 x = *(const LDSP u32x4 *)(part + r * ROW + (lane % LPR) * 16);
+      __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(out + r * a.ld + (lane % LPR) * E));
+    }
+  } else {
+    for (int r = 0; r < rows; ++r)
+      for (int v = lane; v < W && v0 + v < a.V; v += 64)
+        out[r * a.ld + v] = *(const LDSP T *)(part + r * ROW + v * (int)sizeof(T));
+  }
+}
+
 template <class F>
 void by_type(int32_t type, F f) {
   if (type == SD_F32) f(std::integral_constant<int, SD_F32>{});

@@ -28,16 +28,6 @@ struct W4Args {
   uint8_t *zeros;          // [rows][d / G], null in the symmetric form
 };
 
-// f over the G / 8 neighbouring threads of a group: quads, halves of 16 lanes, 16 lanes.
-template <int G, class F>
-__device__ __forceinline__ uint32_t over_group(uint32_t v, F f) {
-  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));                    // lane ^ 1
-  v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));                    // lane ^ 2
-  if (G >= 64) v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));      // 7 - lane of 8
-  if (G >= 128) v = f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));     // 15 - lane of 16
-  return v;
-}
-
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
   return __uint_as_float(over_group<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
