@@ -130,7 +130,7 @@ def _check(fn: str, status: int) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -682,6 +682,9 @@ _TYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 def _rows(t: torch.Tensor, name: str, dtype=None) -> None:
     """A device matrix of an element type the library takes, with contiguous rows."""
+    if (isinstance(t, torch.Tensor) and t.dtype in _TYPE_CODES and dtype in (None, t.dtype)
+            and t.is_cuda and t.dim() == 2 and t.is_contiguous() and t.numel() > 0):
+        return                      # the common case, in half the time
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _TYPE_CODES or (dtype is not None and t.dtype != dtype):
@@ -695,7 +698,8 @@ def _rows(t: torch.Tensor, name: str, dtype=None) -> None:
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1])
+    stride, columns = t.stride(0), t.shape[1]
+    return stride if stride > columns else columns
 
 
 def _same_device(dev: torch.device, **tensors) -> None:
@@ -706,8 +710,9 @@ def _same_device(dev: torch.device, **tensors) -> None:
 
 def _call(name: str, dev: torch.device, stream, *args) -> None:
     """The entry point on dev's current stream (or `stream`), with dev current."""
-    if dev.index == torch.cuda.current_device():
-        _check(name, getattr(_lib, name)(*args, _stream(stream)))
+    if dev.index == torch._C._cuda_getDevice():
+        handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+        _check(name, getattr(_lib, name)(*args, handle))
         return
     with torch.cuda.device(dev):
         _check(name, getattr(_lib, name)(*args, _stream(stream)))
@@ -897,28 +902,32 @@ def _bytes(t: Optional[torch.Tensor], name: str, shape, dev, stream, dtype=torch
 def _norm_inputs(x, weight, residual, eps, weight_offset, total):
     """The arguments of the norms up to `sum`, checked."""
     _rows(x, "x")
-    rows, d = x.shape
+    shape, dev, kind = x.shape, x.device, x.dtype
+    res, res_type, res_stride = None, 0, 0
     if residual is not None:
         _rows(residual, "residual")
-        if tuple(residual.shape) != (rows, d):
-            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(rows, d)}")
-        if residual.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"residual must be {x.dtype} or float32, got {residual.dtype}")
+        if residual.shape != shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(shape)}")
+        if residual.dtype not in (kind, torch.float32):
+            raise TypeError(f"residual must be {kind} or float32, got {residual.dtype}")
+        res, res_type = residual.data_ptr(), _TYPE_CODES[residual.dtype]
+        res_stride = _row_stride(residual)
+    w, w_type = None, 0
     if weight is not None:
-        _need(weight, "weight", weight.dtype if isinstance(weight, torch.Tensor)
-              and weight.dtype in _TYPE_CODES else x.dtype, (d,))
+        _need(weight, "weight", getattr(weight, "dtype", None)
+              if getattr(weight, "dtype", None) in _TYPE_CODES else kind, shape[1:])
+        w, w_type = weight.data_ptr(), _TYPE_CODES[weight.dtype]
+    out, out_stride = None, 0
     if total is not None:
         if residual is None:
             raise ValueError("total is the sum with a residual, and there is none")
         _rows(total, "total", residual.dtype)
-        if tuple(total.shape) != (rows, d):
-            raise ValueError(f"total has shape {tuple(total.shape)}, expected {(rows, d)}")
-    _same_device(x.device, residual=residual, weight=weight, total=total)
-    kind = 0 if residual is None else _TYPE_CODES[residual.dtype]
-    return (_ptr(x), _TYPE_CODES[x.dtype], _row_stride(x), _ptr(residual), kind,
-            0 if residual is None else _row_stride(residual), _ptr(weight),
-            0 if weight is None else _TYPE_CODES[weight.dtype], float(weight_offset), float(eps),
-            rows, d, _ptr(total), 0 if total is None else _row_stride(total))
+        if total.shape != shape:
+            raise ValueError(f"total has shape {tuple(total.shape)}, expected {tuple(shape)}")
+        out, out_stride = total.data_ptr(), _row_stride(total)
+    _same_device(dev, residual=residual, weight=weight, total=total)
+    return (x.data_ptr(), _TYPE_CODES[kind], _row_stride(x), res, res_type, res_stride, w, w_type,
+            weight_offset, eps, shape[0], shape[1], out, out_stride)
 
 
 def sd_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,

@@ -607,6 +607,138 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
   }
 }
 
+// ---------------------------------------------------------------- many hidden rows, 16-bit logits
+// D += A B^T over 128 columns of e4m3 under block scales, by the 8-bit matrix instruction: lane l
+// holds columns 16 (l / 16) .. + 15 and 64 + 16 (l / 16) .. + 15 of row l % 16 of each operand and,
+// in byte SEL of the A side's word and in byte 0 of the other, the scales of its row at block
+// l / 16. The LM head is A, so a lane's four results are consecutive ids of hidden row l % 16.
+// Accumulators are operand and result at once: left a choice the compiler may give the result the
+// register of a scale, which the instruction reads while it writes. It knows no hazards of inline
+// assembly: two idle states stand before each (a vector write of an operand needs them), and
+// settle() between the last one and the first read of a result.
+template <int SEL>
+__device__ __forceinline__ void mfma8(f32x4 &c, const i32x8 &w, int sw, const i32x8 &h, int sh) {
+#define SD_MFMA8(LO, HI)                                                                           \
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" #LO  \
+               ",0,0] op_sel_hi:[" #HI ",0,0]"                                                     \
+               : "+a"(c) : "v"(w), "v"(h), "v"(sw), "v"(sh) : "memory")
+  if constexpr (SEL == 0) SD_MFMA8(0, 0);
+  else if constexpr (SEL == 1) SD_MFMA8(1, 0);
+  else if constexpr (SEL == 2) SD_MFMA8(0, 1);
+  else SD_MFMA8(1, 1);
+#undef SD_MFMA8
+}
+
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15"); }
+
+// The 8-bit instructions cut the products of eight columns to 13 bits under the largest before
+// they add them, which leaves normal data 1.4e-5 off: too much for an fp32 logit, nothing beside
+// the rounding of a 16-bit one (2^-9, 2^-12). They run at twice the 16-bit rate and take codes as they
+// are. Otherwise as k_narrow_tiled: 4 WM waves, each 64 ids by 16 TM rows, 256 ids by
+// 16 TM WM rows a workgroup; chunk c of row r of a step's codes lies at place c ^ (r / 2 % 8).
+template <int TM, int WM>
+__global__ __launch_bounds__(256 * WM, 2) void k_mx8_tiled(NarrowArgs a, int n_mt, int n_vt) {
+  constexpr int NS = 3, ROWS = 16 * TM * WM, STAGE = ROWS * 132, LOADS = TM / 2;
+  __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wv = wave & 3, wm = wave >> 2, q = lane >> 4, r = lane & 15;
+  const int nb = n_mt * n_vt, hb = blockIdx.x;
+  const int per = nb / 8, rem = nb % 8, xcd = hb % 8, pos = hb / 8;
+  const int logical = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + pos;
+  const int mt = logical % n_mt, vt = logical / n_mt;
+  const int64_t row0 = (int64_t)mt * ROWS, left = a.M - 1 - row0;
+  const int64_t tile0 = min((int64_t)vt * 4 + wv, (int64_t)(a.V - 1) / 64) * a.steps;
+  const uint8_t *codes = reinterpret_cast<const uint8_t *>(a.hidden) + row0 * a.hstride;
+  const uint8_t *scales = a.hscales + row0 * (a.hstride / 32);
+  int src[LOADS];
+#pragma unroll
+  for (int n = 0; n < LOADS; ++n) {
+    const int at = 8 * (wave * LOADS + n) + (lane >> 3);     // row of the tile
+    src[n] = (int)(min((int64_t)at, left) * a.hstride) + ((lane & 7) ^ (at >> 1 & 7)) * 16;
+  }
+  const int block = wave % (ROWS / 64);                      // 64 rows' scales a load
+  const int scale_src = (int)(min((int64_t)64 * block + lane, left) * (a.hstride / 32));
+  auto issue = [&](int k) __attribute__((always_inline)) {
+    LDSP uint8_t *dst = (LDSP uint8_t *)S + (k % NS) * STAGE;
+    const int kk = min(k, a.steps - 1);
+#pragma unroll
+    for (int n = 0; n < LOADS; ++n) to_lds16(codes, src[n], kk * 128, dst + (wave * LOADS + n) * 1024);
+    to_lds4(scales, scale_src, kk * 4, dst + ROWS * 128 + block * 256);
+    asm volatile("" ::: "memory");
+  };
+  struct Weights {
+    i32x8 w[4];
+    int s;
+  } st[2];
+  auto load = [&](int k, Weights &to) __attribute__((always_inline)) {
+    const int64_t tile = tile0 + min(k, a.steps - 1);
+    const u32x4 *c = reinterpret_cast<const u32x4 *>(a.codes + tile * kMx8Tile) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 x = c[128 * i], y = c[128 * i + 64];
+      to.w[i] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    }
+    to.s = reinterpret_cast<const int *>(a.scales + tile * kMx8Scales)[lane];
+    asm volatile("" ::: "memory");
+  };
+  f32x4 acc[4][TM];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](int k, Weights &now) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(now.w[i]));
+    asm volatile("" : "+v"(now.s));
+    raw_barrier();                     // and every wave has read step k - 1 out of LDS
+    issue(k + NS - 1);
+    const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE + wm * TM * 16 * 128;
+    const LDSP uint8_t *sb = (const LDSP uint8_t *)S + (k % NS) * STAGE + ROWS * 128 + (wm * TM * 16 + r) * 4 + q;
+    i32x8 h[3];
+    int s[3];
+    auto fetch = [&](int m) __attribute__((always_inline)) {
+      const LDSP uint8_t *p = b + (16 * m + r) * 128;
+      const u32x4 x = *(const LDSP u32x4 *)(p + (q ^ (r >> 1)) * 16), y = *(const LDSP u32x4 *)(p + ((4 + q) ^ (r >> 1)) * 16);
+      h[m % 3] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+      s[m % 3] = sb[64 * m];
+    };
+    fetch(0);
+    fetch(1);
+    each<TM>([&](auto m) __attribute__((always_inline)) {
+      if constexpr (m + 2 < TM) fetch(m + 2);
+      each<4>([&](auto i) __attribute__((always_inline)) { mfma8<i>(acc[i][m], now.w[i], now.s, h[m % 3], s[m % 3]); });
+    });
+    load(k + 2, now);
+  };
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    issue(k);
+    load(k, st[k]);
+  }
+  int k = 0;
+  for (; k + 1 < a.steps; k += 2) {
+    step(k, st[0]);
+    step(k + 1, st[1]);
+  }
+  if (k < a.steps) step(k, st[0]);
+  settle();
+  wait_loads<0>();                     // the trailing loads land before LDS is used again
+  raw_barrier();
+  const int v0 = vt * 256 + wv * 64;
+  constexpr int PART = NS * STAGE / (4 * WM) / 16 * 16, ROW = 64 * 2 + 16, HALF = TM / 2;
+  static_assert(ROW * HALF * 16 <= PART, "half the rows in 16 bits");
+  LDSP uint8_t *part = (LDSP uint8_t *)S + wave * PART;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int m = 0; m < HALF; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(LDSP u32x2 *)(part + (16 * m + r) * ROW + (16 * i + 4 * q) * 2) = pack4(acc[i][half * HALF + m], a.type);
+    store_rows<uint16_t, 64, ROW>(a, part, row0 + wm * TM * 16 + half * HALF * 16, HALF * 16, v0, lane);
+  }
+}
+
 // ---------------------------------------------------------------- hidden rows made ready
 // Whole 128-column steps of 16-bit rows, zeros behind column d (out null: not stored), and each
 // group's sum of a row times `factor` (sums null: not formed): [ceil(rows / 64)][kp / G][64], rows
@@ -683,6 +815,14 @@ hipError_t launch_tiled(const NarrowArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int TM, int WM>
+hipError_t launch_mx8_tiled(const NarrowArgs &a, hipStream_t stream) {
+  const int n_mt = (a.M + 16 * TM * WM - 1) / (16 * TM * WM), n_vt = (a.V + 255) / 256;
+  hipLaunchKernelGGL((k_mx8_tiled<TM, WM>), dim3((unsigned)((int64_t)n_mt * n_vt)), dim3(256 * WM), 0, stream, a, n_mt,
+                     n_vt);
+  return hipGetLastError();
+}
+
 template <int H, int NG>
 hipError_t launch_w4_of(const NarrowArgs &a, hipStream_t stream) {
   if (a.M > kFewRows)
@@ -741,7 +881,7 @@ hipError_t launch_w4_head(const uint8_t *codes, const uint16_t *scales, const ui
   return hipGetLastError();
 }
 
-// Codes and scales of few rows, or many rows in bf16.
+// Codes and scales, or many rows in bf16.
 size_t mx8_logits_workspace_bytes(int M, int d) {
   const size_t kp = mx_padded(d);
   return align_up(sizeof(WsHeader) + (M <= kFewRows ? M * kp + M * (kp / 32) : 2 * M * kp), 256);
@@ -755,16 +895,20 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
   NarrowArgs a{hidden, hidden_scales, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, 0, M, V, kp / 128,
                logits, type, ld, vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8),
                nullptr};
-  const bool coded = hidden_type == SD_MXFP8;
+  const bool coded = hidden_type == SD_MXFP8, wide = M > kFewRows && type == SD_F32;
   hipError_t e = hipSuccess;
-  if (M <= kFewRows) {
+  if (!wide) {
     if (!coded) {
       uint8_t *scales = ws + (size_t)M * kp;
       e = launch_mx8_quantize(hidden, hidden_type, M, d, stride, ws, scales, stream);
       a.hidden = ws;
       a.hscales = scales;
     }
-    return e != hipSuccess ? e : launch_skinny<Mx8, 4, 4, 2>(a, stream);
+    if (e != hipSuccess) return e;
+    if (M <= kFewRows) return launch_skinny<Mx8, 4, 4, 2>(a, stream);
+    if (M <= 64) return launch_mx8_tiled<4, 1>(a, stream);
+    if (M <= 128) return launch_mx8_tiled<8, 1>(a, stream);
+    return launch_mx8_tiled<8, 2>(a, stream);
   }
   uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
   const dim3 grid = item_groups((int64_t)M * (kp / 8));
