@@ -231,7 +231,8 @@ struct Mx8 {
 
 // 4-bit codes of NG groups a step, hidden rows in 16 bits as they are. Of each group the sum of
 // code products c h and the sum of the h (a product with ones) are formed in fp32, and
-// s (sum c h - z sum h) is added to the logit: no weight is rounded.
+// s (sum c h - z sum h) is added to the logit: no weight is rounded. Where z is 8 throughout, the
+// code products start from -8 sum h.
 template <int H, int NG, bool ASYM>
 struct W4 {
   template <int TV, int MT>
@@ -280,12 +281,15 @@ struct W4 {
         sum[m] = zero4;
 #pragma unroll
         for (int t = 0; t < KS; ++t) sum[m] = mfma16<H>(st.h[m][g * KS + t], ones, sum[m]);
+        if (!ASYM)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[m][e] *= -8.f;
       }
 #pragma unroll
       for (int i = 0; i < TV; ++i) {
         f32x4 part[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) part[m] = zero4;
+        for (int m = 0; m < MT; ++m) part[m] = ASYM ? zero4 : sum[m];
 #pragma unroll
         for (int t = 0; t < KS; ++t) {
           const u32x4 w = decode4<H>(st.w[i][g * KS + t]);
@@ -293,11 +297,12 @@ struct W4 {
           for (int m = 0; m < MT; ++m) part[m] = mfma16<H>(st.h[m][g * KS + t], w, part[m]);
         }
         const float s = wide_scale(st.s[i / 4][g][i % 4 / 2] >> (16 * (i % 2)) & 0xffff, a.scale_f16);
-        const float z = ASYM ? (float)(st.z[i / 4][g] >> (8 * (i % 4)) & 255) : 8.f;
+        const float z = ASYM ? (float)(st.z[i / 4][g] >> (8 * (i % 4)) & 255) : 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][m][e] = fmaf(s, fmaf(-z, sum[m][e], part[m][e]), acc[i][m][e]);
+          for (int e = 0; e < 4; ++e)
+            acc[i][m][e] = fmaf(s, ASYM ? fmaf(-z, sum[m][e], part[m][e]) : part[m][e], acc[i][m][e]);
       }
     }
   }
@@ -309,7 +314,7 @@ struct W4 {
 // weight is used by one wave only, so LDS would add a copy and share nothing. The hidden rows are
 // read by every workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
 template <class F, int TV, int MT, int NW, int D>
-__global__ __launch_bounds__(64 * NW) void k_narrow_skinny(NarrowArgs a) {
+__global__ __launch_bounds__(64 * NW, 2) void k_narrow_skinny(NarrowArgs a) {
   constexpr int IDS = 16 * TV, LDR = IDS + 4;
   __shared__ float red[NW][16 * MT * LDR];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -505,9 +510,9 @@ __device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, L
 // arrived the latter have, and behind the barrier those of all waves.
 template <class F, int TM>
 __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt, int n_vt) {
-  constexpr int NS = 3, ROWS = 16 * TM, STAGE = ROWS * 256 + F::kSums * ROWS * 4;
+  constexpr int NS = 3, ROWS = 16 * TM, STAGE = ROWS * 256 + F::kSums * 256;
   constexpr int LOADS = ROWS / 16;                 // of four rows, by each wave
-  static_assert(F::kSums == 0 || ROWS == 64, "a wave's load of a group's sums is 64 rows");
+  static_assert(ROWS <= 64, "a wave's load of a group's sums is 64 rows");
   __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
@@ -534,8 +539,8 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
     for (int n = 0; n < LOADS; ++n)
       to_lds16(rows, src[n], kk * 256, dst + (wave * LOADS + n) * 1024);
     if constexpr (F::kSums > 0)
-      to_lds4(sums, lane * 4, (kk * F::kSums + wave % F::kSums) * ROWS * 4,
-              dst + ROWS * 256 + (wave % F::kSums) * ROWS * 4);
+      to_lds4(sums, lane % ROWS * 4, (kk * F::kSums + wave % F::kSums) * ROWS * 4,
+              dst + ROWS * 256 + (wave % F::kSums) * 256);
     asm volatile("" ::: "memory");
   };
   f32x4 acc[4][TM];
@@ -553,7 +558,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
       return *(const LDSP u32x4 *)(b + (16 * m + r) * 256 + ((F::chunk(t, q) ^ r) * 16));
     };
     auto sum = [&](int g, int m) __attribute__((always_inline)) {
-      return *(const LDSP f32x4 *)(b + ROWS * 256 + (g * ROWS + 16 * m + 4 * q) * 4);
+      return *(const LDSP f32x4 *)(b + ROWS * 256 + (g * 64 + 16 * m + 4 * q) * 4);
     };
     now.template use<TM>(a, frag, sum, acc);
     now.load(a, tile0 + min(k + 2, a.steps - 1), lane);
@@ -616,16 +621,19 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
 // register of a scale, which the instruction reads while it writes. It knows no hazards of inline
 // assembly: two idle states stand before each (a vector write of an operand needs them), and
 // settle() between the last one and the first read of a result.
-template <int SEL>
+// ACC: accumulators in accumulation registers, of which a wave has half of its share.
+template <int SEL, bool ACC>
 __device__ __forceinline__ void mfma8(f32x4 &c, const i32x8 &w, int sw, const i32x8 &h, int sh) {
-#define SD_MFMA8(LO, HI)                                                                           \
+#define SD_MFMA8(TO, LO, HI)                                                                       \
   asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" #LO  \
                ",0,0] op_sel_hi:[" #HI ",0,0]"                                                     \
-               : "+a"(c) : "v"(w), "v"(h), "v"(sw), "v"(sh) : "memory")
-  if constexpr (SEL == 0) SD_MFMA8(0, 0);
-  else if constexpr (SEL == 1) SD_MFMA8(1, 0);
-  else if constexpr (SEL == 2) SD_MFMA8(0, 1);
-  else SD_MFMA8(1, 1);
+               : TO(c) : "v"(w), "v"(h), "v"(sw), "v"(sh) : "memory")
+#define SD_MFMA8_IN(LO, HI) do { if constexpr (ACC) SD_MFMA8("+a", LO, HI); else SD_MFMA8("+v", LO, HI); } while (0)
+  if constexpr (SEL == 0) SD_MFMA8_IN(0, 0);
+  else if constexpr (SEL == 1) SD_MFMA8_IN(1, 0);
+  else if constexpr (SEL == 2) SD_MFMA8_IN(0, 1);
+  else SD_MFMA8_IN(1, 1);
+#undef SD_MFMA8_IN
 #undef SD_MFMA8
 }
 
@@ -634,20 +642,21 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15");
 // The 8-bit instructions cut the products of eight columns to 13 bits under the largest before
 // they add them, which leaves normal data 1.4e-5 off: too much for an fp32 logit, nothing beside
 // the rounding of a 16-bit one (2^-9, 2^-12). They run at twice the 16-bit rate and take codes as they
-// are. Otherwise as k_narrow_tiled: 4 WM waves, each 64 ids by 16 TM rows, 256 ids by
-// 16 TM WM rows a workgroup; chunk c of row r of a step's codes lies at place c ^ (r / 2 % 8).
-template <int TM, int WM>
-__global__ __launch_bounds__(256 * WM, 2) void k_mx8_tiled(NarrowArgs a, int n_mt, int n_vt) {
-  constexpr int NS = 3, ROWS = 16 * TM * WM, STAGE = ROWS * 132, LOADS = TM / 2;
+// are. Otherwise as k_narrow_tiled: four waves, each 64 ids by 16 TM rows; chunk c of row r of a
+// step's codes lies at place c ^ (r / 2 % 8).
+template <int TM, int NS, int WB>
+__global__ __launch_bounds__(256, TM > 8 ? 1 : 2) void k_mx8_tiled(NarrowArgs a, int n_mt, int n_vt) {
+  static_assert(WB <= NS, "a step's weights are issued behind its hidden rows");
+  constexpr int ROWS = 16 * TM, STAGE = ROWS * 132, LOADS = TM / 2;
   __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wv = wave & 3, wm = wave >> 2, q = lane >> 4, r = lane & 15;
+  const int q = lane >> 4, r = lane & 15;
   const int nb = n_mt * n_vt, hb = blockIdx.x;
   const int per = nb / 8, rem = nb % 8, xcd = hb % 8, pos = hb / 8;
   const int logical = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + pos;
   const int mt = logical % n_mt, vt = logical / n_mt;
   const int64_t row0 = (int64_t)mt * ROWS, left = a.M - 1 - row0;
-  const int64_t tile0 = min((int64_t)vt * 4 + wv, (int64_t)(a.V - 1) / 64) * a.steps;
+  const int64_t tile0 = min((int64_t)vt * 4 + wave, (int64_t)(a.V - 1) / 64) * a.steps;
   const uint8_t *codes = reinterpret_cast<const uint8_t *>(a.hidden) + row0 * a.hstride;
   const uint8_t *scales = a.hscales + row0 * (a.hstride / 32);
   int src[LOADS];
@@ -669,7 +678,7 @@ __global__ __launch_bounds__(256 * WM, 2) void k_mx8_tiled(NarrowArgs a, int n_m
   struct Weights {
     i32x8 w[4];
     int s;
-  } st[2];
+  } st[WB];
   auto load = [&](int k, Weights &to) __attribute__((always_inline)) {
     const int64_t tile = tile0 + min(k, a.steps - 1);
     const u32x4 *c = reinterpret_cast<const u32x4 *>(a.codes + tile * kMx8Tile) + lane;
@@ -686,46 +695,57 @@ __global__ __launch_bounds__(256 * WM, 2) void k_mx8_tiled(NarrowArgs a, int n_m
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int m = 0; m < TM; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](int k, Weights &now) __attribute__((always_inline)) {
+  // Fragment m of step k into one of four register sets.
+  i32x8 h[4];
+  int s[4];
+  auto fetch = [&](int k, int m) __attribute__((always_inline)) {
+    const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE;
+    const LDSP uint8_t *p = b + (16 * m + r) * 128;
+    const u32x4 x = *(const LDSP u32x4 *)(p + (q ^ (r >> 1)) * 16), y = *(const LDSP u32x4 *)(p + ((4 + q) ^ (r >> 1)) * 16);
+    h[m % 4] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    s[m % 4] = b[ROWS * 128 + (16 * m + r) * 4 + q];
+  };
+  // Behind this step k's weights have arrived, and so have its hidden rows, for every wave; and
+  // every wave has step k - 1 out of LDS, so its buffer takes step k + NS - 1.
+  auto enter = [&](int k, Weights &now) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(now.w[i]));
     asm volatile("" : "+v"(now.s));
-    raw_barrier();                     // and every wave has read step k - 1 out of LDS
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    raw_barrier();
     issue(k + NS - 1);
-    const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE + wm * TM * 16 * 128;
-    const LDSP uint8_t *sb = (const LDSP uint8_t *)S + (k % NS) * STAGE + ROWS * 128 + (wm * TM * 16 + r) * 4 + q;
-    i32x8 h[3];
-    int s[3];
-    auto fetch = [&](int m) __attribute__((always_inline)) {
-      const LDSP uint8_t *p = b + (16 * m + r) * 128;
-      const u32x4 x = *(const LDSP u32x4 *)(p + (q ^ (r >> 1)) * 16), y = *(const LDSP u32x4 *)(p + ((4 + q) ^ (r >> 1)) * 16);
-      h[m % 3] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-      s[m % 3] = sb[64 * m];
-    };
-    fetch(0);
-    fetch(1);
+  };
+  // Step k: its first two fragments are on their way; the next step is entered before the last two
+  // are used, so that its first ones come meanwhile.
+  auto step = [&](int k, Weights &now, Weights &next) __attribute__((always_inline)) {
     each<TM>([&](auto m) __attribute__((always_inline)) {
-      if constexpr (m + 2 < TM) fetch(m + 2);
-      each<4>([&](auto i) __attribute__((always_inline)) { mfma8<i>(acc[i][m], now.w[i], now.s, h[m % 3], s[m % 3]); });
+      if constexpr (m == TM - 2) enter(k + 1, next);
+      if constexpr (m < TM - 2) fetch(k, m + 2);
+      else fetch(k + 1, m + 2 - TM);
+      each<4>([&](auto i) __attribute__((always_inline)) { mfma8<i, (TM > 4)>(acc[i][m], now.w[i], now.s, h[m % 4], s[m % 4]); });
     });
-    load(k + 2, now);
+    load(k + WB, now);
   };
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < NS - 1; ++k) {
     issue(k);
-    load(k, st[k]);
+    if (k < WB) load(k, st[k]);
   }
+  enter(0, st[0]);
+  if constexpr (WB == NS) load(WB - 1, st[WB - 1]);
+  fetch(0, 0);
+  fetch(0, 1);
   int k = 0;
-  for (; k + 1 < a.steps; k += 2) {
-    step(k, st[0]);
-    step(k + 1, st[1]);
-  }
-  if (k < a.steps) step(k, st[0]);
+  for (; k + WB <= a.steps; k += WB)
+    each<WB>([&](auto x) __attribute__((always_inline)) { step(k + x, st[x], st[(x + 1) % WB]); });
+  each<WB - 1>([&](auto x) __attribute__((always_inline)) {
+    if (k + x < a.steps) step(k + x, st[x], st[x + 1]);
+  });
   settle();
   wait_loads<0>();                     // the trailing loads land before LDS is used again
   raw_barrier();
-  const int v0 = vt * 256 + wv * 64;
-  constexpr int PART = NS * STAGE / (4 * WM) / 16 * 16, ROW = 64 * 2 + 16, HALF = TM / 2;
+  const int v0 = vt * 256 + wave * 64;
+  constexpr int PART = NS * STAGE / 4 / 16 * 16, ROW = 64 * 2 + 16, HALF = TM / 2;
   static_assert(ROW * HALF * 16 <= PART, "half the rows in 16 bits");
   LDSP uint8_t *part = (LDSP uint8_t *)S + wave * PART;
 #pragma unroll
@@ -735,17 +755,17 @@ __global__ __launch_bounds__(256 * WM, 2) void k_mx8_tiled(NarrowArgs a, int n_m
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *(LDSP u32x2 *)(part + (16 * m + r) * ROW + (16 * i + 4 * q) * 2) = pack4(acc[i][half * HALF + m], a.type);
-    store_rows<uint16_t, 64, ROW>(a, part, row0 + wm * TM * 16 + half * HALF * 16, HALF * 16, v0, lane);
+    store_rows<uint16_t, 64, ROW>(a, part, row0 + half * HALF * 16, HALF * 16, v0, lane);
   }
 }
 
 // ---------------------------------------------------------------- hidden rows made ready
 // Whole 128-column steps of 16-bit rows, zeros behind column d (out null: not stored), and each
-// group's sum of a row times `factor` (sums null: not formed): [ceil(rows / 64)][kp / G][64], rows
-// past the last left. An item is eight columns.
+// group's sum of a row times `factor` (sums null: not formed): [ceil(rows / tile)][kp / G][tile],
+// rows past the last left. An item is eight columns.
 template <int H, int G>
 __global__ __launch_bounds__(256) void k_w4_rows(const uint16_t *x, int64_t rows, int64_t stride, int d, int kp,
-                                                 bool vec, uint16_t *out, float *sums, float factor) {
+                                                 bool vec, uint16_t *out, float *sums, int tile, float factor) {
   const int per = kp / 8;
   const int64_t base = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256, row0 = base / per;
   const Item it = item_at(row0, (int)(base - row0 * per), threadIdx.x, per);
@@ -761,7 +781,7 @@ __global__ __launch_bounds__(256) void k_w4_rows(const uint16_t *x, int64_t rows
     return __float_as_uint(__uint_as_float(p) + __uint_as_float(q));
   }));
   if (it.row < rows && it.c % (G / 8) == 0)
-    sums[(it.row / 64 * (kp / G) + it.c / (G / 8)) * 64 + it.row % 64] = factor * s;
+    sums[(it.row / tile * (kp / G) + it.c / (G / 8)) * tile + it.row % tile] = factor * s;
 }
 
 // Hidden rows of any type as the bf16 numbers of their MXFP8 form, [M][kp].
@@ -798,7 +818,20 @@ dim3 item_groups(int64_t items) {
   return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
-constexpr int kFewRows = 32;      // rows from which on the tiled kernel runs
+// Rows that the streaming kernel takes: 16, and 32 of an LM head that gives the tiled kernels less
+// than a workgroup of 256 ids for each compute unit. us, streaming / tiled of 32 rows, M = 32:
+//   4 bits, G = 128:   129280 x 7168: 115 / 94    32000 x 4096: 18 / 30    8000 x 2048: 12.5 / 20.5
+//   4 bits, G = 32:    151936 x 4096:  95 / 92
+//   MXFP8, fp32:       129280 x 7168: 197 / 170   32000 x 4096: 30 / 31    8000 x 2048: 9.9 / 15.7
+constexpr int kFewRows = 16;
+bool few_rows(int M, int V) { return M <= kFewRows || (M <= 2 * kFewRows && V <= 256 * 256); }
+
+// What the workgroups of 256 ids by `rows` rows cost that one of the 256 compute units gets: two at a
+// time at `both` each, one alone at `one`.
+double paired(const NarrowArgs &a, int rows, double one, double both) {
+  const int64_t n = ((int64_t)a.V + 255) / 256 * (((int64_t)a.M + rows - 1) / rows), each = (n + 255) / 256;
+  return (double)(each / 2) * 2 * both + (double)(each % 2) * one;
+}
 
 template <class F, int TV, int NW, int D>
 hipError_t launch_skinny(const NarrowArgs &a, hipStream_t stream) {
@@ -815,18 +848,28 @@ hipError_t launch_tiled(const NarrowArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int TM, int WM>
+template <int TM, int NS, int WB>
 hipError_t launch_mx8_tiled(const NarrowArgs &a, hipStream_t stream) {
-  const int n_mt = (a.M + 16 * TM * WM - 1) / (16 * TM * WM), n_vt = (a.V + 255) / 256;
-  hipLaunchKernelGGL((k_mx8_tiled<TM, WM>), dim3((unsigned)((int64_t)n_mt * n_vt)), dim3(256 * WM), 0, stream, a, n_mt,
-                     n_vt);
+  const int n_mt = (a.M + 16 * TM - 1) / (16 * TM), n_vt = (a.V + 255) / 256;
+  hipLaunchKernelGGL((k_mx8_tiled<TM, NS, WB>), dim3((unsigned)((int64_t)n_mt * n_vt)), dim3(256), 0, stream, a, n_mt, n_vt);
   return hipGetLastError();
+}
+
+// Rows of a tile of k_narrow_tiled, as for launch_mx8_logits. 4 bits, G = 128, us, 32 / 64 rows a tile, V x
+// depth, M:
+//   129280 x 7168:  64: 160 / 138    128: 292 / 254    512: 1068 / 908
+//    32000 x 4096:  64: 31 / 43      128: 48 / 45      256: 81 / 72     512: 153 / 133
+//     8000 x 2048:  64: 21 / 29      256: 22 / 30      512: 32 / 32
+int tile_rows(const NarrowArgs &a) { return paired(a, 32, 0.92, 0.70) < paired(a, 64, 1.27, 1.0) ? 32 : 64; }
+
+template <int H, int NG, bool ASYM>
+hipError_t launch_w4_tiled(const NarrowArgs &a, hipStream_t stream) {
+  return tile_rows(a) == 32 ? launch_tiled<W4Tile<H, NG, ASYM>, 2>(a, stream) : launch_tiled<W4Tile<H, NG, ASYM>, 4>(a, stream);
 }
 
 template <int H, int NG>
 hipError_t launch_w4_of(const NarrowArgs &a, hipStream_t stream) {
-  if (a.M > kFewRows)
-    return a.zeros ? launch_tiled<W4Tile<H, NG, true>, 4>(a, stream) : launch_tiled<W4Tile<H, NG, false>, 4>(a, stream);
+  if (!few_rows(a.M, a.V)) return a.zeros ? launch_w4_tiled<H, NG, true>(a, stream) : launch_w4_tiled<H, NG, false>(a, stream);
   return a.zeros ? launch_skinny<W4<H, NG, true>, 8, 4, 2>(a, stream)
                  : launch_skinny<W4<H, NG, false>, 8, 4, 2>(a, stream);
 }
@@ -838,11 +881,11 @@ hipError_t launch_w4_group(NarrowArgs a, int d, uint16_t *copy, float *sums, hip
   const bool vec = vec_rows(a.hidden, H, a.hstride, 8);
   // 64 rows of a tile are addressed by 32 bits
   if (vec && kp == d && a.hstride < 1 << 24) copy = nullptr;
-  if (a.M <= kFewRows) sums = nullptr;
+  if (few_rows(a.M, a.V)) sums = nullptr;
   if (copy || sums) {
     hipLaunchKernelGGL((k_w4_rows<H, G>), item_groups((int64_t)a.M * (kp / 8)), dim3(256), 0, stream,
                        reinterpret_cast<const uint16_t *>(a.hidden), (int64_t)a.M, a.hstride, d, kp, vec, copy, sums,
-                       a.zeros ? -1.f : -8.f);
+                       tile_rows(a), a.zeros ? -1.f : -8.f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -895,7 +938,7 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
   NarrowArgs a{hidden, hidden_scales, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, 0, M, V, kp / 128,
                logits, type, ld, vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8),
                nullptr};
-  const bool coded = hidden_type == SD_MXFP8, wide = M > kFewRows && type == SD_F32;
+  const bool coded = hidden_type == SD_MXFP8, few = few_rows(M, V), wide = !few && type == SD_F32;
   hipError_t e = hipSuccess;
   if (!wide) {
     if (!coded) {
@@ -905,10 +948,19 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
       a.hscales = scales;
     }
     if (e != hipSuccess) return e;
-    if (M <= kFewRows) return launch_skinny<Mx8, 4, 4, 2>(a, stream);
-    if (M <= 64) return launch_mx8_tiled<4, 1>(a, stream);
-    if (M <= 128) return launch_mx8_tiled<8, 1>(a, stream);
-    return launch_mx8_tiled<8, 2>(a, stream);
+    if (few) return launch_skinny<Mx8, 4, 4, 2>(a, stream);
+    // Rows of a tile by what the workgroups that a compute unit gets cost, in those of 256 rows, of
+    // which it holds one; of 128 and 64 rows it holds two, one of them alone costs more. Measured (us,
+    // 64 / 128 / 256 rows a tile), V x depth, M:
+    //   129280 x 7168:   64: 164 / 168 / 218    128: 217 / 180 / 237    256: 349 / 280 / 281
+    //                   320: 421 / 365 / 477    512: 615 / 481 / 449   1024: 1155 / 890 / 826
+    //    32000 x 4096:   64: 31 / 41 / 52       128: 31 / 43 / 55       256: 46 / 44 / 60
+    //                   512: 82 / 69 / 64
+    //     8000 x 2048:  256: 12 / 19 / 30       512: 14 / 19 / 31      1024: 23 / 21 / 31
+    const double cost[3] = {paired(a, 64, 0.50, 0.33), paired(a, 128, 0.70, 0.53), paired(a, 256, 1.0, 1.0)};
+    if (cost[2] <= cost[0] && cost[2] <= cost[1]) return launch_mx8_tiled<16, 3, 3>(a, stream);
+    if (cost[1] <= cost[0]) return launch_mx8_tiled<8, 3, 2>(a, stream);
+    return launch_mx8_tiled<4, 4, 3>(a, stream);
   }
   uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
   const dim3 grid = item_groups((int64_t)M * (kp / 8));
@@ -922,7 +974,8 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
     });
   e = hipGetLastError();
   a.hidden = rows;
-  return e != hipSuccess ? e : launch_tiled<Mx8Tile, 4>(a, stream);
+  return e != hipSuccess ? e : tile_rows(a) == 32 ? launch_tiled<Mx8Tile, 2>(a, stream)
+                         : launch_tiled<Mx8Tile, 4>(a, stream);
 }
 
 // Where the group sums of many rows lie behind a copy of the rows.

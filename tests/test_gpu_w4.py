@@ -119,7 +119,8 @@ def test_logits(M, V, d, group, out, symmetric, dtype):
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,V,d,group", [(40, 70001, 160, 32), (64, 65600, 256, 128), (130, 32000, 320, 64),
-                                         (500, 32001, 256, 128), (257, 40000, 384, 128), (1030, 140, 128, 64)])
+                                         (500, 32001, 256, 128), (257, 40000, 384, 128), (1030, 140, 128, 64),
+                                         (17, 66000, 384, 32), (32, 70001, 128, 128), (20, 65537, 1152, 64), (300, 65600, 384, 64)])
 def test_logits_many_ids(M, V, d, group, out):
     got, want, tol = logits_case(M, V, d, group, False, torch.bfloat16, out, 3)
     assert bool(((got - want).abs() <= tol).all())
