@@ -33,11 +33,29 @@ dim3 groups_of(int64_t n) {
   return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
+// v plus the value of the lane that is CTRL's source, by a lane exchange inside rows of 16.
+template <int CTRL>
+__device__ __forceinline__ double add_lane(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  const u32x2 o = {(uint32_t)__builtin_amdgcn_mov_dpp((int)w[0], CTRL, 0xf, 0xf, true),
+                   (uint32_t)__builtin_amdgcn_mov_dpp((int)w[1], CTRL, 0xf, 0xf, true)};
+  return v + __builtin_bit_cast(double, o);
+}
+
+__device__ __forceinline__ double of_lane(double v, int lane) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)w[0], lane),
+                                          (uint32_t)__builtin_amdgcn_readlane((int)w[1], lane)});
+}
+
 // Sum over the row's NT threads, in all of them; `part` holds a wave's sum each.
 template <int NT>
 __device__ __forceinline__ double row_sum(double v, double *part) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  v = add_lane<0xb1>(v);        // lane ^ 1
+  v = add_lane<0x4e>(v);        // lane ^ 2
+  v = add_lane<0x141>(v);       // 7 - lane of 8: the other four
+  v = add_lane<0x140>(v);       // 15 - lane of 16: the other eight
+  v = (of_lane(v, 0) + of_lane(v, 16)) + (of_lane(v, 32) + of_lane(v, 48));
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();

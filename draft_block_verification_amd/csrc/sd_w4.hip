@@ -28,15 +28,49 @@ struct W4Args {
   uint8_t *zeros;          // [rows][d / G], null in the symmetric form
 };
 
-template <int G>
-__device__ __forceinline__ float group_max(float v) {
-  return __uint_as_float(over_group<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
+// The largest of eight values and of their negatives, 0 at least, as bits of the row's type: such
+// numbers order as integers do, NaN and infinity on top.
+struct Ends { uint32_t most, least; };
+
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ i16x2 max2(i16x2 a, i16x2 b) { return __builtin_elementwise_max(a, b); }
+
+// Over the group: {most, least} as fp32 bits.
+template <int T, int G>
+__device__ __forceinline__ Ends group_ends(const Raw8<T> &r) {
+  if constexpr (T == SD_F32) {
+    int most = 0, least = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = __float_as_int(r.a[i]), b = __float_as_int(r.b[i]);
+      most = max(most, max(a, b));
+      least = max(least, max(a ^ INT32_MIN, b ^ INT32_MIN));
+    }
+    const auto larger = [](uint32_t p, uint32_t q) { return max(p, q); };
+    return {over_group<G>(most, larger), over_group<G>(least, larger)};
+  } else {
+    i16x2 most = {0, 0}, least = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      most = max2(most, __builtin_bit_cast(i16x2, (uint32_t)r.w[i]));
+      least = max2(least, __builtin_bit_cast(i16x2, (uint32_t)(r.w[i] ^ 0x80008000u)));
+    }
+    // most in the low half, least in the high one
+    const uint32_t m = __builtin_bit_cast(uint32_t, most), l = __builtin_bit_cast(uint32_t, least);
+    const i16x2 both = max2(__builtin_bit_cast(i16x2, (m & 0xffffu) | l << 16), __builtin_bit_cast(i16x2, m >> 16 | (l & 0xffff0000u)));
+    const uint32_t e = over_group<G>(__builtin_bit_cast(uint32_t, both), [](uint32_t p, uint32_t q) {
+      return __builtin_bit_cast(uint32_t, max2(__builtin_bit_cast(i16x2, p), __builtin_bit_cast(i16x2, q)));
+    });
+    if constexpr (T == SD_BF16) return {e << 16, e & 0xffff0000u};
+    const f16x2 h = pair<f16x2>(e);
+    return {__float_as_uint((float)h[0]), __float_as_uint((float)h[1])};
+  }
 }
 
-// x / s rounded to nearest, r being 1 / s rounded: the quotient's error is taken from x by one
-// fused operation (exact but near the ends of fp32's range) and corrected by another.
+// x / s rounded to nearest, r being near 1 / s: the quotient's error is taken from x by one fused
+// operation (exactly but near the ends of fp32's range) and corrected by another, which leaves it
+// 2^-44 off before it is rounded: quotients halfway between integers, fp32 numbers, come out exact.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
   return fmaf(fmaf(-q, s, x), r, q);
@@ -65,20 +99,15 @@ __global__ __launch_bounds__(256) void k_w4_quantize(W4Args a) {
   for (int u = 0; u < U; ++u) {
     f32x4 lo, hi;
     widen8<T>(raw[u], lo, hi);
-    const uint32_t top = over_group<G>(top8<T>(raw[u]), [](uint32_t p, uint32_t q) { return max(p, q); });
-    float s, most = 0.f, least = 0.f;
+    const Ends ends = group_ends<T, G>(raw[u]);
+    const uint32_t top = max(ends.most, ends.least);
+    const float least = __uint_as_float(ends.least);
+    float s;
     if (a.symmetric) {
-      s = __uint_as_float(top) / 7.f;
+      s = quotient(__uint_as_float(top), 7.f, 1.f / 7);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        most = fmaxf(most, fmaxf(lo[i], hi[i]));
-        least = fmaxf(least, fmaxf(-lo[i], -hi[i]));
-      }
-      most = group_max<G>(most);
-      least = group_max<G>(least);
       // The sum over 15, corrected as quotient() is.
-      const double w = (double)most + (double)least, q = w * (1.0 / 15);
+      const double w = (double)__uint_as_float(ends.most) + (double)least, q = w * (1.0 / 15);
       s = (float)fma(fma(-15.0, q, w), 1.0 / 15, q);
     }
     const u32x2 packed = pack4(f32x4{s, s, s, s}, a.scale_type);
@@ -87,16 +116,19 @@ __global__ __launch_bounds__(256) void k_w4_quantize(W4Args a) {
     const bool bad = top >= 0x7f800000u || s > 3.4028234e38f, none = s < 1.17549435e-38f;
     if (bad) bits = a.scale_type == SD_BF16 ? 0x7fc0 : 0x7e00;
     else if (none) bits = 0;
-    const float r = 1.f / s;
-    float z = a.symmetric ? 8.f : fminf(rintf(quotient(least, s, r)), 15.f);
-    if (!a.symmetric && (bad || none)) z = 0.f;
+    const float r = __builtin_amdgcn_rcpf(s);
+    int z = a.symmetric ? 8 : (int)fminf(rintf(quotient(least, s, r)), 15.f);
+    if (!a.symmetric && (bad || none)) z = 0;
+    // A sum with 1.5 * 2^23 is rounded to an integer, which its low bits hold.
+    constexpr float kInt = 12582912.f;
+    const int off = z - __float_as_int(kInt);
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float c = rintf(quotient(i < 4 ? lo[i & 3] : hi[i & 3], s, r)) + z;
-      c = bad || none ? z : __builtin_amdgcn_fmed3f(c, 0.f, 15.f);
-      word |= (uint32_t)c << (4 * i);
+      const int c = __float_as_int(quotient(i < 4 ? lo[i & 3] : hi[i & 3], s, r) + kInt) + off;
+      word |= (uint32_t)min(max(c, 0), 15) << (4 * i);
     }
+    if (bad || none) word = (uint32_t)z * 0x11111111u;
     const int64_t row = it[u].row;
     const int c = it[u].c;
     if (row >= a.rows) continue;
