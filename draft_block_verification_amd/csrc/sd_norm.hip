@@ -150,8 +150,8 @@ __device__ __forceinline__ double squares(const f32x4 &lo, const f32x4 &hi, doub
 // Rows of up to 8 NT U columns. Blocks of four threads that share an MXFP8 block are whole:
 // chunks are a multiple of 16 then.
 template <int XT, int RT, int NT, int U>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormLaunch a) {
-  constexpr int PER = NT < 256 ? 256 / NT : 1;       // rows a workgroup
+__global__ __launch_bounds__(NT < 128 ? 256 : NT) void k_norm(NormLaunch a) {
+  constexpr int PER = NT < 128 ? 256 / NT : 1;       // rows a workgroup
   constexpr int RR = RT == kNone ? XT : RT;
   __shared__ double part[NT / 64];
   const int t = threadIdx.x % NT;
@@ -224,18 +224,24 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormLaunch a) {
 
 template <int XT, int RT, int NT, int U>
 void launch_rows(const NormLaunch &a, hipStream_t stream) {
-  constexpr int PER = NT < 256 ? 256 / NT : 1;
+  constexpr int PER = NT < 128 ? 256 / NT : 1;
   hipLaunchKernelGGL((k_norm<XT, RT, NT, U>), groups_of((a.rows + PER - 1) / PER),
-                     dim3(NT < 256 ? 256 : NT), 0, stream, a);
+                     dim3(NT < 128 ? 256 : NT), 0, stream, a);
 }
 
 template <int XT, int RT>
 hipError_t launch_norm_of(const NormLaunch &a, hipStream_t stream) {
+  // Few rows wait for themselves, one chunk a thread is quickest; many fill the chip, and two a thread
+  // keep more loads on their way. us for a row of bf16 with residual and sum, threads x chunks:
+  //      1 x 4096: 512 x 1 2.9, 256 x 2 3.5, 1024 x 1 3.1       128 x 7168: 1024 x 1 4.3, 512 x 2 4.6, 256 x 4 5.7
+  //   2176 x 7168: 512 x 2 26, 256 x 4 30, 1024 x 1 32          2176 x 4096: 256 x 2 14.8, 512 x 1 14.8
+  //  16000 x 2048: 128 x 2 44, 256 x 1 46 (5.9 TB/s), 512 x 1 62   16000 x 1024: 64 x 2 22.6, 128 x 1 22.3, 256 x 1 25
+  const bool few = a.rows < 2048;
   if (a.chunks <= 64) launch_rows<XT, RT, 64, 1>(a, stream);
-  else if (a.chunks <= 128) launch_rows<XT, RT, 64, 2>(a, stream);
-  else if (a.chunks <= 256) launch_rows<XT, RT, 256, 1>(a, stream);
-  else if (a.chunks <= 512) launch_rows<XT, RT, 256, 2>(a, stream);
-  else if (a.chunks <= 1024) launch_rows<XT, RT, 256, 4>(a, stream);
+  else if (a.chunks <= 128) few ? launch_rows<XT, RT, 128, 1>(a, stream) : launch_rows<XT, RT, 64, 2>(a, stream);
+  else if (a.chunks <= 256) few ? launch_rows<XT, RT, 256, 1>(a, stream) : launch_rows<XT, RT, 128, 2>(a, stream);
+  else if (a.chunks <= 512) few ? launch_rows<XT, RT, 512, 1>(a, stream) : launch_rows<XT, RT, 256, 2>(a, stream);
+  else if (a.chunks <= 1024) few ? launch_rows<XT, RT, 1024, 1>(a, stream) : launch_rows<XT, RT, 512, 2>(a, stream);
   else if (a.chunks <= 2048) launch_rows<XT, RT, 1024, 2>(a, stream);
   else if (a.chunks <= 4096) launch_rows<XT, RT, 1024, 4>(a, stream);
   else hipLaunchKernelGGL((k_norm_long<XT, RT>), groups_of(a.rows), dim3(1024), 0, stream, a);

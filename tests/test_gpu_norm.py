@@ -114,9 +114,10 @@ def test_offset_zeros_and_not_finite(d):
         assert np.array_equal(scales.cpu().numpy(), rs) and np.array_equal(codes.cpu().numpy(), rc)
 
 
-def test_many_rows_repeat():
-    """More rows than the chip holds at once; the same bytes from call to call."""
-    x = N.rand(20011, 264, torch.bfloat16, 6)
+@pytest.mark.parametrize("rows,d", [(2048, 500), (20011, 264), (2050, 1000), (2049, 1500), (2051, 4001), (2048, 7168)])
+def test_many_rows_repeat(rows, d):
+    """The launch shapes of many rows; the same bytes from call to call."""
+    x = N.rand(rows, d, torch.bfloat16, 6)
     _, y = N.norm(x)
     got = sd.sd_rms_norm(x.cuda(), dtype=torch.float32)
     N.check_rounded(got, y, torch.float32)
