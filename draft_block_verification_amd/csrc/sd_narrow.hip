@@ -342,7 +342,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_narrow_skinny(NarrowArgs a) {
     }
   }
 #pragma unroll
-  for (int x = 0; x < D - 1; ++x)
+  for (int x = 0; x + 1 < D; ++x)
     if (j + x < n) F::template use<TV, MT>(a, st[x], lane, acc);
   const int col = lane & 15, q = lane >> 4;
 #pragma unroll
@@ -870,8 +870,16 @@ hipError_t launch_w4_tiled(const NarrowArgs &a, hipStream_t stream) {
 template <int H, int NG>
 hipError_t launch_w4_of(const NarrowArgs &a, hipStream_t stream) {
   if (!few_rows(a.M, a.V)) return a.zeros ? launch_w4_tiled<H, NG, true>(a, stream) : launch_w4_tiled<H, NG, false>(a, stream);
-  return a.zeros ? launch_skinny<W4<H, NG, true>, 8, 4, 2>(a, stream)
-                 : launch_skinny<W4<H, NG, false>, 8, 4, 2>(a, stream);
+  // 128 ids a workgroup share the hidden rows' loads; an LM head that gives few workgroups then is dealt
+  // in 64s. G = 128, us, ids x waves x steps ahead 128 x 8 x 1 / 128 x 4 x 2 / 64 x 4 x 2, V x depth, M:
+  //   129280 x 7168:  1: 77 / 80 / 76         16: 83 / 89 / 101
+  //    32768 x 2048:  1: 8.1 / 8.7 / 8.3      16: 8.8 / 9.1 / 10.5    32: 11.7 / 12.2 / 16.1
+  //     8000 x 2048:  1: 7.1 / 6.9 / 4.9      16: 7.5 / 7.9 / 5.9     32: 10.3 / 10.8 / 8.6
+  if (a.V <= 128 * 128)
+    return a.zeros ? launch_skinny<W4<H, NG, true>, 4, 4, 2>(a, stream)
+                   : launch_skinny<W4<H, NG, false>, 4, 4, 2>(a, stream);
+  return a.zeros ? launch_skinny<W4<H, NG, true>, 8, 8, 1>(a, stream)
+                 : launch_skinny<W4<H, NG, false>, 8, 8, 1>(a, stream);
 }
 
 // The rows of a call made ready, its group sums among them where the tiled kernel runs, and the call.
