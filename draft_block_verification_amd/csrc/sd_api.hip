@@ -699,7 +699,7 @@ int32_t sd_rms_norm(const void *x, int32_t x_type, int64_t x_stride, const void 
                     int64_t sum_stride, void *y, int32_t y_type, int64_t y_stride, void *stream) {
   const NormArgs a{x, x_type, x_stride, residual, residual_type, residual_stride, weight, weight_type,
                    weight_offset, eps, rows, d, sum, sum_stride, y, y_type, y_stride, nullptr, nullptr};
-  if (!y || !known_type(y_type)) return SD_EINVAL;
+  if (!y || !known_type(y_type) || y == sum) return SD_EINVAL;
   const int32_t st = check_norm(a);
   if (st != SD_OK) return st;
   if (!stride_fits(y_stride, d)) return SD_ESHAPE;

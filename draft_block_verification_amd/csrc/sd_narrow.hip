@@ -4,8 +4,9 @@
 // Both run on the 16-bit matrix instructions: an e4m3 value under its block's scale and a code
 // 0 .. 15 are bf16 numbers (the latter fp16 numbers too), products of bf16 or fp16 numbers are
 // exact in fp32, and these instructions add in fp32. The 8-bit instructions do not: they align
-// the products of a block and cut them, and sums of 4096 terms come out 1.4e-5 off (relative,
-// normal data) where the 16-bit ones are 9e-8 off.
+// the products of eight columns and cut them, and sums of 4096 terms come out 1.4e-5 off
+// (relative, normal data) where the 16-bit ones are 9e-8 off. They serve logits of many rows
+// that are rounded to 16 bits, at twice the rate.
 //
 // Weights are re-laid once into tiles of 64 rows by 128 columns, each four fragments of 16 rows
 // in the order the matrix instruction takes them: lane l holds row l % 16, q = l / 16, and of the
@@ -313,6 +314,9 @@ struct W4 {
 // per 16 TV ids; its NW waves take the 128-column steps in turn, straight into registers: each
 // weight is used by one wave only, so LDS would add a copy and share nothing. The hidden rows are
 // read by every workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
+// 129280 x 7168, us: MXFP8 under 1 row 141 (6.8 TB/s), 16 rows 147; 4 bits in groups of 128 under 1
+// row 77 (6.3 TB/s), 16 rows 83; 151936 x 4096 in groups of 32, 16 rows 71 (4.9 TB/s: a quarter of
+// the scales' and sums' work a column comes back at every 32, the vector units bound it).
 template <class F, int TV, int MT, int NW, int D>
 __global__ __launch_bounds__(64 * NW, 2) void k_narrow_skinny(NarrowArgs a) {
   constexpr int IDS = 16 * TV, LDR = IDS + 4;
@@ -507,7 +511,15 @@ __device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, L
 // used by one wave alone: it comes from memory into that wave's registers, two steps ahead,
 // and is decoded there. Every wave issues the same loads every step, past the end the last
 // step's again: a step's weights are issued behind its hidden rows, so when the former have
-// arrived the latter have, and behind the barrier those of all waves.
+// arrived the latter have, and behind the barrier those of all waves. Two workgroups a compute
+// unit: one decodes and scales while the other multiplies.
+//
+// 512 rows by 129280 ids at depth 7168: 4 bits with zeros in groups of 128 930 us (1.02 PFLOP/s;
+// 860 us: what the library's bf16 product of that shape takes, with nothing to decode), without zeros
+// 853, in groups of 64 1070, of 32 1430. In copies of the kernel for timing, without the scaling
+// of a group's sums 720 us, without the decoding too 670; without the weights' loads 840. Vector
+// and matrix work hardly overlap, in whatever order they are written: the scales cost their own
+// time. MXFP8 with fp32 logits, 2048 rows: 3000 us (1.27 PFLOP/s).
 template <class F, int TM>
 __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt, int n_vt) {
   constexpr int NS = 3, ROWS = 16 * TM, STAGE = ROWS * 256 + F::kSums * 256;
@@ -643,7 +655,11 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15");
 // they add them, which leaves normal data 1.4e-5 off: too much for an fp32 logit, nothing beside
 // the rounding of a 16-bit one (2^-9, 2^-12). They run at twice the 16-bit rate and take codes as they
 // are. Otherwise as k_narrow_tiled: four waves, each 64 ids by 16 TM rows; chunk c of row r of a
-// step's codes lies at place c ^ (r / 2 % 8).
+// step's codes lies at place c ^ (r / 2 % 8). NS LDS buffers, WB sets of a step's weights.
+// 2048 rows by 129280 ids at depth 7168 in 256 x 256 tiles: 1640 us (2.3 PFLOP/s; the library's
+// 8-bit product reaches 2.6 on 8192^3). In copies for timing, without the loads 1180 us, without the
+// LDS reads too 1130 (3.4). More buffers, weights further ahead and eight waves on the tile were all
+// within 3%: what the loads cost is not their latency.
 template <int TM, int NS, int WB>
 __global__ __launch_bounds__(256, TM > 8 ? 1 : 2) void k_mx8_tiled(NarrowArgs a, int n_mt, int n_vt) {
   static_assert(WB <= NS, "a step's weights are issued behind its hidden rows");

@@ -4,7 +4,7 @@
 //   s = x + r, rounded to r's type (x itself without a residual)
 //   y = s / sqrt(mean(s^2) + eps) * (offset + w)
 //
-// A row belongs to NT threads of one workgroup, eight neighbouring columns a thread and turn,
+// A row belongs to NT threads of one workgroup, eight neighbouring columns (a chunk) a thread and turn,
 // and stays in their registers between the sum of its squares and its output, so it is read
 // once; rows past 32768 columns are read a second time. Squares and their sum, the root and the
 // product are formed in fp64: the memory bounds the kernel (two conversions and three fp64

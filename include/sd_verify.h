@@ -601,7 +601,7 @@ SD_API int32_t sd_mxfp4_logits(const void *hidden, int32_t hidden_type, int32_t 
  * A NaN makes its row NaN. In a row with an infinity that column is NaN and the finite ones 0;
  * as MXFP8, where a block that holds a NaN reads as NaN, the other blocks 0.
  * Errors: SD_EINVAL (null pointer, unknown type, eps or weight_offset not finite, eps < 0, a sum
- * without a residual), SD_ESHAPE (rows < 1, d outside [1, 2^20], d % 8 != 0 for MXFP8, short
+ * without a residual, y and sum the same), SD_ESHAPE (rows < 1, d outside [1, 2^20], d % 8 != 0 for MXFP8, short
  * strides), SD_EALIGN (an array not aligned to its elements; codes 16 bytes, scales 4), SD_EDEVICE.
  */
 SD_API int32_t sd_rms_norm(const void *x, int32_t x_type, int64_t x_stride, const void *residual,
@@ -652,9 +652,15 @@ SD_API int32_t sd_mxfp8_head(const uint8_t *codes, const uint8_t *scales, int32_
  *            hidden_stride kp
  *   head     the [V][d] LM head as sd_mxfp8_head wrote it
  *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
- *   workspace  sd_mxfp8_logits_workspace_bytes(M, d) bytes
- * logits[m][v] = the sum of the products of the values, every product exact, accumulated in
- * fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives NaN.
+ *   workspace  sd_mxfp8_logits_workspace_bytes(M, d) bytes; its header is left alone and need not
+ *            have been prepared
+ * logits[m][v] = the sum of the products of the values. fp32 logits, and any of up to 16 rows: every
+ * product exact, accumulated in fp32, rounded once to logits_type. 16-bit logits of more rows may
+ * come from the 8-bit matrix instructions, which cut the products of eight consecutive columns (8 i
+ * .. 8 i + 7) to 13 bits under the power of two in the largest before they add them in fp32: on normal data
+ * 1.4e-5 of the logits' size, beside 2^-9 or 2^-12 for their rounding. Values are formed in bf16
+ * (exact but outside its range: scale bytes over 246, or products of scales that leave fp32's).
+ * A row of hidden with a NaN or an infinity gives NaN.
  * Errors: as for sd_mxfp4_logits; SD_EINVAL also for hidden_scales that do not go with hidden_type.
  */
 SD_API size_t sd_mxfp8_logits_workspace_bytes(int32_t M, int32_t d);
@@ -713,7 +719,7 @@ SD_API int32_t sd_w4_head(const uint8_t *codes, const void *scales, int32_t scal
  *   hidden   [M][d] of hidden_type SD_BF16 or SD_F16, row stride hidden_stride elements
  *   head, V, d, group, scale_type, has_zeros   as sd_w4_head wrote it
  *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
- *   workspace  sd_w4_logits_workspace_bytes(M, d, group) bytes
+ *   workspace  sd_w4_logits_workspace_bytes(M, d, group) bytes, as for sd_mxfp8_logits
  * logits[m][v] = sum over groups of scale * (sum code * hidden - zero * sum hidden), products
  * exact, sums in fp32, rounded once to logits_type. A row of hidden with a NaN or an infinity gives
  * NaN, and so may one whose sum of 15 |hidden| over a group passes the largest fp32 number.

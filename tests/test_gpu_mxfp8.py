@@ -132,7 +132,7 @@ def logits_case(M, V, d, dtype, out, seed, hidden=None, coded=False, spread=Fals
 
 SHAPES = [(1, 1, 8), (1, 15, 32), (2, 17, 128), (3, 64, 136), (16, 100, 256), (17, 1000, 512), (5, 257, 2048),
           (33, 515, 640), (64, 1023, 384), (65, 300, 1152), (129, 777, 1024), (256, 1536, 512), (300, 2049, 768),
-          (1, 5003, 4096)]
+          (1, 5003, 4096), (16, 17001, 1160), (32, 20003, 136)]
 
 
 @pytest.mark.parametrize("coded", [False, True])

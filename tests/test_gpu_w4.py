@@ -104,7 +104,8 @@ def logits_case(M, V, d, group, symmetric, dtype, out, seed, kind=torch.bfloat16
 
 SHAPES = [(1, 1, 32, 32), (1, 15, 64, 64), (2, 17, 128, 128), (3, 64, 160, 32), (16, 100, 256, 64), (17, 1000, 512, 128),
           (5, 257, 2048, 32), (33, 515, 640, 64), (64, 1023, 384, 128), (65, 300, 1152, 32), (129, 777, 1024, 64),
-          (256, 1536, 512, 128), (300, 2049, 768, 128), (1, 5003, 4096, 128), (1, 300, 4096, 32), (40, 333, 192, 64)]
+          (256, 1536, 512, 128), (300, 2049, 768, 128), (1, 5003, 4096, 128), (1, 300, 4096, 32), (40, 333, 192, 64),
+          (1, 16385, 160, 32), (16, 20003, 1216, 64), (32, 17001, 1152, 128), (17, 20001, 96, 32)]
 
 
 @pytest.mark.parametrize("dtype", HALF)

@@ -13,6 +13,7 @@ import draft_block_verification_amd as sd
 lib = ctypes.CDLL(sd.LIB_PATH)
 FAKE = ctypes.c_void_p(0x10000)          # aligned, never dereferenced on the host
 EIGHT, TWO, ODD = (ctypes.c_void_p(0x10000 + k) for k in (8, 2, 1))
+OTHER = ctypes.c_void_p(0x20000)
 i64, sz, f32 = ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 for _f in ("sd_mxfp8_head_bytes", "sd_mxfp8_logits_workspace_bytes", "sd_w4_head_bytes", "sd_w4_logits_workspace_bytes"):
     getattr(lib, _f).restype = sz
@@ -33,7 +34,7 @@ def norm_args(**tail):
 @pytest.mark.parametrize("mx", [False, True])
 def test_norm_refusals(mx):
     f = lib.sd_rms_norm_mxfp8 if mx else lib.sd_rms_norm
-    ok = norm_args(codes=FAKE, scales=FAKE) if mx else norm_args(y=FAKE, yt=1, ys=i64(256))
+    ok = norm_args(codes=FAKE, scales=FAKE) if mx else norm_args(y=OTHER, yt=1, ys=i64(256))
     for p in ("x", "codes", "scales") if mx else ("x", "y"):
         assert call(f, ok, **{p: None}) == EINVAL
     for p in ("xt", "wt") + (() if mx else ("yt",)):
@@ -41,6 +42,8 @@ def test_norm_refusals(mx):
             assert call(f, ok, **{p: t}) == EINVAL
     assert call(f, ok, rt=2) == EINVAL and call(f, ok, xt=0, rt=1) == EINVAL and call(f, ok, rt=3) == EINVAL
     assert call(f, ok, res=None) == EINVAL                               # a sum without a residual
+    if not mx:
+        assert call(f, ok, y=EIGHT, sum=EIGHT) == EINVAL                 # two results in one place
     for bad in (float("nan"), float("inf"), -1e-9):
         assert call(f, ok, eps=f32(bad)) == EINVAL
     for bad in (float("nan"), -float("inf")):
