@@ -758,6 +758,13 @@ __global__ __launch_bounds__(256, TM > 8 ? 1 : 2) void k_mx8_tiled(NarrowArgs a,
     if (k + x < a.steps) step(k + x, st[x], st[x + 1]);
   });
   settle();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {     // read behind it, not before
+      if constexpr (TM > 4) asm volatile("" : "+a"(acc[i][m]));
+      else asm volatile("" : "+v"(acc[i][m]));
+    }
   wait_loads<0>();                     // the trailing loads land before LDS is used again
   raw_barrier();
   const int v0 = vt * 256 + wave * 64;
