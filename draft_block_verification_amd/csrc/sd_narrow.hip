@@ -123,11 +123,11 @@ __device__ __forceinline__ float byte_scale(uint32_t word, int i) {
   return __uint_as_float((word >> (8 * i) & 255) << 23);
 }
 
-// A 16-bit scale; f16: all ones for fp16, 0 for bf16 (bits, as a choice between the two would be
-// a branch around every use).
-__device__ __forceinline__ float wide_scale(uint32_t bits, uint32_t f16) {
-  const uint32_t h = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)bits));
-  return __uint_as_float((h & f16) | (bits << 16 & ~f16));
+// A half of a word as a scale in fp16 (F16) or bf16.
+template <bool F16>
+__device__ __forceinline__ float wide_scale(uint32_t word, int half) {
+  if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)(word >> (16 * half)));
+  return __uint_as_float(half ? word & 0xffff0000u : word << 16);
 }
 
 struct NarrowArgs {
@@ -137,7 +137,7 @@ struct NarrowArgs {
   const uint8_t *codes;     // LM head, tiled
   const uint8_t *scales;
   const uint8_t *zeros;
-  uint32_t scale_f16;       // scales of the 4-bit form: ~0 in fp16, 0 in bf16
+  bool scale_f16;           // scales of the 4-bit form in fp16, else bf16
   int M, V, steps;          // steps: 128-column steps
   void *out;
   int32_t type;
@@ -206,7 +206,7 @@ struct Mx8 {
     }
   }
   template <int TV, int MT>
-  static __device__ __forceinline__ void use(const NarrowArgs &a, const Step<TV, MT> &st, int lane, f32x4 (&acc)[TV][MT]) {
+  static __device__ __forceinline__ void use(const Step<TV, MT> &st, int lane, f32x4 (&acc)[TV][MT]) {
     const int q = lane >> 4;
     u32x4 h[MT][4];
 #pragma unroll
@@ -234,7 +234,7 @@ struct Mx8 {
 // code products c h and the sum of the h (a product with ones) are formed in fp32, and
 // s (sum c h - z sum h) is added to the logit: no weight is rounded. Where z is 8 throughout, the
 // code products start from -8 sum h.
-template <int H, int NG, bool ASYM>
+template <int H, int NG, bool ASYM, bool SF16>
 struct W4 {
   template <int TV, int MT>
   struct Step {
@@ -269,7 +269,7 @@ struct W4 {
     }
   }
   template <int TV, int MT>
-  static __device__ __forceinline__ void use(const NarrowArgs &a, const Step<TV, MT> &st, int lane, f32x4 (&acc)[TV][MT]) {
+  static __device__ __forceinline__ void use(const Step<TV, MT> &st, int lane, f32x4 (&acc)[TV][MT]) {
     constexpr int KS = 4 / NG;
     const uint32_t one = H == SD_F16 ? 0x3c003c00u : 0x3f803f80u;
     const u32x4 ones = {one, one, one, one};
@@ -297,7 +297,7 @@ struct W4 {
 #pragma unroll
           for (int m = 0; m < MT; ++m) part[m] = mfma16<H>(st.h[m][g * KS + t], w, part[m]);
         }
-        const float s = wide_scale(st.s[i / 4][g][i % 4 / 2] >> (16 * (i % 2)) & 0xffff, a.scale_f16);
+        const float s = wide_scale<SF16>(st.s[i / 4][g][i % 4 / 2], i % 2);
         const float z = ASYM ? (float)(st.z[i / 4][g] >> (8 * (i % 4)) & 255) : 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -315,8 +315,9 @@ struct W4 {
 // weight is used by one wave only, so LDS would add a copy and share nothing. The hidden rows are
 // read by every workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
 // 129280 x 7168, us: MXFP8 under 1 row 141 (6.8 TB/s), 16 rows 147; 4 bits in groups of 128 under 1
-// row 77 (6.3 TB/s), 16 rows 83; 151936 x 4096 in groups of 32, 16 rows 71 (4.9 TB/s: a quarter of
-// the scales' and sums' work a column comes back at every 32, the vector units bound it).
+// row 76 (6.4 TB/s), 16 rows 80; in groups of 64 with zeros under 16 rows 88, of 32 108, without zeros 96:
+// scales and sums come back at every 32 columns, and the vector units bound it. Held to 128 registers,
+// so that two workgroups of eight waves fit a compute unit, these two take 115 and 144 us (spills).
 template <class F, int TV, int MT, int NW, int D>
 __global__ __launch_bounds__(64 * NW, 2) void k_narrow_skinny(NarrowArgs a) {
   constexpr int IDS = 16 * TV, LDR = IDS + 4;
@@ -341,13 +342,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_narrow_skinny(NarrowArgs a) {
   for (; j + D <= n; j += D) {
 #pragma unroll
     for (int x = 0; x < D; ++x) {
-      F::template use<TV, MT>(a, st[x], lane, acc);
+      F::template use<TV, MT>(st[x], lane, acc);
       load(j + x + D, st[x]);
     }
   }
 #pragma unroll
   for (int x = 0; x + 1 < D; ++x)
-    if (j + x < n) F::template use<TV, MT>(a, st[x], lane, acc);
+    if (j + x < n) F::template use<TV, MT>(st[x], lane, acc);
   const int col = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -396,7 +397,7 @@ struct Mx8Tile {
   }
   static __device__ __forceinline__ int chunk(int t, int q) { return 2 * q + (t & 1) + 8 * (t >> 1); }
   template <int TM, class Frag, class Sum>
-  __device__ __forceinline__ void use(const NarrowArgs &, Frag frag, Sum, f32x4 (&acc)[4][TM]) const {
+  __device__ __forceinline__ void use(Frag frag, Sum, f32x4 (&acc)[4][TM]) const {
     u32x4 h[2][TM];
 #pragma unroll
     for (int m = 0; m < TM; ++m) h[0][m] = frag(m, 0);
@@ -417,7 +418,7 @@ struct Mx8Tile {
 
 // The products of a group start from -zero times the row's sum over the group (sum(g, m): the
 // four rows of fragment m, times -8 already in the symmetric form).
-template <int H, int NG, bool ASYM>
+template <int H, int NG, bool ASYM, bool SF16>
 struct W4Tile {
   static constexpr int kSums = NG;
   u32x4 w[4];
@@ -445,7 +446,7 @@ struct W4Tile {
   }
   static __device__ __forceinline__ int chunk(int t, int q) { return 4 * t + q; }
   template <int TM, class Frag, class Sum>
-  __device__ __forceinline__ void use(const NarrowArgs &a, Frag frag, Sum sum, f32x4 (&acc)[4][TM]) const {
+  __device__ __forceinline__ void use(Frag frag, Sum sum, f32x4 (&acc)[4][TM]) const {
     constexpr int KS = 4 / NG;
     u32x4 h[2][TM];
     f32x4 part[4][TM];
@@ -481,7 +482,7 @@ struct W4Tile {
       if (t % KS == KS - 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float sc = wide_scale(s[g][i / 2] >> (16 * (i % 2)) & 0xffff, a.scale_f16);
+          const float sc = wide_scale<SF16>(s[g][i / 2], i % 2);
 #pragma unroll
           for (int m = 0; m < TM; ++m)
 #pragma unroll
@@ -516,7 +517,7 @@ __device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, L
 //
 // 512 rows by 129280 ids at depth 7168: 4 bits with zeros in groups of 128 930 us (1.02 PFLOP/s;
 // 860 us: what the library's bf16 product of that shape takes, with nothing to decode), without zeros
-// 853, in groups of 64 1070, of 32 1430. In copies of the kernel for timing, without the scaling
+// 850, in groups of 64 1050, of 32 1335. In copies of the kernel for timing, without the scaling
 // of a group's sums 720 us, without the decoding too 670; without the weights' loads 840. Vector
 // and matrix work hardly overlap, in whatever order they are written: the scales cost their own
 // time. MXFP8 with fp32 logits, 2048 rows: 3000 us (1.27 PFLOP/s).
@@ -572,7 +573,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
     auto sum = [&](int g, int m) __attribute__((always_inline)) {
       return *(const LDSP f32x4 *)(b + ROWS * 256 + (g * 64 + 16 * m + 4 * q) * 4);
     };
-    now.template use<TM>(a, frag, sum, acc);
+    now.template use<TM>(frag, sum, acc);
     now.load(a, tile0 + min(k + 2, a.steps - 1), lane);
   };
 #pragma unroll
@@ -885,24 +886,25 @@ hipError_t launch_mx8_tiled(const NarrowArgs &a, hipStream_t stream) {
 //     8000 x 2048:  64: 21 / 29      256: 22 / 30      512: 32 / 32
 int tile_rows(const NarrowArgs &a) { return paired(a, 32, 0.92, 0.70) < paired(a, 64, 1.27, 1.0) ? 32 : 64; }
 
-template <int H, int NG, bool ASYM>
-hipError_t launch_w4_tiled(const NarrowArgs &a, hipStream_t stream) {
-  return tile_rows(a) == 32 ? launch_tiled<W4Tile<H, NG, ASYM>, 2>(a, stream) : launch_tiled<W4Tile<H, NG, ASYM>, 4>(a, stream);
-}
-
-template <int H, int NG>
-hipError_t launch_w4_of(const NarrowArgs &a, hipStream_t stream) {
-  if (!few_rows(a.M, a.V)) return a.zeros ? launch_w4_tiled<H, NG, true>(a, stream) : launch_w4_tiled<H, NG, false>(a, stream);
+template <int H, int NG, bool ASYM, bool SF16>
+hipError_t launch_w4_form(const NarrowArgs &a, hipStream_t stream) {
+  if (!few_rows(a.M, a.V)) {
+    using F = W4Tile<H, NG, ASYM, SF16>;
+    return tile_rows(a) == 32 ? launch_tiled<F, 2>(a, stream) : launch_tiled<F, 4>(a, stream);
+  }
   // 128 ids a workgroup share the hidden rows' loads; an LM head that gives few workgroups then is dealt
   // in 64s. G = 128, us, ids x waves x steps ahead 128 x 8 x 1 / 128 x 4 x 2 / 64 x 4 x 2, V x depth, M:
   //   129280 x 7168:  1: 77 / 80 / 76         16: 83 / 89 / 101
   //    32768 x 2048:  1: 8.1 / 8.7 / 8.3      16: 8.8 / 9.1 / 10.5    32: 11.7 / 12.2 / 16.1
   //     8000 x 2048:  1: 7.1 / 6.9 / 4.9      16: 7.5 / 7.9 / 5.9     32: 10.3 / 10.8 / 8.6
-  if (a.V <= 128 * 128)
-    return a.zeros ? launch_skinny<W4<H, NG, true>, 4, 4, 2>(a, stream)
-                   : launch_skinny<W4<H, NG, false>, 4, 4, 2>(a, stream);
-  return a.zeros ? launch_skinny<W4<H, NG, true>, 8, 8, 1>(a, stream)
-                 : launch_skinny<W4<H, NG, false>, 8, 8, 1>(a, stream);
+  using F = W4<H, NG, ASYM, SF16>;
+  return a.V <= 128 * 128 ? launch_skinny<F, 4, 4, 2>(a, stream) : launch_skinny<F, 8, 8, 1>(a, stream);
+}
+
+template <int H, int NG>
+hipError_t launch_w4_of(const NarrowArgs &a, hipStream_t stream) {
+  if (a.zeros) return a.scale_f16 ? launch_w4_form<H, NG, true, true>(a, stream) : launch_w4_form<H, NG, true, false>(a, stream);
+  return a.scale_f16 ? launch_w4_form<H, NG, false, true>(a, stream) : launch_w4_form<H, NG, false, false>(a, stream);
 }
 
 // The rows of a call made ready, its group sums among them where the tiled kernel runs, and the call.
@@ -966,7 +968,7 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
                              void *workspace, hipStream_t stream) {
   const int kp = mx_padded(d);
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace) + sizeof(WsHeader);
-  NarrowArgs a{hidden, hidden_scales, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, 0, M, V, kp / 128,
+  NarrowArgs a{hidden, hidden_scales, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, false, M, V, kp / 128,
                logits, type, ld, vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8),
                nullptr};
   const bool coded = hidden_type == SD_MXFP8, few = few_rows(M, V), wide = !few && type == SD_F32;
@@ -1026,7 +1028,7 @@ hipError_t launch_w4_logits(const void *hidden, int32_t hidden_type, int M, int 
   float *sums = reinterpret_cast<float *>(ws + w4_sums_at(M, d));
   uint16_t *copy = reinterpret_cast<uint16_t *>(ws + sizeof(WsHeader));
   const NarrowArgs a{hidden, nullptr, stride, head, s, zeros ? s + n * (128 / group) * 128 : nullptr,
-                     scale_type == SD_F16 ? ~0u : 0u, M, V, mx_padded(d) / 128, logits, type, ld, vec_rows(logits, type, ld, 4),
+                     scale_type == SD_F16, M, V, mx_padded(d) / 128, logits, type, ld, vec_rows(logits, type, ld, 4),
                      vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8), nullptr};
   if (hidden_type == SD_BF16) {
     if (group == 128) return launch_w4_group<SD_BF16, 128>(a, d, copy, sums, stream);
