@@ -171,35 +171,59 @@ __device__ inline void store4(const NarrowArgs &a, int m, int v, const f32x4 &z)
 // One step's weights of 64 G ids and their use. `Hid` is what a step of the hidden rows is.
 //
 // MXFP8 x MXFP8: each weight and hidden value is decoded under its scale into bf16.
+template <int TV>
+struct Mx8Step {
+  u32x4 w[TV][2];
+  uint32_t s[TV / 4][2];
+  __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int k, int lane) {
+#pragma unroll
+    for (int i = 0; i < TV; ++i) {
+      const int64_t tile = min(group + i / 4, (int64_t)(a.V - 1) / 64) * a.steps + k;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[i][h] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4 *>(a.codes + tile * kMx8Tile + (i % 4) * 2048 + h * 1024) + lane);
+      if (i % 4 == 0) {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(a.scales + tile * kMx8Scales) + (lane & 15);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[i / 4][h] = __builtin_nontemporal_load(p + 16 * (2 * h + (lane >> 5)));
+      }
+    }
+  }
+  template <int MT>
+  __device__ __forceinline__ void use(const u32x4 (&h)[MT][4], f32x4 (&acc)[TV][MT]) const {
+#pragma unroll
+    for (int i = 0; i < TV; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const u32x4 x = decode8(w[i][t / 2][t % 2 * 2], w[i][t / 2][t % 2 * 2 + 1], byte_scale(s[i / 4][t / 2], i % 4));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[i][m] = mfma16<SD_BF16>(h[m][t], x, acc[i][m]);
+      }
+  }
+};
+
+// Eight codes under a scale byte in bf16; NaN under byte 255.
+__device__ __forceinline__ u32x4 decode_row8(uint32_t w0, uint32_t w1, uint32_t byte) {
+  const uint32_t nan = byte == 255 ? ~0u : 0u;
+  return decode8(w0 | nan, w1 | nan, __uint_as_float(min(byte, 254u) << 23));
+}
+
+// Hidden rows in MXFP8 already.
 struct Mx8 {
   template <int TV, int MT>
-  struct Step {
-    u32x4 w[TV][2];
-    uint32_t s[TV / 4][2];
+  struct Step : Mx8Step<TV> {
     u32x4 h[MT][2];
     uint32_t hs[MT];
   };
   template <int TV, int MT>
   static __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int k, int lane,
                                               Step<TV, MT> &st) {
-    const int q = lane >> 4;
-#pragma unroll
-    for (int i = 0; i < TV; ++i) {
-      const int64_t tile = min(group + i / 4, (int64_t)(a.V - 1) / 64) * a.steps + k;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        st.w[i][h] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4 *>(a.codes + tile * kMx8Tile + (i % 4) * 2048 + h * 1024) + lane);
-      if (i % 4 == 0) {
-        const uint32_t *s = reinterpret_cast<const uint32_t *>(a.scales + tile * kMx8Scales) + (lane & 15);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) st.s[i / 4][h] = __builtin_nontemporal_load(s + 16 * (2 * h + q / 2));
-      }
-    }
+    st.Mx8Step<TV>::load(a, group, k, lane);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int64_t row = min(16 * m + (lane & 15), a.M - 1);
-      const uint8_t *p = reinterpret_cast<const uint8_t *>(a.hidden) + row * a.hstride + 128 * k + 16 * q;
+      const uint8_t *p = reinterpret_cast<const uint8_t *>(a.hidden) + row * a.hstride + 128 * k + 16 * (lane >> 4);
       st.h[m][0] = *reinterpret_cast<const u32x4 *>(p);
       st.h[m][1] = *reinterpret_cast<const u32x4 *>(p + 64);
       st.hs[m] = *reinterpret_cast<const uint32_t *>(a.hscales + row * (a.hstride / 32) + 4 * k);
@@ -212,21 +236,52 @@ struct Mx8 {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t byte = st.hs[m] >> (8 * (t / 2 * 2 + q / 2)) & 255;
-        const uint32_t nan = byte == 255 ? ~0u : 0u;
-        h[m][t] = decode8(st.h[m][t / 2][t % 2 * 2] | nan, st.h[m][t / 2][t % 2 * 2 + 1] | nan,
-                          __uint_as_float(min(byte, 254u) << 23));
+      for (int t = 0; t < 4; ++t)
+        h[m][t] = decode_row8(st.h[m][t / 2][t % 2 * 2], st.h[m][t / 2][t % 2 * 2 + 1],
+                              st.hs[m] >> (8 * (t / 2 * 2 + q / 2)) & 255);
+    st.template use<MT>(h, acc);
+  }
+};
+
+// Hidden rows of a 16-bit type T, quantised by every workgroup for itself: a block's 32 columns lie in
+// this lane and the one 16 further or before. The codes are those of k_mx8_quantize.
+template <int T>
+struct Mx8Of {
+  template <int TV, int MT>
+  struct Step : Mx8Step<TV> {
+    Raw8<T> x[MT][4];
+  };
+  template <int TV, int MT>
+  static __device__ __forceinline__ void load(const NarrowArgs &a, int64_t group, int k, int lane,
+                                              Step<TV, MT> &st) {
+    st.Mx8Step<TV>::load(a, group, k, lane);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int64_t row = min(16 * m + (lane & 15), a.M - 1);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        st.x[m][t] = load8<T>(a.hidden, row * a.hstride + 128 * k + 64 * (t / 2) + 16 * (lane >> 4) + 8 * (t % 2), 8, true);
+    }
+  }
+  template <int TV, int MT>
+  static __device__ __forceinline__ void use(const Step<TV, MT> &st, int, f32x4 (&acc)[TV][MT]) {
+    u32x4 h[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t top = max(top8<T>(st.x[m][2 * half]), top8<T>(st.x[m][2 * half + 1]));
+        top = max(top, (uint32_t)__builtin_amdgcn_ds_swizzle((int)top, 0x401f));     // lane ^ 16
+        const int byte = mx8_scale(top);
+#pragma unroll
+        for (int t = 2 * half; t < 2 * half + 2; ++t) {
+          f32x4 lo, hi;
+          widen8<T>(st.x[m][t], lo, hi);
+          const u32x2 w = mx8_codes(lo, hi, min(byte, 246));     // of byte 255: unused
+          h[m][t] = decode_row8(w[0], w[1], byte);
+        }
       }
-#pragma unroll
-    for (int i = 0; i < TV; ++i)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const u32x4 w = decode8(st.w[i][t / 2][t % 2 * 2], st.w[i][t / 2][t % 2 * 2 + 1],
-                                byte_scale(st.s[i / 4][t / 2], i % 4));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[i][m] = mfma16<SD_BF16>(h[m][t], w, acc[i][m]);
-      }
+    st.template use<MT>(h, acc);
   }
 };
 
@@ -857,12 +912,16 @@ double paired(const NarrowArgs &a, int rows, double one, double both) {
   return (double)(each / 2) * 2 * both + (double)(each % 2) * one;
 }
 
+template <class F, int TV, int MT, int NW, int D>
+hipError_t launch_skinny_of(const NarrowArgs &a, hipStream_t stream) {
+  const unsigned n = (unsigned)((a.V + 16 * TV - 1) / (16 * TV));
+  hipLaunchKernelGGL((k_narrow_skinny<F, TV, MT, NW, D>), dim3(n), dim3(64 * NW), 0, stream, a);
+  return hipGetLastError();
+}
+
 template <class F, int TV, int NW, int D>
 hipError_t launch_skinny(const NarrowArgs &a, hipStream_t stream) {
-  const unsigned n = (unsigned)((a.V + 16 * TV - 1) / (16 * TV));
-  auto *k = a.M <= 16 ? &k_narrow_skinny<F, TV, 1, NW, D> : &k_narrow_skinny<F, TV, 2, NW, D>;
-  hipLaunchKernelGGL(k, dim3(n), dim3(64 * NW), 0, stream, a);
-  return hipGetLastError();
+  return a.M <= 16 ? launch_skinny_of<F, TV, 1, NW, D>(a, stream) : launch_skinny_of<F, TV, 2, NW, D>(a, stream);
 }
 
 template <class F, int TM>
@@ -974,6 +1033,15 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
   const bool coded = hidden_type == SD_MXFP8, few = few_rows(M, V), wide = !few && type == SD_F32;
   hipError_t e = hipSuccess;
   if (!wide) {
+    // Whole 16-bit rows of one tile are quantised by each workgroup, not by a launch before: measured
+    // (us, each workgroup / a launch before, 1 and 16 rows) 1000 x 1024: 4.2 / 5.3, 4.5 / 6.1;
+    // 8000 x 2048: 6.6 / 8.0, 7.7 / 9.1; 32768 x 2048: 13.8 / 14.4, 15.4 / 16.2; but 129280 x 7168:
+    // 142.5 / 142.2, 152.8 / 149.5, and 32768 x 2048 of fp32 rows 14.7 / 14.3, 19.3 / 16.0.
+    if (M <= 16 && V <= 65536 && d == kp && hidden_type != SD_F32 && vec_rows(hidden, hidden_type, stride, 8) && !coded) {
+      a.hstride = stride;
+      return hidden_type == SD_BF16 ? launch_skinny_of<Mx8Of<SD_BF16>, 4, 1, 4, 2>(a, stream)
+                                    : launch_skinny_of<Mx8Of<SD_F16>, 4, 1, 4, 2>(a, stream);
+    }
     if (!coded) {
       uint8_t *scales = ws + (size_t)M * kp;
       e = launch_mx8_quantize(hidden, hidden_type, M, d, stride, ws, scales, stream);

@@ -180,6 +180,30 @@ def test_logits_not_finite_row(M, coded, out):
     assert bool(((got - want)[rest].abs() <= tol[rest]).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [1, 203, 9001])
+@pytest.mark.parametrize("M,d", [(1, 128), (3, 256), (7, 1152), (16, 640), (15, 2048)])
+def test_logits_of_rows_quantised_inside(M, d, V, dtype):
+    """Few whole 16-bit rows give bit for bit the logits of their codes: rows of a wider buffer, the
+    type's largest and smallest numbers, a block of zeros, and a row's NaN and infinity."""
+    x = N.rand(M, d + 24, dtype, M + d, spread=True).cuda()
+    h = x[:, 8:8 + d]
+    h[M - 1, :32] = 0
+    h[M - 1, 32], h[M // 2, 64] = torch.finfo(dtype).max, -torch.finfo(dtype).max
+    h[M // 2, 96:] = torch.finfo(dtype).smallest_normal * 2.0 ** -5
+    head = sd.Mxfp8Weights.from_tensor(N.rand(V, d, torch.bfloat16, 4).cuda() * 2.0 ** -8)  # sums stay finite
+    for bad in (False, True):
+        if bad:
+            h[0, d - 1] = float("nan")
+            h[M // 2, 65] = float("-inf")
+        for out in TYPES:
+            want = sd.sd_mxfp8_logits(sd.sd_mxfp8_quantize(h), head, dtype=out)
+            got = sd.sd_mxfp8_logits(h, head, dtype=out)
+            nan = torch.isnan(want)
+            assert bool(nan.any()) == bad
+            assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
+
+
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M", [1, 20, 50, 100, 200])
 def test_logits_nan_blocks_of_any_codes(M, out):
