@@ -570,8 +570,8 @@ __device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, L
 // arrived the latter have, and behind the barrier those of all waves. Two workgroups a compute
 // unit: one decodes and scales while the other multiplies.
 //
-// 512 rows by 129280 ids at depth 7168: 4 bits with zeros in groups of 128 930 us (1.02 PFLOP/s;
-// 860 us: what the library's bf16 product of that shape takes, with nothing to decode), without zeros
+// 512 rows by 129280 ids at depth 7168: 4 bits with zeros in groups of 128 920 us (1.03 PFLOP/s;
+// 860 us: what torch.matmul takes for bf16 weights of that shape, with nothing to decode), without zeros
 // 850, in groups of 64 1050, of 32 1335. In copies of the kernel for timing, without the scaling
 // of a group's sums 720 us, without the decoding too 670; without the weights' loads 840. Vector
 // and matrix work hardly overlap, in whatever order they are written: the scales cost their own
@@ -712,8 +712,8 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15");
 // the rounding of a 16-bit one (2^-9, 2^-12). They run at twice the 16-bit rate and take codes as they
 // are. Otherwise as k_narrow_tiled: four waves, each 64 ids by 16 TM rows; chunk c of row r of a
 // step's codes lies at place c ^ (r / 2 % 8). NS LDS buffers, WB sets of a step's weights.
-// 2048 rows by 129280 ids at depth 7168 in 256 x 256 tiles: 1640 us (2.3 PFLOP/s; the library's
-// 8-bit product reaches 2.6 on 8192^3). In copies for timing, without the loads 1180 us, without the
+// 2048 rows by 129280 ids at depth 7168 in 256 x 256 tiles: 1640 us (2.3 PFLOP/s; torch's product of
+// e4m3 matrices of 8192^3 reaches 2.6). In copies for timing, without the loads 1180 us, without the
 // LDS reads too 1130 (3.4). More buffers, weights further ahead and eight waves on the tile were all
 // within 3%: what the loads cost is not their latency.
 template <int TM, int NS, int WB>
