@@ -619,6 +619,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
   F st[2];
   auto step = [&](int k, F &now) __attribute__((always_inline)) {
     now.arrived();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     raw_barrier();                     // and every wave has read step k - 1 out of LDS
     issue(k + NS - 1);
     const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE;
