@@ -882,6 +882,11 @@ def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
 _MXFP8 = 3      # hidden rows that are MXFP8 already
 
 
+def _count(t: torch.Tensor) -> int:
+    """Rows of a tensor; 0 of what has none, which its check of shapes then refuses."""
+    return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() > 0 else 0
+
+
 def _output(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev, stream):
     """`t` as a matrix of this shape, or a new one of `dtype`."""
     if t is None:
@@ -1002,7 +1007,7 @@ def sd_mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int,
                         stream=None) -> torch.Tensor:
     """The values that MXFP8 rows stand for, [rows][d] of `dtype` (or into out)."""
     kp = mxfp4_columns(d)
-    rows = codes.shape[0] if isinstance(codes, torch.Tensor) and codes.dim() > 0 else 0
+    rows = _count(codes)
     _need(codes, "codes", torch.uint8, (rows, kp))
     _need(scales, "scales", torch.uint8, (rows, kp // 32))
     _same_device(codes.device, scales=scales)
@@ -1021,7 +1026,7 @@ class Mxfp8Weights(_Handle):
         kp = mxfp4_columns(d)
         _need(codes, "codes", torch.uint8)
         _need(scales, "scales", torch.uint8)
-        V = codes.shape[0]
+        V = _count(codes)
         if d % 32 == 0 and kp != d and tuple(codes.shape) == (V, d):
             _need(scales, "scales", torch.uint8, (V, d // 32))
             with _current(stream, codes.device):
@@ -1064,10 +1069,12 @@ def sd_mxfp8_logits(hidden, lm_head: Mxfp8Weights, logits: Optional[torch.Tensor
         raise TypeError("lm_head must be Mxfp8Weights")
     scales = None
     if isinstance(hidden, (tuple, list)):
+        if len(hidden) != 2:
+            raise ValueError("MXFP8 hidden rows are a pair (codes, scales)")
         hidden, scales = hidden
         kp = mxfp4_columns(lm_head.d)
         _need(hidden, "hidden codes", torch.uint8)
-        M, d = hidden.shape[0], lm_head.d
+        M, d = _count(hidden), lm_head.d
         _need(hidden, "hidden codes", torch.uint8, (M, kp))
         _need(scales, "hidden scales", torch.uint8, (M, kp // 32))
         kind, stride = _MXFP8, kp
@@ -1093,7 +1100,7 @@ def _w4_form(codes, scales, zeros, d) -> int:
     _need(codes, "codes", torch.uint8)
     _need(scales, "scales", scales.dtype if isinstance(scales, torch.Tensor)
           and scales.dtype == torch.float16 else torch.bfloat16)
-    rows = codes.shape[0]
+    rows = _count(codes)
     if scales.dim() != 2 or scales.shape[1] < 1 or d % scales.shape[1] != 0:
         raise ValueError(f"scales must be [rows][d / group], got shape {tuple(scales.shape)}")
     group = d // scales.shape[1]
@@ -1418,12 +1425,9 @@ class VerifyRound:
             u_resample=None, stream=None, conf_stale=None, residual=None):
         if self.norm is not None:
             shape = (self.B, self.gamma + 1, self.d)
-            for name, t in (("hidden", hidden), ("residual", residual)):
-                if t is not None and tuple(t.shape) != shape:
-                    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-            _need(hidden, "hidden", hidden.dtype)
+            _need(hidden, "hidden", getattr(hidden, "dtype", None), shape)
             if residual is not None:
-                _need(residual, "residual", residual.dtype)
+                _need(residual, "residual", getattr(residual, "dtype", None), shape)
                 residual = residual.view(-1, self.d)
             sd_rms_norm(hidden.view(-1, self.d), self.norm.weight, residual, self.norm.eps,
                         self.norm.weight_offset, out=self.hidden.view(-1, self.d), stream=stream)

@@ -167,3 +167,28 @@ def test_verify_round_with_norm_in_a_graph():
         want = plain.run(hidden, head, drafts)
         assert torch.equal(vr.accept_len, want[0]) and torch.equal(vr.next_token, want[1])
         assert int(vr.accept_len[0]) == g
+
+
+def test_refusals_of_device_tensors():
+    """Scalars for matrices, rows in more or fewer parts than two, inputs that are no tensors or have
+    another shape."""
+    scalar = torch.zeros((), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((1, 1), dtype=torch.bfloat16, device="cuda")
+    head = sd.Mxfp8Weights.from_tensor(torch.ones(8, 128, device="cuda"))
+    codes, scales = sd.sd_mxfp8_quantize(torch.ones(2, 128, device="cuda"))
+    for f in (lambda: sd.Mxfp8Weights(scalar, scalar, 128), lambda: sd.sd_mxfp8_dequantize(scalar, scalar, 128),
+              lambda: sd.W4Weights(scalar, scale, None, 64), lambda: sd.sd_w4_dequantize(scalar, scale, None, 64),
+              lambda: sd.sd_mxfp8_logits((scalar, scalar), head), lambda: sd.sd_mxfp8_logits((codes,), head),
+              lambda: sd.sd_mxfp8_logits((codes, scales, scales), head),
+              lambda: sd.sd_mxfp8_logits((codes, scales[:1]), head)):
+        with pytest.raises(ValueError):
+            f()
+    vr = sd.VerifyRound(1, 1, 128, 8, 0.0, False, norm=sd.RmsNorm())
+    x = torch.ones((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    lm, drafts = torch.ones((8, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    for hidden, residual in ((None, None), ([1.0], None), (x, [1.0])):
+        with pytest.raises(TypeError):
+            vr.run(hidden, lm, drafts, residual=residual)
+    for hidden, residual in ((x[:, :1], None), (x, x.view(1, 1, 256))):
+        with pytest.raises(ValueError):
+            vr.run(hidden, lm, drafts, residual=residual)
