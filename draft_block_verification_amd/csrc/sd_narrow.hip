@@ -3,10 +3,10 @@
 //
 // Both run on the 16-bit matrix instructions: an e4m3 value under its block's scale and a code
 // 0 .. 15 are bf16 numbers (the latter fp16 numbers too), products of bf16 or fp16 numbers are
-// exact in fp32, and these instructions add in fp32. The 8-bit instructions do not: they align
-// the products of eight columns and cut them, and sums of 4096 terms come out 1.4e-5 off
-// (relative, normal data) where the 16-bit ones are 9e-8 off. They serve logits of many rows
-// that are rounded to 16 bits, at twice the rate.
+// exact in fp32, and these instructions add in fp32: 4096 terms of normal data come out 9e-8 off
+// (relative). The 8-bit instructions have twice the rate and are not used: they cut the products of
+// eight columns to 13 bits under the largest before they add them, 1.4e-5 on normal data but whole
+// logits where large products cancel (224 and -224 in turn beside products of 0.012).
 //
 // Weights are re-laid once into tiles of 64 rows by 128 columns, each four fragments of 16 rows
 // in the order the matrix instruction takes them: lane l holds row l % 16, q = l / 16, and of the
@@ -575,7 +575,7 @@ __device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, L
 // 850, in groups of 64 1050, of 32 1335. In copies of the kernel for timing, without the scaling
 // of a group's sums 720 us, without the decoding too 670; without the weights' loads 840. Vector
 // and matrix work hardly overlap, in whatever order they are written: the scales cost their own
-// time. MXFP8 with fp32 logits, 2048 rows: 3000 us (1.27 PFLOP/s).
+// time. MXFP8, 2048 rows: 3030 us (1.25 PFLOP/s).
 template <class F, int TM>
 __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt, int n_vt) {
   constexpr int NS = 3, ROWS = 16 * TM, STAGE = ROWS * 256 + F::kSums * 256;
@@ -681,164 +681,6 @@ __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt,
   }
 }
 
-// ---------------------------------------------------------------- many hidden rows, 16-bit logits
-// D += A B^T over 128 columns of e4m3 under block scales, by the 8-bit matrix instruction: lane l
-// holds columns 16 (l / 16) .. + 15 and 64 + 16 (l / 16) .. + 15 of row l % 16 of each operand and,
-// in byte SEL of the A side's word and in byte 0 of the other, the scales of its row at block
-// l / 16. The LM head is A, so a lane's four results are consecutive ids of hidden row l % 16.
-// Accumulators are operand and result at once: left a choice the compiler may give the result the
-// register of a scale, which the instruction reads while it writes. It knows no hazards of inline
-// assembly: two idle states stand before each (a vector write of an operand needs them), and
-// settle() between the last one and the first read of a result.
-// ACC: accumulators in accumulation registers, of which a wave has half of its share.
-template <int SEL, bool ACC>
-__device__ __forceinline__ void mfma8(f32x4 &c, const i32x8 &w, int sw, const i32x8 &h, int sh) {
-#define SD_MFMA8(TO, LO, HI)                                                                       \
-  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" #LO  \
-               ",0,0] op_sel_hi:[" #HI ",0,0]"                                                     \
-               : TO(c) : "v"(w), "v"(h), "v"(sw), "v"(sh) : "memory")
-#define SD_MFMA8_IN(LO, HI) do { if constexpr (ACC) SD_MFMA8("+a", LO, HI); else SD_MFMA8("+v", LO, HI); } while (0)
-  if constexpr (SEL == 0) SD_MFMA8_IN(0, 0);
-  else if constexpr (SEL == 1) SD_MFMA8_IN(1, 0);
-  else if constexpr (SEL == 2) SD_MFMA8_IN(0, 1);
-  else SD_MFMA8_IN(1, 1);
-#undef SD_MFMA8_IN
-#undef SD_MFMA8
-}
-
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15"); }
-
-// The 8-bit instructions cut the products of eight columns to 13 bits under the largest before
-// they add them, which leaves normal data 1.4e-5 off: too much for an fp32 logit, nothing beside
-// the rounding of a 16-bit one (2^-9, 2^-12). They run at twice the 16-bit rate and take codes as they
-// are. Otherwise as k_narrow_tiled: four waves, each 64 ids by 16 TM rows; chunk c of row r of a
-// step's codes lies at place c ^ (r / 2 % 8). NS LDS buffers, WB sets of a step's weights.
-// 2048 rows by 129280 ids at depth 7168 in 256 x 256 tiles: 1640 us (2.3 PFLOP/s; torch's product of
-// e4m3 matrices of 8192^3 reaches 2.6). In copies for timing, without the loads 1180 us, without the
-// LDS reads too 1130 (3.4). More buffers, weights further ahead and eight waves on the tile were all
-// within 3%: what the loads cost is not their latency.
-template <int TM, int NS, int WB>
-__global__ __launch_bounds__(256, TM > 8 ? 1 : 2) void k_mx8_tiled(NarrowArgs a, int n_mt, int n_vt) {
-  static_assert(WB <= NS, "a step's weights are issued behind its hidden rows");
-  constexpr int ROWS = 16 * TM, STAGE = ROWS * 132, LOADS = TM / 2;
-  __shared__ __attribute__((aligned(16))) uint8_t S[NS * STAGE];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int q = lane >> 4, r = lane & 15;
-  const int nb = n_mt * n_vt, hb = blockIdx.x;
-  const int per = nb / 8, rem = nb % 8, xcd = hb % 8, pos = hb / 8;
-  const int logical = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + pos;
-  const int mt = logical % n_mt, vt = logical / n_mt;
-  const int64_t row0 = (int64_t)mt * ROWS, left = a.M - 1 - row0;
-  const int64_t tile0 = min((int64_t)vt * 4 + wave, (int64_t)(a.V - 1) / 64) * a.steps;
-  const uint8_t *codes = reinterpret_cast<const uint8_t *>(a.hidden) + row0 * a.hstride;
-  const uint8_t *scales = a.hscales + row0 * (a.hstride / 32);
-  int src[LOADS];
-#pragma unroll
-  for (int n = 0; n < LOADS; ++n) {
-    const int at = 8 * (wave * LOADS + n) + (lane >> 3);     // row of the tile
-    src[n] = (int)(min((int64_t)at, left) * a.hstride) + ((lane & 7) ^ (at >> 1 & 7)) * 16;
-  }
-  const int block = wave % (ROWS / 64);                      // 64 rows' scales a load
-  const int scale_src = (int)(min((int64_t)64 * block + lane, left) * (a.hstride / 32));
-  auto issue = [&](int k) __attribute__((always_inline)) {
-    LDSP uint8_t *dst = (LDSP uint8_t *)S + (k % NS) * STAGE;
-    const int kk = min(k, a.steps - 1);
-#pragma unroll
-    for (int n = 0; n < LOADS; ++n) to_lds16(codes, src[n], kk * 128, dst + (wave * LOADS + n) * 1024);
-    to_lds4(scales, scale_src, kk * 4, dst + ROWS * 128 + block * 256);
-    asm volatile("" ::: "memory");
-  };
-  struct Weights {
-    i32x8 w[4];
-    int s;
-  } st[WB];
-  auto load = [&](int k, Weights &to) __attribute__((always_inline)) {
-    const int64_t tile = tile0 + min(k, a.steps - 1);
-    const u32x4 *c = reinterpret_cast<const u32x4 *>(a.codes + tile * kMx8Tile) + lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 x = c[128 * i], y = c[128 * i + 64];
-      to.w[i] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-    }
-    to.s = reinterpret_cast<const int *>(a.scales + tile * kMx8Scales)[lane];
-    asm volatile("" ::: "memory");
-  };
-  f32x4 acc[4][TM];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int m = 0; m < TM; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // Fragment m of step k into one of four register sets.
-  i32x8 h[4];
-  int s[4];
-  auto fetch = [&](int k, int m) __attribute__((always_inline)) {
-    const LDSP uint8_t *b = (const LDSP uint8_t *)S + (k % NS) * STAGE;
-    const LDSP uint8_t *p = b + (16 * m + r) * 128;
-    const u32x4 x = *(const LDSP u32x4 *)(p + (q ^ (r >> 1)) * 16), y = *(const LDSP u32x4 *)(p + ((4 + q) ^ (r >> 1)) * 16);
-    h[m % 4] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-    s[m % 4] = b[ROWS * 128 + (16 * m + r) * 4 + q];
-  };
-  // Behind this step k's weights have arrived, and so have its hidden rows, for every wave; and
-  // every wave has step k - 1 out of LDS, so its buffer takes step k + NS - 1.
-  auto enter = [&](int k, Weights &now) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(now.w[i]));
-    asm volatile("" : "+v"(now.s));
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    raw_barrier();
-    issue(k + NS - 1);
-  };
-  // Step k: its first two fragments are on their way; the next step is entered before the last two
-  // are used, so that its first ones come meanwhile.
-  auto step = [&](int k, Weights &now, Weights &next) __attribute__((always_inline)) {
-    each<TM>([&](auto m) __attribute__((always_inline)) {
-      if constexpr (m == TM - 2) enter(k + 1, next);
-      if constexpr (m < TM - 2) fetch(k, m + 2);
-      else fetch(k + 1, m + 2 - TM);
-      each<4>([&](auto i) __attribute__((always_inline)) { mfma8<i, (TM > 4)>(acc[i][m], now.w[i], now.s, h[m % 4], s[m % 4]); });
-    });
-    load(k + WB, now);
-  };
-#pragma unroll
-  for (int k = 0; k < NS - 1; ++k) {
-    issue(k);
-    if (k < WB) load(k, st[k]);
-  }
-  enter(0, st[0]);
-  if constexpr (WB == NS) load(WB - 1, st[WB - 1]);
-  fetch(0, 0);
-  fetch(0, 1);
-  int k = 0;
-  for (; k + WB <= a.steps; k += WB)
-    each<WB>([&](auto x) __attribute__((always_inline)) { step(k + x, st[x], st[(x + 1) % WB]); });
-  each<WB - 1>([&](auto x) __attribute__((always_inline)) {
-    if (k + x < a.steps) step(k + x, st[x], st[x + 1]);
-  });
-  settle();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int m = 0; m < TM; ++m) {     // read behind it, not before
-      if constexpr (TM > 4) asm volatile("" : "+a"(acc[i][m]));
-      else asm volatile("" : "+v"(acc[i][m]));
-    }
-  wait_loads<0>();                     // the trailing loads land before LDS is used again
-  raw_barrier();
-  const int v0 = vt * 256 + wave * 64;
-  constexpr int PART = NS * STAGE / 4 / 16 * 16, ROW = 64 * 2 + 16, HALF = TM / 2;
-  static_assert(ROW * HALF * 16 <= PART, "half the rows in 16 bits");
-  LDSP uint8_t *part = (LDSP uint8_t *)S + wave * PART;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll
-    for (int m = 0; m < HALF; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *(LDSP u32x2 *)(part + (16 * m + r) * ROW + (16 * i + 4 * q) * 2) = pack4(acc[i][half * HALF + m], a.type);
-    store_rows<uint16_t, 64, ROW>(a, part, row0 + half * HALF * 16, HALF * 16, v0, lane);
-  }
-}
-
 // ---------------------------------------------------------------- hidden rows made ready
 // Whole 128-column steps of 16-bit rows, zeros behind column d (out null: not stored), and each
 // group's sum of a row times `factor` (sums null: not formed): [ceil(rows / tile)][kp / G][tile],
@@ -932,18 +774,16 @@ hipError_t launch_tiled(const NarrowArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int TM, int NS, int WB>
-hipError_t launch_mx8_tiled(const NarrowArgs &a, hipStream_t stream) {
-  const int n_mt = (a.M + 16 * TM - 1) / (16 * TM), n_vt = (a.V + 255) / 256;
-  hipLaunchKernelGGL((k_mx8_tiled<TM, NS, WB>), dim3((unsigned)((int64_t)n_mt * n_vt)), dim3(256), 0, stream, a, n_mt, n_vt);
-  return hipGetLastError();
-}
-
-// Rows of a tile of k_narrow_tiled, as for launch_mx8_logits. 4 bits, G = 128, us, 32 / 64 rows a tile, V x
-// depth, M:
+// Rows of a tile of k_narrow_tiled by what the workgroups that a compute unit gets cost, in pairs of
+// 64-row ones. us, 32 / 64 rows a tile, V x depth, M:
+//   4 bits, G = 128
 //   129280 x 7168:  64: 160 / 138    128: 292 / 254    512: 1068 / 908
 //    32000 x 4096:  64: 31 / 43      128: 48 / 45      256: 81 / 72     512: 153 / 133
 //     8000 x 2048:  64: 21 / 29      256: 22 / 30      512: 32 / 32
+//   MXFP8, bf16 logits
+//   129280 x 7168:  64: 224 / 173    128: 323 / 258    512: 985 / 788   2048: 3685 / 3027
+//    32000 x 4096:  64: 31 / 37      128: 47 / 40      256: 79 / 64     512: 143 / 118
+//     8000 x 2048:  64: 16.5 / 19.8  256: 19.5 / 21.1  512: 27 / 24     1024: 46 / 38
 int tile_rows(const NarrowArgs &a) { return paired(a, 32, 0.92, 0.70) < paired(a, 64, 1.27, 1.0) ? 32 : 64; }
 
 template <int H, int NG, bool ASYM, bool SF16>
@@ -1031,9 +871,9 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
   NarrowArgs a{hidden, hidden_scales, kp, head, head + tiles_of(V, d) * kMx8Tile, nullptr, false, M, V, kp / 128,
                logits, type, ld, vec_rows(logits, type, ld, 4), vec_rows(logits, type, ld, type == SD_F32 ? 4 : 8),
                nullptr};
-  const bool coded = hidden_type == SD_MXFP8, few = few_rows(M, V), wide = !few && type == SD_F32;
+  const bool coded = hidden_type == SD_MXFP8;
   hipError_t e = hipSuccess;
-  if (!wide) {
+  if (few_rows(M, V)) {
     // Whole 16-bit rows of one tile are quantised by each workgroup, not by a launch before: measured
     // (us, each workgroup / a launch before, 1 and 16 rows) 1000 x 1024: 4.2 / 5.3, 4.5 / 6.1;
     // 8000 x 2048: 6.6 / 8.0, 7.7 / 9.1; 32768 x 2048: 13.8 / 14.4, 15.4 / 16.2; but 129280 x 7168:
@@ -1050,19 +890,7 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
       a.hscales = scales;
     }
     if (e != hipSuccess) return e;
-    if (few) return launch_skinny<Mx8, 4, 4, 2>(a, stream);
-    // Rows of a tile by what the workgroups that a compute unit gets cost, in those of 256 rows, of
-    // which it holds one; of 128 and 64 rows it holds two, one of them alone costs more. Measured (us,
-    // 64 / 128 / 256 rows a tile), V x depth, M:
-    //   129280 x 7168:   64: 164 / 168 / 218    128: 217 / 180 / 237    256: 349 / 280 / 281
-    //                   320: 421 / 365 / 477    512: 615 / 481 / 449   1024: 1155 / 890 / 826
-    //    32000 x 4096:   64: 31 / 41 / 52       128: 31 / 43 / 55       256: 46 / 44 / 60
-    //                   512: 82 / 69 / 64
-    //     8000 x 2048:  256: 12 / 19 / 30       512: 14 / 19 / 31      1024: 23 / 21 / 31
-    const double cost[3] = {paired(a, 64, 0.50, 0.33), paired(a, 128, 0.70, 0.53), paired(a, 256, 1.0, 1.0)};
-    if (cost[2] <= cost[0] && cost[2] <= cost[1]) return launch_mx8_tiled<16, 3, 3>(a, stream);
-    if (cost[1] <= cost[0]) return launch_mx8_tiled<8, 3, 2>(a, stream);
-    return launch_mx8_tiled<4, 4, 3>(a, stream);
+    return launch_skinny<Mx8, 4, 4, 2>(a, stream);
   }
   uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
   const dim3 grid = item_groups((int64_t)M * (kp / 8));

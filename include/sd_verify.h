@@ -654,12 +654,9 @@ SD_API int32_t sd_mxfp8_head(const uint8_t *codes, const uint8_t *scales, int32_
  *   logits   [M][V] of type logits_type, row stride logits_stride elements (>= V): out
  *   workspace  sd_mxfp8_logits_workspace_bytes(M, d) bytes; its header is left alone and need not
  *            have been prepared
- * logits[m][v] = the sum of the products of the values. fp32 logits, and any of up to 16 rows: every
- * product exact, accumulated in fp32, rounded once to logits_type. 16-bit logits of more rows may
- * come from the 8-bit matrix instructions, which cut the products of eight consecutive columns (8 i
- * .. 8 i + 7) to 13 bits under the power of two in the largest before they add them in fp32: on normal data
- * 1.4e-5 of the logits' size, beside 2^-9 or 2^-12 for their rounding. Values are formed in bf16
- * (exact but outside its range: scale bytes over 246, or products of scales that leave fp32's).
+ * logits[m][v] = the sum of the products of the values: every product exact, accumulated in fp32,
+ * rounded once to logits_type, for any number of rows. Values are formed in bf16 (exact for scale
+ * bytes 3 .. 246; smaller ones give values under bf16's smallest number, larger ones over its largest).
  * A row of hidden with a NaN or an infinity gives NaN.
  * Errors: as for sd_mxfp4_logits; SD_EINVAL also for hidden_scales that do not go with hidden_type.
  */
