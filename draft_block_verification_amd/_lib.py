@@ -680,13 +680,14 @@ def sd_verify_rejection(hidden: torch.Tensor, lm_head, draft_tokens: torch.Tenso
 # --------------------------------------------------------------- MXFP4 and sampling
 
 _F32_MAX = torch.finfo(torch.float32).max
+_I32_MAX = 2 ** 31 - 1      # sizes go to the library in 32 bits: a larger one would arrive as another
 _TYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 def _rows(t: torch.Tensor, name: str, dtype=None) -> None:
     """A device matrix of an element type the library takes, with contiguous rows."""
     if (isinstance(t, torch.Tensor) and t.dtype in _TYPE_CODES and dtype in (None, t.dtype)
-            and t.is_cuda and t.dim() == 2 and t.is_contiguous() and t.numel() > 0):
+            and t.is_cuda and t.dim() == 2 and t.is_contiguous() and 0 < t.numel() <= _I32_MAX):
         return                      # the common case, in half the time
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -696,6 +697,8 @@ def _rows(t: torch.Tensor, name: str, dtype=None) -> None:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    if max(t.shape) > _I32_MAX:
+        raise ValueError(f"{name} has more than {_I32_MAX} rows or columns: {tuple(t.shape)}")
     if t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1:
         raise ValueError(f"{name} must have contiguous, separate rows, got strides {t.stride()}")
 
@@ -750,22 +753,27 @@ def _workspace(nbytes: int, dev: torch.device, stream) -> torch.Tensor:
 
 def mxfp4_columns(d: int) -> int:
     """Stored columns of an MXFP4 or MXFP8 row: d rounded up to a multiple of 128."""
-    kp = int(_lib.sd_mxfp4_columns(d))
+    kp = int(_lib.sd_mxfp4_columns(d)) if 0 < d <= _I32_MAX else 0
     if kp == 0:
         raise ValueError(f"MXFP4 and MXFP8 rows need a positive multiple of 8 columns, got {d}")
     return kp
 
 
+def _size(name: str, *sizes: int) -> int:
+    """A size from the library, which gives 0 for arguments out of its range."""
+    return int(getattr(_lib, name)(*sizes)) if max(sizes) <= _I32_MAX and min(sizes) >= 0 else 0
+
+
 def mxfp4_logits_workspace_bytes(rows: int, d: int) -> int:
-    return int(_lib.sd_mxfp4_logits_workspace_bytes(rows, d))
+    return _size("sd_mxfp4_logits_workspace_bytes", rows, d)
 
 
 def sample_workspace_bytes(rows: int, V: int) -> int:
-    return int(_lib.sd_sample_workspace_bytes(rows, V))
+    return _size("sd_sample_workspace_bytes", rows, V)
 
 
 def accept_filtered_workspace_bytes(B: int, gamma: int, V: int) -> int:
-    return int(_lib.sd_accept_filtered_workspace_bytes(B, gamma, V))
+    return _size("sd_accept_filtered_workspace_bytes", B, gamma, V)
 
 
 def sd_mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
@@ -832,7 +840,7 @@ class Mxfp4Weights(_Handle):
         _need(codes, "codes", torch.uint8, (V, kp // 2))
         _need(scales, "scales", torch.uint8, (V, kp // 32))
         _same_device(codes.device, scales=scales)
-        nbytes = int(_lib.sd_mxfp4_head_bytes(V, d))
+        nbytes = _size("sd_mxfp4_head_bytes", V, d)
         if nbytes == 0:
             raise ValueError(f"no MXFP4 LM head of [{V}][{d}]")
         self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
@@ -1035,7 +1043,7 @@ class Mxfp8Weights(_Handle):
         _need(codes, "codes", torch.uint8, (V, kp))
         _need(scales, "scales", torch.uint8, (V, kp // 32))
         _same_device(codes.device, scales=scales)
-        nbytes = int(_lib.sd_mxfp8_head_bytes(V, d))
+        nbytes = _size("sd_mxfp8_head_bytes", V, d)
         if nbytes == 0:
             raise ValueError(f"no MXFP8 LM head of [{V}][{d}]")
         self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
@@ -1052,11 +1060,11 @@ class Mxfp8Weights(_Handle):
 
 
 def mxfp8_logits_workspace_bytes(rows: int, d: int) -> int:
-    return int(_lib.sd_mxfp8_logits_workspace_bytes(rows, d))
+    return _size("sd_mxfp8_logits_workspace_bytes", rows, d)
 
 
 def w4_logits_workspace_bytes(rows: int, d: int, group: int) -> int:
-    return int(_lib.sd_w4_logits_workspace_bytes(rows, d, group))
+    return _size("sd_w4_logits_workspace_bytes", rows, d, group)
 
 
 def sd_mxfp8_logits(hidden, lm_head: Mxfp8Weights, logits: Optional[torch.Tensor] = None,
@@ -1110,6 +1118,8 @@ def _w4_form(codes, scales, zeros, d) -> int:
     _need(scales, "scales", scales.dtype, (rows, d // group))
     if zeros is not None:
         _need(zeros, "zeros", torch.uint8, (rows, d // group))
+    if rows > _I32_MAX or d > _I32_MAX:
+        raise ValueError(f"more than {_I32_MAX} rows or columns: {rows}, {d}")
     _same_device(codes.device, scales=scales, zeros=zeros)
     return group
 
@@ -1165,7 +1175,7 @@ class W4Weights(_Handle):
                  d: int, stream=None):
         group = _w4_form(codes, scales, zeros, d)
         V = codes.shape[0]
-        nbytes = int(_lib.sd_w4_head_bytes(V, d, group, int(zeros is not None)))
+        nbytes = _size("sd_w4_head_bytes", V, d, group, int(zeros is not None))
         if nbytes == 0:
             raise ValueError(f"no 4-bit LM head of [{V}][{d}] in groups of {group}")
         self.V, self.d, self.shape, self.device = int(V), int(d), (int(V), int(d)), codes.device
