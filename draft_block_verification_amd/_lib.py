@@ -174,6 +174,18 @@ def new_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     return ws
 
 
+def _space(workspace: torch.Tensor):
+    """Address and size of a caller's workspace: one block on a device (an expanded tensor counts
+    bytes that it does not have)."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not workspace.is_cuda:
+        raise ValueError("workspace must be a device tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel()
+
+
 def device_flags(workspace: torch.Tensor, clear: bool = True, stream=None) -> int:
     out = ctypes.c_uint32(0)
     _check("sd_device_flags", _lib.sd_device_flags(_ptr(workspace), _stream(stream),
@@ -428,8 +440,7 @@ def sd_verify_logits(hidden: torch.Tensor, lm_head: torch.Tensor,
     name = "sd_verify_logits" + fmt
     _check(name, getattr(_lib, name)(_ptr(hidden), head, _ptr(draft_tokens), _ptr(verify_len),
                                      _ptr(row_offsets), B, g, d, V, float(temperature),
-                                     _ptr(logits), _ptr(stats), _ptr(workspace),
-                                     workspace.numel(), _stream(stream)))
+                                     _ptr(logits), _ptr(stats), *_space(workspace), _stream(stream)))
     return logits, stats
 
 
@@ -451,7 +462,7 @@ def sd_verify_contraction(hidden: torch.Tensor, lm_head: torch.Tensor,
     name = "sd_verify_contraction" + fmt
     _check(name, getattr(_lib, name)(_ptr(hidden), head, _ptr(verify_len), _ptr(row_offsets), B,
                                      g1 - 1, d, V, float(temperature), _ptr(logits),
-                                     _ptr(workspace), workspace.numel(), _stream(stream)))
+                                     *_space(workspace), _stream(stream)))
     return logits
 
 
@@ -489,8 +500,7 @@ def sd_verify_greedy(hidden: torch.Tensor, lm_head: torch.Tensor, draft_tokens: 
     name = "sd_verify_greedy" + fmt
     _check(name, getattr(_lib, name)(_ptr(hidden), head, _ptr(draft_tokens), _ptr(verify_len),
                                      _ptr(row_offsets), B, g, d, V, _ptr(stats), _ptr(accept_len),
-                                     _ptr(next_token), _ptr(counters), _ptr(workspace),
-                                     workspace.numel(), _stream(stream)))
+                                     _ptr(next_token), _ptr(counters), *_space(workspace), _stream(stream)))
     return stats, accept_len, next_token
 
 
@@ -616,7 +626,7 @@ def _accept_rejection(name, logits, stats, draft_logits, draft_tokens, verify_le
     if name == "sd_accept_rejection_ex":
         _need(accept_rate, "accept_rate", torch.float64, (B, g))
         args.append(_ptr(accept_rate))
-    args += [_ptr(workspace), workspace.numel(), _stream(stream)]
+    args += [*_space(workspace), _stream(stream)]
     _check(name, getattr(_lib, name)(*args))
     return accept_len, next_token, accept_rate
 
@@ -710,8 +720,9 @@ def _row_stride(t: torch.Tensor) -> int:
 
 def _same_device(dev: torch.device, **tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and t.device != dev and t.device is not None:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        device = getattr(t, "device", None)
+        if device != dev and device is not None:
+            raise ValueError(f"{name} is on {device}, expected {dev}")
 
 
 def _call(name: str, dev: torch.device, stream, *args) -> None:
@@ -881,7 +892,7 @@ def sd_mxfp4_logits(hidden: torch.Tensor, lm_head: Mxfp4Weights,
     _same_device(dev, lm_head=lm_head, logits=logits, workspace=workspace)
     _call("sd_mxfp4_logits", dev, stream, _ptr(hidden), _TYPE_CODES[hidden.dtype], M, d,
           _row_stride(hidden), _ptr(lm_head.buf), lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
-          _row_stride(logits), _ptr(workspace), workspace.numel())
+          _row_stride(logits), *_space(workspace))
     return logits
 
 
@@ -1099,7 +1110,7 @@ def sd_mxfp8_logits(hidden, lm_head: Mxfp8Weights, logits: Optional[torch.Tensor
     _same_device(dev, lm_head=lm_head, scales=scales, workspace=workspace)
     _call("sd_mxfp8_logits", dev, stream, _ptr(hidden), kind, _ptr(scales), M, d, stride,
           _ptr(lm_head.buf), lm_head.V, _ptr(logits), _TYPE_CODES[logits.dtype],
-          _row_stride(logits), _ptr(workspace), workspace.numel())
+          _row_stride(logits), *_space(workspace))
     return logits
 
 
@@ -1216,7 +1227,7 @@ def sd_w4_logits(hidden: torch.Tensor, lm_head: W4Weights, logits: Optional[torc
     _call("sd_w4_logits", dev, stream, _ptr(hidden), _TYPE_CODES[hidden.dtype], M, d,
           _row_stride(hidden), _ptr(lm_head.buf), lm_head.V, lm_head.group,
           _TYPE_CODES[lm_head.scale_dtype], int(lm_head.has_zeros), _ptr(logits),
-          _TYPE_CODES[logits.dtype], _row_stride(logits), _ptr(workspace), workspace.numel())
+          _TYPE_CODES[logits.dtype], _row_stride(logits), *_space(workspace))
     return logits
 
 
@@ -1323,7 +1334,7 @@ def sd_sample(logits: torch.Tensor, u: torch.Tensor, params: SamplingParams,
                  workspace=workspace)
     _call("sd_sample", dev, stream, _ptr(logits), _TYPE_CODES[logits.dtype], _row_stride(logits), R,
           V, _ptr(u), params._ref, R // params.n, _ptr(tokens), max(1, tokens.stride(0)),
-          _ptr(kept), _ptr(logprob), _ptr(workspace), workspace.numel())
+          _ptr(kept), _ptr(logprob), *_space(workspace))
     return tokens, kept, logprob
 
 
@@ -1368,8 +1379,7 @@ def sd_accept_filtered(logits: torch.Tensor, draft_logits: torch.Tensor,
                  workspace=workspace)
     _call("sd_accept_filtered", dev, stream, _ptr(logits), _ptr(draft_logits), _ptr(draft_tokens),
           _ptr(verify_len), _ptr(row_offsets), _ptr(u_accept), _ptr(u_resample), params._ref, B, g,
-          V, _ptr(accept_len), _ptr(next_token), _ptr(counters), _ptr(workspace),
-          workspace.numel())
+          V, _ptr(accept_len), _ptr(next_token), _ptr(counters), *_space(workspace))
     return accept_len, next_token
 
 
