@@ -88,3 +88,46 @@ def test_size_of_the_error(M):
     slack = 6 * (d / 3) ** 0.5 * 2.0 ** -24 * float(want.square().mean().sqrt())
     half = want.abs() * torch.finfo(torch.float16).eps / 2 + 2.0 ** -25
     assert bool(((got.double() - want).abs() <= half + slack).all())
+
+
+@pytest.mark.parametrize("M", [16, 247])
+@pytest.mark.parametrize("swap", [False, True])
+def test_every_code_under_every_scale(M, swap):
+    """Logits of one product each: every e4m3 code under scale bytes 3 .. 246, whose values are bf16
+    numbers, subnormal ones among them, times 2^60 (below byte 127) or 2^-60, exact in fp32; as LM head
+    and as hidden rows."""
+    B = 247
+    d = 32 * B
+    kp = N.padded(d)
+    codes, scales = np.zeros((256, kp), np.uint8), np.zeros((256, kp // 32), np.uint8)
+    codes[:, :d:32] = np.arange(256)[:, None]
+    codes[127] = codes[255] = 0                          # NaN codes would fill every logit of their id
+    scales[:, :B] = np.arange(B)[None]
+    value = N.mx8_values(codes, scales, d)[:, ::32]      # [code][byte]
+    ones, by = np.zeros((B, kp), np.uint8), np.zeros((B, kp // 32), np.uint8)
+    power = np.where(np.arange(B) < 127, 60, -60)
+    ones[np.arange(B), 32 * np.arange(B)] = 0x38         # 1.0, in a block of its own for each byte
+    by[np.arange(B), np.arange(B)] = 127 + power
+    dev = lambda a: torch.from_numpy(a).cuda()
+    head = sd.Mxfp8Weights(dev(ones), dev(by), d) if swap else sd.Mxfp8Weights(dev(codes), dev(scales), d)
+    h, s = (codes, scales) if swap else (ones, by)
+    got = torch.cat([sd.sd_mxfp8_logits((dev(h[i:i + M].copy()), dev(s[i:i + M].copy())), head) for i in range(0, len(h), M)])
+    want = value * 2.0 ** power
+    want = want if swap else want.T
+    got = got.cpu().double().numpy()
+    keep = np.arange(B) >= 3
+    assert np.array_equal(got[:, keep], want[:, keep]) if swap else np.array_equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("M", [3, 100])
+@pytest.mark.parametrize("dtype,tiny", [(torch.float16, 2.0 ** -24), (torch.bfloat16, 2.0 ** -130)])
+def test_subnormal_hidden_rows_under_4_bits(M, dtype, tiny):
+    """Hidden values under the type's smallest normal number count in full."""
+    h = torch.zeros((M, 128), dtype=dtype)
+    h[:, 0], h[:, 5] = tiny, 3 * tiny
+    w = torch.zeros((64, 128))
+    w[:, 0], w[:, 5], w[:, 9] = torch.arange(64) % 15 - 7.0, 7.0 - torch.arange(64) % 15, 7.0
+    codes, scales, _ = sd.sd_w4_quantize(w.cuda(), 128, True)
+    v = sd.sd_w4_dequantize(codes, scales, None, 128).cpu().double()
+    got = sd.sd_w4_logits(h.cuda(), sd.W4Weights(codes, scales, None, 128)).cpu().double()
+    assert torch.equal(got, h.double() @ v.t())
