@@ -17,8 +17,8 @@ struct Mx8Args {
 };
 
 // An item is eight columns, four neighbouring threads hold a block. A thread takes U items 256
-// apart, its loads issued together. Bound by memory: 129280 x 7168 bf16 in 500 us (2.81 GB, 5.6 TB/s),
-// back in 445 us (6.3 TB/s).
+// apart, its loads issued together. Bound by memory: 129280 x 7168 bf16 in 513 us (2.81 GB, 5.5 TB/s),
+// back in 450 us (6.2 TB/s).
 template <int T, int U>
 __global__ __launch_bounds__(256) void k_mx8_quantize(Mx8Args a) {
   const int per = a.kp / 8;       // a multiple of 16: a block's items are all in or all out

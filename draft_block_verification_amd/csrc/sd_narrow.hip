@@ -33,6 +33,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kMx8Tile = 8192, kMx8Scales = 256, kW4Tile = 4096;
 
 // ---------------------------------------------------------------- LM heads, re-laid
+// 129280 x 7168: 560 us (1.9 GB, 3.4 TB/s), once per model load.
 __global__ __launch_bounds__(256) void k_mx8_head(const uint8_t *codes, const uint8_t *scales, int V, int kp,
                                                   uint8_t *out, uint8_t *out_scales) {
   const int steps = kp / 128, lane = threadIdx.x & 63, frag = threadIdx.x >> 6;
@@ -62,6 +63,7 @@ __device__ __forceinline__ uint32_t interleave(uint32_t w) {
   return r;
 }
 
+// 129280 x 7168 with zeros in groups of 128: 390 us (1.0 GB, 2.5 TB/s), once per model load.
 __global__ __launch_bounds__(256) void k_w4_head(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
                                                  int V, int d, int group, int steps, uint8_t *out,
                                                  uint16_t *out_scales, uint8_t *out_zeros) {
@@ -369,10 +371,12 @@ struct W4 {
 // per 16 TV ids; its NW waves take the 128-column steps in turn, straight into registers: each
 // weight is used by one wave only, so LDS would add a copy and share nothing. The hidden rows are
 // read by every workgroup and come from L2. The waves' partial sums meet in LDS in wave order.
-// 129280 x 7168, us: MXFP8 under 1 row 141 (6.8 TB/s), 16 rows 147; 4 bits in groups of 128 under 1
-// row 76 (6.4 TB/s), 16 rows 80; in groups of 64 with zeros under 16 rows 88, of 32 108, without zeros 96:
+// 129280 x 7168, us: MXFP8 under 1 row 142 (6.7 TB/s), 16 rows 149; 4 bits with zeros in groups of 128
+// under 1 row 80 (6.0 TB/s), 16 rows 82; in groups of 64 under 16 rows 90, of 32 107, without zeros 90:
 // scales and sums come back at every 32 columns, and the vector units bound it. Held to 128 registers,
-// so that two workgroups of eight waves fit a compute unit, these two take 115 and 144 us (spills).
+// so that two workgroups of eight waves fit a compute unit, the last two took 115 and 144 us when they
+// took 108 and 96 (spills). fp16 scales cost the same, but for 32 rows under zeros in groups of 64: that
+// form spills 5 registers and takes 26 us at 32000 x 4096, with bf16 scales 20.
 template <class F, int TV, int MT, int NW, int D>
 __global__ __launch_bounds__(64 * NW, 2) void k_narrow_skinny(NarrowArgs a) {
   constexpr int IDS = 16 * TV, LDR = IDS + 4;
@@ -572,10 +576,11 @@ __device__ __forceinline__ void to_lds4(const void *base, int lane_at, int at, L
 //
 // 512 rows by 129280 ids at depth 7168: 4 bits with zeros in groups of 128 920 us (1.03 PFLOP/s;
 // 860 us: what torch.matmul takes for bf16 weights of that shape, with nothing to decode), without zeros
-// 850, in groups of 64 1050, of 32 1335. In copies of the kernel for timing, without the scaling
-// of a group's sums 720 us, without the decoding too 670; without the weights' loads 840. Vector
+// 835 - 850, in groups of 64 1050, of 32 1335 - 1350. In copies of the kernel for timing, without the
+// scaling of a group's sums 720 us, without the decoding too 670; without the weights' loads 840. Vector
 // and matrix work hardly overlap, in whatever order they are written: the scales cost their own
-// time. MXFP8, 2048 rows: 3030 us (1.25 PFLOP/s).
+// time. fp16 scales are within 3% of these, which are of bf16, but for zeros in groups of 64: that form
+// spills 35 registers and takes 1600 us. MXFP8, 2048 rows: 3030 us (1.25 PFLOP/s).
 template <class F, int TM>
 __global__ __launch_bounds__(256, 2) void k_narrow_tiled(NarrowArgs a, int n_mt, int n_vt) {
   constexpr int NS = 3, ROWS = 16 * TM, STAGE = ROWS * 256 + F::kSums * 256;
@@ -741,10 +746,13 @@ dim3 item_groups(int64_t items) {
 }
 
 // Rows that the streaming kernel takes: 16, and 32 of an LM head that gives the tiled kernels less
-// than a workgroup of 256 ids for each compute unit. us, streaming / tiled of 32 rows, M = 32:
-//   4 bits, G = 128:   129280 x 7168: 115 / 94    32000 x 4096: 18 / 30    8000 x 2048: 12.5 / 20.5
-//   4 bits, G = 32:    151936 x 4096:  95 / 92
-//   MXFP8, fp32:       129280 x 7168: 197 / 170   32000 x 4096: 30 / 31    8000 x 2048: 9.9 / 15.7
+// than a workgroup of 256 ids for each compute unit. us, streaming / tiled of 32 rows, M = 32, at two
+// depths each (with zeros; what a call's host side takes, some 8 us, is in the smallest):
+//                      129280 x 7168, 2048          32000 x 7168, 2048         8000 x 7168, 2048
+//   4 bits, G = 128:   130 / 115, 45 / 35           28 / 47, 11.6 / 18.4       19 / 45, 8.3 / 16.6
+//   4 bits, G = 32:    156 / 146, 57 / 45           39 / 76, 15.0 / 25.6       21 / 75, 9.2 / 25.4
+//   MXFP8, bf16:       179 / 164, 63 / 53           45 / 56, 17.6 / 16.2       21 / 40, 8.8 / 15.1
+//   MXFP8, fp32:       195 / 168, 70 / 55           45 / 57, 17.9 / 16.4       21 / 40, 8.8 / 15.2
 constexpr int kFewRows = 16;
 bool few_rows(int M, int V) { return M <= kFewRows || (M <= 2 * kFewRows && V <= 256 * 256); }
 
@@ -794,8 +802,10 @@ hipError_t launch_w4_form(const NarrowArgs &a, hipStream_t stream) {
   }
   // 128 ids a workgroup share the hidden rows' loads; an LM head that gives few workgroups then is dealt
   // in 64s. G = 128, us, ids x waves x steps ahead 128 x 8 x 1 / 128 x 4 x 2 / 64 x 4 x 2, V x depth, M:
-  //   129280 x 7168:  1: 77 / 80 / 76         16: 83 / 89 / 101
+  //   129280 x 7168:  1: 81 / 81 / 80         16: 82 / 87 / 101
+  //    32768 x 7168:  1: 21.3 / 21.8 / 20.9   16: 22.1 / 22.6 / 27.1  32: 28.6 / 29.0 / 40.9
   //    32768 x 2048:  1: 8.1 / 8.7 / 8.3      16: 8.8 / 9.1 / 10.5    32: 11.7 / 12.2 / 16.1
+  //     8000 x 7168:  1: 16.4 / 16.2 / 10.1   16: 17.3 / 17.7 / 12.6  32: 23.6 / 24.2 / 19.2
   //     8000 x 2048:  1: 7.1 / 6.9 / 4.9      16: 7.5 / 7.9 / 5.9     32: 10.3 / 10.8 / 8.6
   using F = W4<H, NG, ASYM, SF16>;
   return a.V <= 128 * 128 ? launch_skinny<F, 4, 4, 2>(a, stream) : launch_skinny<F, 8, 8, 1>(a, stream);
@@ -877,7 +887,8 @@ hipError_t launch_mx8_logits(const void *hidden, int32_t hidden_type, const uint
     // Whole 16-bit rows of one tile are quantised by each workgroup, not by a launch before: measured
     // (us, each workgroup / a launch before, 1 and 16 rows) 1000 x 1024: 4.2 / 5.3, 4.5 / 6.1;
     // 8000 x 2048: 6.6 / 8.0, 7.7 / 9.1; 32768 x 2048: 13.8 / 14.4, 15.4 / 16.2; but 129280 x 7168:
-    // 142.5 / 142.2, 152.8 / 149.5, and 32768 x 2048 of fp32 rows 14.7 / 14.3, 19.3 / 16.0.
+    // 142.5 / 142.2, 152.8 / 149.5, and 32768 x 2048 of fp32 rows 14.7 / 14.3, 19.3 / 16.0. Ids decide, not
+    // the depth: 8000 x 7168 14.7 / 16.1, 17.7 / 19.2; 129280 x 2048 46.0 / 45.6, 53.6 / 51.2.
     if (M <= 16 && V <= 65536 && d == kp && hidden_type != SD_F32 && vec_rows(hidden, hidden_type, stride, 8) && !coded) {
       a.hstride = stride;
       return hidden_type == SD_BF16 ? launch_skinny_of<Mx8Of<SD_BF16>, 4, 1, 4, 2>(a, stream)

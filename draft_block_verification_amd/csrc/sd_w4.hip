@@ -81,9 +81,9 @@ __device__ __forceinline__ float scale_value(uint16_t bits, int32_t type) {
 }
 
 // An item is eight columns, G / 8 neighbouring threads hold a group; a thread takes U items 256
-// apart, its loads issued together. 151936 x 4096 fp16 in groups of 32: 320 us (1.6 GB, 5.0 TB/s);
-// 32768 x 2048 bf16 with zeros in groups of 128: 44 us (170 MB, 3.9 TB/s; some 13 vector operations a
-// column, the rounding of its quotient above all).
+// apart, its loads issued together. 151936 x 4096 fp16 in groups of 32: 310 us (1.6 GB, 5.1 TB/s);
+// 32768 x 2048 bf16 with zeros in groups of 128: 44 us in a row of calls (170 MB, 3.9 TB/s; some 13
+// vector operations a column, the rounding of its quotient above all), 51 alone under the profiler.
 template <int T, int U, int G>
 __global__ __launch_bounds__(256) void k_w4_quantize(W4Args a) {
   const int per = a.d / 8;        // a multiple of G / 8: a group's items are all in or all out
@@ -143,8 +143,8 @@ __global__ __launch_bounds__(256) void k_w4_quantize(W4Args a) {
   }
 }
 
-// x[row][8 c ..]: (code - zero) scale, exact in fp32, rounded once. 151936 x 4096 into bf16: 275 us
-// (5.8 TB/s).
+// x[row][8 c ..]: (code - zero) scale, exact in fp32, rounded once. 151936 x 4096 into bf16: 280 us
+// (5.7 TB/s).
 template <int T, int U, int G>
 __global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a, void *x) {
   const int per = a.d / 8;
